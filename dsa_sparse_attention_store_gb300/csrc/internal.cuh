@@ -111,4 +111,28 @@ dsa_status launch_topk(dsa_ctx* ctx, const void* q, const float* head_w, const v
                        int32_t B, int32_t Tq, int32_t causal, int32_t k, int32_t* out_idx,
                        float* out_score, void* workspace, size_t ws_bytes, cudaStream_t stream);
 
+dsa_status rope_create(dsa_ctx* ctx, dsa_rope** out, const dsa_rope_desc& desc);
+
+dsa_status launch_rope(dsa_ctx* ctx, const dsa_rope* rope, const void* x, void* y, dsa_dtype dtype,
+                       const int32_t* pos, int32_t T, int32_t H, int32_t D, int32_t start, long long xt,
+                       long long xh, long long yt, long long yh, int32_t inverse, cudaStream_t stream);
+
+size_t kv_page_bytes(int32_t kv_heads, int32_t head_dim, dsa_fmt fmt);
+
+dsa_status launch_kv_store(dsa_ctx* ctx, const void* k, const void* v, long long kt, long long kh, long long vt,
+                           long long vh, const int32_t* cache_pos, const int32_t* seq_id,
+                           const int32_t* page_table, int32_t T, int32_t B, int32_t max_pages, int32_t kv_heads,
+                           int32_t head_dim, void* cache, int32_t num_pages, dsa_fmt fmt, const dsa_rope* rope,
+                           const int32_t* rope_pos, int32_t start, cudaStream_t stream);
+
+dsa_status launch_kv_load(dsa_ctx* ctx, const void* cache, int32_t num_pages, dsa_fmt fmt, int32_t kv_heads,
+                          int32_t head_dim, const int32_t* cache_pos, const int32_t* seq_id,
+                          const int32_t* page_table, int32_t T, int32_t B, int32_t max_pages, void* k, void* v,
+                          long long kt, long long kh, long long vt, long long vh, cudaStream_t stream);
+
+size_t attn_workspace(const dsa_ctx* ctx, int32_t head_dim);
+
+// sel NULL: the tree form
+dsa_status launch_attn(dsa_ctx* ctx, const dsa_attn_args& args, const int32_t* sel, int32_t k, cudaStream_t stream);
+
 }  // namespace dsa

@@ -1,0 +1,101 @@
+// The K/V cache's page layout and its fp8 / fp4 codes.
+//
+// A page holds 64 tokens. It is one block per kv head, and a head's block is
+//   K codes [64][CB]  V codes [64][CB]  K scales [64][D/32]  V scales [64][D/32]
+// (no scales in bf16), so one head's keys of a page are one contiguous tile.
+// In fp8 (e4m3) and fp4 (e2m1) 32 dimensions share a power-of-two scale, a
+// byte holding its exponent + 127: the OCP microscaling formats MXFP8 and
+// MXFP4, with the exponent rounded up so that no value saturates. A stored
+// value is then a bf16 number exactly: a code has at most 4 significant bits
+// and the scale moves only the exponent. Reading back loses nothing, and the
+// attention's bf16 tensor-core operands are the stored values themselves.
+#pragma once
+#include <cuda_bf16.h>
+
+#include "internal.cuh"
+
+namespace dsa {
+namespace kvf {
+
+constexpr int kPage = 64;
+constexpr int kBlock = 32;  // dimensions that share a scale
+
+template <int FMT, int D>
+struct Layout {
+  static constexpr int CB = FMT == DSA_FMT_BF16 ? 2 * D : FMT == DSA_FMT_FP8 ? D : D / 2;  // code bytes a row
+  static constexpr int SB = FMT == DSA_FMT_BF16 ? 0 : D / kBlock;                          // scale bytes a row
+  static constexpr int K_CODES = 0;
+  static constexpr int V_CODES = kPage * CB;
+  static constexpr int K_SCALES = 2 * kPage * CB;
+  static constexpr int V_SCALES = 2 * kPage * CB + kPage * SB;
+  static constexpr int HEAD_BYTES = 2 * kPage * (CB + SB);
+};
+
+// Exponent limits: the smallest keeps every code's value a normal bf16
+// number, the largest keeps the largest code finite in bf16.
+template <int FMT>
+struct Scale {
+  static constexpr int LO = FMT == DSA_FMT_FP8 ? -117 : -125;
+  static constexpr int HI = FMT == DSA_FMT_FP8 ? 119 : 125;
+  // smallest e with amax <= MAX 2^e, MAX = 448 = 1.75 2^8 or 6 = 1.5 2^2,
+  // from amax's bits (finite): its exponent, one more if the mantissa is above MAX's
+  static __device__ __forceinline__ int exponent(uint32_t amax) {
+    const int e = static_cast<int>(amax >> 23) - 127 - (FMT == DSA_FMT_FP8 ? 8 : 2) +
+                  ((amax & 0x7FFFFFu) > (FMT == DSA_FMT_FP8 ? 0x600000u : 0x400000u) ? 1 : 0);
+    return min(max(e, LO), HI);
+  }
+};
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  __nv_bfloat162 x, y;
+  memcpy(&x, &a, 4);
+  memcpy(&y, &b, 4);
+  const __nv_bfloat162 r = __hmul2_rn(x, y);
+  uint32_t o;
+  memcpy(&o, &r, 4);
+  return o;
+}
+
+// The factors that turn a code placed in a bf16's bits into its value. The
+// code's sign, exponent and mantissa are moved to where bf16 has them; read
+// as bf16 that is value * 2^-BIAS (the subnormal codes too, as bf16
+// subnormals), so one multiplication by 2^(BIAS + e) gives the value,
+// exactly. Above 2^127 it takes two. Scale byte 255 stands for NaN.
+template <int FMT>
+struct Factor {
+  static constexpr int BIAS = FMT == DSA_FMT_FP8 ? 120 : 126;
+  static constexpr uint32_t ONE = 254 - BIAS;  // the largest scale byte one factor covers
+  uint32_t f, g;  // bf16x2 factors; g only where `two`
+  bool two;
+  __device__ __forceinline__ explicit Factor(uint32_t byte) {
+    two = byte > ONE;
+    const uint32_t f1 = (two ? 127u + BIAS : byte + BIAS) << 7;
+    const uint32_t g1 = byte == 255u ? 0x7FFFu : byte << 7;
+    f = f1 | (f1 << 16);
+    g = g1 | (g1 << 16);
+  }
+  __device__ __forceinline__ uint32_t apply(uint32_t r) const {
+    r = mul_bf16x2(r, f);
+    return two ? mul_bf16x2(r, g) : r;
+  }
+};
+
+// four e4m3 codes -> four bf16 (two words)
+__device__ __forceinline__ void widen_e4m3(uint32_t w, const Factor<DSA_FMT_FP8>& s, uint32_t (&o)[2]) {
+  const uint32_t a = __byte_perm(w, 0, 0x1404), b = __byte_perm(w, 0, 0x3424);  // codes in the high bytes
+  o[0] = s.apply((a & 0x80008000u) | ((a >> 4) & 0x07F007F0u));
+  o[1] = s.apply((b & 0x80008000u) | ((b >> 4) & 0x07F007F0u));
+}
+
+// eight e2m1 codes (the even dimension in the low nibble) -> eight bf16
+__device__ __forceinline__ void widen_e2m1(uint32_t w, const Factor<DSA_FMT_FP4>& s, uint32_t (&o)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t b = w >> (8 * i);
+    const uint32_t t = (b & 0xFu) | ((b & 0xF0u) << 12);  // codes in the low nibbles of both halves
+    o[i] = s.apply(((t & 0x00080008u) << 12) | ((t & 0x00070007u) << 6));
+  }
+}
+
+}  // namespace kvf
+}  // namespace dsa

@@ -1,6 +1,6 @@
 """Python binding of libdsaidx: argument marshalling only.
 
-Every step of the indexer runs in the library's CUDA kernels; this module
+Every step of the indexer, and of the attention after it, runs in the library's CUDA kernels; this module
 checks tensor shapes/dtypes, passes device pointers and the current CUDA
 stream through the C ABI declared in include/dsaidx.h, and raises on a
 non-zero status. There is no fallback: without the built library every call
@@ -14,7 +14,8 @@ import os
 FMT_BF16 = 0
 FMT_FP8 = 1
 FMT_FP4 = 2
-KERNEL_KINDS = ("store", "plan", "score_bf16", "score_fp8", "score_fp4")
+KERNEL_KINDS = ("store", "plan", "score_bf16", "score_fp8", "score_fp4", "rope", "kv_store", "kv_load",
+                "attn", "attn_join")
 HEADS = 64
 HEAD_DIM = 128
 PAGE_SIZE = 64
@@ -24,8 +25,28 @@ LIB_PATH = os.path.join(_HERE, "libdsaidx.so")
 _lib = None
 
 _c_int = ctypes.c_int32
+_c_i64 = ctypes.c_int64
 _c_ptr = ctypes.c_void_p
 _c_size = ctypes.c_size_t
+_c_f64 = ctypes.c_double
+
+ROPE_LAYOUTS = ("half", "interleaved")
+ROPE_SCALINGS = ("none", "linear", "by_parts")
+
+
+class _RopeDesc(ctypes.Structure):  # dsa_rope_desc
+    _fields_ = [("theta", _c_f64), ("rot_dim", _c_int), ("max_pos", _c_int), ("layout", _c_int),
+                ("scaling", _c_int), ("factor", _c_f64), ("orig_max_pos", _c_f64), ("beta_slow", _c_f64),
+                ("beta_fast", _c_f64), ("mscale", _c_f64)]
+
+
+class _AttnArgs(ctypes.Structure):  # dsa_attn_args
+    _fields_ = [("q", _c_ptr), ("q_stride_t", _c_i64), ("q_stride_h", _c_i64), ("out", _c_ptr),
+                ("out_stride_t", _c_i64), ("out_stride_h", _c_i64), ("lse", _c_ptr), ("cache", _c_ptr),
+                ("num_pages", _c_int), ("fmt", ctypes.c_int), ("heads", _c_int), ("kv_heads", _c_int),
+                ("head_dim", _c_int), ("page_table", _c_ptr), ("max_pages", _c_int), ("seq_lens", _c_ptr),
+                ("cu_q", _c_ptr), ("B", _c_int), ("Tq", _c_int), ("mask", _c_ptr), ("mask_words", _c_int),
+                ("scale", _c_f64), ("workspace", _c_ptr), ("ws_bytes", _c_size)]
 
 
 class DsaError(RuntimeError):
@@ -72,6 +93,24 @@ def lib() -> ctypes.CDLL:
         L.dsa_profile_enable.restype = ctypes.c_int
         L.dsa_profile_read.argtypes = [_c_ptr, ctypes.POINTER(ctypes.c_float), ctypes.POINTER(_c_int)]
         L.dsa_profile_read.restype = ctypes.c_int
+        L.dsa_rope_create.argtypes = [_c_ptr, ctypes.POINTER(_c_ptr), ctypes.POINTER(_RopeDesc)]
+        L.dsa_rope_destroy.argtypes = [_c_ptr]
+        L.dsa_rope_apply.argtypes = [_c_ptr, _c_ptr, _c_ptr, _c_ptr, ctypes.c_int, _c_ptr, _c_int, _c_int,
+                                     _c_int, _c_int, _c_i64, _c_i64, _c_i64, _c_i64, _c_int, _c_ptr]
+        L.dsa_kv_page_bytes.argtypes = [_c_int, _c_int, ctypes.c_int]
+        L.dsa_kv_page_bytes.restype = _c_size
+        L.dsa_kv_store.argtypes = [_c_ptr, _c_ptr, _c_ptr, _c_i64, _c_i64, _c_i64, _c_i64, _c_ptr, _c_ptr, _c_ptr,
+                                   _c_int, _c_int, _c_int, _c_int, _c_int, _c_ptr, _c_int, ctypes.c_int, _c_ptr,
+                                   _c_ptr, _c_int, _c_ptr]
+        L.dsa_kv_load.argtypes = [_c_ptr, _c_ptr, _c_int, ctypes.c_int, _c_int, _c_int, _c_ptr, _c_ptr, _c_ptr,
+                                  _c_int, _c_int, _c_int, _c_ptr, _c_ptr, _c_i64, _c_i64, _c_i64, _c_i64, _c_ptr]
+        L.dsa_attn_workspace_size.argtypes = [_c_ptr, _c_int]
+        L.dsa_attn_workspace_size.restype = _c_size
+        L.dsa_tree_attn.argtypes = [_c_ptr, ctypes.POINTER(_AttnArgs), _c_ptr]
+        L.dsa_sparse_attn.argtypes = [_c_ptr, ctypes.POINTER(_AttnArgs), _c_ptr, _c_int, _c_ptr]
+        for f in (L.dsa_rope_create, L.dsa_rope_destroy, L.dsa_rope_apply, L.dsa_kv_store, L.dsa_kv_load,
+                  L.dsa_tree_attn, L.dsa_sparse_attn):
+            f.restype = ctypes.c_int
         L.dsa_status_str.argtypes = [ctypes.c_int]
         L.dsa_status_str.restype = ctypes.c_char_p
         _lib = L
@@ -87,6 +126,11 @@ def status_str(s: int) -> str:
 
 def page_bytes(fmt: int) -> int:
     return int(lib().dsa_cache_page_bytes(int(fmt)))
+
+
+def kv_page_bytes(kv_heads: int, head_dim: int, fmt: int) -> int:
+    """Bytes of a K/V cache page (64 tokens, every kv head)."""
+    return int(lib().dsa_kv_page_bytes(_c_int(kv_heads), _c_int(head_dim), int(fmt)))
 
 
 def _stream_ptr(stream):
@@ -109,6 +153,66 @@ def _dev(t, dtype, shape=None, name="tensor"):
     if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     return _c_ptr(t.data_ptr())
+
+
+def _rows(t, dtype, shape, name):
+    """Pointer and (token, head) strides of a [tokens, heads, dims] tensor whose
+    dims are contiguous."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 3 or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    # a dimension of one element has no stride to speak of
+    st = 0 if t.shape[0] <= 1 else t.stride(0)
+    sh = 0 if t.shape[1] <= 1 else t.stride(1)
+    return _c_ptr(t.data_ptr()), _c_i64(st), _c_i64(sh)
+
+
+class Rope:
+    """A rotary plan (dsa_rope): the cos/sin table of one set of parameters.
+
+    layout: "half" pairs (i, i + rot_dim/2), "interleaved" (2i, 2i+1).
+    scaling: "none", "linear" (frequencies / factor) or "by_parts" (divided
+    where a pair turns fewer than beta_slow times over orig_max_pos, kept where
+    more than beta_fast times, blended between). mscale multiplies cos and sin.
+    """
+
+    def __init__(self, ctx: "Context", rot_dim: int, max_pos: int, theta: float = 10000.0, layout: str = "half",
+                 scaling: str = "none", factor: float = 1.0, orig_max_pos: float = 32768, beta_slow: float = 1.0,
+                 beta_fast: float = 32.0, mscale: float = 1.0):
+        if layout not in ROPE_LAYOUTS:
+            raise ValueError(f"layout must be one of {ROPE_LAYOUTS}")
+        if scaling not in ROPE_SCALINGS:
+            raise ValueError(f"scaling must be one of {ROPE_SCALINGS}")
+        self.rot_dim, self.max_pos = int(rot_dim), int(max_pos)
+        d = _RopeDesc(float(theta), self.rot_dim, self.max_pos, ROPE_LAYOUTS.index(layout),
+                      ROPE_SCALINGS.index(scaling), float(factor), float(orig_max_pos), float(beta_slow),
+                      float(beta_fast), float(mscale))
+        h = _c_ptr()
+        st = lib().dsa_rope_create(ctx.handle, ctypes.byref(h), ctypes.byref(d))
+        if st != 0:
+            raise DsaError("dsa_rope_create", st)
+        self._h = h
+
+    @property
+    def handle(self):
+        return self._h
+
+    def close(self):
+        if getattr(self, "_h", None):
+            lib().dsa_rope_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
 
 
 class Context:
@@ -203,6 +307,123 @@ class Context:
             _dev(out_score, torch.float32, (Tq, k), "out_score"), _stream_ptr(stream))
         if st != 0:
             raise DsaError("dsa_index_topk_static", st)
+
+    def rope_apply(self, x, pos, rope: Rope, out=None, rot_start: int = 0, inverse: bool = False, stream=None):
+        """dsa_rope_apply: rotate [T, H, D] rows (bf16, fp16 or fp32) to their
+        positions, into `out` or in place. `inverse` turns back (the gradient)."""
+        import torch
+        dt = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+        if not isinstance(x, torch.Tensor) or x.dtype not in dt:
+            raise TypeError("x must be a bf16, fp16 or fp32 CUDA tensor")
+        if x.dim() != 3:
+            raise ValueError(f"x must be [T, H, D], got {tuple(x.shape)}")
+        out = x if out is None else out
+        xp, xt, xh = _rows(x, x.dtype, x.shape, "x")
+        yp, yt, yh = _rows(out, x.dtype, x.shape, "out")
+        T, H, D = (int(n) for n in x.shape)
+        st = lib().dsa_rope_apply(self._h, rope.handle, xp, yp, dt[x.dtype], _dev(pos, torch.int32, (T,), "pos"),
+                                  _c_int(T), _c_int(H), _c_int(D), _c_int(rot_start), xt, xh, yt, yh,
+                                  _c_int(1 if inverse else 0), _stream_ptr(stream))
+        if st != 0:
+            raise DsaError("dsa_rope_apply", st)
+
+    def kv_store(self, k, v, cache_pos, seq_id, page_table, cache, num_pages: int, fmt: int, rope=None,
+                 rope_pos=None, rot_start: int = 0, stream=None):
+        """dsa_kv_store: write [T, kv_heads, head_dim] bf16 keys (rotated when a
+        plan is given) and values into the paged K/V cache."""
+        import torch
+        shape = tuple(k.shape)
+        kp, kt, kh = _rows(k, torch.bfloat16, shape, "k")
+        vp, vt, vh = _rows(v, torch.bfloat16, shape, "v")
+        T, n, D = (int(x) for x in shape)
+        B, max_pages = int(page_table.shape[0]), int(page_table.shape[1])
+        self._kv_cache(cache, num_pages, n, D, fmt)
+        st = lib().dsa_kv_store(
+            self._h, kp, vp, kt, kh, vt, vh, _dev(cache_pos, torch.int32, (T,), "cache_pos"),
+            _dev(seq_id, torch.int32, (T,), "seq_id"), _dev(page_table, torch.int32, None, "page_table"), _c_int(T),
+            _c_int(B), _c_int(max_pages), _c_int(n), _c_int(D), _dev(cache, torch.uint8, None, "cache"),
+            _c_int(num_pages), int(fmt), None if rope is None else rope.handle,
+            None if rope_pos is None else _dev(rope_pos, torch.int32, (T,), "rope_pos"), _c_int(rot_start),
+            _stream_ptr(stream))
+        if st != 0:
+            raise DsaError("dsa_kv_store", st)
+
+    def kv_load(self, cache, num_pages: int, fmt: int, cache_pos, seq_id, page_table, k, v, stream=None):
+        """dsa_kv_load: read tokens of the K/V cache back into k and v, [T,
+        kv_heads, head_dim] bf16."""
+        import torch
+        shape = tuple(k.shape)
+        kp, kt, kh = _rows(k, torch.bfloat16, shape, "k")
+        vp, vt, vh = _rows(v, torch.bfloat16, shape, "v")
+        T, n, D = (int(x) for x in shape)
+        B, max_pages = int(page_table.shape[0]), int(page_table.shape[1])
+        self._kv_cache(cache, num_pages, n, D, fmt)
+        st = lib().dsa_kv_load(
+            self._h, _dev(cache, torch.uint8, None, "cache"), _c_int(num_pages), int(fmt), _c_int(n), _c_int(D),
+            _dev(cache_pos, torch.int32, (T,), "cache_pos"), _dev(seq_id, torch.int32, (T,), "seq_id"),
+            _dev(page_table, torch.int32, None, "page_table"), _c_int(T), _c_int(B), _c_int(max_pages), kp, vp, kt,
+            kh, vt, vh, _stream_ptr(stream))
+        if st != 0:
+            raise DsaError("dsa_kv_load", st)
+
+    @staticmethod
+    def _kv_cache(cache, num_pages, kv_heads, head_dim, fmt):
+        need = int(num_pages) * kv_page_bytes(kv_heads, head_dim, fmt)
+        if need and cache.numel() < need:
+            raise ValueError(f"cache must have at least {need} bytes, got {cache.numel()}")
+
+    def attn_workspace_size(self, head_dim: int) -> int:
+        return int(lib().dsa_attn_workspace_size(self._h, _c_int(head_dim)))
+
+    def _attn_args(self, q, cache, num_pages, fmt, kv_heads, page_table, seq_lens, cu_q, out, workspace, mask, lse,
+                   scale):
+        import torch
+        if not isinstance(q, torch.Tensor) or q.dim() != 3:
+            raise ValueError("q must be a [Tq, heads, head_dim] tensor")
+        Tq, H, D = (int(n) for n in q.shape)
+        qp, qt, qh = _rows(q, torch.bfloat16, q.shape, "q")
+        op, ot, oh = _rows(out, torch.bfloat16, q.shape, "out")
+        B, max_pages = int(page_table.shape[0]), int(page_table.shape[1])
+        self._kv_cache(cache, num_pages, kv_heads, D, fmt)
+        mp, words = None, 0
+        if mask is not None:
+            if mask.dim() != 2:
+                raise ValueError("mask must be [Tq, words]")
+            words = int(mask.shape[1])
+            mp = _dev(mask, torch.int32, (Tq, words), "mask")
+        return _AttnArgs(
+            qp, qt, qh, op, ot, oh, None if lse is None else _dev(lse, torch.float32, (Tq, H), "lse"),
+            _dev(cache, torch.uint8, None, "cache"), _c_int(num_pages), int(fmt), _c_int(H), _c_int(kv_heads),
+            _c_int(D), _dev(page_table, torch.int32, None, "page_table"), _c_int(max_pages),
+            _dev(seq_lens, torch.int32, (B,), "seq_lens"), _dev(cu_q, torch.int32, (B + 1,), "cu_q"), _c_int(B),
+            _c_int(Tq), mp, _c_int(words), D ** -0.5 if scale is None else float(scale),
+            _dev(workspace, torch.uint8, None, "workspace"), _c_size(workspace.numel()))
+
+    def tree_attn(self, q, cache, num_pages: int, fmt: int, kv_heads: int, page_table, seq_lens, cu_q, out,
+                  workspace, mask=None, lse=None, scale=None, stream=None):
+        """dsa_tree_attn: attention of each sequence's new tokens over its cache.
+        mask: int32 [Tq, words], bit j of a row: it sees the sequence's j-th new
+        token; None: token i sees the new tokens up to i."""
+        a = self._attn_args(q, cache, num_pages, fmt, kv_heads, page_table, seq_lens, cu_q, out, workspace, mask,
+                            lse, scale)
+        st = lib().dsa_tree_attn(self._h, ctypes.byref(a), _stream_ptr(stream))
+        if st != 0:
+            raise DsaError("dsa_tree_attn", st)
+
+    def sparse_attn(self, q, sel, cache, num_pages: int, fmt: int, kv_heads: int, page_table, seq_lens, cu_q, out,
+                    workspace, mask=None, lse=None, scale=None, stream=None):
+        """dsa_sparse_attn: attention of each query over its selected keys (topk()'s
+        out_idx) and, with a mask, over the new tokens whose bits are set."""
+        import torch
+        if not isinstance(sel, torch.Tensor) or sel.dim() != 2:
+            raise ValueError("sel must be a [Tq, k] tensor")
+        k = int(sel.shape[1])
+        a = self._attn_args(q, cache, num_pages, fmt, kv_heads, page_table, seq_lens, cu_q, out, workspace, mask,
+                            lse, scale)
+        st = lib().dsa_sparse_attn(self._h, ctypes.byref(a), _dev(sel, torch.int32, (int(q.shape[0]), k), "sel"),
+                                   _c_int(k), _stream_ptr(stream))
+        if st != 0:
+            raise DsaError("dsa_sparse_attn", st)
 
     def set_hadamard(self, on: bool = True):
         """Store keys (and rotate queries) with the 128-point Walsh-Hadamard transform."""

@@ -1,6 +1,8 @@
 /*
  * libdsaidx -- the DeepSeek Sparse Attention (DSA) indexer hot path on one
- * GB300 GPU: the index-key store and the score + top-k selection.
+ * GB300 GPU: the index-key store and the score + top-k selection; and the
+ * attention it serves: rotary positions, the K/V cache, attention of drafted
+ * tokens over it and over the selection.
  *
  * Sources (web pages on the bf16 index-K fix in the DSA indexer):
  *  [VAL] "The Moment of Validation: Diagnosing an OOM Crash in the bf16 Index-K
@@ -229,6 +231,161 @@ dsa_status dsa_index_topk_static(dsa_ctx* ctx, const void* q, const float* head_
                                  int32_t Tq, int32_t causal, int32_t k, int32_t* out_idx,
                                  float* out_score, dsa_stream_t stream);
 
+/* ---------------------------------------------------------------- attention
+ * What follows the indexer in a serving step: rotating the queries, the main
+ * K/V cache, and attention over it, for all keys or for the selected ones.
+ * These calls keep the conventions above; element strides are in elements,
+ * the innermost dimension is contiguous. */
+
+/* A rotary plan: the cos/sin table of one set of rotary parameters. The
+ * rotated part of a head has rot_dim dimensions; pair i of it is (i, i +
+ * rot_dim/2) in the half layout, (2i, 2i+1) in the interleaved one, and turns
+ * by position * f_i, f_i = theta^(-2i/rot_dim), scaled for long contexts:
+ *  DSA_ROPE_LINEAR    f_i / factor
+ *  DSA_ROPE_BY_PARTS  with turns r_i = orig_max_pos f_i / (2 pi) and
+ *                     g = clamp((r_i - beta_slow) / (beta_fast - beta_slow), 0, 1):
+ *                     f_i / factor * (1 - g) + f_i * g
+ * Every cos and sin is multiplied by mscale (1 leaves lengths as they are).
+ * Angles are computed in double, cos and sin rounded once to fp32. */
+typedef enum { DSA_ROPE_HALF = 0, DSA_ROPE_INTERLEAVED = 1 } dsa_rope_layout;
+typedef enum { DSA_ROPE_PLAIN = 0, DSA_ROPE_LINEAR = 1, DSA_ROPE_BY_PARTS = 2 } dsa_rope_scaling;
+typedef enum { DSA_BF16 = 0, DSA_F16 = 1, DSA_F32 = 2 } dsa_dtype;
+typedef struct {
+  double theta;         /* > 0 */
+  int32_t rot_dim;      /* even, 2 .. 1024 */
+  int32_t max_pos;      /* positions 0 .. max_pos-1; the table takes max_pos * rot_dim * 4 bytes */
+  int32_t layout;       /* dsa_rope_layout */
+  int32_t scaling;      /* dsa_rope_scaling */
+  double factor;        /* LINEAR, BY_PARTS: > 0 */
+  double orig_max_pos;  /* BY_PARTS: > 0 */
+  double beta_slow;     /* BY_PARTS: < beta_fast */
+  double beta_fast;
+  double mscale;        /* > 0 */
+} dsa_rope_desc;
+typedef struct dsa_rope dsa_rope;
+
+/* Allocates the table on the context's device and fills it; synchronises, so
+ * not during a stream capture. dsa_rope_destroy synchronises the device. */
+dsa_status dsa_rope_create(dsa_ctx* ctx, dsa_rope** out, const dsa_rope_desc* desc);
+dsa_status dsa_rope_destroy(dsa_rope* rope);
+
+/* y[t][h] = x[t][h] with dimensions rot_start .. rot_start + rot_dim - 1
+ * rotated to position pos[t] and the others copied; `inverse` turns the other
+ * way, which is also the gradient with respect to x of a forward rotation.
+ * fp32 arithmetic, every product and sum rounded separately, one rounding to
+ * the type.
+ *  x, y   (device) [T][H][D] of dtype, any strides of tokens and heads. y == x
+ *         with the same strides rotates in place; otherwise they must not overlap.
+ *  pos    (device) [T] int32. A token whose position is out of range is not
+ *         written and DSA_ERR_DEVICE_BOUNDS is recorded.
+ * Any D, H and alignment of the type's own size; 16-byte aligned rows and
+ * parts run 16 bytes at a time. */
+dsa_status dsa_rope_apply(dsa_ctx* ctx, const dsa_rope* rope, const void* x, void* y, dsa_dtype dtype,
+                          const int32_t* pos, int32_t T, int32_t H, int32_t D, int32_t rot_start,
+                          int64_t x_stride_t, int64_t x_stride_h, int64_t y_stride_t,
+                          int64_t y_stride_h, int32_t inverse, dsa_stream_t stream);
+
+/* The K/V cache: pages of 64 tokens like the index cache (a page table can
+ * serve both), for kv_heads heads of head_dim 64 or 128. A page is kv_heads
+ * blocks of
+ *   K codes [64][CB], V codes [64][CB], K scales [64][SB], V scales [64][SB]
+ *   DSA_FMT_BF16  CB = 2 head_dim, SB = 0
+ *   DSA_FMT_FP8   CB = head_dim (e4m3), SB = head_dim / 32
+ *   DSA_FMT_FP4   CB = head_dim / 2 (e2m1, the even dimension in the low
+ *                 nibble), SB = head_dim / 32
+ * In fp8 and fp4, 32 dimensions share the power of two 2^e, stored as the
+ * byte e + 127: e is the smallest integer with max|y| <= 448 * 2^e (fp8) or
+ * 6 * 2^e (fp4), within -117 .. 119 or -125 .. 125, so a code never saturates
+ * and a stored value is a bf16 number exactly (OCP microscaling layouts with
+ * the exponent rounded up). 32 dimensions of which one is not finite get the
+ * byte 255 and read as NaN. Not the index cache's scales: those are one fp32
+ * per token. Returns 0 for unsupported arguments. */
+size_t dsa_kv_page_bytes(int32_t kv_heads, int32_t head_dim, dsa_fmt fmt);
+
+/* Write tokens: k (rotated first, when rope is given) and v to slot
+ * cache_pos % 64 of page page_table[seq_id][cache_pos / 64], rounded to
+ * nearest even once, from fp32.
+ *  k, v        (device) [T][kv_heads][head_dim] bf16, 16-byte aligned, strides
+ *              multiples of 8 elements.
+ *  cache_pos   (device) [T] int32: the token's place in its sequence's pages.
+ *  rope_pos    (device) [T] int32 rotary positions, or NULL for cache_pos
+ *              (drafted tokens of a tree lie one after another in the cache
+ *              but their positions follow their depth).
+ *  rope        rotates dimensions rot_start .. of k; NULL for none.
+ *  cache       (device) num_pages * dsa_kv_page_bytes bytes, 256-byte aligned.
+ * Tokens must not share a slot within one call. A token whose sequence,
+ * place, page or rotary position is out of range is skipped and
+ * DSA_ERR_DEVICE_BOUNDS recorded. */
+dsa_status dsa_kv_store(dsa_ctx* ctx, const void* k, const void* v, int64_t k_stride_t, int64_t k_stride_h,
+                        int64_t v_stride_t, int64_t v_stride_h, const int32_t* cache_pos,
+                        const int32_t* seq_id, const int32_t* page_table, int32_t T, int32_t B,
+                        int32_t max_pages, int32_t kv_heads, int32_t head_dim, void* cache,
+                        int32_t num_pages, dsa_fmt fmt, const dsa_rope* rope, const int32_t* rope_pos,
+                        int32_t rot_start, dsa_stream_t stream);
+
+/* Read tokens back as bf16 (exact: the values the cache stands for) into k
+ * and v, laid out and aligned as dsa_kv_store's. A token whose sequence,
+ * place or page is out of range reads as zeros, and DSA_ERR_DEVICE_BOUNDS is
+ * recorded. */
+dsa_status dsa_kv_load(dsa_ctx* ctx, const void* cache, int32_t num_pages, dsa_fmt fmt, int32_t kv_heads,
+                       int32_t head_dim, const int32_t* cache_pos, const int32_t* seq_id,
+                       const int32_t* page_table, int32_t T, int32_t B, int32_t max_pages, void* k,
+                       void* v, int64_t k_stride_t, int64_t k_stride_h, int64_t v_stride_t,
+                       int64_t v_stride_h, dsa_stream_t stream);
+
+/* Arguments of the attention calls. Rows cu_q[b] .. cu_q[b+1]-1 of q are the
+ * n_b query tokens of sequence b, whose own keys and values are the last n_b
+ * of its seq_lens[b] cache places (written before the call); the others are
+ * its committed context. Query head h reads kv head h / (heads / kv_heads). */
+typedef struct {
+  const void* q;            /* (device) [Tq][heads][head_dim] bf16, 16-byte aligned */
+  int64_t q_stride_t, q_stride_h;      /* multiples of 8 */
+  void* out;                /* (device) [Tq][heads][head_dim] bf16, 16-byte aligned */
+  int64_t out_stride_t, out_stride_h;  /* multiples of 8 */
+  float* lse;               /* (device) [Tq][heads] log of the sum of exp(score), or NULL */
+  const void* cache;        /* (device) as written by dsa_kv_store, 256-byte aligned */
+  int32_t num_pages;
+  dsa_fmt fmt;
+  int32_t heads, kv_heads, head_dim;
+  const int32_t* page_table;  /* (device) [B][max_pages] */
+  int32_t max_pages;
+  const int32_t* seq_lens;    /* (device) [B], n_b <= seq_lens[b] <= 64 * max_pages */
+  const int32_t* cu_q;        /* (device) [B+1], cu_q[0] = 0, non-decreasing, cu_q[B] = Tq */
+  int32_t B, Tq;
+  const uint32_t* mask;       /* (device) [Tq][mask_words] bits, or NULL */
+  int32_t mask_words;
+  double scale;               /* of q.k, > 0 */
+  void* workspace;            /* (device) >= dsa_attn_workspace_size bytes, 256-byte aligned, scratch */
+  size_t ws_bytes;
+} dsa_attn_args;
+
+/* Workspace of both calls: two partial results per CTA, whatever the sizes
+ * of the call. 0 for an unsupported head_dim. */
+size_t dsa_attn_workspace_size(const dsa_ctx* ctx, int32_t head_dim);
+
+/* Attention of drafted tokens over the cache: query i of sequence b sees the
+ * whole committed context and the drafted token j of its own sequence where
+ * bit j of its mask row is set (usually its ancestors in the tree and
+ * itself), or where j <= i without a mask (a chain: a chunk of a prefill; one
+ * token: a decode step). out = softmax(scale q.k) v; a row that sees no key
+ * gives zeros and lse -inf. What the cache holds in places a row does not see
+ * does not reach it, infinities and NaN included. Keys of a page out of range
+ * are left out and DSA_ERR_DEVICE_BOUNDS recorded; so are whole sequences
+ * whose lengths are inconsistent (their rows are not written).
+ * Tq * heads < 2^31. Results do not depend on timing. */
+dsa_status dsa_tree_attn(dsa_ctx* ctx, const dsa_attn_args* args, dsa_stream_t stream);
+
+/* Attention over a selection: query row t sees the keys sel[t][0 .. k-1] of
+ * its sequence (as dsa_index_topk writes them: positions, or cache slots when
+ * slot output is on; negative entries are skipped), and, with a mask, the
+ * drafted tokens whose bits are set. An entry out of range (a position at or
+ * past seq_lens[b], a slot past the cache) is left out and
+ * DSA_ERR_DEVICE_BOUNDS recorded; a key listed twice counts twice. Otherwise
+ * as dsa_tree_attn (a query of an inconsistent sequence gives zeros).
+ *  sel  (device) [Tq][k] int32, 1 <= k <= 65536.  heads / kv_heads <= 128. */
+dsa_status dsa_sparse_attn(dsa_ctx* ctx, const dsa_attn_args* args, const int32_t* sel, int32_t k,
+                           dsa_stream_t stream);
+
 /* Kernel timing, for benchmarks and profiling. While enabled, the library
  * records a CUDA event pair on the launch stream around each kernel it
  * launches (at most 8192 pairs between reads; later launches are counted but
@@ -241,7 +398,12 @@ typedef enum {
   DSA_K_SCORE_BF16 = 2, /* dsa_index_topk: tensor-core scorer + running top-k, bf16 cache */
   DSA_K_SCORE_FP8 = 3,  /* the same, fp8 cache */
   DSA_K_SCORE_FP4 = 4,  /* the same, fp4 cache */
-  DSA_K_COUNT = 5
+  DSA_K_ROPE = 5,       /* dsa_rope_apply */
+  DSA_K_KV_STORE = 6,   /* dsa_kv_store */
+  DSA_K_KV_LOAD = 7,    /* dsa_kv_load */
+  DSA_K_ATTN = 8,       /* dsa_tree_attn, dsa_sparse_attn: the attention */
+  DSA_K_ATTN_JOIN = 9,  /* the same: joining units that were divided */
+  DSA_K_COUNT = 10
 } dsa_kernel_kind;
 dsa_status dsa_profile_enable(dsa_ctx* ctx, int on);
 dsa_status dsa_profile_read(dsa_ctx* ctx, float* ms /* [DSA_K_COUNT] */,
