@@ -17,8 +17,8 @@
 // divides leaves partial sums in the workspace and the join kernel adds them
 // in a fixed order.
 //
-// A CTA: 4 softmax warps (a row per thread and TMEM lane), 4 loader warps, 1
-// MMA warp; two CTAs per SM, so that one's softmax runs under the other's
+// A CTA: 4 softmax warps (a row per thread and TMEM lane; one thread of them
+// issues the products) and 4 loader warps; two CTAs per SM, so that one's softmax runs under the other's
 // products. TMEM columns: accumulator [0, D), scores [D, D + 64) with the
 // bf16 weights over them, queries [D + 64, D + 64 + D/2): both products take
 // their A operand from TMEM, and shared memory holds only a ring of 64-key K
@@ -41,7 +41,7 @@ namespace at {
 
 constexpr int kTile = 64;
 constexpr int kRows = 128;
-constexpr int kThreads = 288;
+constexpr int kThreads = 256;
 constexpr int kRing = 8;  // entries of the per-tile and per-segment rings; loaders run at most 5 tiles ahead
 
 struct AttnArgs {
@@ -85,7 +85,7 @@ struct Cfg {
 struct Shared {
   uint64_t full[10], empty[10];
   uint64_t mfull[kRing], vdone[kRing];
-  uint64_t s_full, p_ready, q_ready, o_full, fin;
+  uint64_t s_full, o_full, fin;
   unsigned long long vmask[kRing];  // visible keys of a tile, as far as the loader knows
   int bad[kRing];                   // segment number + 1 where a loader replaced a value
   long long scan[16];
@@ -349,14 +349,12 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(const __grid_constant
       sh.bad[i] = 0;
     }
     mbar_init(&sh.s_full, 1);
-    mbar_init(&sh.p_ready, 4);
-    mbar_init(&sh.q_ready, 4);
     mbar_init(&sh.o_full, 1);
     mbar_init(&sh.fin, 1);
     sh.abort = 0;
     fence_mbar_init();
   }
-  if (warp == 8) {
+  if (warp == 0) {
     tmem_alloc(&sh.tmem, C::TMEM);
     tmem_relinquish();
   }
@@ -369,9 +367,10 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(const __grid_constant
   long long begin, count;
   make_plan<SPARSE>(a, sh, cta, grid, begin, count);
   volatile int* abort_flag = &sh.abort;
-  // a wait that runs out is recorded once and stops every role
+  // a wait that runs out is recorded once and stops every role (the others'
+  // next waits run out too)
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    if (mbar_wait(bar, parity)) return !*abort_flag;
+    if (mbar_wait(bar, parity)) return true;
     if (!*abort_flag) atomicOr(a.status, DSA_DEV_TIMEOUT);
     *abort_flag = 1;
     return false;
@@ -393,6 +392,39 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(const __grid_constant
     bool more = it.next(s), run = true;
     int seg = 0, n = 0;
     int4 m0 = make_int4(0, 0, 0, 0), m1 = m0;
+    // the ring slot the next product reads, and the products themselves: one
+    // thread of warp 0 issues them, after a barrier of the four warps
+    int slot = 0, round = 0;
+    auto advance = [&]() {
+      if (++slot == C::NS) {
+        slot = 0;
+        round ^= 1;
+      }
+    };
+    constexpr uint32_t kIdescQk = idesc_f16(128, kTile, true);
+    constexpr uint32_t kIdescPv = idesc_f16(128, D, true) | kIdescBMn;
+    const uint64_t kdesc = sw128_desc(smem_u32(smem)), vdesc = sw128_mn_desc(smem_u32(smem), kTile * 128);
+    // Called by the whole warp; the operands come from lane 0, so that the
+    // compiler keeps them in uniform registers (issue took 1100 cycles a tile
+    // without, most of it moving operands)
+    auto scores = [&](int at) {
+      const uint64_t k = kdesc + __shfl_sync(0xffffffffu, at, 0) * (C::SLOT >> 4);
+      if (!elect_one()) return;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+        tc_mma_f16_ta(tb + C::S, tb + C::Q + 8 * i, k + (((i / 4) * (kTile * 128) + (i % 4) * 32) >> 4), kIdescQk, i > 0);
+      tc_commit(&sh.empty[at]);
+      tc_commit(&sh.s_full);
+    };
+    auto values = [&](int at, bool first, bool last) {
+      const uint64_t v = vdesc + __shfl_sync(0xffffffffu, at, 0) * (C::SLOT >> 4);
+      if (!elect_one()) return;
+#pragma unroll
+      for (int i = 0; i < kTile / 16; ++i)
+        tc_mma_f16_ta(tb + C::O, tb + C::S + 8 * i, v + ((i * 2048) >> 4), kIdescPv, !first || i > 0);
+      tc_commit(&sh.empty[at]);
+      if (last) tc_commit(&sh.o_full);
+    };
     auto load_q = [&](const Seg& g) {
       const bool valid = tid < g.rows;
       const int r = g.r0 + tid;
@@ -413,44 +445,64 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(const __grid_constant
       }
       tmem_st_wait();
       tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.q_ready);
+      if (warp == 0) run = run && wait_warp(&sh.full[slot], round);
+      run = named_bar_all(1, 128, run);  // the four warps go on, or stop, together
+      if (warp == 0 && run) {
+        tc_fence_after();
+        scores(slot);
+        __syncwarp();
+      }
+      advance();
     };
     if (more) load_q(s);
-    while (more && run) {
+    while (more) {
       const bool active = warp * 32 < s.rows;  // some row of this warp is real
       const bool valid = tid < s.rows;
       const int qi = (s.r0 + tid) / a.G;       // the row's query in its sequence
       float m = -INFINITY, l = 0.f;
       for (int t = s.t0; t < s.t1; ++t, ++n) {
-        if (!wait_warp(&sh.mfull[n % kRing], (n / kRing) & 1) || !wait_warp(&sh.s_full, n & 1)) {
-          run = false;
-          break;
-        }
+        run = run && wait_warp(&sh.mfull[n % kRing], (n / kRing) & 1);
         const unsigned long long vm = sh.vmask[n % kRing];
+        // V of this tile and K of the next, usually long there: looked at
+        // while the scores are on their way
+        const bool more_tiles = t + 1 < s.t1;
+        const int vslot = slot, vround = round;
+        advance();
+        bool there = true;
+        if (warp == 0)
+          there = __all_sync(0xffffffffu, mbar_try_wait(smem_u32(&sh.full[vslot]), vround) &&
+                                              (!more_tiles || mbar_try_wait(smem_u32(&sh.full[slot]), round)));
+        run = run && wait_warp(&sh.s_full, n & 1);
         tc_fence_after();
-        if (active) {
+        if (active && run) {
           uint32_t x0[32], x1[32];
           tmem_ld32(tS, x0);
-          tmem_ld32(tS + 32, x1);
           tmem_ld_wait32(x0);
-          tmem_ld_wait32(x1);
+          tmem_ld32(tS + 32, x1);
           const int p0 = t * kTile;
-          if (SPARSE ? vm != ~0ull : (vm != ~0ull || p0 + kTile > s.full)) {
-            unsigned long long see = vm;
-            if (!SPARSE && valid) see &= row_mask(a, s, qi, p0);
-            const uint32_t lo = static_cast<uint32_t>(see), hi = static_cast<uint32_t>(see >> 32);
+          unsigned long long see = vm;
+          if (!SPARSE && valid && p0 + kTile > s.full) see &= row_mask(a, s, qi, p0);
+          const bool some = __any_sync(0xffffffffu, see != ~0ull);  // a key that some row does not see
+          if (some) {
+            const uint32_t lo = static_cast<uint32_t>(see);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
+            for (int i = 0; i < 32; ++i)
               if (!((lo >> i) & 1)) x0[i] = 0xFF800000u;
-              if (!((hi >> i) & 1)) x1[i] = 0xFF800000u;
-            }
           }
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            mx[i & 3] = fmaxf(mx[i & 3], fmaxf(__uint_as_float(x0[i]), __uint_as_float(x1[i])));
+          for (int i = 0; i < 32; i += 2)
+            mx[(i >> 1) & 3] = fmaxf(mx[(i >> 1) & 3], fmaxf(__uint_as_float(x0[i]), __uint_as_float(x0[i + 1])));
+          tmem_ld_wait32(x1);
+          if (some) {
+            const uint32_t hi = static_cast<uint32_t>(see >> 32);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!((hi >> i) & 1)) x1[i] = 0xFF800000u;
           }
+#pragma unroll
+          for (int i = 0; i < 32; i += 2)
+            mx[(i >> 1) & 3] = fmaxf(mx[(i >> 1) & 3], fmaxf(__uint_as_float(x1[i]), __uint_as_float(x1[i + 1])));
           const float mnew = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale2;
           // the running maximum moves only when it grows by more than 2^8:
           // the weights stay below 2^8 and the accumulator is rarely rescaled
@@ -461,42 +513,46 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(const __grid_constant
             if (t > s.t0) {  // s_full of this tile follows the last tile's second product
               l *= alpha;
 #pragma unroll 1
-              for (int c = 0; c < D / 32; ++c) {
-                uint32_t o[32];
-                tmem_ld32(tO + 32 * c, o);
-                tmem_ld_wait32(o);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-                tmem_st32(tO + 32 * c, o);
-              }
+              for (int c = 0; c < D / 16; ++c) tmem_scale16(tO + 16 * c, alpha);
               tmem_st_wait();
             }
             m = to;
           }
           const float sub = m == -INFINITY ? 0.f : m;
           float sum[4] = {0.f, 0.f, 0.f, 0.f};
-          uint32_t p[32];
+          auto weigh = [&](const uint32_t (&x)[32], uint32_t at) {
+            uint32_t p[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float e0 = ex2(fmaf(__uint_as_float(x0[2 * i]), a.scale2, -sub));
-            const float e1 = ex2(fmaf(__uint_as_float(x0[2 * i + 1]), a.scale2, -sub));
-            const float e2 = ex2(fmaf(__uint_as_float(x1[2 * i]), a.scale2, -sub));
-            const float e3 = ex2(fmaf(__uint_as_float(x1[2 * i + 1]), a.scale2, -sub));
-            sum[0] += e0;
-            sum[1] += e1;
-            sum[2] += e2;
-            sum[3] += e3;
-            const __nv_bfloat162 a0 = __floats2bfloat162_rn(e0, e1), a1 = __floats2bfloat162_rn(e2, e3);
-            memcpy(&p[i], &a0, 4);
-            memcpy(&p[16 + i], &a1, 4);
-          }
+            for (int i = 0; i < 16; ++i) {
+              const float e0 = ex2(fmaf(__uint_as_float(x[2 * i]), a.scale2, -sub));
+              const float e1 = ex2(fmaf(__uint_as_float(x[2 * i + 1]), a.scale2, -sub));
+              sum[(2 * i) & 3] += e0;
+              sum[(2 * i + 1) & 3] += e1;
+              const __nv_bfloat162 w = __floats2bfloat162_rn(e0, e1);
+              memcpy(&p[i], &w, 4);
+            }
+            tmem_st16(at, p);
+          };
+          weigh(x0, tS);  // over scores that are in registers by now
+          weigh(x1, tS + 16);
           l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-          tmem_st32(tS, p);
-          tmem_st_wait();
         }
+        if (warp == 0 && run && !there) {
+          run = wait_warp(&sh.full[vslot], vround);
+          if (run && more_tiles) run = wait_warp(&sh.full[slot], round);
+        }
+        tmem_st_wait();
         tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.p_ready);
+        run = named_bar_all(1, 128, run);
+        if (warp == 0 && run) {
+          tc_fence_after();
+          values(vslot, t == s.t0, !more_tiles);
+          __syncwarp();
+          if (more_tiles) scores(slot);
+          __syncwarp();
+        }
+        if (more_tiles) advance();
+        if (!run) break;
       }
       if (!run) break;
       // the next unit's queries go up before this one's sums come down: every
@@ -504,10 +560,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(const __grid_constant
       const Seg done = s;
       more = it.next(s);
       if (more) load_q(s);
-      if (!wait_warp(&sh.o_full, seg & 1)) break;
-      if (!SPARSE) {
-        if (!wait_warp(&sh.vdone[seg % kRing], (seg / kRing) & 1)) break;
-      }
+      run = run && wait_warp(&sh.o_full, seg & 1);
+      if (!SPARSE) run = run && wait_warp(&sh.vdone[seg % kRing], (seg / kRing) & 1);
       tc_fence_after();
       const bool first = done.t0 == 0, last = done.t1 == done.nt;
       if (!first) {
@@ -518,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(const __grid_constant
         m0.w = done.rows;
         m1 = make_int4(done.r0, done.q0, done.h, 0);
       }
-      if (active) {
+      if (active && run) {
         if (!SPARSE && *static_cast<volatile int*>(&sh.bad[seg % kRing]) == seg + 1)
           fix_nonfinite<FMT, D>(a, done, max(done.t0, done.full / kTile), done.t1, qi, valid, tO);
         const int r = done.r0 + tid;
@@ -567,8 +621,11 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(const __grid_constant
     if (tid == 0) {
       a.meta[2 * cta] = m0;
       a.meta[2 * cta + 1] = m1;
+      // products in flight end before their TMEM goes back, after an abort too
+      tc_commit(&sh.fin);
+      mbar_wait(&sh.fin, 0);
     }
-  } else if (warp < 8) {
+  } else {
     // ------------------------------------------------------------ loaders
     constexpr int CPB = FMT == DSA_FMT_BF16 ? 8 : FMT == DSA_FMT_FP8 ? 4 : 2;  // 16-byte chunks of a row's 64 dimensions
     constexpr int RL = 8 / CPB;            // rows that 8 lanes cover: their stores hit all 32 banks
@@ -815,69 +872,10 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(const __grid_constant
       }
     }
     __syncwarp();
-  } else {
-    // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t idesc_qk = idesc_f16(128, kTile, true);
-      constexpr uint32_t idesc_pv = idesc_f16(128, D, true) | kIdescBMn;
-      Iter<SPARSE> it(a, sh.start, count);
-      Seg s;
-      int seg = 0, n = 0, slot = 0, round = 0;
-      bool run = true;
-      auto advance = [&]() {
-        if (++slot == C::NS) {
-          slot = 0;
-          round ^= 1;
-        }
-      };
-      auto scores = [&]() -> bool {
-        if (!wait(&sh.full[slot], round)) return false;
-        tc_fence_after();
-        const uint32_t k = smem_u32(smem + slot * C::SLOT);
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i)
-          tc_mma_f16_ta(tb + C::S, tb + C::Q + 8 * i, sw128_desc(k + (i / 4) * (kTile * 128) + (i % 4) * 32), idesc_qk, i > 0);
-        tc_commit(&sh.empty[slot]);
-        tc_commit(&sh.s_full);
-        advance();
-        return true;
-      };
-      while (run && it.next(s)) {
-        if (!wait(&sh.q_ready, seg & 1)) break;
-        tc_fence_after();
-        if (!scores()) break;
-        for (int t = s.t0; t < s.t1; ++t, ++n) {
-          if (!wait(&sh.p_ready, n & 1) || !wait(&sh.full[slot], round)) {
-            run = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t v = smem_u32(smem + slot * C::SLOT);
-#pragma unroll
-          for (int i = 0; i < kTile / 16; ++i)
-            tc_mma_f16_ta(tb + C::O, tb + C::S + 8 * i, sw128_mn_desc(v + i * 2048, kTile * 128), idesc_pv, t > s.t0 || i > 0);
-          tc_commit(&sh.empty[slot]);
-          advance();
-          if (t + 1 < s.t1) {
-            if (!scores()) {
-              run = false;
-              break;
-            }
-          } else {
-            tc_commit(&sh.o_full);
-          }
-        }
-        ++seg;
-      }
-      // products in flight end before their TMEM goes back, after an abort too
-      tc_commit(&sh.fin);
-      mbar_wait(&sh.fin, 0);
-    }
-    __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) {
+  if (warp == 0) {
     tc_fence_after();
     tmem_dealloc(tb, C::TMEM);
   }
