@@ -17,7 +17,7 @@ namespace at {
 constexpr int kFew = 16;
 
 template <int D>
-__global__ void __launch_bounds__(256) join_kernel(const AttnArgs a, int grid) {
+__global__ void __launch_bounds__(256) join_kernel(const AttnArgs a, int grid, int rows) {
   constexpr int E = D / 32;  // dimensions a lane holds
   pdl_wait();
   pdl_trigger();
@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnArgs a, int grid) {
       a.lse[tok * a.kv_heads * a.G + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
   };
   auto add = [&](int p, int row, float w, float (&o)[E]) {
-    const float* src = a.part + (slot(p) * kRows + row) * D + lane * E;
+    const float* src = a.part + (slot(p) * rows + row) * D + lane * E;
     if constexpr (E == 4) {
       const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
       o[0] = fmaf(v.x, w, o[0]);
@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnArgs a, int grid) {
   // the largest maximum over the pieces; a piece without a visible key has -inf and a weight of 0
   auto top = [&](int row) {
     float m = -INFINITY;
-    for (int p = lane; p < n; p += 32) m = fmaxf(m, __ldcg(a.ml + slot(p) * kRows + row).x);
+    for (int p = lane; p < n; p += 32) m = fmaxf(m, __ldcg(a.ml + slot(p) * rows + row).x);
 #pragma unroll
     for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
     return m;
@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnArgs a, int grid) {
       float o[E] = {}, l = 0.f;
 #pragma unroll 4
       for (int p = 0; p < n; ++p) {
-        const float2 v = __ldcg(a.ml + slot(p) * kRows + row);
+        const float2 v = __ldcg(a.ml + slot(p) * rows + row);
         const float w = weight(v, m);
         l = fmaf(v.y, w, l);
         add(p, row, w, o);
@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnArgs a, int grid) {
       float o[E] = {}, l = 0.f;
 #pragma unroll 4
       for (int p = warp; p < n; p += 8) {
-        const float2 v = __ldcg(a.ml + slot(p) * kRows + row);
+        const float2 v = __ldcg(a.ml + slot(p) * rows + row);
         const float w = weight(v, m);
         l = fmaf(v.y, w, l);
         add(p, row, w, o);
@@ -124,26 +124,25 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnArgs a, int grid) {
   }
 }
 
-dsa_status run_bf16(dsa_ctx* ctx, bool sparse, int D, const CUtensorMap& tm, const AttnArgs& a, int grid, cudaStream_t stream) {
-  return run_fmt<DSA_FMT_BF16>(ctx, sparse, D, tm, a, grid, stream);
+dsa_status run_bf16(dsa_ctx* ctx, int form, int D, const CUtensorMap& tm, const AttnArgs& a, int grid, cudaStream_t stream) {
+  return run_fmt<DSA_FMT_BF16>(ctx, form, D, tm, a, grid, stream);
 }
 
 typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
+// Two pieces a CTA, 256 rows on each SM whatever the form.
 struct Workspace {
   size_t ml, part, bytes;
-  int grid;
 };
 
 Workspace layout(const dsa_ctx* ctx, int D) {
+  const size_t rows = 2 * 256 * static_cast<size_t>(ctx->num_sms);
   Workspace w;
-  w.grid = 2 * ctx->num_sms;
-  const size_t pieces = 2 * static_cast<size_t>(w.grid);
-  w.ml = (pieces * sizeof(int4) + 255) / 256 * 256;
-  w.part = w.ml + pieces * kRows * sizeof(float2);
-  w.bytes = w.part + pieces * kRows * D * sizeof(float);
+  w.ml = (4 * static_cast<size_t>(ctx->num_sms) * sizeof(int4) + 255) / 256 * 256;
+  w.part = w.ml + rows * sizeof(float2);
+  w.bytes = w.part + rows * D * sizeof(float);
   return w;
 }
 
@@ -186,9 +185,9 @@ dsa_status launch_attn(dsa_ctx* ctx, const dsa_attn_args& p, const int32_t* sel,
   CUtensorMap tm = {};
   if (p.fmt == DSA_FMT_BF16) {  // the cache as rows of D elements; a page's K or V of one head is 64 of them
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(p.head_dim),
-                                static_cast<cuuint64_t>(p.num_pages) * p.kv_heads * 2 * kTile};
+                                static_cast<cuuint64_t>(p.num_pages) * p.kv_heads * 2 * kPage};
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(p.head_dim) * 2};
-    const cuuint32_t box[2] = {64, kTile};
+    const cuuint32_t box[2] = {64, kPage};
     const cuuint32_t estr[2] = {1, 1};
     if (reinterpret_cast<EncodeFn>(ctx->encode_tiled)(
             &tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p.cache), dims, strides, box, estr,
@@ -196,12 +195,16 @@ dsa_status launch_attn(dsa_ctx* ctx, const dsa_attn_args& p, const int32_t* sel,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return DSA_ERR_CUDA;
   }
+  // the wide form where the sequences' rows fill more than one 128-row unit on average
+  const bool wide = static_cast<long long>(p.Tq) * a.G > 128LL * p.B;
+  const int form = sel ? kSparse : wide ? kWide : kTree;
+  const int grid = form == kWide ? ctx->num_sms : 2 * ctx->num_sms, rows = form == kWide ? 256 : 128;
   const auto run = p.fmt == DSA_FMT_BF16 ? run_bf16 : p.fmt == DSA_FMT_FP8 ? run_fp8 : run_fp4;
-  const dsa_status st = run(ctx, sel != nullptr, p.head_dim, tm, a, w.grid, stream);
+  const dsa_status st = run(ctx, form, p.head_dim, tm, a, grid, stream);
   if (st != DSA_OK) return st;
   LaunchScope scope(ctx, DSA_K_ATTN_JOIN, stream);
-  const cudaError_t e = launch_pdl(p.head_dim == 128 ? join_kernel<128> : join_kernel<64>, dim3(w.grid, 8), dim3(256),
-                                   0, stream, a, w.grid);
+  const cudaError_t e = launch_pdl(p.head_dim == 128 ? join_kernel<128> : join_kernel<64>, dim3(grid, 8), dim3(256), 0,
+                                   stream, a, grid, rows);
   return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 

@@ -9,40 +9,49 @@
 // operands share a type, and a weight's relative error of 2^-9 is that of
 // the output's own rounding); their sum is of the unrounded weights.
 //
-// Layout. A unit is one kv head of one sequence and up to 128 of its rows
-// (tokens x the G query heads that share the kv head), or, over a selection,
-// one kv head of one token (G rows). The units' 64-key tiles (a page each, or
-// 64 selected keys) are laid end to end and cut into equal ranges, one per
-// CTA, so ragged batches balance whatever their lengths. A unit that a cut
-// divides leaves partial sums in the workspace and the join kernel adds them
-// in a fixed order.
+// Layout. A unit is one kv head of one sequence and up to 128 or 256 of its
+// rows (tokens x the G query heads that share the kv head), or, over a
+// selection, one kv head of one token (G rows). The units' key tiles are laid
+// end to end and cut into equal ranges, one per CTA, so ragged batches balance
+// whatever their lengths. A unit that a cut divides leaves partial sums in the
+// workspace and the join kernel adds them in a fixed order.
 //
-// A CTA: 4 softmax warps (a row per thread and TMEM lane; one thread of them
-// issues the products) and 4 loader warps; two CTAs per SM, so that one's softmax runs under the other's
-// products. TMEM columns: accumulator [0, D), scores [D, D + 64) with the
-// bf16 weights over them, queries [D + 64, D + 64 + D/2): both products take
-// their A operand from TMEM, and shared memory holds only a ring of 64-key K
-// and V tiles in the 128-byte swizzle (K is read K-major, V MN-major, from
-// the same layout).
+// Forms. Rows up to 128 (a decode step, small trees, selections) are bound by
+// reading the cache: 64-key tiles, two CTAs per SM, so that one's softmax runs
+// under the other's products; the queries stay in TMEM as the A operand of the
+// first product, which leaves shared memory to the tiles. Rows beyond that
+// (kWide: large trees, chunks of a prefill) are bound by the tensor cores and
+// by what L2 delivers: 128-key tiles (a product over 64 keys takes as long as
+// one over 128), one CTA per SM with two groups of four softmax warps that
+// share every tile between 256 rows; queries in shared memory.
 //
-// Loaders: in bf16, tiles that every row sees whole come by TMA; all others
-// (fp8 and fp4 codes, selections, the tiles where visibility ends) are read
-// into registers one tile ahead, widened, and stored swizzled. Rows of no
-// visible key are zeros there, never what the page holds: a weight of zero
-// times a stale NaN would be NaN. In tiles that only some rows see, values
-// that are not finite are replaced by zeros too and added afterwards to the
-// rows that do see them (fix_nonfinite).
+// A CTA: one or two groups of 4 softmax warps (a row per thread and TMEM lane;
+// one thread of a group issues its products) and 4 loader warps. TMEM columns
+// of a group: accumulator [0, D), scores after it with the bf16 weights over
+// them, then the queries where they are in TMEM. Keys and values pass through
+// a ring of tiles in the 128-byte swizzle: K is read K-major, V MN-major.
+//
+// Loaders: in bf16, tiles that every row sees whole come by TMA; other bf16
+// tiles (selections, the tiles where visibility ends) by 16-byte asynchronous
+// copies straight into the swizzle; fp8 and fp4 codes by asynchronous copies
+// into a ring private to each thread, several tiles ahead, from where the
+// thread widens them into the operand tile. Rows of no visible key are zeros
+// there, never what the page holds: a weight of zero times a stale NaN would
+// be NaN. In tiles that only some rows see, values that are not finite are
+// replaced by zeros too and added afterwards to the rows that do see them
+// (fix_nonfinite).
 #pragma once
+#include <type_traits>
+
 #include "kv_format.cuh"
 #include "ptx.cuh"
 
 namespace dsa {
 namespace at {
 
-constexpr int kTile = 64;
-constexpr int kRows = 128;
-constexpr int kThreads = 256;
-constexpr int kRing = 8;  // entries of the per-tile and per-segment rings; loaders run at most 5 tiles ahead
+constexpr int kPage = kvf::kPage;
+constexpr int kRing = 16;  // entries of the per-tile and per-segment rings; loaders run at most 9 tiles ahead
+enum Form { kTree = 0, kSparse = 1, kWide = 2 };
 
 struct AttnArgs {
   const __nv_bfloat16* q;
@@ -54,8 +63,8 @@ struct AttnArgs {
   const uint32_t* mask;
   unsigned int* status;
   int4* meta;     // [2 x grid]
-  float2* ml;     // [2 x grid][128]
-  float* part;    // [2 x grid][128][D]
+  float2* ml;     // [2 x grid][rows of a unit]
+  float* part;    // [2 x grid][rows of a unit][D]
   float scale2;   // scale * log2 e
   int B, Tq, max_pages, num_pages, kv_heads, G, k, mask_words, slots;
 };
@@ -73,37 +82,61 @@ struct Start {
   int b, h, r, tile;
 };
 
-template <int D>
+template <int FMT, int D, int FORM>
 struct Cfg {
+  static constexpr bool SPARSE = FORM == kSparse;
+  static constexpr int WG = FORM == kWide ? 2 : 1;     // groups of four softmax warps
+  static constexpr int ROWS = 128 * WG;                // rows of a unit
+  static constexpr int KT = FORM == kWide ? 128 : 64;  // keys of a tile
+  static constexpr int HALVES = KT / kPage;
+  static constexpr int THREADS = 128 * WG + 128;
+  static constexpr int CTAS = FORM == kWide ? 1 : 2;   // per SM
   static constexpr int NBLK = D / 64;
-  static constexpr int SLOT = kTile * D * 2;
-  static constexpr int NS = D == 128 ? 6 : 10;
-  static constexpr int TMEM = 256;  // a power of two; two CTAs share the SM's 512
-  static constexpr uint32_t O = 0, S = D, Q = D + 64;
+  static constexpr int SLOT = KT * D * 2;
+  // chunks of 16 code bytes: of a row's 64 dimensions, and a thread's per 64 keys
+  static constexpr int CPB = FMT == DSA_FMT_BF16 ? 8 : FMT == DSA_FMT_FP8 ? 4 : 2;
+  static constexpr int NCH = NBLK * CPB / 2;
+  static constexpr bool RAW = FMT != DSA_FMT_BF16;
+  static constexpr int RAW_SLOT = RAW ? NCH * 128 * 20 + (D == 64 ? 128 * 4 : 0) : 0;  // codes, a scale word per chunk, flags
+  // ring depths that fill the shared memory (113 KB or 227 KB a CTA)
+  static constexpr int P = !RAW ? 3 : FORM == kWide ? (FMT == DSA_FMT_FP8 ? 3 : 6) : (FMT == DSA_FMT_FP8 ? 4 : 6);
+  static constexpr int NS = FORM == kWide ? (D == 64 ? 8 : RAW ? 4 : 5)
+                                          : (D == 64 ? 8 : FMT == DSA_FMT_BF16 ? 6 : FMT == DSA_FMT_FP8 ? 4 : 5);
+  static constexpr int QBYTES = FORM == kWide ? ROWS * D * 2 : 0;
+  // TMEM columns of a group, and of the CTA (two CTAs share the SM's 512)
+  static constexpr uint32_t O = 0, S = D, Q = D + 64, STRIDE = 256, TMEM = 256 * WG;
 };
 
 struct Shared {
-  uint64_t full[10], empty[10];
+  uint64_t full[8], empty[8];
   uint64_t mfull[kRing], vdone[kRing];
-  uint64_t s_full, o_full, fin;
-  unsigned long long vmask[kRing];  // visible keys of a tile, as far as the loader knows
-  int bad[kRing];                   // segment number + 1 where a loader replaced a value
+  uint64_t s_full[2], o_full[2], fin[2];
+  unsigned long long vmask[kRing][2];  // visible keys of a tile, as far as the loader knows
+  int bad[kRing];                      // segment number + 1 where a loader replaced a value
+  int info[4][8];                      // a loader warp's tiles on their way
   long long scan[16];
   Start start;
-  long long total;
   uint32_t tmem;
   int abort;
 };
 
-template <int D>
-constexpr int smem_bytes() { return Cfg<D>::NS * Cfg<D>::SLOT + static_cast<int>(sizeof(Shared)); }
+template <class C>
+constexpr int smem_bytes() {
+  return C::NS * C::SLOT + C::QBYTES + C::P * C::RAW_SLOT + static_cast<int>(sizeof(Shared));
+}
 
 // Key tiles of the row tile that starts at row r0 (at least one, so that
 // rows without a key are written too).
+template <class C>
 __device__ __forceinline__ int tiles_of(const AttnArgs& a, int nd, int len, int r) {
   int end = len;
-  if (!a.mask) end = len - nd + min(nd, static_cast<int>((static_cast<long long>(r + 1) * kRows - 1) / a.G) + 1);
-  return max(1, (end + kTile - 1) / kTile);
+  if (!a.mask) end = len - nd + min(nd, static_cast<int>((static_cast<long long>(r + 1) * C::ROWS - 1) / a.G) + 1);
+  return max(1, (end + C::KT - 1) / C::KT);
+}
+
+// 64-key tiles of a query's selection and, after them, the drafted tokens
+__device__ __forceinline__ int selection_tiles(const AttnArgs& a) {
+  return (a.k + kPage - 1) / kPage + (a.mask ? (a.mask_words + 1) / 2 : 0);
 }
 
 __device__ __forceinline__ bool read_seq(const AttnArgs& a, int b, int& q0, int& nd, int& len) {
@@ -114,7 +147,7 @@ __device__ __forceinline__ bool read_seq(const AttnArgs& a, int b, int& q0, int&
   return q0 >= 0 && q1 >= q0 && q1 <= a.Tq && len >= nd && static_cast<long long>(len) <= 64LL * a.max_pages;
 }
 
-template <bool SPARSE>
+template <class C>
 struct Iter {
   const AttnArgs& a;
   long long left;
@@ -123,17 +156,17 @@ struct Iter {
   bool ok;
   __device__ Iter(const AttnArgs& a_, const Start& s, long long n) : a(a_), left(n), b(s.b), h(s.h), r(s.r), tile(s.tile) {
     ok = read_seq(a, b, q0, nd, len);
-    nrt = static_cast<int>((static_cast<long long>(nd) * a.G + kRows - 1) / kRows);
+    nrt = static_cast<int>((static_cast<long long>(nd) * a.G + C::ROWS - 1) / C::ROWS);
   }
   // the next stretch; a selection's r is its query
   __device__ bool next(Seg& s) {
     if (left <= 0) return false;
-    if constexpr (SPARSE) {
+    if constexpr (C::SPARSE) {
       while (b + 1 < a.B && a.cu_q[b + 1] <= r) {
         ++b;
         ok = read_seq(a, b, q0, nd, len);
       }
-      s.nt = max(1, (a.k + kTile - 1) / kTile + (a.mask ? (a.mask_words + 1) / 2 : 0));
+      s.nt = selection_tiles(a);
       s.r0 = 0;
       s.rows = a.G;
       s.q0 = r;
@@ -145,12 +178,12 @@ struct Iter {
       while (!ok || nrt == 0) {
         if (++b >= a.B) return false;
         ok = read_seq(a, b, q0, nd, len);
-        nrt = static_cast<int>((static_cast<long long>(nd) * a.G + kRows - 1) / kRows);
+        nrt = static_cast<int>((static_cast<long long>(nd) * a.G + C::ROWS - 1) / C::ROWS);
         h = r = tile = 0;
       }
-      s.nt = tiles_of(a, nd, len, r);
-      s.r0 = r * kRows;
-      s.rows = min(kRows, nd * a.G - s.r0);
+      s.nt = tiles_of<C>(a, nd, len, r);
+      s.r0 = r * C::ROWS;
+      s.rows = min(C::ROWS, nd * a.G - s.r0);
       s.q0 = q0;
       s.nd = nd;
       s.len = len;
@@ -163,7 +196,7 @@ struct Iter {
     s.t1 = left < room ? tile + static_cast<int>(left) : s.nt;
     left -= s.t1 - s.t0;
     tile = 0;
-    if constexpr (SPARSE) {
+    if constexpr (C::SPARSE) {
       if (++h == a.kv_heads) {
         h = 0;
         ++r;
@@ -183,12 +216,13 @@ struct Iter {
 
 // The launch's tiles, and where this CTA's range begins. Every thread of
 // the block calls it; the result is in sh.
-template <bool SPARSE>
+template <class C>
 __device__ __forceinline__ void make_plan(const AttnArgs& a, Shared& sh, int cta, int grid, long long& begin, long long& count) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   long long total;
-  if constexpr (SPARSE) {
-    const int nt = max(1, (a.k + kTile - 1) / kTile + (a.mask ? (a.mask_words + 1) / 2 : 0));
+  constexpr int kThreads = C::THREADS;
+  if constexpr (C::SPARSE) {
+    const int nt = selection_tiles(a);
     total = static_cast<long long>(a.Tq) * a.kv_heads * nt;
     const long long n = total < grid ? total : grid;
     begin = cta < n ? total * cta / n : total;
@@ -218,12 +252,12 @@ __device__ __forceinline__ void make_plan(const AttnArgs& a, Shared& sh, int cta
       if (cta == 0) atomicOr(a.status, DSA_DEV_BOUNDS);
       return 0;
     }
-    const int nrt = static_cast<int>((static_cast<long long>(nd) * a.G + kRows - 1) / kRows);
+    const int nrt = static_cast<int>((static_cast<long long>(nd) * a.G + C::ROWS - 1) / C::ROWS);
     long long n = 0;
     if (a.mask)
-      n = static_cast<long long>(nrt) * tiles_of(a, nd, len, 0);
+      n = static_cast<long long>(nrt) * tiles_of<C>(a, nd, len, 0);
     else
-      for (int r = 0; r < nrt; ++r) n += tiles_of(a, nd, len, r);
+      for (int r = 0; r < nrt; ++r) n += tiles_of<C>(a, nd, len, r);
     return n * a.kv_heads;
   };
   long long sum = 0, last = 0;
@@ -264,7 +298,7 @@ __device__ __forceinline__ void make_plan(const AttnArgs& a, Shared& sh, int cta
     x -= h * ph;
     int r = 0;
     while (true) {
-      const int nt = tiles_of(a, nd, len, r);
+      const int nt = tiles_of<C>(a, nd, len, r);
       if (x < nt) break;
       x -= nt;
       ++r;
@@ -279,7 +313,7 @@ __device__ __forceinline__ unsigned long long low_bits(int n) {
   return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1;
 }
 
-// Keys of the tile at position p0 that a row of query i may see (tree form).
+// Of the 64 keys from position p0 on, those that a row of query i may see (tree form).
 __device__ __forceinline__ unsigned long long row_mask(const AttnArgs& a, const Seg& s, int i, int p0) {
   const int ctx = s.len - s.nd;
   if (!a.mask) return low_bits(ctx + i + 1 - p0);
@@ -298,8 +332,8 @@ __device__ __forceinline__ unsigned long long row_mask(const AttnArgs& a, const 
 
 __device__ __forceinline__ float widen_one(uint32_t bits) { return __uint_as_float(bits << 16); }
 
-// Adds the values that are not finite, of the partially visible tiles
-// [t0, t1), to the rows that see their keys. Only reached where a loader
+// Adds the values that are not finite, of the pages [t0, t1) that hold keys
+// only some rows see, to the rows that see them. Only reached where a loader
 // found one.
 template <int FMT, int D>
 __device__ __noinline__ void fix_nonfinite(const AttnArgs& a, const Seg& s, int t0, int t1, int i, bool valid, uint32_t o_taddr) {
@@ -307,11 +341,11 @@ __device__ __noinline__ void fix_nonfinite(const AttnArgs& a, const Seg& s, int 
   for (int d = 0; d < D; ++d) {
     float add = 0.f;
     for (int t = t0; t < t1; ++t) {
-      if (t * kTile >= s.len) break;
+      if (t * kPage >= s.len) break;
       const int page = a.page_table[static_cast<long long>(s.b) * a.max_pages + t];
       if (page < 0 || page >= a.num_pages) continue;
       const uint8_t* blk = a.cache + (static_cast<long long>(page) * a.kv_heads + s.h) * L::HEAD_BYTES;
-      unsigned long long m = valid ? row_mask(a, s, i, t * kTile) & low_bits(s.len - t * kTile) : 0ull;
+      unsigned long long m = valid ? row_mask(a, s, i, t * kPage) & low_bits(s.len - t * kPage) : 0ull;
       while (m) {
         const int j = __ffsll(static_cast<long long>(m)) - 1;
         m &= m - 1;
@@ -329,28 +363,34 @@ __device__ __noinline__ void fix_nonfinite(const AttnArgs& a, const Seg& s, int 
   }
 }
 
-template <int FMT, int D, bool SPARSE>
-__global__ void __launch_bounds__(kThreads, 2) attn_kernel(const __grid_constant__ CUtensorMap tm, const AttnArgs a) {
-  using C = Cfg<D>;
+template <int FMT, int D, int FORM>
+__global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>::CTAS)
+    attn_kernel(const __grid_constant__ CUtensorMap tm, const AttnArgs a) {
+  using C = Cfg<FMT, D, FORM>;
   using L = kvf::Layout<FMT, D>;
+  constexpr int NSW = 4 * C::WG;  // softmax warps
   extern __shared__ __align__(1024) uint8_t smem[];
-  Shared& sh = *reinterpret_cast<Shared*>(smem + C::NS * C::SLOT);
+  uint8_t* const qsm = smem + C::NS * C::SLOT;
+  uint8_t* const raw = qsm + C::QBYTES;
+  Shared& sh = *reinterpret_cast<Shared*>(raw + C::P * C::RAW_SLOT);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cta = blockIdx.x, grid = gridDim.x;
 
   if (tid == 0) {
     for (int i = 0; i < C::NS; ++i) {
-      mbar_init(&sh.full[i], 4);
-      mbar_init(&sh.empty[i], 1);
+      mbar_init(&sh.full[i], 4 * C::HALVES);  // a loader warp and 64 keys
+      mbar_init(&sh.empty[i], C::WG);
     }
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&sh.mfull[i], 1);
       mbar_init(&sh.vdone[i], 4);
       sh.bad[i] = 0;
     }
-    mbar_init(&sh.s_full, 1);
-    mbar_init(&sh.o_full, 1);
-    mbar_init(&sh.fin, 1);
+    for (int i = 0; i < C::WG; ++i) {
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.o_full[i], 1);
+      mbar_init(&sh.fin[i], 1);
+    }
     sh.abort = 0;
     fence_mbar_init();
   }
@@ -361,11 +401,10 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(const __grid_constant
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tb = sh.tmem;
   pdl_wait();
   pdl_trigger();
   long long begin, count;
-  make_plan<SPARSE>(a, sh, cta, grid, begin, count);
+  make_plan<C>(a, sh, cta, grid, begin, count);
   volatile int* abort_flag = &sh.abort;
   // a wait that runs out is recorded once and stops every role (the others'
   // next waits run out too)
@@ -375,134 +414,170 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(const __grid_constant
     *abort_flag = 1;
     return false;
   };
-
   // the same by a whole warp, with one answer for all its lanes
   auto wait_warp = [&](uint64_t* bar, uint32_t parity) -> bool {
     return __all_sync(0xffffffffu, wait(bar, parity));
   };
+  int slot = 0, round = 0;  // of the operand ring, for every role
+  auto advance = [&]() {
+    if (++slot == C::NS) {
+      slot = 0;
+      round ^= 1;
+    }
+  };
 
   if (count <= 0) {
     if (tid == 0) a.meta[2 * cta] = make_int4(0, 0, 0, 0);
-  } else if (warp < 4) {
+  } else if (warp < NSW) {
     // ------------------------------------------------------------ softmax
-    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
-    const uint32_t tO = tb + C::O + lanes, tS = tb + C::S + lanes, tQ = tb + C::Q + lanes;
-    Iter<SPARSE> it(a, sh.start, count);
+    const int wg = warp >> 2, gw = warp & 3;  // group, and warp of the group
+    const int row = tid;                      // of the unit
+    const uint32_t tb = sh.tmem + wg * C::STRIDE;
+    const uint32_t lanes = static_cast<uint32_t>(gw * 32) << 16;
+    const uint32_t tO = tb + C::O + lanes, tS = tb + C::S + lanes;
+    Iter<C> it(a, sh.start, count);
     Seg s;
     bool more = it.next(s), run = true;
-    int seg = 0, n = 0;
+    int seg = 0, n = 0;   // segments, tiles
+    int ns = 0, no = 0;   // this group's first products and accumulators so far
     int4 m0 = make_int4(0, 0, 0, 0), m1 = m0;
-    // the ring slot the next product reads, and the products themselves: one
-    // thread of warp 0 issues them, after a barrier of the four warps
-    int slot = 0, round = 0;
-    auto advance = [&]() {
-      if (++slot == C::NS) {
-        slot = 0;
-        round ^= 1;
-      }
-    };
-    constexpr uint32_t kIdescQk = idesc_f16(128, kTile, true);
+    constexpr uint32_t kIdescQk = idesc_f16(128, C::KT, true);
     constexpr uint32_t kIdescPv = idesc_f16(128, D, true) | kIdescBMn;
-    const uint64_t kdesc = sw128_desc(smem_u32(smem)), vdesc = sw128_mn_desc(smem_u32(smem), kTile * 128);
-    // Called by the whole warp; the operands come from lane 0, so that the
-    // compiler keeps them in uniform registers (issue took 1100 cycles a tile
-    // without, most of it moving operands)
+    const uint64_t kdesc = sw128_desc(smem_u32(smem)), vdesc = sw128_mn_desc(smem_u32(smem), C::KT * 128);
+    const uint64_t qdesc = sw128_desc(smem_u32(qsm) + wg * (128 * D * 2));
+    // The products. Called by a whole warp; the operands come from lane 0, so
+    // that the compiler keeps them in uniform registers (issuing a tile's took
+    // 1100 cycles without, most of it moving operands; 700 with)
     auto scores = [&](int at) {
       const uint64_t k = kdesc + __shfl_sync(0xffffffffu, at, 0) * (C::SLOT >> 4);
       if (!elect_one()) return;
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i)
-        tc_mma_f16_ta(tb + C::S, tb + C::Q + 8 * i, k + (((i / 4) * (kTile * 128) + (i % 4) * 32) >> 4), kIdescQk, i > 0);
+      for (int i = 0; i < D / 16; ++i) {
+        const uint64_t b = k + (((i / 4) * (C::KT * 128) + (i % 4) * 32) >> 4);
+        if constexpr (FORM == kWide)
+          tc_mma_f16(tb + C::S, qdesc + (((i / 4) * (128 * 128) + (i % 4) * 32) >> 4), b, kIdescQk, i > 0);
+        else
+          tc_mma_f16_ta(tb + C::S, tb + C::Q + 8 * i, b, kIdescQk, i > 0);
+      }
       tc_commit(&sh.empty[at]);
-      tc_commit(&sh.s_full);
+      tc_commit(&sh.s_full[wg]);
     };
     auto values = [&](int at, bool first, bool last) {
       const uint64_t v = vdesc + __shfl_sync(0xffffffffu, at, 0) * (C::SLOT >> 4);
       if (!elect_one()) return;
 #pragma unroll
-      for (int i = 0; i < kTile / 16; ++i)
+      for (int i = 0; i < C::KT / 16; ++i)
         tc_mma_f16_ta(tb + C::O, tb + C::S + 8 * i, v + ((i * 2048) >> 4), kIdescPv, !first || i > 0);
       tc_commit(&sh.empty[at]);
-      if (last) tc_commit(&sh.o_full);
+      if (last) tc_commit(&sh.o_full[wg]);
     };
-    auto load_q = [&](const Seg& g) {
-      const bool valid = tid < g.rows;
-      const int r = g.r0 + tid;
+    // the unit's queries, then the first tile's scores
+    auto start_unit = [&](const Seg& g) {
+      const bool valid = row < g.rows;
+      const int r = g.r0 + row;
       const uint4* src = reinterpret_cast<const uint4*>(
           a.q + (valid ? static_cast<long long>(g.q0 + r / a.G) * a.qt + static_cast<long long>(g.h * a.G + r % a.G) * a.qh : 0));
+      if constexpr (FORM == kWide) {
+        uint8_t* dst = qsm + wg * (128 * D * 2) + (row & 127) * 128;
 #pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-        uint32_t w[32];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint4 v = valid ? __ldg(src + c * 8 + i) : make_uint4(0, 0, 0, 0);
-          w[4 * i] = v.x;
-          w[4 * i + 1] = v.y;
-          w[4 * i + 2] = v.z;
-          w[4 * i + 3] = v.w;
+        for (int i = 0; i < D / 8; ++i) {
+          const uint4 v = valid ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(dst + (i / 8) * (128 * 128) + (((i & 7) ^ (row & 7)) << 4)) = v;
         }
-        tmem_st32(tQ + 32 * c, w);
+        fence_proxy_async_smem();
+      } else {
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+          uint32_t w[32];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint4 v = valid ? __ldg(src + c * 8 + i) : make_uint4(0, 0, 0, 0);
+            w[4 * i] = v.x;
+            w[4 * i + 1] = v.y;
+            w[4 * i + 2] = v.z;
+            w[4 * i + 3] = v.w;
+          }
+          tmem_st32(tb + C::Q + lanes + 32 * c, w);
+        }
+        tmem_st_wait();
+        tc_fence_before();
       }
-      tmem_st_wait();
-      tc_fence_before();
-      if (warp == 0) run = run && wait_warp(&sh.full[slot], round);
-      run = named_bar_all(1, 128, run);  // the four warps go on, or stop, together
-      if (warp == 0 && run) {
+      if (gw == 0) run = run && wait_warp(&sh.full[slot], round);
+      run = named_bar_all(1 + wg, 128, run);  // the group's warps go on, or stop, together
+      if (gw == 0 && run) {
         tc_fence_after();
         scores(slot);
         __syncwarp();
       }
       advance();
     };
-    if (more) load_q(s);
+    auto has_rows = [&](const Seg& g) { return wg * 128 < g.rows; };
+    if (more && has_rows(s)) start_unit(s);
     while (more) {
+      if (FORM == kWide && !has_rows(s)) {
+        // a unit of at most 128 rows: this group only passes the tiles on
+        for (int t = s.t0; t < s.t1; ++t, ++n) {
+          for (int v = 0; v < 2; ++v) {
+            if (gw == 0 && run) {
+              run = wait_warp(&sh.full[slot], round);
+              if (run && lane == 0) mbar_arrive(&sh.empty[slot]);
+            }
+            advance();
+          }
+        }
+        run = named_bar_all(1 + wg, 128, run);
+        ++seg;
+        more = it.next(s);
+        if (more && has_rows(s)) start_unit(s);
+        if (!run) break;
+        continue;
+      }
       const bool active = warp * 32 < s.rows;  // some row of this warp is real
-      const bool valid = tid < s.rows;
-      const int qi = (s.r0 + tid) / a.G;       // the row's query in its sequence
+      const bool valid = row < s.rows;
+      const int qi = (s.r0 + row) / a.G;       // the row's query in its sequence
       float m = -INFINITY, l = 0.f;
-      for (int t = s.t0; t < s.t1; ++t, ++n) {
+      for (int t = s.t0; t < s.t1; ++t, ++n, ++ns) {
         run = run && wait_warp(&sh.mfull[n % kRing], (n / kRing) & 1);
-        const unsigned long long vm = sh.vmask[n % kRing];
+        unsigned long long see[C::HALVES];
+#pragma unroll
+        for (int h = 0; h < C::HALVES; ++h) see[h] = sh.vmask[n % kRing][h];
         // V of this tile and K of the next, usually long there: looked at
         // while the scores are on their way
         const bool more_tiles = t + 1 < s.t1;
         const int vslot = slot, vround = round;
         advance();
         bool there = true;
-        if (warp == 0)
+        if (gw == 0)
           there = __all_sync(0xffffffffu, mbar_try_wait(smem_u32(&sh.full[vslot]), vround) &&
                                               (!more_tiles || mbar_try_wait(smem_u32(&sh.full[slot]), round)));
-        run = run && wait_warp(&sh.s_full, n & 1);
+        run = run && wait_warp(&sh.s_full[wg], ns & 1);
         tc_fence_after();
         if (active && run) {
-          uint32_t x0[32], x1[32];
-          tmem_ld32(tS, x0);
-          tmem_ld_wait32(x0);
-          tmem_ld32(tS + 32, x1);
-          const int p0 = t * kTile;
-          unsigned long long see = vm;
-          if (!SPARSE && valid && p0 + kTile > s.full) see &= row_mask(a, s, qi, p0);
-          const bool some = __any_sync(0xffffffffu, see != ~0ull);  // a key that some row does not see
-          if (some) {
-            const uint32_t lo = static_cast<uint32_t>(see);
+          uint32_t x[C::KT / 32][32];
+          tmem_ld32(tS, x[0]);
+          const int p0 = t * C::KT;
+          bool all = true;
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (!((lo >> i) & 1)) x0[i] = 0xFF800000u;
+          for (int h = 0; h < C::HALVES; ++h) {
+            if (!C::SPARSE && valid && p0 + (h + 1) * kPage > s.full) see[h] &= row_mask(a, s, qi, p0 + h * kPage);
+            all = all && see[h] == ~0ull;
           }
+          const bool some = !__all_sync(0xffffffffu, all);  // a key that some row does not see
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int i = 0; i < 32; i += 2)
-            mx[(i >> 1) & 3] = fmaxf(mx[(i >> 1) & 3], fmaxf(__uint_as_float(x0[i]), __uint_as_float(x0[i + 1])));
-          tmem_ld_wait32(x1);
-          if (some) {
-            const uint32_t hi = static_cast<uint32_t>(see >> 32);
+          for (int c = 0; c < C::KT / 32; ++c) {
+            tmem_ld_wait32(x[c]);
+            if (c + 1 < C::KT / 32) tmem_ld32(tS + 32 * (c + 1), x[c + 1]);
+            if (some) {
+              const uint32_t bits = static_cast<uint32_t>(see[c / 2] >> (32 * (c & 1)));
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (!((hi >> i) & 1)) x1[i] = 0xFF800000u;
+              for (int i = 0; i < 32; ++i)
+                if (!((bits >> i) & 1)) x[c][i] = 0xFF800000u;
+            }
+#pragma unroll
+            for (int i = 0; i < 32; i += 2)
+              mx[(i >> 1) & 3] = fmaxf(mx[(i >> 1) & 3], fmaxf(__uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1])));
           }
-#pragma unroll
-          for (int i = 0; i < 32; i += 2)
-            mx[(i >> 1) & 3] = fmaxf(mx[(i >> 1) & 3], fmaxf(__uint_as_float(x1[i]), __uint_as_float(x1[i + 1])));
           const float mnew = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale2;
           // the running maximum moves only when it grows by more than 2^8:
           // the weights stay below 2^8 and the accumulator is rarely rescaled
@@ -519,32 +594,35 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(const __grid_constant
             m = to;
           }
           const float sub = m == -INFINITY ? 0.f : m;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
-          auto weigh = [&](const uint32_t (&x)[32], uint32_t at) {
+          const unsigned long long sc = pack2(a.scale2, a.scale2), sb = pack2(-sub, -sub);
+          unsigned long long sum[2] = {0ull, 0ull};  // pairs of fp32 zeros
+#pragma unroll
+          for (int c = 0; c < C::KT / 32; ++c) {
             uint32_t p[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              const float e0 = ex2(fmaf(__uint_as_float(x[2 * i]), a.scale2, -sub));
-              const float e1 = ex2(fmaf(__uint_as_float(x[2 * i + 1]), a.scale2, -sub));
-              sum[(2 * i) & 3] += e0;
-              sum[(2 * i + 1) & 3] += e1;
+              float e0, e1;
+              unpack2(fma2(pack2(__uint_as_float(x[c][2 * i]), __uint_as_float(x[c][2 * i + 1])), sc, sb), e0, e1);
+              e0 = ex2(e0);
+              e1 = ex2(e1);
+              sum[i & 1] = add2(sum[i & 1], pack2(e0, e1));
               const __nv_bfloat162 w = __floats2bfloat162_rn(e0, e1);
               memcpy(&p[i], &w, 4);
             }
-            tmem_st16(at, p);
-          };
-          weigh(x0, tS);  // over scores that are in registers by now
-          weigh(x1, tS + 16);
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            tmem_st16(tS + 16 * c, p);  // over scores that are in registers by now
+          }
+          float l0, l1;
+          unpack2(add2(sum[0], sum[1]), l0, l1);
+          l += l0 + l1;
         }
-        if (warp == 0 && run && !there) {
+        if (gw == 0 && run && !there) {
           run = wait_warp(&sh.full[vslot], vround);
           if (run && more_tiles) run = wait_warp(&sh.full[slot], round);
         }
         tmem_st_wait();
         tc_fence_before();
-        run = named_bar_all(1, 128, run);
-        if (warp == 0 && run) {
+        run = named_bar_all(1 + wg, 128, run);
+        if (gw == 0 && run) {
           tc_fence_after();
           values(vslot, t == s.t0, !more_tiles);
           __syncwarp();
@@ -559,9 +637,10 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(const __grid_constant
       // product with the old ones has completed (s_full of the last tile)
       const Seg done = s;
       more = it.next(s);
-      if (more) load_q(s);
-      run = run && wait_warp(&sh.o_full, seg & 1);
-      if (!SPARSE) run = run && wait_warp(&sh.vdone[seg % kRing], (seg / kRing) & 1);
+      if (more && has_rows(s)) start_unit(s);
+      run = run && wait_warp(&sh.o_full[wg], no & 1);
+      ++no;
+      if (!C::SPARSE) run = run && wait_warp(&sh.vdone[seg % kRing], (seg / kRing) & 1);
       tc_fence_after();
       const bool first = done.t0 == 0, last = done.t1 == done.nt;
       if (!first) {
@@ -573,15 +652,15 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(const __grid_constant
         m1 = make_int4(done.r0, done.q0, done.h, 0);
       }
       if (active && run) {
-        if (!SPARSE && *static_cast<volatile int*>(&sh.bad[seg % kRing]) == seg + 1)
-          fix_nonfinite<FMT, D>(a, done, max(done.t0, done.full / kTile), done.t1, qi, valid, tO);
-        const int r = done.r0 + tid;
+        if (!C::SPARSE && *static_cast<volatile int*>(&sh.bad[seg % kRing]) == seg + 1)
+          fix_nonfinite<FMT, D>(a, done, max(done.t0, done.full / C::KT) * C::HALVES, done.t1 * C::HALVES, qi, valid, tO);
+        const int r = done.r0 + row;
         const long long tok = done.q0 + r / a.G;
         const int head = done.h * a.G + r % a.G;
-        const int slot = 2 * cta + (first ? 1 : 0);
+        const int piece = 2 * cta + (first ? 1 : 0);
         const float inv = l > 0.f ? 1.f / l : 0.f;
         __nv_bfloat16* dst = a.out + tok * a.ot + head * a.oh;
-        float* part = a.part + (static_cast<long long>(slot) * kRows + tid) * D;
+        float* part = a.part + (static_cast<long long>(piece) * C::ROWS + row) * D;
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
@@ -611,145 +690,166 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(const __grid_constant
           if (first && last) {
             if (a.lse) a.lse[tok * a.kv_heads * a.G + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
           } else {
-            a.ml[static_cast<long long>(slot) * kRows + tid] = make_float2(m, l);
+            a.ml[static_cast<long long>(piece) * C::ROWS + row] = make_float2(m, l);
           }
         }
         tc_fence_before();
       }
       ++seg;
     }
-    if (tid == 0) {
+    if (tid == 0) {  // the first group has rows in every unit
       a.meta[2 * cta] = m0;
       a.meta[2 * cta + 1] = m1;
-      // products in flight end before their TMEM goes back, after an abort too
-      tc_commit(&sh.fin);
-      mbar_wait(&sh.fin, 0);
+    }
+    // products in flight end before their TMEM goes back, after an abort too
+    if (gw == 0) {
+      __syncwarp();
+      if (elect_one()) {
+        tc_commit(&sh.fin[wg]);
+        mbar_wait(&sh.fin[wg], 0);
+      }
+      __syncwarp();
     }
   } else {
     // ------------------------------------------------------------ loaders
-    constexpr int CPB = FMT == DSA_FMT_BF16 ? 8 : FMT == DSA_FMT_FP8 ? 4 : 2;  // 16-byte chunks of a row's 64 dimensions
+    constexpr int CPB = C::CPB, NCH = C::NCH;
     constexpr int RL = 8 / CPB;            // rows that 8 lanes cover: their stores hit all 32 banks
-    constexpr int NCH = C::NBLK * CPB / 2; // chunks a thread moves per tile
     constexpr int RSTEP = RL * 16 / C::NBLK;
-    const int lt = tid - 128, lw = warp - 4;
+    const int lt = tid - 32 * NSW, lw = warp - NSW;
     const int chunk = lt % CPB, blk = (lt / 8) % C::NBLK;
-    const int row0 = (lt / (8 * C::NBLK)) * RL + (lt / CPB) % RL;
+    const int row0 = (lt / (8 * C::NBLK)) * RL + (lt / CPB) % RL;  // of 64; this thread's are RSTEP apart
     const int code_off = (blk * CPB + chunk) * 16;
     const int scale_off = (blk * 64 + chunk * (64 / CPB)) / kvf::kBlock;
-    struct Tile {
-      uint4 raw[NCH];
-      uint32_t sc[FMT == DSA_FMT_BF16 ? 1 : NCH];
+    const uint32_t raw_at = smem_u32(raw);
+    // where a row's 16-byte unit u lies in the operand tile
+    auto place = [&](int at, int half, int i, int u) -> uint8_t* {
+      const int r = row0 + i * RSTEP;
+      return smem + at * C::SLOT + blk * (C::KT * 128) + (half * kPage + r) * 128 + ((u ^ (r & 7)) << 4);
     };
-    int slot = 0, round = 0, issued = 0;  // the next ring slot
-    auto advance = [&]() {
-      ++issued;
-      if (++slot == C::NS) {
-        slot = 0;
-        round ^= 1;
-      }
-    };
-    // where each of this thread's rows lies: a page and an offset, or none
-    auto fetch = [&](Tile& t, const int (&at)[NCH], int h, bool v) {
-#pragma unroll
-      for (int i = 0; i < NCH; ++i) {
-        t.raw[i] = make_uint4(0, 0, 0, 0);
-        if (FMT != DSA_FMT_BF16) t.sc[FMT == DSA_FMT_BF16 ? 0 : i] = 0;
-        if (at[i] >= 0) {
-          const uint8_t* b = a.cache + (static_cast<long long>(at[i] >> 6) * a.kv_heads + h) * L::HEAD_BYTES;
-          const int off = at[i] & 63;
-          t.raw[i] = __ldg(reinterpret_cast<const uint4*>(b + (v ? L::V_CODES : L::K_CODES) + off * L::CB + code_off));
-          if (FMT != DSA_FMT_BF16)
-            t.sc[FMT == DSA_FMT_BF16 ? 0 : i] = __ldg(b + (v ? L::V_SCALES : L::K_SCALES) + off * L::SB + scale_off);
-        }
-      }
-    };
-    // widened, into the ring; `clean` replaces what is not finite and reports it
-    auto commit = [&](const Tile& t, bool clean, int seg) -> bool {
-      if (!wait_warp(&sh.empty[slot], round ^ 1)) return false;
-      uint8_t* base = smem + slot * C::SLOT + blk * (kTile * 128);
+
+    Iter<C> it(a, sh.start, count);
+    Seg s;
+    int n = 0, issued = 0, sent = 0;  // tiles; 64-key parts asked for, and handed over
+    int slots = 0;                    // operand slots that TMA or copies have been asked to fill
+    bool run = true;
+
+    // 64 keys have landed in this thread's part of the ring: hand them to the
+    // products. info: slot, half and what to do with them
+    //   bits 0-2 slot, 3 half, 4 replace what is not finite, 5 a segment's last, 8.. segment
+    auto hand_over = [&](int info) {
+      const int at = info & 7, half = (info >> 3) & 1, seg = info >> 8;
       bool found = false;
+      if constexpr (C::RAW) {
+        const uint8_t* src = raw + (sent % C::P) * C::RAW_SLOT;
+        uint32_t odd = 0;
+        if constexpr (D == 64) odd = reinterpret_cast<const uint32_t*>(src + NCH * 128 * 20)[lt];
 #pragma unroll
-      for (int i = 0; i < NCH; ++i) {
-        const int row = row0 + i * RSTEP;
-        uint32_t w[32 / CPB];
-        if constexpr (FMT == DSA_FMT_BF16) {
-          w[0] = t.raw[i].x;
-          w[1] = t.raw[i].y;
-          w[2] = t.raw[i].z;
-          w[3] = t.raw[i].w;
-        } else if constexpr (FMT == DSA_FMT_FP8) {
-          const kvf::Factor<FMT> f(t.sc[i]);
-          const uint32_t c[4] = {t.raw[i].x, t.raw[i].y, t.raw[i].z, t.raw[i].w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t o[2];
-            kvf::widen_e4m3(c[j], f, o);
-            w[2 * j] = o[0];
-            w[2 * j + 1] = o[1];
-          }
-        } else {
-          const kvf::Factor<FMT> f(t.sc[i]);
-          const uint32_t c[4] = {t.raw[i].x, t.raw[i].y, t.raw[i].z, t.raw[i].w};
+        for (int i = 0; i < NCH; ++i) {
+          const uint4 v = reinterpret_cast<const uint4*>(src)[i * 128 + lt];
+          const uint32_t sw = reinterpret_cast<const uint32_t*>(src + NCH * 128 * 16)[i * 128 + lt];
+          const uint32_t sc = (sw >> (8 * (scale_off + (D == 64 ? 2 * ((odd >> i) & 1) : 0)))) & 0xFFu;
+          const uint32_t c[4] = {v.x, v.y, v.z, v.w};
+          uint32_t w[32 / CPB];
+          const kvf::Factor<C::RAW ? FMT : DSA_FMT_FP8> f(sc);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            uint32_t o[4];
-            kvf::widen_e2m1(c[j], f, o);
+            if constexpr (FMT == DSA_FMT_FP8) {
+              uint32_t o[2];
+              kvf::widen_e4m3(c[j], f, o);
+              w[2 * j] = o[0];
+              w[2 * j + 1] = o[1];
+            } else {
+              uint32_t o[4];
+              kvf::widen_e2m1(c[j], f, o);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) w[4 * j + e] = o[e];
-          }
-        }
-        if (clean) {
-#pragma unroll
-          for (int j = 0; j < 32 / CPB; ++j) {
-            if ((w[j] & 0x7F800000u) == 0x7F800000u) {
-              w[j] &= 0x0000FFFFu;
-              found = true;
-            }
-            if ((w[j] & 0x7F80u) == 0x7F80u) {
-              w[j] &= 0xFFFF0000u;
-              found = true;
+              for (int e = 0; e < 4; ++e) w[4 * j + e] = o[e];
             }
           }
-        }
+          if (info & 16) found |= kvf::zero_nonfinite(w);
 #pragma unroll
-        for (int j = 0; j < 8 / CPB; ++j) {
-          const int unit = (chunk * (8 / CPB) + j) ^ (row & 7);
-          *reinterpret_cast<uint4*>(base + row * 128 + unit * 16) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+          for (int j = 0; j < 8 / CPB; ++j)
+            *reinterpret_cast<uint4*>(place(at, half, i, chunk * (8 / CPB) + j)) =
+                make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+        }
+      } else if (info & 16) {
+#pragma unroll
+        for (int i = 0; i < NCH; ++i) {
+          uint4* p = reinterpret_cast<uint4*>(place(at, half, i, chunk));
+          const uint4 v = *p;
+          uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          if (kvf::zero_nonfinite(w)) {
+            found = true;
+            *p = make_uint4(w[0], w[1], w[2], w[3]);
+          }
         }
       }
       if (found) *static_cast<volatile int*>(&sh.bad[seg % kRing]) = seg + 1;
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.full[slot]);
-      advance();
+      if (lane == 0) {
+        mbar_arrive(&sh.full[at]);
+        if (info & 32) mbar_arrive(&sh.vdone[seg % kRing]);
+      }
+      ++sent;
+    };
+    // hand over the oldest part; `left` younger ones may stay in flight
+    auto settle = [&](auto left) -> bool {
+      cp_async_wait<decltype(left)::value>();
+      const int info = sh.info[lw][sent & 7];
+      // codes are widened into a slot that has to be free; copies into the
+      // slot itself waited for that before they were issued
+      if (C::RAW && !wait_warp(&sh.empty[info & 7], ((info >> 6) & 1) ^ 1)) return false;
+      hand_over(info);
+      return true;
+    };
+    // ask for 64 keys: `at`, where each of this thread's rows lies (page * 64 + offset, or -1)
+    auto ask = [&](const int (&at)[NCH], int h, bool v, int half, bool clean, bool last, int seg) -> bool {
+      if constexpr (!C::RAW) {
+        if (half == 0 && !__all_sync(0xffffffffu, mbar_try_wait(smem_u32(&sh.empty[slot]), round ^ 1))) {
+          // what has landed goes out before this warp waits for a slot
+          cp_async_wait<0>();
+          while (sent < issued) hand_over(sh.info[lw][sent & 7]);
+          if (!wait_warp(&sh.empty[slot], round ^ 1)) return false;
+        }
+      }
+      const uint32_t dst = raw_at + (issued % C::P) * C::RAW_SLOT;
+      uint32_t odd = 0;
+#pragma unroll
+      for (int i = 0; i < NCH; ++i) {
+        const bool ok = at[i] >= 0;
+        const int where = ok ? at[i] : 0;
+        const uint8_t* b = a.cache + (static_cast<long long>(where >> 6) * a.kv_heads + h) * L::HEAD_BYTES;
+        const uint8_t* code = b + (v ? L::V_CODES : L::K_CODES) + (where & 63) * L::CB + code_off;
+        if constexpr (C::RAW) {
+          cp_async16(dst + (i * 128 + lt) * 16, code, ok);
+          cp_async4(dst + NCH * 128 * 16 + (i * 128 + lt) * 4,
+                    b + (v ? L::V_SCALES : L::K_SCALES) + (((where & 63) * L::SB) & ~3), ok);
+          odd |= (where & 1) << i;
+        } else {
+          cp_async16(smem_u32(place(slot, half, i, chunk)), code, ok);
+        }
+      }
+      if constexpr (C::RAW && D == 64)
+        reinterpret_cast<uint32_t*>(raw + (issued % C::P) * C::RAW_SLOT + NCH * 128 * 20)[lt] = odd;
+      cp_async_commit();
+      if (lane == 0)
+        sh.info[lw][issued & 7] = slot | (half << 3) | (clean ? 16 : 0) | (last ? 32 : 0) | (round << 6) | (seg << 8);
+      __syncwarp();
+      ++issued;
+      if (half + 1 == C::HALVES) {
+        advance();
+        ++slots;
+      }
+      if (issued - sent == C::P) return settle(std::integral_constant<int, C::P - 1>());
       return true;
     };
 
-    Iter<SPARSE> it(a, sh.start, count);
-    Seg s;
-    int seg = 0, n = 0;
-    bool run = true;
-    Tile hold;                                   // a V tile on its way from memory
-    bool pending = false, hold_clean = false;
-    int hold_seg = 0, hold_last = 0;
-    auto flush = [&]() -> bool {                 // it goes into the ring
-      if (!pending) return true;
-      pending = false;
-      if (!commit(hold, hold_clean, hold_seg)) return false;
-      if (hold_last) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.vdone[hold_seg % kRing]);
-      }
-      return true;
-    };
-    while (run && it.next(s)) {
+    for (int seg = 0; run && it.next(s); ++seg) {
       const int32_t* pt = a.page_table + static_cast<long long>(s.b) * a.max_pages;
-      int pg = -1;
-      const int npg = (s.len + kTile - 1) / kTile;
-      // a selection: this lane's two keys of a tile, as cache slots
+      const int npg = (s.len + kPage - 1) / kPage;
+      // a selection: a key of the tile as a cache slot
       auto slot_of = [&](int t, int j) -> int {
-        int x = t * kTile + j, pos;
-        const int ksel = (a.k + kTile - 1) / kTile * kTile;
+        int x = t * kPage + j, pos;
         if (x < a.k) {
           pos = a.sel[static_cast<long long>(s.q0) * a.k + x];
           if (pos < 0 || s.len == 0) return -1;
@@ -763,7 +863,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(const __grid_constant
             return -1;
           }
         } else {
-          x -= ksel;
+          x -= (a.k + kPage - 1) / kPage * kPage;
           if (x < 0 || !a.mask || x >= s.nd || (x >> 5) >= a.mask_words) return -1;
           if (!((a.mask[static_cast<long long>(s.q0) * a.mask_words + (x >> 5)] >> (x & 31)) & 1)) return -1;
           pos = s.len - s.nd + x;
@@ -775,99 +875,117 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(const __grid_constant
         }
         return page * 64 + (pos & 63);
       };
-      int k0 = -1, k1 = -1;
-      if (SPARSE) {
+      int k0 = -1, k1 = -1, pg = -1;
+      if (C::SPARSE) {
         k0 = slot_of(s.t0, lane);
         k1 = slot_of(s.t0, lane + 32);
       }
-      for (int t = s.t0; t < s.t1; ++t, ++n) {
-        int at[NCH];
-        unsigned long long vm;
-        bool tma = false, clean = false;
-        int page = -1;
-        if constexpr (SPARSE) {
-          vm = __ballot_sync(0xffffffffu, k0 >= 0) |
-               (static_cast<unsigned long long>(__ballot_sync(0xffffffffu, k1 >= 0)) << 32);
+      for (int t = s.t0; run && t < s.t1; ++t, ++n) {
+        const bool last = t + 1 == s.t1;
+        if constexpr (C::SPARSE) {
+          const unsigned long long vm = __ballot_sync(0xffffffffu, k0 >= 0) |
+                                        (static_cast<unsigned long long>(__ballot_sync(0xffffffffu, k1 >= 0)) << 32);
+          int at[NCH];
 #pragma unroll
           for (int i = 0; i < NCH; ++i) {
-            const int row = row0 + i * RSTEP;
-            const int u = __shfl_sync(0xffffffffu, k0, row & 31), v = __shfl_sync(0xffffffffu, k1, row & 31);
-            at[i] = row < 32 ? u : v;
+            const int r = row0 + i * RSTEP;
+            const int u = __shfl_sync(0xffffffffu, k0, r & 31), v = __shfl_sync(0xffffffffu, k1, r & 31);
+            at[i] = r < 32 ? u : v;
           }
-          if (t + 1 < s.t1) {
+          if (!last) {
             k0 = slot_of(t + 1, lane);
             k1 = slot_of(t + 1, lane + 32);
           }
-        } else {
-          const int rel = (t - s.t0) & 31;
-          if (rel == 0) pg = t + lane < min(s.t1, npg) ? pt[t + lane] : -1;
-          page = __shfl_sync(0xffffffffu, pg, rel);
-          const bool ok = page >= 0 && page < a.num_pages;
-          if (!ok && t < npg && lw == 0 && lane == 0) atomicOr(a.status, DSA_DEV_BOUNDS);
-          vm = ok ? low_bits(s.len - t * kTile) : 0ull;
-          tma = FMT == DSA_FMT_BF16 && ok && (t + 1) * kTile <= s.full;
-          clean = (t + 1) * kTile > s.full;
-#pragma unroll
-          for (int i = 0; i < NCH; ++i) {
-            const int row = row0 + i * RSTEP;
-            at[i] = (vm >> row) & 1 ? page * 64 + row : -1;
+          if (lw == 0 && lane == 0) {
+            sh.vmask[n % kRing][0] = vm;
+            mbar_arrive(&sh.mfull[n % kRing]);
           }
-        }
-        Tile kt;
-        if (!tma) fetch(kt, at, s.h, false);
-        if (!flush()) {
-          run = false;
-          break;
-        }
-        if (lw == 0 && lane == 0) {
-          sh.vmask[n % kRing] = vm;
-          mbar_arrive(&sh.mfull[n % kRing]);
-        }
-        if (tma) {
-          // K, then V: a page's 64 rows, 64 dimensions a box
+          run = ask(at, s.h, false, 0, false, false, seg) && ask(at, s.h, true, 0, false, last, seg);
+        } else {
+          // the tile's pages: 32 page ids at a time
+          constexpr int PER = 32 / C::HALVES;
+          const int rel = (t - s.t0) % PER;
+          if (rel == 0) {
+            const int x = t * C::HALVES + lane;
+            pg = x < min(s.t1 * C::HALVES, npg) ? pt[x] : -1;
+          }
+          int page[C::HALVES];
+          unsigned long long vm[C::HALVES];
+          bool whole = true;  // every row sees every key
 #pragma unroll
-          for (int v = 0; v < 2; ++v) {
-            if (!wait_warp(&sh.empty[slot], round ^ 1)) {
-              run = false;
-              break;
-            }
-            if (lane == 0) {
-              if (lw == 0) {
-                mbar_arrive_expect_tx(&sh.full[slot], C::SLOT);
-                const int y = ((page * a.kv_heads + s.h) * 2 + v) * kTile;
+          for (int h = 0; h < C::HALVES; ++h) {
+            const int x = t * C::HALVES + h;
+            page[h] = __shfl_sync(0xffffffffu, pg, rel * C::HALVES + h);
+            const bool ok = page[h] >= 0 && page[h] < a.num_pages;
+            if (!ok && x < npg && lw == 0 && lane == 0) atomicOr(a.status, DSA_DEV_BOUNDS);
+            vm[h] = ok ? low_bits(s.len - x * kPage) : 0ull;
+            whole = whole && ok;
+          }
+          const bool clean = (t + 1) * C::KT > s.full;
+          whole = whole && !clean;
+          if (lw == 0 && lane == 0) {
 #pragma unroll
-                for (int c = 0; c < C::NBLK; ++c)
-                  tma_load_2d(smem + slot * C::SLOT + c * (kTile * 128), &tm, c * 64, y, &sh.full[slot]);
-              } else {
-                mbar_arrive(&sh.full[slot]);
+            for (int h = 0; h < C::HALVES; ++h) sh.vmask[n % kRing][h] = vm[h];
+            mbar_arrive(&sh.mfull[n % kRing]);
+          }
+#pragma unroll 1
+          for (int v = 0; run && v < 2; ++v) {
+            if (FMT == DSA_FMT_BF16 && whole) {
+              // by TMA: 64 keys of 64 dimensions a box
+              if (!__all_sync(0xffffffffu, mbar_try_wait(smem_u32(&sh.empty[slot]), round ^ 1))) {
+                cp_async_wait<0>();
+                while (sent < issued) hand_over(sh.info[lw][sent & 7]);
+                run = wait_warp(&sh.empty[slot], round ^ 1);
+                if (!run) break;
+              }
+              if (lane == 0) {
+#pragma unroll
+                for (int h = 0; h < C::HALVES; ++h) {
+                  if (lw != 0) {
+                    mbar_arrive(&sh.full[slot]);
+                    continue;
+                  }
+                  mbar_arrive_expect_tx(&sh.full[slot], kPage * D * 2);
+                  const int y = ((page[h] * a.kv_heads + s.h) * 2 + v) * kPage;
+#pragma unroll
+                  for (int c = 0; c < C::NBLK; ++c)
+                    tma_load_2d(smem + slot * C::SLOT + c * (C::KT * 128) + h * (kPage * 128), &tm, c * 64, y, &sh.full[slot]);
+                }
+                if (v && last) mbar_arrive(&sh.vdone[seg % kRing]);
+              }
+              advance();
+              ++slots;
+              if (v) {
+                cp_async_wait<0>();
+                while (sent < issued) hand_over(sh.info[lw][sent & 7]);
+              }
+            } else {
+#pragma unroll
+              for (int h = 0; run && h < C::HALVES; ++h) {
+                int at[NCH];
+#pragma unroll
+                for (int i = 0; i < NCH; ++i) {
+                  const int r = row0 + i * RSTEP;
+                  at[i] = (vm[h] >> r) & 1 ? page[h] * 64 + r : -1;
+                }
+                run = ask(at, s.h, v, h, clean && v, v && last && h + 1 == C::HALVES, seg);
               }
             }
-            advance();
           }
-          if (!run) break;
-          if (t + 1 == s.t1) {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.vdone[seg % kRing]);
-          }
-        } else {
-          fetch(hold, at, s.h, true);
-          if (!commit(kt, false, seg)) {
-            run = false;
-            break;
-          }
-          pending = true;
-          hold_clean = clean;
-          hold_seg = seg;
-          hold_last = t + 1 == s.t1;
         }
       }
-      ++seg;
     }
-    if (run) run = flush();
-    // after a wait that ran out, copies in flight land before the CTA exits
+    if constexpr (C::RAW) {
+      while (run && sent < issued) run = settle(std::integral_constant<int, 0>());
+    } else {
+      cp_async_wait<0>();
+      while (run && sent < issued) hand_over(sh.info[lw][sent & 7]);
+    }
+    cp_async_wait<0>();
+    // after a wait that ran out, TMA copies in flight land before the CTA exits
     if (*abort_flag && FMT == DSA_FMT_BF16 && lw == 0 && lane == 0) {
-      for (int i = 1; i <= C::NS && issued - i >= 0; ++i) {
-        const int x = issued - i;
+      for (int i = 1; i <= C::NS && slots - i >= 0; ++i) {
+        const int x = slots - i;
         mbar_wait(&sh.full[x % C::NS], (x / C::NS) & 1, 20000000LL);
       }
     }
@@ -877,32 +995,36 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(const __grid_constant
   __syncthreads();
   if (warp == 0) {
     tc_fence_after();
-    tmem_dealloc(tb, C::TMEM);
+    tmem_dealloc(sh.tmem, C::TMEM);
   }
 }
 
-typedef dsa_status (*RunFn)(dsa_ctx*, bool, int, const CUtensorMap&, const AttnArgs&, int, cudaStream_t);
-
-template <int FMT, int D, bool SPARSE>
+template <int FMT, int D, int FORM>
 dsa_status run_one(dsa_ctx* ctx, const CUtensorMap& tm, const AttnArgs& a, int grid, cudaStream_t stream) {
-  auto kern = attn_kernel<FMT, D, SPARSE>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<D>()) != cudaSuccess)
-    return DSA_ERR_CUDA;
+  using C = Cfg<FMT, D, FORM>;
+  auto kern = attn_kernel<FMT, D, FORM>;
+  constexpr int bytes = smem_bytes<C>();
+  static_assert(bytes * C::CTAS <= 233472 - 1024 * C::CTAS, "shared memory of an SM");
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return DSA_ERR_CUDA;
   LaunchScope scope(ctx, DSA_K_ATTN, stream);
-  return launch_pdl(kern, dim3(grid), dim3(kThreads), smem_bytes<D>(), stream, tm, a) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+  return launch_pdl(kern, dim3(grid), dim3(C::THREADS), bytes, stream, tm, a) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 
 template <int FMT>
-dsa_status run_fmt(dsa_ctx* ctx, bool sparse, int D, const CUtensorMap& tm, const AttnArgs& a, int grid, cudaStream_t stream) {
+dsa_status run_fmt(dsa_ctx* ctx, int form, int D, const CUtensorMap& tm, const AttnArgs& a, int grid, cudaStream_t stream) {
   if (D == 128)
-    return sparse ? run_one<FMT, 128, true>(ctx, tm, a, grid, stream) : run_one<FMT, 128, false>(ctx, tm, a, grid, stream);
-  return sparse ? run_one<FMT, 64, true>(ctx, tm, a, grid, stream) : run_one<FMT, 64, false>(ctx, tm, a, grid, stream);
+    return form == kSparse ? run_one<FMT, 128, kSparse>(ctx, tm, a, grid, stream)
+           : form == kWide ? run_one<FMT, 128, kWide>(ctx, tm, a, grid, stream)
+                           : run_one<FMT, 128, kTree>(ctx, tm, a, grid, stream);
+  return form == kSparse ? run_one<FMT, 64, kSparse>(ctx, tm, a, grid, stream)
+         : form == kWide ? run_one<FMT, 64, kWide>(ctx, tm, a, grid, stream)
+                         : run_one<FMT, 64, kTree>(ctx, tm, a, grid, stream);
 }
 
 // One cache format's kernels: attn.cu (bf16), attn_fp8.cu, attn_fp4.cu.
-dsa_status run_bf16(dsa_ctx* ctx, bool sparse, int D, const CUtensorMap& tm, const AttnArgs& a, int grid, cudaStream_t stream);
-dsa_status run_fp8(dsa_ctx* ctx, bool sparse, int D, const CUtensorMap& tm, const AttnArgs& a, int grid, cudaStream_t stream);
-dsa_status run_fp4(dsa_ctx* ctx, bool sparse, int D, const CUtensorMap& tm, const AttnArgs& a, int grid, cudaStream_t stream);
+dsa_status run_bf16(dsa_ctx* ctx, int form, int D, const CUtensorMap& tm, const AttnArgs& a, int grid, cudaStream_t stream);
+dsa_status run_fp8(dsa_ctx* ctx, int form, int D, const CUtensorMap& tm, const AttnArgs& a, int grid, cudaStream_t stream);
+dsa_status run_fp4(dsa_ctx* ctx, int form, int D, const CUtensorMap& tm, const AttnArgs& a, int grid, cudaStream_t stream);
 
 }  // namespace at
 }  // namespace dsa

@@ -5,8 +5,8 @@
 namespace dsa {
 namespace at {
 
-dsa_status run_fp8(dsa_ctx* ctx, bool sparse, int D, const CUtensorMap& tm, const AttnArgs& a, int grid, cudaStream_t stream) {
-  return run_fmt<DSA_FMT_FP8>(ctx, sparse, D, tm, a, grid, stream);
+dsa_status run_fp8(dsa_ctx* ctx, int form, int D, const CUtensorMap& tm, const AttnArgs& a, int grid, cudaStream_t stream) {
+  return run_fmt<DSA_FMT_FP8>(ctx, form, D, tm, a, grid, stream);
 }
 
 }  // namespace at

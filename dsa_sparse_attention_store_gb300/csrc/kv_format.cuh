@@ -97,5 +97,23 @@ __device__ __forceinline__ void widen_e2m1(uint32_t w, const Factor<DSA_FMT_FP4>
   }
 }
 
+// bf16 pairs: what is not finite becomes zero; whether anything did
+template <int N>
+__device__ __forceinline__ bool zero_nonfinite(uint32_t (&w)[N]) {
+  bool found = false;
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    if ((w[j] & 0x7F800000u) == 0x7F800000u) {
+      w[j] &= 0x0000FFFFu;
+      found = true;
+    }
+    if ((w[j] & 0x7F80u) == 0x7F80u) {
+      w[j] &= 0xFFFF0000u;
+      found = true;
+    }
+  }
+  return found;
+}
+
 }  // namespace kvf
 }  // namespace dsa

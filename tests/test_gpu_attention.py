@@ -142,6 +142,21 @@ def test_chain_matches_reference(ctx, fmt, D):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("ctx_lens,nds,kv,G,masked", [
+    ([0, 500, 0], [33, 70, 1], 1, 8, True),     # units of 264, 560 and 8 rows: whole, part of and none of the second group
+    ([1000], [17], 2, 16, True),                # 272 rows: the last unit has 16
+    ([2000, 300], [100, 64], 1, 12, False),
+    ([64, 128], [96, 160], 4, 2, False),        # rows that end with the tiles
+    ([5000], [130], 1, 3, True),                # a unit divided among many CTAs
+])
+def test_wide_units_match_reference(ctx, fmt, D, ctx_lens, nds, kv, G, masked):
+    c = Case(hash((fmt, D, kv, G, len(nds), 2)) % 10000, ctx_lens, nds, kv, G, D, fmt, masked=masked)
+    c.check(*c.run(ctx))
+    assert ctx.device_status() == 0
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("q_gain", [0.0, 8.0])
 def test_flat_and_peaked_scores(ctx, fmt, q_gain):
     # all weights equal, and weights that one key dominates (the running maximum moves late)
@@ -257,6 +272,31 @@ def test_hidden_values_do_not_reach_a_row(ctx, fmt, D, what, part):
         assert np.array_equal(np.isnan(got), np.isnan(o[3])) and np.array_equal(np.isposinf(got), np.isposinf(o[3]))
         assert not np.any(np.isfinite(got[:, :n])) and np.all(np.isfinite(got[:, n:]))
         assert np.all(np.abs(got[:, n:] - clean[0][3][:, n:]) <= A.tolerance(*clean, c.scale, D, 200.0)[0][3][:, n:])
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("ctx_len", [0, 100, 130, 199])
+def test_hidden_values_in_wide_units(ctx, fmt, D, ctx_len):
+    # 70 drafted tokens, 280 rows; a committed token and a drafted one hold
+    # what is not finite in the same 128-key tile as keys others do not see
+    c = Case(43, [ctx_len], [70], 1, 4, D, fmt)
+    bits = c.bits.copy()
+    bits[:, 9] = False
+    bits[9, 9] = bits[60, 9] = True
+    c.set_bits(bits)
+    clean = c.reference()
+    _poison(c, 0, 9, "nan")
+    out, lse = c.run(ctx)
+    rows = [i for i in range(70) if i not in (9, 60)]
+    c.check(out, lse, ref=clean, rows=rows)
+    got, o = out.double().cpu().numpy(), c.reference()[0]
+    assert np.array_equal(np.isnan(got), np.isnan(o)) and np.isnan(got[9]).any() and np.isnan(got[60]).any()
+    if ctx_len:                                 # a committed token is seen by every row
+        _poison(c, 0, -3, "nan")
+        out, lse = c.run(ctx)
+        got, o = out.double().cpu().numpy(), c.reference()[0]
+        assert np.array_equal(np.isnan(got), np.isnan(o)) and np.isnan(got).any(-1).all()
 
 
 @pytest.mark.parametrize("fmt", FMTS)
