@@ -185,9 +185,9 @@ dsa_status launch_attn(dsa_ctx* ctx, const dsa_attn_args& p, const int32_t* sel,
   CUtensorMap tm = {};
   if (p.fmt == DSA_FMT_BF16) {  // the cache as rows of D elements; a page's K or V of one head is 64 of them
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(p.head_dim),
-                                static_cast<cuuint64_t>(p.num_pages) * p.kv_heads * 2 * kPage};
+                                static_cast<cuuint64_t>(p.num_pages) * p.kv_heads * 2 * kTile};
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(p.head_dim) * 2};
-    const cuuint32_t box[2] = {64, kPage};
+    const cuuint32_t box[2] = {64, kTile};
     const cuuint32_t estr[2] = {1, 1};
     if (reinterpret_cast<EncodeFn>(ctx->encode_tiled)(
             &tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p.cache), dims, strides, box, estr,

@@ -17,19 +17,24 @@
 // workspace and the join kernel adds them in a fixed order.
 //
 // Forms. Rows up to 128 (a decode step, small trees, selections) are bound by
-// reading the cache: 64-key tiles, two CTAs per SM, so that one's softmax runs
-// under the other's products; the queries stay in TMEM as the A operand of the
-// first product, which leaves shared memory to the tiles. Rows beyond that
-// (kWide: large trees, chunks of a prefill) are bound by the tensor cores and
-// by what L2 delivers: 128-key tiles (a product over 64 keys takes as long as
-// one over 128), one CTA per SM with two groups of four softmax warps that
-// share every tile between 256 rows; queries in shared memory.
+// reading the cache: two CTAs per SM, so that one's softmax runs under the
+// other's products, and the queries stay in TMEM as the A operand of the first
+// product, which leaves shared memory to the tiles. Rows beyond that (kWide:
+// large trees, chunks of a prefill) are bound by the tensor cores and by what
+// L2 delivers: one CTA per SM with two groups of four softmax warps that share
+// every tile between 256 rows; queries in shared memory, which leaves TMEM for
+// two score buffers, so that the next tile's scores are there when a tile's
+// softmax ends.
 //
-// A CTA: one or two groups of 4 softmax warps (a row per thread and TMEM lane;
-// one thread of a group issues its products) and 4 loader warps. TMEM columns
-// of a group: accumulator [0, D), scores after it with the bf16 weights over
-// them, then the queries where they are in TMEM. Keys and values pass through
-// a ring of tiles in the 128-byte swizzle: K is read K-major, V MN-major.
+// A CTA: one or two groups of 4 softmax warps (a row per thread and TMEM lane)
+// and 4 loader warps. One thread issues a group's products: of the group's
+// first warp where scores and softmax take turns anyway (a barrier of the four
+// warps is cheaper than a hop to another warp), of a warp of its own in the
+// wide form, because issuing waits for the tensor cores' queue. TMEM columns
+// of a group: accumulator [0, D), then one or two score buffers of 64 with the
+// bf16 weights over them, then the queries where they are in TMEM. Keys and
+// values pass through a ring of 64-key tiles in the 128-byte swizzle: K is
+// read K-major, V MN-major.
 //
 // Loaders: in bf16, tiles that every row sees whole come by TMA; other bf16
 // tiles (selections, the tiles where visibility ends) by 16-byte asynchronous
@@ -49,7 +54,7 @@
 namespace dsa {
 namespace at {
 
-constexpr int kPage = kvf::kPage;
+constexpr int kTile = kvf::kPage;  // keys of a tile: a page's, or 64 selected ones
 constexpr int kRing = 16;  // entries of the per-tile and per-segment rings; loaders run at most 9 tiles ahead
 enum Form { kTree = 0, kSparse = 1, kWide = 2 };
 
@@ -87,31 +92,34 @@ struct Cfg {
   static constexpr bool SPARSE = FORM == kSparse;
   static constexpr int WG = FORM == kWide ? 2 : 1;     // groups of four softmax warps
   static constexpr int ROWS = 128 * WG;                // rows of a unit
-  static constexpr int KT = FORM == kWide ? 128 : 64;  // keys of a tile
-  static constexpr int HALVES = KT / kPage;
-  static constexpr int THREADS = 128 * WG + 128;
+  static constexpr int SBUF = FORM == kWide ? 2 : 1;   // score buffers
+  static constexpr int THREADS = 128 * WG + 128 + (FORM == kWide ? 64 : 0);
   static constexpr int CTAS = FORM == kWide ? 1 : 2;   // per SM
   static constexpr int NBLK = D / 64;
-  static constexpr int SLOT = KT * D * 2;
+  static constexpr int SLOT = kTile * D * 2;
   // chunks of 16 code bytes: of a row's 64 dimensions, and a thread's per 64 keys
   static constexpr int CPB = FMT == DSA_FMT_BF16 ? 8 : FMT == DSA_FMT_FP8 ? 4 : 2;
   static constexpr int NCH = NBLK * CPB / 2;
   static constexpr bool RAW = FMT != DSA_FMT_BF16;
   static constexpr int RAW_SLOT = RAW ? NCH * 128 * 20 + (D == 64 ? 128 * 4 : 0) : 0;  // codes, a scale word per chunk, flags
-  // ring depths that fill the shared memory (113 KB or 227 KB a CTA)
-  static constexpr int P = !RAW ? 3 : FORM == kWide ? (FMT == DSA_FMT_FP8 ? 3 : 6) : (FMT == DSA_FMT_FP8 ? 4 : 6);
-  static constexpr int NS = FORM == kWide ? (D == 64 ? 8 : RAW ? 4 : 5)
-                                          : (D == 64 ? 8 : FMT == DSA_FMT_BF16 ? 6 : FMT == DSA_FMT_FP8 ? 4 : 5);
+  // ring depths that fill the shared memory (113 KB or 227 KB a CTA): tiles, and
+  // codes on their way
+  static constexpr int P = !RAW ? 3 : FMT == DSA_FMT_FP8 ? 4 : 6;
+  static constexpr int NS = D == 64 ? (FORM == kWide ? 12 : 8)
+                            : FORM == kWide ? (!RAW ? 10 : FMT == DSA_FMT_FP8 ? 7 : 8)
+                                            : (!RAW ? 6 : FMT == DSA_FMT_FP8 ? 4 : 5);
   static constexpr int QBYTES = FORM == kWide ? ROWS * D * 2 : 0;
   // TMEM columns of a group, and of the CTA (two CTAs share the SM's 512)
-  static constexpr uint32_t O = 0, S = D, Q = D + 64, STRIDE = 256, TMEM = 256 * WG;
+  static constexpr uint32_t O = 0, S = D, Q = D + 64 * SBUF, STRIDE = 256, TMEM = 256 * WG;
 };
 
 struct Shared {
-  uint64_t full[8], empty[8];
+  uint64_t full[12], empty[12];
   uint64_t mfull[kRing], vdone[kRing];
-  uint64_t s_full[2], o_full[2], fin[2];
-  unsigned long long vmask[kRing][2];  // visible keys of a tile, as far as the loader knows
+  // by group and score buffer (a barrier per buffer: no phase can complete twice
+  // before a wait for it): scores there, weights there, their product done
+  uint64_t s_full[2][2], o_full[2][2], p_ready[2][2], q_ready[2], fin[2];
+  unsigned long long vmask[kRing];  // visible keys of a tile, as far as the loader knows
   int bad[kRing];                      // segment number + 1 where a loader replaced a value
   int info[4][8];                      // a loader warp's tiles on their way
   long long scan[16];
@@ -131,12 +139,12 @@ template <class C>
 __device__ __forceinline__ int tiles_of(const AttnArgs& a, int nd, int len, int r) {
   int end = len;
   if (!a.mask) end = len - nd + min(nd, static_cast<int>((static_cast<long long>(r + 1) * C::ROWS - 1) / a.G) + 1);
-  return max(1, (end + C::KT - 1) / C::KT);
+  return max(1, (end + kTile - 1) / kTile);
 }
 
 // 64-key tiles of a query's selection and, after them, the drafted tokens
 __device__ __forceinline__ int selection_tiles(const AttnArgs& a) {
-  return (a.k + kPage - 1) / kPage + (a.mask ? (a.mask_words + 1) / 2 : 0);
+  return (a.k + kTile - 1) / kTile + (a.mask ? (a.mask_words + 1) / 2 : 0);
 }
 
 __device__ __forceinline__ bool read_seq(const AttnArgs& a, int b, int& q0, int& nd, int& len) {
@@ -341,11 +349,11 @@ __device__ __noinline__ void fix_nonfinite(const AttnArgs& a, const Seg& s, int 
   for (int d = 0; d < D; ++d) {
     float add = 0.f;
     for (int t = t0; t < t1; ++t) {
-      if (t * kPage >= s.len) break;
+      if (t * kTile >= s.len) break;
       const int page = a.page_table[static_cast<long long>(s.b) * a.max_pages + t];
       if (page < 0 || page >= a.num_pages) continue;
       const uint8_t* blk = a.cache + (static_cast<long long>(page) * a.kv_heads + s.h) * L::HEAD_BYTES;
-      unsigned long long m = valid ? row_mask(a, s, i, t * kPage) & low_bits(s.len - t * kPage) : 0ull;
+      unsigned long long m = valid ? row_mask(a, s, i, t * kTile) & low_bits(s.len - t * kTile) : 0ull;
       while (m) {
         const int j = __ffsll(static_cast<long long>(m)) - 1;
         m &= m - 1;
@@ -378,7 +386,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
 
   if (tid == 0) {
     for (int i = 0; i < C::NS; ++i) {
-      mbar_init(&sh.full[i], 4 * C::HALVES);  // a loader warp and 64 keys
+      mbar_init(&sh.full[i], 4);
       mbar_init(&sh.empty[i], C::WG);
     }
     for (int i = 0; i < kRing; ++i) {
@@ -387,8 +395,13 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
       sh.bad[i] = 0;
     }
     for (int i = 0; i < C::WG; ++i) {
-      mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.o_full[i], 1);
+      mbar_init(&sh.s_full[i][0], 1);
+      mbar_init(&sh.s_full[i][1], 1);
+      mbar_init(&sh.p_ready[i][0], 4);
+      mbar_init(&sh.p_ready[i][1], 4);
+      mbar_init(&sh.q_ready[i], 4);
+      mbar_init(&sh.o_full[i][0], 1);
+      mbar_init(&sh.o_full[i][1], 1);
       mbar_init(&sh.fin[i], 1);
     }
     sh.abort = 0;
@@ -426,6 +439,53 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
     }
   };
 
+  constexpr uint32_t kIdescQk = idesc_f16(128, kTile, true);
+  constexpr uint32_t kIdescPv = idesc_f16(128, D, true) | kIdescBMn;
+  const uint64_t kdesc = sw128_desc(smem_u32(smem)), vdesc = sw128_mn_desc(smem_u32(smem), kTile * 128);
+  const uint64_t qdesc0 = sw128_desc(smem_u32(qsm));
+  // The products. Called by a whole warp; the operands come from lane 0, so
+  // that the compiler keeps them in uniform registers (issuing a tile's took
+  // 1100 cycles without, most of it moving operands; 700 with)
+  auto scores = [&](int wg, int at, int buf) {
+    const uint32_t tb = __shfl_sync(0xffffffffu, sh.tmem + wg * C::STRIDE, 0);
+    const uint64_t qdesc = qdesc0 + __shfl_sync(0xffffffffu, wg, 0) * ((128 * D * 2) >> 4);
+    const uint64_t k = kdesc + __shfl_sync(0xffffffffu, at, 0) * (C::SLOT >> 4);
+    const uint32_t d = tb + C::S + __shfl_sync(0xffffffffu, buf, 0) * 64;
+    if (!elect_one()) return;
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+      const uint64_t b = k + (((i / 4) * (kTile * 128) + (i % 4) * 32) >> 4);
+      if constexpr (FORM == kWide)
+        tc_mma_f16(d, qdesc + (((i / 4) * (128 * 128) + (i % 4) * 32) >> 4), b, kIdescQk, i > 0);
+      else
+        tc_mma_f16_ta(d, tb + C::Q + 8 * i, b, kIdescQk, i > 0);
+    }
+    tc_commit(&sh.empty[at]);
+    tc_commit(&sh.s_full[wg][buf]);
+  };
+  auto values = [&](int wg, int at, int buf, bool first) {
+    const uint32_t tb = __shfl_sync(0xffffffffu, sh.tmem + wg * C::STRIDE, 0);
+    const uint64_t v = vdesc + __shfl_sync(0xffffffffu, at, 0) * (C::SLOT >> 4);
+    const uint32_t p = tb + C::S + __shfl_sync(0xffffffffu, buf, 0) * 64;
+    if (!elect_one()) return;
+#pragma unroll
+    for (int i = 0; i < kTile / 16; ++i)
+      tc_mma_f16_ta(tb + C::O, p + 8 * i, v + ((i * 2048) >> 4), kIdescPv, !first || i > 0);
+    tc_commit(&sh.empty[at]);
+    tc_commit(&sh.o_full[wg][buf]);
+  };
+
+  // products in flight end before their TMEM goes back, after an abort too
+  auto settle_products = [&](int wg) {
+    __syncwarp();
+    if (elect_one()) {
+      tc_commit(&sh.fin[wg]);
+      mbar_wait(&sh.fin[wg], 0);
+    }
+    __syncwarp();
+  };
+  auto has_rows = [&](int wg, const Seg& g) { return wg * 128 < g.rows; };
+
   if (count <= 0) {
     if (tid == 0) a.meta[2 * cta] = make_int4(0, 0, 0, 0);
   } else if (warp < NSW) {
@@ -434,44 +494,14 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
     const int row = tid;                      // of the unit
     const uint32_t tb = sh.tmem + wg * C::STRIDE;
     const uint32_t lanes = static_cast<uint32_t>(gw * 32) << 16;
-    const uint32_t tO = tb + C::O + lanes, tS = tb + C::S + lanes;
+    const uint32_t tO = tb + C::O + lanes;
     Iter<C> it(a, sh.start, count);
     Seg s;
     bool more = it.next(s), run = true;
     int seg = 0, n = 0;   // segments, tiles
-    int ns = 0, no = 0;   // this group's first products and accumulators so far
+    int ns = 0;           // tiles this group has worked on: score buffers and accumulator phases
     int4 m0 = make_int4(0, 0, 0, 0), m1 = m0;
-    constexpr uint32_t kIdescQk = idesc_f16(128, C::KT, true);
-    constexpr uint32_t kIdescPv = idesc_f16(128, D, true) | kIdescBMn;
-    const uint64_t kdesc = sw128_desc(smem_u32(smem)), vdesc = sw128_mn_desc(smem_u32(smem), C::KT * 128);
-    const uint64_t qdesc = sw128_desc(smem_u32(qsm) + wg * (128 * D * 2));
-    // The products. Called by a whole warp; the operands come from lane 0, so
-    // that the compiler keeps them in uniform registers (issuing a tile's took
-    // 1100 cycles without, most of it moving operands; 700 with)
-    auto scores = [&](int at) {
-      const uint64_t k = kdesc + __shfl_sync(0xffffffffu, at, 0) * (C::SLOT >> 4);
-      if (!elect_one()) return;
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        const uint64_t b = k + (((i / 4) * (C::KT * 128) + (i % 4) * 32) >> 4);
-        if constexpr (FORM == kWide)
-          tc_mma_f16(tb + C::S, qdesc + (((i / 4) * (128 * 128) + (i % 4) * 32) >> 4), b, kIdescQk, i > 0);
-        else
-          tc_mma_f16_ta(tb + C::S, tb + C::Q + 8 * i, b, kIdescQk, i > 0);
-      }
-      tc_commit(&sh.empty[at]);
-      tc_commit(&sh.s_full[wg]);
-    };
-    auto values = [&](int at, bool first, bool last) {
-      const uint64_t v = vdesc + __shfl_sync(0xffffffffu, at, 0) * (C::SLOT >> 4);
-      if (!elect_one()) return;
-#pragma unroll
-      for (int i = 0; i < C::KT / 16; ++i)
-        tc_mma_f16_ta(tb + C::O, tb + C::S + 8 * i, v + ((i * 2048) >> 4), kIdescPv, !first || i > 0);
-      tc_commit(&sh.empty[at]);
-      if (last) tc_commit(&sh.o_full[wg]);
-    };
-    // the unit's queries, then the first tile's scores
+    // the unit's queries, then its first tiles' scores
     auto start_unit = [&](const Seg& g) {
       const bool valid = row < g.rows;
       const int r = g.r0 + row;
@@ -502,34 +532,29 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
         tmem_st_wait();
         tc_fence_before();
       }
-      if (gw == 0) run = run && wait_warp(&sh.full[slot], round);
-      run = named_bar_all(1 + wg, 128, run);  // the group's warps go on, or stop, together
-      if (gw == 0 && run) {
-        tc_fence_after();
-        scores(slot);
+      if constexpr (FORM == kWide) {
         __syncwarp();
-      }
-      advance();
-    };
-    auto has_rows = [&](const Seg& g) { return wg * 128 < g.rows; };
-    if (more && has_rows(s)) start_unit(s);
-    while (more) {
-      if (FORM == kWide && !has_rows(s)) {
-        // a unit of at most 128 rows: this group only passes the tiles on
-        for (int t = s.t0; t < s.t1; ++t, ++n) {
-          for (int v = 0; v < 2; ++v) {
-            if (gw == 0 && run) {
-              run = wait_warp(&sh.full[slot], round);
-              if (run && lane == 0) mbar_arrive(&sh.empty[slot]);
-            }
-            advance();
-          }
+        if (lane == 0) mbar_arrive(&sh.q_ready[wg]);
+      } else {
+        if (gw == 0) run = run && wait_warp(&sh.full[slot], round);
+        run = named_bar_all(1, 128, run);  // the group's warps go on, or stop, together
+        if (gw == 0 && run) {
+          tc_fence_after();
+          scores(0, slot, 0);
+          __syncwarp();
         }
-        run = named_bar_all(1 + wg, 128, run);
+        advance();
+      }
+    };
+    // the second product of the last tile has completed
+    auto wait_product = [&]() { return wait_warp(&sh.o_full[wg][(ns - 1) & (C::SBUF - 1)], ((ns - 1) / C::SBUF) & 1); };
+    if (more && has_rows(wg, s)) start_unit(s);
+    while (more && run) {
+      if (!has_rows(wg, s)) {  // a unit of at most 128 rows: nothing for the second group
+        n += s.t1 - s.t0;
         ++seg;
         more = it.next(s);
-        if (more && has_rows(s)) start_unit(s);
-        if (!run) break;
+        if (more && has_rows(wg, s)) start_unit(s);
         continue;
       }
       const bool active = warp * 32 < s.rows;  // some row of this warp is real
@@ -538,46 +563,46 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
       float m = -INFINITY, l = 0.f;
       for (int t = s.t0; t < s.t1; ++t, ++n, ++ns) {
         run = run && wait_warp(&sh.mfull[n % kRing], (n / kRing) & 1);
-        unsigned long long see[C::HALVES];
-#pragma unroll
-        for (int h = 0; h < C::HALVES; ++h) see[h] = sh.vmask[n % kRing][h];
-        // V of this tile and K of the next, usually long there: looked at
-        // while the scores are on their way
-        const bool more_tiles = t + 1 < s.t1;
+        unsigned long long see = sh.vmask[n % kRing];
+        const int buf = ns & (C::SBUF - 1);
+        // V of this tile and the next K, usually long there: looked at while
+        // the scores are on their way
+        const bool more_scores = t + 1 < s.t1;
         const int vslot = slot, vround = round;
-        advance();
         bool there = true;
-        if (gw == 0)
-          there = __all_sync(0xffffffffu, mbar_try_wait(smem_u32(&sh.full[vslot]), vround) &&
-                                              (!more_tiles || mbar_try_wait(smem_u32(&sh.full[slot]), round)));
-        run = run && wait_warp(&sh.s_full[wg], ns & 1);
+        if constexpr (FORM != kWide) {
+          advance();
+          if (gw == 0)
+            there = __all_sync(0xffffffffu, mbar_try_wait(smem_u32(&sh.full[vslot]), vround) &&
+                                                (!more_scores || mbar_try_wait(smem_u32(&sh.full[slot]), round)));
+        }
+        run = run && wait_warp(&sh.s_full[wg][buf], (ns / C::SBUF) & 1);
         tc_fence_after();
+        const uint32_t tS = tb + C::S + 64 * buf + lanes;
         if (active && run) {
-          uint32_t x[C::KT / 32][32];
+          uint32_t x[2][32];
           tmem_ld32(tS, x[0]);
-          const int p0 = t * C::KT;
-          bool all = true;
-#pragma unroll
-          for (int h = 0; h < C::HALVES; ++h) {
-            if (!C::SPARSE && valid && p0 + (h + 1) * kPage > s.full) see[h] &= row_mask(a, s, qi, p0 + h * kPage);
-            all = all && see[h] == ~0ull;
-          }
-          const bool some = !__all_sync(0xffffffffu, all);  // a key that some row does not see
+          tmem_ld32(tS + 32, x[1]);
+          const int p0 = t * kTile;
+          if (!C::SPARSE && valid && p0 + kTile > s.full) see &= row_mask(a, s, qi, p0);
+          const bool some = !__all_sync(0xffffffffu, see == ~0ull);  // a key that some row does not see
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          tmem_ld_wait32(x[0]);
+          tmem_ld_wait32(x[1]);
+          if (some) {
 #pragma unroll
-          for (int c = 0; c < C::KT / 32; ++c) {
-            tmem_ld_wait32(x[c]);
-            if (c + 1 < C::KT / 32) tmem_ld32(tS + 32 * (c + 1), x[c + 1]);
-            if (some) {
-              const uint32_t bits = static_cast<uint32_t>(see[c / 2] >> (32 * (c & 1)));
+            for (int c = 0; c < 2; ++c) {
+              const uint32_t bits = static_cast<uint32_t>(see >> (32 * c));
 #pragma unroll
               for (int i = 0; i < 32; ++i)
                 if (!((bits >> i) & 1)) x[c][i] = 0xFF800000u;
             }
+          }
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
 #pragma unroll
             for (int i = 0; i < 32; i += 2)
               mx[(i >> 1) & 3] = fmaxf(mx[(i >> 1) & 3], fmaxf(__uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1])));
-          }
           const float mnew = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale2;
           // the running maximum moves only when it grows by more than 2^8:
           // the weights stay below 2^8 and the accumulator is rarely rescaled
@@ -585,7 +610,9 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
           if (__any_sync(0xffffffffu, grow)) {
             const float to = grow ? mnew : m;
             const float alpha = grow ? ex2(m - mnew) : 1.f;
-            if (t > s.t0) {  // s_full of this tile follows the last tile's second product
+            if (t > s.t0) {  // after the last tile's second product
+              run = run && wait_product();
+              tc_fence_after();
               l *= alpha;
 #pragma unroll 1
               for (int c = 0; c < D / 16; ++c) tmem_scale16(tO + 16 * c, alpha);
@@ -597,7 +624,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
           const unsigned long long sc = pack2(a.scale2, a.scale2), sb = pack2(-sub, -sub);
           unsigned long long sum[2] = {0ull, 0ull};  // pairs of fp32 zeros
 #pragma unroll
-          for (int c = 0; c < C::KT / 32; ++c) {
+          for (int c = 0; c < 2; ++c) {
             uint32_t p[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
@@ -615,31 +642,38 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
           unpack2(add2(sum[0], sum[1]), l0, l1);
           l += l0 + l1;
         }
-        if (gw == 0 && run && !there) {
-          run = wait_warp(&sh.full[vslot], vround);
-          if (run && more_tiles) run = wait_warp(&sh.full[slot], round);
-        }
-        tmem_st_wait();
-        tc_fence_before();
-        run = named_bar_all(1 + wg, 128, run);
-        if (gw == 0 && run) {
-          tc_fence_after();
-          values(vslot, t == s.t0, !more_tiles);
+        if constexpr (FORM == kWide) {
+          tmem_st_wait();
+          tc_fence_before();
           __syncwarp();
-          if (more_tiles) scores(slot);
-          __syncwarp();
+          if (!run) break;
+          if (lane == 0) mbar_arrive(&sh.p_ready[wg][buf]);
+        } else {
+          if (gw == 0 && run && !there) {
+            run = wait_warp(&sh.full[vslot], vround);
+            if (run && more_scores) run = wait_warp(&sh.full[slot], round);
+          }
+          tmem_st_wait();
+          tc_fence_before();
+          run = named_bar_all(1, 128, run);
+          if (gw == 0 && run) {
+            tc_fence_after();
+            values(0, vslot, 0, t == s.t0);
+            __syncwarp();
+            if (more_scores) scores(0, slot, 0);
+            __syncwarp();
+          }
+          if (more_scores) advance();
+          if (!run) break;
         }
-        if (more_tiles) advance();
-        if (!run) break;
       }
       if (!run) break;
       // the next unit's queries go up before this one's sums come down: every
       // product with the old ones has completed (s_full of the last tile)
       const Seg done = s;
       more = it.next(s);
-      if (more && has_rows(s)) start_unit(s);
-      run = run && wait_warp(&sh.o_full[wg], no & 1);
-      ++no;
+      if (more && has_rows(wg, s)) start_unit(s);
+      run = run && wait_product();
       if (!C::SPARSE) run = run && wait_warp(&sh.vdone[seg % kRing], (seg / kRing) & 1);
       tc_fence_after();
       const bool first = done.t0 == 0, last = done.t1 == done.nt;
@@ -653,7 +687,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
       }
       if (active && run) {
         if (!C::SPARSE && *static_cast<volatile int*>(&sh.bad[seg % kRing]) == seg + 1)
-          fix_nonfinite<FMT, D>(a, done, max(done.t0, done.full / C::KT) * C::HALVES, done.t1 * C::HALVES, qi, valid, tO);
+          fix_nonfinite<FMT, D>(a, done, max(done.t0, done.full / kTile), done.t1, qi, valid, tO);
         const int r = done.r0 + row;
         const long long tok = done.q0 + r / a.G;
         const int head = done.h * a.G + r % a.G;
@@ -701,16 +735,48 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
       a.meta[2 * cta] = m0;
       a.meta[2 * cta + 1] = m1;
     }
-    // products in flight end before their TMEM goes back, after an abort too
-    if (gw == 0) {
-      __syncwarp();
-      if (elect_one()) {
-        tc_commit(&sh.fin[wg]);
-        mbar_wait(&sh.fin[wg], 0);
+    if (FORM != kWide && warp == 0) settle_products(0);
+  } else if (FORM == kWide && warp >= NSW + 4) {
+    // ------------------------------------------------------------ products
+    const int wg = warp - NSW - 4;
+    Iter<C> it(a, sh.start, count);
+    Seg s;
+    bool run = true;
+    int ns = 0, units = 0;
+    while (run && it.next(s)) {
+      if (!has_rows(wg, s)) {
+        // nothing for this group: it only passes the tiles on
+        for (int i = 2 * (s.t1 - s.t0); run && i > 0; --i) {
+          run = wait_warp(&sh.full[slot], round);
+          if (run && lane == 0) mbar_arrive(&sh.empty[slot]);
+          advance();
+        }
+        continue;
       }
-      __syncwarp();
+      auto next_scores = [&](int buf) {
+        run = run && wait_warp(&sh.full[slot], round);
+        if (!run) return;
+        tc_fence_after();
+        scores(wg, slot, buf);
+        __syncwarp();
+        advance();
+      };
+      run = wait_warp(&sh.q_ready[wg], units & 1);
+      ++units;
+      for (int i = 0; i < 2 && s.t0 + i < s.t1; ++i) next_scores((ns + i) & 1);
+      for (int t = s.t0; run && t < s.t1; ++t, ++ns) {
+        const int buf = ns & 1;
+        run = wait_warp(&sh.full[slot], round) && wait_warp(&sh.p_ready[wg][buf], (ns >> 1) & 1);
+        if (!run) break;
+        tc_fence_after();
+        values(wg, slot, buf, t == s.t0);
+        __syncwarp();
+        advance();
+        if (t + 2 < s.t1) next_scores(buf);
+      }
     }
-  } else {
+    settle_products(wg);
+  } else if (warp < NSW + 4) {
     // ------------------------------------------------------------ loaders
     constexpr int CPB = C::CPB, NCH = C::NCH;
     constexpr int RL = 8 / CPB;            // rows that 8 lanes cover: their stores hit all 32 banks
@@ -722,9 +788,9 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
     const int scale_off = (blk * 64 + chunk * (64 / CPB)) / kvf::kBlock;
     const uint32_t raw_at = smem_u32(raw);
     // where a row's 16-byte unit u lies in the operand tile
-    auto place = [&](int at, int half, int i, int u) -> uint8_t* {
+    auto place = [&](int at, int i, int u) -> uint8_t* {
       const int r = row0 + i * RSTEP;
-      return smem + at * C::SLOT + blk * (C::KT * 128) + (half * kPage + r) * 128 + ((u ^ (r & 7)) << 4);
+      return smem + at * C::SLOT + blk * (kTile * 128) + r * 128 + ((u ^ (r & 7)) << 4);
     };
 
     Iter<C> it(a, sh.start, count);
@@ -734,10 +800,10 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
     bool run = true;
 
     // 64 keys have landed in this thread's part of the ring: hand them to the
-    // products. info: slot, half and what to do with them
-    //   bits 0-2 slot, 3 half, 4 replace what is not finite, 5 a segment's last, 8.. segment
+    // products. info: bits 0-3 the slot, 4 replace what is not finite, 5 a
+    // segment's last, 6 the slot's round, 8.. the segment
     auto hand_over = [&](int info) {
-      const int at = info & 7, half = (info >> 3) & 1, seg = info >> 8;
+      const int at = info & 15, seg = info >> 8;
       bool found = false;
       if constexpr (C::RAW) {
         const uint8_t* src = raw + (sent % C::P) * C::RAW_SLOT;
@@ -768,13 +834,13 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
           if (info & 16) found |= kvf::zero_nonfinite(w);
 #pragma unroll
           for (int j = 0; j < 8 / CPB; ++j)
-            *reinterpret_cast<uint4*>(place(at, half, i, chunk * (8 / CPB) + j)) =
+            *reinterpret_cast<uint4*>(place(at, i, chunk * (8 / CPB) + j)) =
                 make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
         }
       } else if (info & 16) {
 #pragma unroll
         for (int i = 0; i < NCH; ++i) {
-          uint4* p = reinterpret_cast<uint4*>(place(at, half, i, chunk));
+          uint4* p = reinterpret_cast<uint4*>(place(at, i, chunk));
           const uint4 v = *p;
           uint32_t w[4] = {v.x, v.y, v.z, v.w};
           if (kvf::zero_nonfinite(w)) {
@@ -798,14 +864,14 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
       const int info = sh.info[lw][sent & 7];
       // codes are widened into a slot that has to be free; copies into the
       // slot itself waited for that before they were issued
-      if (C::RAW && !wait_warp(&sh.empty[info & 7], ((info >> 6) & 1) ^ 1)) return false;
+      if (C::RAW && !wait_warp(&sh.empty[info & 15], ((info >> 6) & 1) ^ 1)) return false;
       hand_over(info);
       return true;
     };
     // ask for 64 keys: `at`, where each of this thread's rows lies (page * 64 + offset, or -1)
-    auto ask = [&](const int (&at)[NCH], int h, bool v, int half, bool clean, bool last, int seg) -> bool {
+    auto ask = [&](const int (&at)[NCH], int h, bool v, bool clean, bool last, int seg) -> bool {
       if constexpr (!C::RAW) {
-        if (half == 0 && !__all_sync(0xffffffffu, mbar_try_wait(smem_u32(&sh.empty[slot]), round ^ 1))) {
+        if (!__all_sync(0xffffffffu, mbar_try_wait(smem_u32(&sh.empty[slot]), round ^ 1))) {
           // what has landed goes out before this warp waits for a slot
           cp_async_wait<0>();
           while (sent < issued) hand_over(sh.info[lw][sent & 7]);
@@ -826,30 +892,28 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
                     b + (v ? L::V_SCALES : L::K_SCALES) + (((where & 63) * L::SB) & ~3), ok);
           odd |= (where & 1) << i;
         } else {
-          cp_async16(smem_u32(place(slot, half, i, chunk)), code, ok);
+          cp_async16(smem_u32(place(slot, i, chunk)), code, ok);
         }
       }
       if constexpr (C::RAW && D == 64)
         reinterpret_cast<uint32_t*>(raw + (issued % C::P) * C::RAW_SLOT + NCH * 128 * 20)[lt] = odd;
       cp_async_commit();
       if (lane == 0)
-        sh.info[lw][issued & 7] = slot | (half << 3) | (clean ? 16 : 0) | (last ? 32 : 0) | (round << 6) | (seg << 8);
+        sh.info[lw][issued & 7] = slot | (clean ? 16 : 0) | (last ? 32 : 0) | (round << 6) | (seg << 8);
       __syncwarp();
       ++issued;
-      if (half + 1 == C::HALVES) {
-        advance();
-        ++slots;
-      }
+      advance();
+      ++slots;
       if (issued - sent == C::P) return settle(std::integral_constant<int, C::P - 1>());
       return true;
     };
 
     for (int seg = 0; run && it.next(s); ++seg) {
       const int32_t* pt = a.page_table + static_cast<long long>(s.b) * a.max_pages;
-      const int npg = (s.len + kPage - 1) / kPage;
+      const int npg = (s.len + kTile - 1) / kTile;
       // a selection: a key of the tile as a cache slot
       auto slot_of = [&](int t, int j) -> int {
-        int x = t * kPage + j, pos;
+        int x = t * kTile + j, pos;
         if (x < a.k) {
           pos = a.sel[static_cast<long long>(s.q0) * a.k + x];
           if (pos < 0 || s.len == 0) return -1;
@@ -863,7 +927,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
             return -1;
           }
         } else {
-          x -= (a.k + kPage - 1) / kPage * kPage;
+          x -= (a.k + kTile - 1) / kTile * kTile;
           if (x < 0 || !a.mask || x >= s.nd || (x >> 5) >= a.mask_words) return -1;
           if (!((a.mask[static_cast<long long>(s.q0) * a.mask_words + (x >> 5)] >> (x & 31)) & 1)) return -1;
           pos = s.len - s.nd + x;
@@ -875,102 +939,101 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
         }
         return page * 64 + (pos & 63);
       };
-      int k0 = -1, k1 = -1, pg = -1;
+      // K of tile x, then V of tile x - LAG: the order the products take them in
+      constexpr int LAG = C::SBUF - 1;
+      int k0 = -1, k1 = -1;                  // a selection: this lane's two keys of the next K tile
+      int at[NCH], was[LAG + 1][NCH];        // where this thread's rows lie, now and LAG tiles ago
+      int pg = -1, pages[LAG + 1];           // 32 page ids; the page of the tiles whose V is to come
+      unsigned long long masks[LAG + 1];
+      bool wholes[LAG + 1];
       if (C::SPARSE) {
         k0 = slot_of(s.t0, lane);
         k1 = slot_of(s.t0, lane + 32);
       }
-      for (int t = s.t0; run && t < s.t1; ++t, ++n) {
-        const bool last = t + 1 == s.t1;
-        if constexpr (C::SPARSE) {
-          const unsigned long long vm = __ballot_sync(0xffffffffu, k0 >= 0) |
-                                        (static_cast<unsigned long long>(__ballot_sync(0xffffffffu, k1 >= 0)) << 32);
-          int at[NCH];
+      // by TMA: 64 keys of 64 dimensions a box
+      auto by_tma = [&](int page, bool v, bool last) -> bool {
+        if (!__all_sync(0xffffffffu, mbar_try_wait(smem_u32(&sh.empty[slot]), round ^ 1))) {
+          cp_async_wait<0>();
+          while (sent < issued) hand_over(sh.info[lw][sent & 7]);
+          if (!wait_warp(&sh.empty[slot], round ^ 1)) return false;
+        }
+        if (lane == 0) {
+          if (lw != 0) {
+            mbar_arrive(&sh.full[slot]);
+          } else {
+            mbar_arrive_expect_tx(&sh.full[slot], C::SLOT);
+            const int y = ((page * a.kv_heads + s.h) * 2 + v) * kTile;
 #pragma unroll
-          for (int i = 0; i < NCH; ++i) {
-            const int r = row0 + i * RSTEP;
-            const int u = __shfl_sync(0xffffffffu, k0, r & 31), v = __shfl_sync(0xffffffffu, k1, r & 31);
-            at[i] = r < 32 ? u : v;
+            for (int c = 0; c < C::NBLK; ++c)
+              tma_load_2d(smem + slot * C::SLOT + c * (kTile * 128), &tm, c * 64, y, &sh.full[slot]);
           }
-          if (!last) {
-            k0 = slot_of(t + 1, lane);
-            k1 = slot_of(t + 1, lane + 32);
-          }
-          if (lw == 0 && lane == 0) {
-            sh.vmask[n % kRing][0] = vm;
-            mbar_arrive(&sh.mfull[n % kRing]);
-          }
-          run = ask(at, s.h, false, 0, false, false, seg) && ask(at, s.h, true, 0, false, last, seg);
-        } else {
-          // the tile's pages: 32 page ids at a time
-          constexpr int PER = 32 / C::HALVES;
-          const int rel = (t - s.t0) % PER;
-          if (rel == 0) {
-            const int x = t * C::HALVES + lane;
-            pg = x < min(s.t1 * C::HALVES, npg) ? pt[x] : -1;
-          }
-          int page[C::HALVES];
-          unsigned long long vm[C::HALVES];
-          bool whole = true;  // every row sees every key
+          if (last) mbar_arrive(&sh.vdone[seg % kRing]);
+        }
+        advance();
+        ++slots;
+        if (sent < issued) {  // copies asked for before go out too
+          cp_async_wait<0>();
+          while (sent < issued) hand_over(sh.info[lw][sent & 7]);
+        }
+        return true;
+      };
+      for (int x = s.t0; run && x < s.t1 + LAG; ++x) {
 #pragma unroll
-          for (int h = 0; h < C::HALVES; ++h) {
-            const int x = t * C::HALVES + h;
-            page[h] = __shfl_sync(0xffffffffu, pg, rel * C::HALVES + h);
-            const bool ok = page[h] >= 0 && page[h] < a.num_pages;
-            if (!ok && x < npg && lw == 0 && lane == 0) atomicOr(a.status, DSA_DEV_BOUNDS);
-            vm[h] = ok ? low_bits(s.len - x * kPage) : 0ull;
-            whole = whole && ok;
-          }
-          const bool clean = (t + 1) * C::KT > s.full;
-          whole = whole && !clean;
-          if (lw == 0 && lane == 0) {
+        for (int j = LAG; j > 0; --j) {
+          pages[j] = pages[j - 1];
+          masks[j] = masks[j - 1];
+          wholes[j] = wholes[j - 1];
+          if (C::SPARSE)
 #pragma unroll
-            for (int h = 0; h < C::HALVES; ++h) sh.vmask[n % kRing][h] = vm[h];
-            mbar_arrive(&sh.mfull[n % kRing]);
-          }
-#pragma unroll 1
-          for (int v = 0; run && v < 2; ++v) {
-            if (FMT == DSA_FMT_BF16 && whole) {
-              // by TMA: 64 keys of 64 dimensions a box
-              if (!__all_sync(0xffffffffu, mbar_try_wait(smem_u32(&sh.empty[slot]), round ^ 1))) {
-                cp_async_wait<0>();
-                while (sent < issued) hand_over(sh.info[lw][sent & 7]);
-                run = wait_warp(&sh.empty[slot], round ^ 1);
-                if (!run) break;
-              }
-              if (lane == 0) {
+            for (int i = 0; i < NCH; ++i) was[j][i] = was[j - 1][i];
+        }
+        if (x < s.t1) {
+          unsigned long long vm;
+          if constexpr (C::SPARSE) {
+            vm = __ballot_sync(0xffffffffu, k0 >= 0) |
+                 (static_cast<unsigned long long>(__ballot_sync(0xffffffffu, k1 >= 0)) << 32);
 #pragma unroll
-                for (int h = 0; h < C::HALVES; ++h) {
-                  if (lw != 0) {
-                    mbar_arrive(&sh.full[slot]);
-                    continue;
-                  }
-                  mbar_arrive_expect_tx(&sh.full[slot], kPage * D * 2);
-                  const int y = ((page[h] * a.kv_heads + s.h) * 2 + v) * kPage;
-#pragma unroll
-                  for (int c = 0; c < C::NBLK; ++c)
-                    tma_load_2d(smem + slot * C::SLOT + c * (C::KT * 128) + h * (kPage * 128), &tm, c * 64, y, &sh.full[slot]);
-                }
-                if (v && last) mbar_arrive(&sh.vdone[seg % kRing]);
-              }
-              advance();
-              ++slots;
-              if (v) {
-                cp_async_wait<0>();
-                while (sent < issued) hand_over(sh.info[lw][sent & 7]);
-              }
-            } else {
-#pragma unroll
-              for (int h = 0; run && h < C::HALVES; ++h) {
-                int at[NCH];
-#pragma unroll
-                for (int i = 0; i < NCH; ++i) {
-                  const int r = row0 + i * RSTEP;
-                  at[i] = (vm[h] >> r) & 1 ? page[h] * 64 + r : -1;
-                }
-                run = ask(at, s.h, v, h, clean && v, v && last && h + 1 == C::HALVES, seg);
-              }
+            for (int i = 0; i < NCH; ++i) {
+              const int r = row0 + i * RSTEP;
+              const int u = __shfl_sync(0xffffffffu, k0, r & 31), v = __shfl_sync(0xffffffffu, k1, r & 31);
+              was[0][i] = r < 32 ? u : v;
             }
+            if (x + 1 < s.t1) {
+              k0 = slot_of(x + 1, lane);
+              k1 = slot_of(x + 1, lane + 32);
+            }
+          } else {
+            const int rel = (x - s.t0) & 31;
+            if (rel == 0) pg = x + lane < min(s.t1, npg) ? pt[x + lane] : -1;
+            const int page = __shfl_sync(0xffffffffu, pg, rel);
+            const bool ok = page >= 0 && page < a.num_pages;
+            if (!ok && x < npg && lw == 0 && lane == 0) atomicOr(a.status, DSA_DEV_BOUNDS);
+            vm = ok ? low_bits(s.len - x * kTile) : 0ull;
+            pages[0] = page;
+            masks[0] = vm;
+            wholes[0] = ok && (x + 1) * kTile <= s.full;  // every row sees every key
+          }
+          if (lw == 0 && lane == 0) {
+            sh.vmask[n % kRing] = vm;
+            mbar_arrive(&sh.mfull[n % kRing]);
+          }
+          ++n;
+        }
+#pragma unroll 1
+        for (int v = 0; run && v < 2; ++v) {
+          if (v ? x < s.t0 + LAG : x >= s.t1) continue;
+          const int j = v ? LAG : 0;
+          const bool last = v && x + 1 == s.t1 + LAG;
+          const bool whole = !C::SPARSE && (v ? wholes[LAG] : wholes[0]);
+          if (FMT == DSA_FMT_BF16 && whole) {
+            run = by_tma(v ? pages[LAG] : pages[0], v, last);
+          } else {
+            const int page = C::SPARSE ? 0 : v ? pages[LAG] : pages[0];
+            const unsigned long long vm = C::SPARSE ? 0 : v ? masks[LAG] : masks[0];
+#pragma unroll
+            for (int i = 0; i < NCH; ++i)
+              at[i] = C::SPARSE ? (v ? was[LAG][i] : was[0][i]) : (vm >> (row0 + i * RSTEP)) & 1 ? page * 64 + row0 + i * RSTEP : -1;
+            run = ask(at, s.h, v, !C::SPARSE && v && (x - j + 1) * kTile > s.full, last, seg);
           }
         }
       }
