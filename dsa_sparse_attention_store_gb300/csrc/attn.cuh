@@ -97,14 +97,14 @@ struct Cfg {
   static constexpr int CTAS = FORM == kWide ? 1 : 2;   // per SM
   static constexpr int NBLK = D / 64;
   static constexpr int SLOT = kTile * D * 2;
-  // chunks of 16 code bytes: of a row's 64 dimensions, and a thread's per 64 keys
+  // chunks of 16 code bytes: of a row's 64 dimensions, and a loader thread's per tile
   static constexpr int CPB = FMT == DSA_FMT_BF16 ? 8 : FMT == DSA_FMT_FP8 ? 4 : 2;
-  static constexpr int NCH = NBLK * CPB / 2;
+  static constexpr int NCH = NBLK * CPB;
   static constexpr bool RAW = FMT != DSA_FMT_BF16;
-  static constexpr int RAW_SLOT = RAW ? NCH * 128 * 20 + (D == 64 ? 128 * 4 : 0) : 0;  // codes, a scale word per chunk, flags
-  // ring depths that fill the shared memory (113 KB or 227 KB a CTA): tiles, and
-  // codes on their way
-  static constexpr int P = !RAW ? 3 : FMT == DSA_FMT_FP8 ? 4 : 6;
+  static constexpr int RAW_SLOT = RAW ? NCH * 64 * 20 + (D == 64 ? 64 * 4 : 0) : 0;  // codes, a scale word per chunk, flags
+  // ring depths that fill the shared memory (113 KB or 227 KB a CTA): operand tiles, and tiles of codes
+  // on their way of each loader pair
+  static constexpr int P = !RAW ? 3 : FMT == DSA_FMT_FP8 ? 2 : 3;
   static constexpr int NS = D == 64 ? (FORM == kWide ? 12 : 8)
                             : FORM == kWide ? (!RAW ? 10 : FMT == DSA_FMT_FP8 ? 7 : 8)
                                             : (!RAW ? 6 : FMT == DSA_FMT_FP8 ? 4 : 5);
@@ -121,7 +121,7 @@ struct Shared {
   uint64_t s_full[2][2], o_full[2][2], p_ready[2][2], q_ready[2], fin[2];
   unsigned long long vmask[kRing];  // visible keys of a tile, as far as the loader knows
   int bad[kRing];                      // segment number + 1 where a loader replaced a value
-  int info[4][8];                      // a loader warp's tiles on their way
+  int info[4][4];                      // a loader warp's tiles on their way
   long long scan[16];
   Start start;
   uint32_t tmem;
@@ -130,7 +130,7 @@ struct Shared {
 
 template <class C>
 constexpr int smem_bytes() {
-  return C::NS * C::SLOT + C::QBYTES + C::P * C::RAW_SLOT + static_cast<int>(sizeof(Shared));
+  return C::NS * C::SLOT + C::QBYTES + 2 * C::P * C::RAW_SLOT + static_cast<int>(sizeof(Shared));
 }
 
 // Key tiles of the row tile that starts at row r0 (at least one, so that
@@ -380,18 +380,18 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* const qsm = smem + C::NS * C::SLOT;
   uint8_t* const raw = qsm + C::QBYTES;
-  Shared& sh = *reinterpret_cast<Shared*>(raw + C::P * C::RAW_SLOT);
+  Shared& sh = *reinterpret_cast<Shared*>(raw + 2 * C::P * C::RAW_SLOT);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cta = blockIdx.x, grid = gridDim.x;
 
   if (tid == 0) {
     for (int i = 0; i < C::NS; ++i) {
-      mbar_init(&sh.full[i], 4);
+      mbar_init(&sh.full[i], 2);  // a pair of loader warps
       mbar_init(&sh.empty[i], C::WG);
     }
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&sh.mfull[i], 1);
-      mbar_init(&sh.vdone[i], 4);
+      mbar_init(&sh.vdone[i], 2);
       sh.bad[i] = 0;
     }
     for (int i = 0; i < C::WG; ++i) {
@@ -580,35 +580,57 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
         tc_fence_after();
         const uint32_t tS = tb + C::S + 64 * buf + lanes;
         if (active && run) {
-          uint32_t x[2][32];
-          tmem_ld32(tS, x[0]);
-          tmem_ld32(tS + 32, x[1]);
           const int p0 = t * kTile;
           if (!C::SPARSE && valid && p0 + kTile > s.full) see &= row_mask(a, s, qi, p0);
           const bool some = !__all_sync(0xffffffffu, see == ~0ull);  // a key that some row does not see
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          tmem_ld_wait32(x[0]);
-          tmem_ld_wait32(x[1]);
-          if (some) {
+          const unsigned long long sc = pack2(a.scale2, a.scale2);
+          uint32_t p[32];
+          // The weights are taken under the running maximum while the tile's
+          // own is found. Only if that is more than 2^8 above it (a unit's
+          // first tile, rarely later) does the maximum move, are the sums
+          // rescaled and the tile's weights taken again; the weights stay
+          // below 2^8 otherwise.
+          while (true) {
+            uint32_t x[2][32];
+            tmem_ld32(tS, x[0]);
+            tmem_ld32(tS + 32, x[1]);
+            const float sub = m == -INFINITY ? 0.f : m;
+            const unsigned long long sb = pack2(-sub, -sub);
+            unsigned long long sum[2] = {0ull, 0ull};  // pairs of fp32 zeros
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            tmem_ld_wait32(x[0]);
+            tmem_ld_wait32(x[1]);
+            if (some) {
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const uint32_t bits = static_cast<uint32_t>(see >> (32 * c));
+              for (int c = 0; c < 2; ++c) {
+                const uint32_t bits = static_cast<uint32_t>(see >> (32 * c));
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (!((bits >> i) & 1)) x[c][i] = 0xFF800000u;
+                for (int i = 0; i < 32; ++i)
+                  if (!((bits >> i) & 1)) x[c][i] = 0xFF800000u;
+              }
             }
-          }
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
+            for (int c = 0; c < 2; ++c)
 #pragma unroll
-            for (int i = 0; i < 32; i += 2)
-              mx[(i >> 1) & 3] = fmaxf(mx[(i >> 1) & 3], fmaxf(__uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1])));
-          const float mnew = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale2;
-          // the running maximum moves only when it grows by more than 2^8:
-          // the weights stay below 2^8 and the accumulator is rarely rescaled
-          const bool grow = mnew > m + 8.f || (m == -INFINITY && mnew > m);
-          if (__any_sync(0xffffffffu, grow)) {
-            const float to = grow ? mnew : m;
+              for (int i = 0; i < 16; ++i) {
+                const float s0 = __uint_as_float(x[c][2 * i]), s1 = __uint_as_float(x[c][2 * i + 1]);
+                mx[i & 3] = fmaxf(mx[i & 3], fmaxf(s0, s1));
+                float e0, e1;
+                unpack2(fma2(pack2(s0, s1), sc, sb), e0, e1);
+                e0 = ex2(e0);
+                e1 = ex2(e1);
+                sum[i & 1] = add2(sum[i & 1], pack2(e0, e1));
+                const __nv_bfloat162 w = __floats2bfloat162_rn(e0, e1);
+                memcpy(&p[16 * c + i], &w, 4);
+              }
+            const float mnew = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale2;
+            const bool grow = mnew > m + 8.f || (m == -INFINITY && mnew > m);
+            if (!__any_sync(0xffffffffu, grow)) {
+              float l0, l1;
+              unpack2(add2(sum[0], sum[1]), l0, l1);
+              l += l0 + l1;
+              break;
+            }
             const float alpha = grow ? ex2(m - mnew) : 1.f;
             if (t > s.t0) {  // after the last tile's second product
               run = run && wait_product();
@@ -618,29 +640,9 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
               for (int c = 0; c < D / 16; ++c) tmem_scale16(tO + 16 * c, alpha);
               tmem_st_wait();
             }
-            m = to;
+            if (grow) m = mnew;
           }
-          const float sub = m == -INFINITY ? 0.f : m;
-          const unsigned long long sc = pack2(a.scale2, a.scale2), sb = pack2(-sub, -sub);
-          unsigned long long sum[2] = {0ull, 0ull};  // pairs of fp32 zeros
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t p[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              float e0, e1;
-              unpack2(fma2(pack2(__uint_as_float(x[c][2 * i]), __uint_as_float(x[c][2 * i + 1])), sc, sb), e0, e1);
-              e0 = ex2(e0);
-              e1 = ex2(e1);
-              sum[i & 1] = add2(sum[i & 1], pack2(e0, e1));
-              const __nv_bfloat162 w = __floats2bfloat162_rn(e0, e1);
-              memcpy(&p[i], &w, 4);
-            }
-            tmem_st16(tS + 16 * c, p);  // over scores that are in registers by now
-          }
-          float l0, l1;
-          unpack2(add2(sum[0], sum[1]), l0, l1);
-          l += l0 + l1;
+          tmem_st32(tS, p);  // over scores that are not needed any more
         }
         if constexpr (FORM == kWide) {
           tmem_st_wait();
@@ -778,71 +780,82 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
     settle_products(wg);
   } else if (warp < NSW + 4) {
     // ------------------------------------------------------------ loaders
+    // A pair of warps brings the keys, another the values. A thread moves NCH
+    // 16-byte chunks of a tile.
     constexpr int CPB = C::CPB, NCH = C::NCH;
-    constexpr int RL = 8 / CPB;            // rows that 8 lanes cover: their stores hit all 32 banks
-    constexpr int RSTEP = RL * 16 / C::NBLK;
-    const int lt = tid - 32 * NSW, lw = warp - NSW;
-    const int chunk = lt % CPB, blk = (lt / 8) % C::NBLK;
-    const int row0 = (lt / (8 * C::NBLK)) * RL + (lt / CPB) % RL;  // of 64; this thread's are RSTEP apart
+    constexpr int RL = 8 / CPB;              // rows that 8 lanes cover: their stores hit all 32 banks
+    constexpr int RSTEP = RL * 8 / C::NBLK;  // this thread's rows are so far apart
+    const int lw = warp - NSW;
+    const bool v = lw >= 2;
+    const int ti = (lw & 1) * 32 + lane;
+    const int chunk = ti % CPB, blk = (ti / 8) % C::NBLK;
+    const int row0 = (ti / (8 * C::NBLK)) * RL + (ti / CPB) % RL;
     const int code_off = (blk * CPB + chunk) * 16;
     const int scale_off = (blk * 64 + chunk * (64 / CPB)) / kvf::kBlock;
-    const uint32_t raw_at = smem_u32(raw);
-    // where a row's 16-byte unit u lies in the operand tile
-    auto place = [&](int at, int i, int u) -> uint8_t* {
+    uint8_t* const ring = raw + v * (C::P * C::RAW_SLOT);
+    const uint32_t page_step = static_cast<uint32_t>(a.kv_heads) * L::HEAD_BYTES;
+    const int32_t code_at = v ? L::V_CODES : L::K_CODES, scale_at = v ? L::V_SCALES : L::K_SCALES;
+    // where unit u (16 bytes) of row i of this thread lies in an operand tile
+    auto place = [&](uint8_t* tile, int i, int u) -> uint8_t* {
       const int r = row0 + i * RSTEP;
-      return smem + at * C::SLOT + blk * (kTile * 128) + r * 128 + ((u ^ (r & 7)) << 4);
+      return tile + blk * (kTile * 128) + r * 128 + ((u ^ (r & 7)) << 4);
     };
 
     Iter<C> it(a, sh.start, count);
     Seg s;
-    int n = 0, issued = 0, sent = 0;  // tiles; 64-key parts asked for, and handed over
-    int slots = 0;                    // operand slots that TMA or copies have been asked to fill
+    int n = 0, parts = 0;             // tiles; operand tiles of both kinds before this segment
+    int issued = 0, sent = 0;         // tiles asked for by copies, and handed over
+    int mine = -1, mine_round = 0;    // the last operand tile asked for, and its round
     bool run = true;
 
-    // 64 keys have landed in this thread's part of the ring: hand them to the
-    // products. info: bits 0-3 the slot, 4 replace what is not finite, 5 a
-    // segment's last, 6 the slot's round, 8.. the segment
+    // A tile has landed: hand it to the products. info: bits 0-3 the slot, 4
+    // replace what is not finite, 5 a segment's last, 6 the slot's round, 8..
+    // the segment
     auto hand_over = [&](int info) {
       const int at = info & 15, seg = info >> 8;
+      uint8_t* const tile = smem + at * C::SLOT;
       bool found = false;
       if constexpr (C::RAW) {
-        const uint8_t* src = raw + (sent % C::P) * C::RAW_SLOT;
-        uint32_t odd = 0;
-        if constexpr (D == 64) odd = reinterpret_cast<const uint32_t*>(src + NCH * 128 * 20)[lt];
+        const uint8_t* src = ring + (sent % C::P) * C::RAW_SLOT;
+        [[maybe_unused]] uint32_t odd = 0;
+        if constexpr (D == 64) odd = reinterpret_cast<const uint32_t*>(src + NCH * 64 * 20)[ti];
+        constexpr int BATCH = NCH < 4 ? NCH : FMT == DSA_FMT_FP8 ? 4 : 2;  // chunks at a time: enough to overlap their latencies
 #pragma unroll
-        for (int i = 0; i < NCH; ++i) {
-          const uint4 v = reinterpret_cast<const uint4*>(src)[i * 128 + lt];
-          const uint32_t sw = reinterpret_cast<const uint32_t*>(src + NCH * 128 * 16)[i * 128 + lt];
-          const uint32_t sc = (sw >> (8 * (scale_off + (D == 64 ? 2 * ((odd >> i) & 1) : 0)))) & 0xFFu;
-          const uint32_t c[4] = {v.x, v.y, v.z, v.w};
-          uint32_t w[32 / CPB];
-          const kvf::Factor<C::RAW ? FMT : DSA_FMT_FP8> f(sc);
+        for (int i0 = 0; i0 < NCH; i0 += BATCH) {
+          uint32_t w[BATCH][32 / CPB];
+          kvf::Factor<C::RAW ? FMT : DSA_FMT_FP8> f[BATCH];
+          bool two = false;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if constexpr (FMT == DSA_FMT_FP8) {
-              uint32_t o[2];
-              kvf::widen_e4m3(c[j], f, o);
-              w[2 * j] = o[0];
-              w[2 * j + 1] = o[1];
-            } else {
-              uint32_t o[4];
-              kvf::widen_e2m1(c[j], f, o);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) w[4 * j + e] = o[e];
-            }
+          for (int b = 0; b < BATCH; ++b) {
+            const int i = i0 + b;
+            const uint4 c4 = reinterpret_cast<const uint4*>(src)[i * 64 + ti];
+            const uint32_t sw = reinterpret_cast<const uint32_t*>(src + NCH * 64 * 16)[i * 64 + ti];
+            const uint32_t c[4] = {c4.x, c4.y, c4.z, c4.w};
+            f[b].set((sw >> (8 * (scale_off + (D == 64 ? 2 * ((odd >> i) & 1) : 0)))) & 0xFFu);
+            two |= f[b].two;
+            kvf::widen(c, f[b], w[b]);
           }
-          if (info & 16) found |= kvf::zero_nonfinite(w);
+          if (two) {
 #pragma unroll
-          for (int j = 0; j < 8 / CPB; ++j)
-            *reinterpret_cast<uint4*>(place(at, i, chunk * (8 / CPB) + j)) =
-                make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+            for (int b = 0; b < BATCH; ++b) f[b].rest(w[b]);
+          }
+          if (info & 16) {
+#pragma unroll
+            for (int b = 0; b < BATCH; ++b) found |= kvf::zero_nonfinite(w[b]);
+          }
+#pragma unroll
+          for (int b = 0; b < BATCH; ++b)
+#pragma unroll
+            for (int j = 0; j < 8 / CPB; ++j)
+              *reinterpret_cast<uint4*>(place(tile, i0 + b, chunk * (8 / CPB) + j)) =
+                  make_uint4(w[b][4 * j], w[b][4 * j + 1], w[b][4 * j + 2], w[b][4 * j + 3]);
         }
       } else if (info & 16) {
 #pragma unroll
         for (int i = 0; i < NCH; ++i) {
-          uint4* p = reinterpret_cast<uint4*>(place(at, i, chunk));
-          const uint4 v = *p;
-          uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          uint4* p = reinterpret_cast<uint4*>(place(tile, i, chunk));
+          const uint4 c = *p;
+          uint32_t w[4] = {c.x, c.y, c.z, c.w};
           if (kvf::zero_nonfinite(w)) {
             found = true;
             *p = make_uint4(w[0], w[1], w[2], w[3]);
@@ -858,200 +871,186 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
       }
       ++sent;
     };
-    // hand over the oldest part; `left` younger ones may stay in flight
+    auto hand_over_all = [&]() {
+      cp_async_wait<0>();
+      while (sent < issued) hand_over(sh.info[lw][sent & 3]);
+    };
+    // hand over the oldest tile of codes; `left` younger ones may stay in flight
     auto settle = [&](auto left) -> bool {
       cp_async_wait<decltype(left)::value>();
-      const int info = sh.info[lw][sent & 7];
+      const int info = sh.info[lw][sent & 3];
       // codes are widened into a slot that has to be free; copies into the
       // slot itself waited for that before they were issued
       if (C::RAW && !wait_warp(&sh.empty[info & 15], ((info >> 6) & 1) ^ 1)) return false;
       hand_over(info);
       return true;
     };
-    // ask for 64 keys: `at`, where each of this thread's rows lies (page * 64 + offset, or -1)
-    auto ask = [&](const int (&at)[NCH], int h, bool v, bool clean, bool last, int seg) -> bool {
-      if constexpr (!C::RAW) {
-        if (!__all_sync(0xffffffffu, mbar_try_wait(smem_u32(&sh.empty[slot]), round ^ 1))) {
-          // what has landed goes out before this warp waits for a slot
-          cp_async_wait<0>();
-          while (sent < issued) hand_over(sh.info[lw][sent & 7]);
-          if (!wait_warp(&sh.empty[slot], round ^ 1)) return false;
-        }
-      }
-      const uint32_t dst = raw_at + (issued % C::P) * C::RAW_SLOT;
-      uint32_t odd = 0;
+    // an operand tile that copies or TMA will fill; what has landed goes out
+    // before this warp waits for one
+    auto acquire = [&](int at, int rnd) -> bool {
+      if (__all_sync(0xffffffffu, mbar_try_wait(smem_u32(&sh.empty[at]), rnd ^ 1))) return true;
+      hand_over_all();
+      return wait_warp(&sh.empty[at], rnd ^ 1);
+    };
+    // ask for a tile: src(i, ok, off) gives where chunk i's row begins, whether
+    // it is there, and the row's place in its page
+    auto ask = [&](auto src, int at, int rnd, bool clean, bool last, int seg) -> bool {
+      if (!C::RAW && !acquire(at, rnd)) return false;
+      uint8_t* const to = ring + (issued % C::P) * C::RAW_SLOT;
+      const uint32_t dst = smem_u32(to) + ti * 16, dsc = smem_u32(to) + NCH * 64 * 16 + ti * 4;
+      [[maybe_unused]] uint32_t odd = 0;
 #pragma unroll
       for (int i = 0; i < NCH; ++i) {
-        const bool ok = at[i] >= 0;
-        const int where = ok ? at[i] : 0;
-        const uint8_t* b = a.cache + (static_cast<long long>(where >> 6) * a.kv_heads + h) * L::HEAD_BYTES;
-        const uint8_t* code = b + (v ? L::V_CODES : L::K_CODES) + (where & 63) * L::CB + code_off;
+        bool ok;
+        int off;
+        const uint8_t* head = src(i, ok, off);
         if constexpr (C::RAW) {
-          cp_async16(dst + (i * 128 + lt) * 16, code, ok);
-          cp_async4(dst + NCH * 128 * 16 + (i * 128 + lt) * 4,
-                    b + (v ? L::V_SCALES : L::K_SCALES) + (((where & 63) * L::SB) & ~3), ok);
-          odd |= (where & 1) << i;
+          cp_async16(dst + i * 1024, head + code_at + off * L::CB + code_off, ok);
+          cp_async4(dsc + i * 256, head + scale_at + ((off * L::SB) & ~3), ok);
+          if (D == 64) odd |= (off & 1) << i;
         } else {
-          cp_async16(smem_u32(place(slot, i, chunk)), code, ok);
+          cp_async16(smem_u32(place(smem + at * C::SLOT, i, chunk)), head + code_at + off * L::CB + code_off, ok);
         }
       }
-      if constexpr (C::RAW && D == 64)
-        reinterpret_cast<uint32_t*>(raw + (issued % C::P) * C::RAW_SLOT + NCH * 128 * 20)[lt] = odd;
+      if constexpr (C::RAW && D == 64) reinterpret_cast<uint32_t*>(to + NCH * 64 * 20)[ti] = odd;
       cp_async_commit();
-      if (lane == 0)
-        sh.info[lw][issued & 7] = slot | (clean ? 16 : 0) | (last ? 32 : 0) | (round << 6) | (seg << 8);
+      if (lane == 0) sh.info[lw][issued & 3] = at | (clean ? 16 : 0) | (last ? 32 : 0) | (rnd << 6) | (seg << 8);
       __syncwarp();
       ++issued;
-      advance();
-      ++slots;
       if (issued - sent == C::P) return settle(std::integral_constant<int, C::P - 1>());
       return true;
     };
 
     for (int seg = 0; run && it.next(s); ++seg) {
-      const int32_t* pt = a.page_table + static_cast<long long>(s.b) * a.max_pages;
-      const int npg = (s.len + kTile - 1) / kTile;
-      // a selection: a key of the tile as a cache slot
-      auto slot_of = [&](int t, int j) -> int {
-        int x = t * kTile + j, pos;
-        if (x < a.k) {
-          pos = a.sel[static_cast<long long>(s.q0) * a.k + x];
-          if (pos < 0 || s.len == 0) return -1;
-          if (a.slots) {
-            if (pos < a.num_pages * 64) return pos;
-            atomicOr(a.status, DSA_DEV_BOUNDS);
-            return -1;
-          }
-          if (pos >= s.len) {
-            atomicOr(a.status, DSA_DEV_BOUNDS);
-            return -1;
-          }
-        } else {
-          x -= (a.k + kTile - 1) / kTile * kTile;
-          if (x < 0 || !a.mask || x >= s.nd || (x >> 5) >= a.mask_words) return -1;
-          if (!((a.mask[static_cast<long long>(s.q0) * a.mask_words + (x >> 5)] >> (x & 31)) & 1)) return -1;
-          pos = s.len - s.nd + x;
-        }
-        const int page = pt[pos >> 6];
+      const int32_t* table = a.page_table + static_cast<long long>(s.b) * a.max_pages;
+      const uint8_t* const heads = a.cache + static_cast<long long>(s.h) * L::HEAD_BYTES;
+      const int npg = (s.len + kTile - 1) / kTile, nt = s.t1 - s.t0;
+      // A selection's keys go through three steps, a tile apart, so that no
+      // load is waited for: the entry, its page, its cache slot. This lane has
+      // keys `lane` and `lane + 32` of a tile.
+      int e0 = -1, e1 = -1, g0 = -1, g1 = -1, u0 = -1, u1 = -1;  // entries; positions whose pages are on their way; pages
+      auto entry = [&](int t, int j) -> int {  // a position (or cache slot) or -1
+        int x = t * kTile + j;
+        if (t >= s.t1 || s.len == 0) return -1;
+        if (x < a.k) return a.sel[static_cast<long long>(s.q0) * a.k + x];
+        x -= (a.k + kTile - 1) / kTile * kTile;
+        if (x < 0 || !a.mask || x >= s.nd || (x >> 5) >= a.mask_words) return -1;
+        return (a.mask[static_cast<long long>(s.q0) * a.mask_words + (x >> 5)] >> (x & 31)) & 1 ? s.len - s.nd + x : -1;
+      };
+      // the page of tile t's entry e; -2 where e is out of range
+      auto page_of = [&](int e, int t) -> int {
+        if (e < 0) return -1;
+        const bool slot = a.slots && t * kTile < a.k;  // the drafted tokens that follow are positions
+        if (slot ? e < a.num_pages * 64 : e < s.len) return slot ? e >> 6 : table[e >> 6];
+        atomicOr(a.status, DSA_DEV_BOUNDS);
+        return -2;
+      };
+      auto slot_of = [&](int e, int page) -> int {
+        if (e < 0 || page == -2) return -1;
         if (page < 0 || page >= a.num_pages) {
           atomicOr(a.status, DSA_DEV_BOUNDS);
           return -1;
         }
-        return page * 64 + (pos & 63);
+        return page * 64 + (e & 63);
       };
-      // K of tile x, then V of tile x - LAG: the order the products take them in
-      constexpr int LAG = C::SBUF - 1;
-      int k0 = -1, k1 = -1;                  // a selection: this lane's two keys of the next K tile
-      int at[NCH], was[LAG + 1][NCH];        // where this thread's rows lie, now and LAG tiles ago
-      int pg = -1, pages[LAG + 1];           // 32 page ids; the page of the tiles whose V is to come
-      unsigned long long masks[LAG + 1];
-      bool wholes[LAG + 1];
+      int pg = -1;  // page ids of 32 tiles
       if (C::SPARSE) {
-        k0 = slot_of(s.t0, lane);
-        k1 = slot_of(s.t0, lane + 32);
+        g0 = entry(s.t0, lane);
+        g1 = entry(s.t0, lane + 32);
+        e0 = entry(s.t0 + 1, lane);
+        e1 = entry(s.t0 + 1, lane + 32);
+        u0 = page_of(g0, s.t0);
+        u1 = page_of(g1, s.t0);
       }
-      // by TMA: 64 keys of 64 dimensions a box
-      auto by_tma = [&](int page, bool v, bool last) -> bool {
-        if (!__all_sync(0xffffffffu, mbar_try_wait(smem_u32(&sh.empty[slot]), round ^ 1))) {
-          cp_async_wait<0>();
-          while (sent < issued) hand_over(sh.info[lw][sent & 7]);
-          if (!wait_warp(&sh.empty[slot], round ^ 1)) return false;
+      for (int x = 0; run && x < nt; ++x, ++n) {
+        const int t = s.t0 + x;
+        // the tile's place in the order the products take keys and values:
+        // K0 V0 K1 V1 .., or K0 K1 V0 K2 V1 .. with two score buffers
+        const int order = parts + (C::SBUF == 1 ? 2 * x + v : !v ? (x ? 2 * x - 1 : 0) : x + 1 < nt ? 2 * x + 2 : 2 * nt - 1);
+        const int at = order % C::NS, rnd = (order / C::NS) & 1;
+        const bool last = v && x + 1 == nt;
+        unsigned long long vm;
+        int page = -1, k0 = -1, k1 = -1;
+        if constexpr (C::SPARSE) {
+          k0 = slot_of(g0, u0);
+          k1 = slot_of(g1, u1);
+          g0 = e0;
+          g1 = e1;
+          u0 = page_of(g0, t + 1);
+          u1 = page_of(g1, t + 1);
+          e0 = entry(t + 2, lane);
+          e1 = entry(t + 2, lane + 32);
+          vm = __ballot_sync(0xffffffffu, k0 >= 0) | (static_cast<unsigned long long>(__ballot_sync(0xffffffffu, k1 >= 0)) << 32);
+        } else {
+          if ((x & 31) == 0) pg = t + lane < min(s.t1, npg) ? table[t + lane] : -1;
+          page = __shfl_sync(0xffffffffu, pg, x & 31);
+          const bool ok = page >= 0 && page < a.num_pages;
+          if (!ok && t < npg && lw == 0 && lane == 0) atomicOr(a.status, DSA_DEV_BOUNDS);
+          vm = ok ? low_bits(s.len - t * kTile) : 0ull;
         }
-        if (lane == 0) {
-          if (lw != 0) {
-            mbar_arrive(&sh.full[slot]);
-          } else {
-            mbar_arrive_expect_tx(&sh.full[slot], C::SLOT);
-            const int y = ((page * a.kv_heads + s.h) * 2 + v) * kTile;
-#pragma unroll
-            for (int c = 0; c < C::NBLK; ++c)
-              tma_load_2d(smem + slot * C::SLOT + c * (kTile * 128), &tm, c * 64, y, &sh.full[slot]);
-          }
-          if (last) mbar_arrive(&sh.vdone[seg % kRing]);
+        if (lw == 0 && lane == 0) {
+          sh.vmask[n % kRing] = vm;
+          mbar_arrive(&sh.mfull[n % kRing]);
         }
-        advance();
-        ++slots;
-        if (sent < issued) {  // copies asked for before go out too
-          cp_async_wait<0>();
-          while (sent < issued) hand_over(sh.info[lw][sent & 7]);
-        }
-        return true;
-      };
-      for (int x = s.t0; run && x < s.t1 + LAG; ++x) {
-#pragma unroll
-        for (int j = LAG; j > 0; --j) {
-          pages[j] = pages[j - 1];
-          masks[j] = masks[j - 1];
-          wholes[j] = wholes[j - 1];
-          if (C::SPARSE)
-#pragma unroll
-            for (int i = 0; i < NCH; ++i) was[j][i] = was[j - 1][i];
-        }
-        if (x < s.t1) {
-          unsigned long long vm;
-          if constexpr (C::SPARSE) {
-            vm = __ballot_sync(0xffffffffu, k0 >= 0) |
-                 (static_cast<unsigned long long>(__ballot_sync(0xffffffffu, k1 >= 0)) << 32);
-#pragma unroll
-            for (int i = 0; i < NCH; ++i) {
-              const int r = row0 + i * RSTEP;
-              const int u = __shfl_sync(0xffffffffu, k0, r & 31), v = __shfl_sync(0xffffffffu, k1, r & 31);
-              was[0][i] = r < 32 ? u : v;
-            }
-            if (x + 1 < s.t1) {
-              k0 = slot_of(x + 1, lane);
-              k1 = slot_of(x + 1, lane + 32);
-            }
-          } else {
-            const int rel = (x - s.t0) & 31;
-            if (rel == 0) pg = x + lane < min(s.t1, npg) ? pt[x + lane] : -1;
-            const int page = __shfl_sync(0xffffffffu, pg, rel);
-            const bool ok = page >= 0 && page < a.num_pages;
-            if (!ok && x < npg && lw == 0 && lane == 0) atomicOr(a.status, DSA_DEV_BOUNDS);
-            vm = ok ? low_bits(s.len - x * kTile) : 0ull;
-            pages[0] = page;
-            masks[0] = vm;
-            wholes[0] = ok && (x + 1) * kTile <= s.full;  // every row sees every key
-          }
-          if (lw == 0 && lane == 0) {
-            sh.vmask[n % kRing] = vm;
-            mbar_arrive(&sh.mfull[n % kRing]);
-          }
-          ++n;
-        }
-#pragma unroll 1
-        for (int v = 0; run && v < 2; ++v) {
-          if (v ? x < s.t0 + LAG : x >= s.t1) continue;
-          const int j = v ? LAG : 0;
-          const bool last = v && x + 1 == s.t1 + LAG;
-          const bool whole = !C::SPARSE && (v ? wholes[LAG] : wholes[0]);
+        mine = at;
+        mine_round = rnd;
+        if constexpr (C::SPARSE) {
+          run = ask(
+              [&](int i, bool& ok, int& off) {
+                const int r = row0 + i * RSTEP;
+                const int p0 = __shfl_sync(0xffffffffu, k0, r & 31), p1 = __shfl_sync(0xffffffffu, k1, r & 31);
+                const int p = r < 32 ? p0 : p1;
+                ok = p >= 0;
+                off = ok ? p & 63 : 0;
+                return heads + static_cast<uint64_t>(ok ? static_cast<uint32_t>(p) >> 6 : 0u) * page_step;
+              },
+              at, rnd, false, last, seg);
+        } else {
+          const bool whole = vm == ~0ull && (t + 1) * kTile <= s.full;  // every row sees every key
+          const uint8_t* const head = heads + static_cast<uint64_t>(vm ? static_cast<uint32_t>(page) : 0u) * page_step;
           if (FMT == DSA_FMT_BF16 && whole) {
-            run = by_tma(v ? pages[LAG] : pages[0], v, last);
-          } else {
-            const int page = C::SPARSE ? 0 : v ? pages[LAG] : pages[0];
-            const unsigned long long vm = C::SPARSE ? 0 : v ? masks[LAG] : masks[0];
+            // by TMA: 64 keys of 64 dimensions a box
+            run = acquire(at, rnd);
+            if (run && lane == 0) {
+              if (lw & 1) {
+                mbar_arrive(&sh.full[at]);
+              } else {
+                mbar_arrive_expect_tx(&sh.full[at], C::SLOT);
+                const int y = ((page * a.kv_heads + s.h) * 2 + v) * kTile;
 #pragma unroll
-            for (int i = 0; i < NCH; ++i)
-              at[i] = C::SPARSE ? (v ? was[LAG][i] : was[0][i]) : (vm >> (row0 + i * RSTEP)) & 1 ? page * 64 + row0 + i * RSTEP : -1;
-            run = ask(at, s.h, v, !C::SPARSE && v && (x - j + 1) * kTile > s.full, last, seg);
+                for (int c = 0; c < C::NBLK; ++c)
+                  tma_load_2d(smem + at * C::SLOT + c * (kTile * 128), &tm, c * 64, y, &sh.full[at]);
+              }
+              if (last) mbar_arrive(&sh.vdone[seg % kRing]);
+            }
+            __syncwarp();
+            if (run && sent < issued) hand_over_all();  // copies asked for before go out too
+          } else {
+            run = ask(
+                [&](int i, bool& ok, int& off) {
+                  off = row0 + i * RSTEP;
+                  ok = (vm >> off) & 1;
+                  return head;
+                },
+                at, rnd, v && (t + 1) * kTile > s.full, last, seg);
           }
         }
       }
+      parts += 2 * nt;
     }
     if constexpr (C::RAW) {
       while (run && sent < issued) run = settle(std::integral_constant<int, 0>());
-    } else {
-      cp_async_wait<0>();
-      while (run && sent < issued) hand_over(sh.info[lw][sent & 7]);
+    } else if (run) {
+      hand_over_all();
     }
     cp_async_wait<0>();
     // after a wait that ran out, TMA copies in flight land before the CTA exits
-    if (*abort_flag && FMT == DSA_FMT_BF16 && lw == 0 && lane == 0) {
-      for (int i = 1; i <= C::NS && slots - i >= 0; ++i) {
-        const int x = slots - i;
-        mbar_wait(&sh.full[x % C::NS], (x / C::NS) & 1, 20000000LL);
+    // (the last into each slot; `mine` is the last this warp asked for)
+    if (*abort_flag && FMT == DSA_FMT_BF16 && (lw & 1) == 0 && lane == 0 && mine >= 0)
+      for (int i = 0; i < C::NS; ++i) {
+        const int rnd = i <= mine ? mine_round : mine_round ^ 1;
+        mbar_wait(&sh.full[i], rnd, 20000000LL);
       }
-    }
     __syncwarp();
   }
   tc_fence_before();

@@ -200,16 +200,20 @@ __global__ void __launch_bounds__(128) kv_load_kernel(KvArgs a) {
     if constexpr (FMT == DSA_FMT_BF16) {
       w = *reinterpret_cast<const uint4*>(src + 16 * l);
     } else {
-      const Factor<FMT> f(blk[(is_v ? L::V_SCALES : L::K_SCALES) + off * L::SB + (l >> 2)]);
+      Factor<FMT> f;
+      f.set(blk[(is_v ? L::V_SCALES : L::K_SCALES) + off * L::SB + (l >> 2)]);
       if constexpr (FMT == DSA_FMT_FP8) {
-        const uint2 c = *reinterpret_cast<const uint2*>(src + 8 * l);
-        uint32_t lo[2], hi[2];
-        widen_e4m3(c.x, f, lo);
-        widen_e4m3(c.y, f, hi);
-        w = make_uint4(lo[0], lo[1], hi[0], hi[1]);
-      } else {
+        const uint2 v = *reinterpret_cast<const uint2*>(src + 8 * l);
+        const uint32_t c[2] = {v.x, v.y};
         uint32_t o[4];
-        widen_e2m1(*reinterpret_cast<const uint32_t*>(src + 4 * l), f, o);
+        widen(c, f, o);
+        f.rest(o);
+        w = make_uint4(o[0], o[1], o[2], o[3]);
+      } else {
+        const uint32_t c[1] = {*reinterpret_cast<const uint32_t*>(src + 4 * l)};
+        uint32_t o[4];
+        widen(c, f, o);
+        f.rest(o);
         w = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }

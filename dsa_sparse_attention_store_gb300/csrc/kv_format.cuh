@@ -66,35 +66,53 @@ struct Factor {
   static constexpr int BIAS = FMT == DSA_FMT_FP8 ? 120 : 126;
   static constexpr uint32_t ONE = 254 - BIAS;  // the largest scale byte one factor covers
   uint32_t f, g;  // bf16x2 factors; g only where `two`
-  bool two;
-  __device__ __forceinline__ explicit Factor(uint32_t byte) {
+  bool two;       // scales above 2^7 (fp8) or 2 (fp4), and NaN: rare
+  __device__ __forceinline__ void set(uint32_t byte) {
     two = byte > ONE;
-    const uint32_t f1 = (two ? 127u + BIAS : byte + BIAS) << 7;
-    const uint32_t g1 = byte == 255u ? 0x7FFFu : byte << 7;
-    f = f1 | (f1 << 16);
-    g = g1 | (g1 << 16);
+    const uint32_t f1 = min(byte, ONE) + BIAS, g1 = byte + 127 - ONE;  // g: what is left of the exponent
+    f = (f1 << 7) | (f1 << 23);
+    g = byte == 255u ? 0x7FFF7FFFu : (g1 << 7) | (g1 << 23);
   }
-  __device__ __forceinline__ uint32_t apply(uint32_t r) const {
-    r = mul_bf16x2(r, f);
-    return two ? mul_bf16x2(r, g) : r;
+  template <int N>
+  __device__ __forceinline__ void apply(uint32_t (&r)[N]) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) r[i] = mul_bf16x2(r[i], f);
+  }
+  // the second factor, for the codes of a scale that takes two
+  template <int N>
+  __device__ __forceinline__ void rest(uint32_t (&r)[N]) const {
+    if (two) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) r[i] = mul_bf16x2(r[i], g);
+    }
   }
 };
 
-// four e4m3 codes -> four bf16 (two words)
-__device__ __forceinline__ void widen_e4m3(uint32_t w, const Factor<DSA_FMT_FP8>& s, uint32_t (&o)[2]) {
-  const uint32_t a = __byte_perm(w, 0, 0x1404), b = __byte_perm(w, 0, 0x3424);  // codes in the high bytes
-  o[0] = s.apply((a & 0x80008000u) | ((a >> 4) & 0x07F007F0u));
-  o[1] = s.apply((b & 0x80008000u) | ((b >> 4) & 0x07F007F0u));
+// N words of four e4m3 codes -> bf16 pairs, up to the second factor
+template <int N>
+__device__ __forceinline__ void widen(const uint32_t (&w)[N], const Factor<DSA_FMT_FP8>& s, uint32_t (&o)[2 * N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const uint32_t a = __byte_perm(w[i], 0, 0x1404), b = __byte_perm(w[i], 0, 0x3424);  // codes in the high bytes
+    o[2 * i] = (a & 0x80008000u) | ((a >> 4) & 0x07F007F0u);
+    o[2 * i + 1] = (b & 0x80008000u) | ((b >> 4) & 0x07F007F0u);
+  }
+  s.apply(o);
 }
 
-// eight e2m1 codes (the even dimension in the low nibble) -> eight bf16
-__device__ __forceinline__ void widen_e2m1(uint32_t w, const Factor<DSA_FMT_FP4>& s, uint32_t (&o)[4]) {
+// N words of eight e2m1 codes (the even dimension in the low nibble) -> bf16
+// pairs, up to the second factor
+template <int N>
+__device__ __forceinline__ void widen(const uint32_t (&w)[N], const Factor<DSA_FMT_FP4>& s, uint32_t (&o)[4 * N]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t b = w >> (8 * i);
-    const uint32_t t = (b & 0xFu) | ((b & 0xF0u) << 12);  // codes in the low nibbles of both halves
-    o[i] = s.apply(((t & 0x00080008u) << 12) | ((t & 0x00070007u) << 6));
-  }
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t b = w[i] >> (8 * j);
+      const uint32_t t = (b & 0xFu) | ((b & 0xF0u) << 12);  // codes in the low nibbles of both halves
+      o[4 * i + j] = ((t & 0x00080008u) << 12) | ((t & 0x00070007u) << 6);
+    }
+  s.apply(o);
 }
 
 // bf16 pairs: what is not finite becomes zero; whether anything did
