@@ -187,7 +187,7 @@ dsa_status launch_attn(dsa_ctx* ctx, const dsa_attn_args& p, const int32_t* sel,
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(p.head_dim),
                                 static_cast<cuuint64_t>(p.num_pages) * p.kv_heads * 2 * kTile};
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(p.head_dim) * 2};
-    const cuuint32_t box[2] = {64, kTile};
+    const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(sel ? 1 : kTile)};  // a selection gathers rows
     const cuuint32_t estr[2] = {1, 1};
     if (reinterpret_cast<EncodeFn>(ctx->encode_tiled)(
             &tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p.cache), dims, strides, box, estr,
