@@ -56,7 +56,7 @@ namespace at {
 
 constexpr int kTile = kvf::kPage;  // keys of a tile: a page's, or 64 selected ones
 constexpr int kRing = 16;  // entries of the per-tile and per-segment rings; loaders run at most 9 tiles ahead
-enum Form { kTree = 0, kSparse = 1, kWide = 2 };
+enum Form { kTree = 0, kSparse = 1, kWide = 2, kTreeFew = 3, kSparseFew = 4 };
 
 struct AttnArgs {
   const __nv_bfloat16* q;
@@ -89,9 +89,10 @@ struct Start {
 
 template <int FMT, int D, int FORM>
 struct Cfg {
-  static constexpr bool SPARSE = FORM == kSparse;
+  static constexpr bool SPARSE = FORM == kSparse || FORM == kSparseFew;
   static constexpr int WG = FORM == kWide ? 2 : 1;     // groups of four softmax warps
-  static constexpr int ROWS = 128 * WG;                // rows of a unit
+  static constexpr int COPIES = FORM == kTreeFew || FORM == kSparseFew ? 4 : 1;  // of a row
+  static constexpr int ROWS = 128 * WG / COPIES;       // rows of a unit
   static constexpr int SBUF = FORM == kWide ? 2 : 1;   // score buffers
   static constexpr int THREADS = 128 * WG + 128 + (FORM == kWide ? 64 : 0);
   static constexpr int CTAS = FORM == kWide ? 1 : 2;   // per SM
@@ -104,11 +105,12 @@ struct Cfg {
   static constexpr int RAW_SLOT = RAW ? NCH * 64 * 20 + (D == 64 ? 64 * 4 : 0) : 0;  // codes, a scale word per chunk, flags
   // ring depths that fill the shared memory (113 KB or 227 KB a CTA): operand tiles, and tiles of codes
   // on their way of each loader pair
-  static constexpr int P = !RAW ? 3 : FMT == DSA_FMT_FP8 ? 2 : 3;
+  static constexpr int P = !RAW ? 3 : FMT == DSA_FMT_FP8 ? 2 : FORM == kWide ? 3 : 4;
   static constexpr int NS = D == 64 ? (FORM == kWide ? 12 : 8)
                             : FORM == kWide ? (!RAW ? 10 : FMT == DSA_FMT_FP8 ? 7 : 8)
-                                            : (!RAW ? 6 : FMT == DSA_FMT_FP8 ? 4 : 5);
+                                            : (!RAW ? 6 : 4);
   static constexpr int QBYTES = FORM == kWide ? ROWS * D * 2 : 0;
+  static constexpr int PBYTES = COPIES > 1 ? ROWS * 128 : 0;  // weights, where they meet in shared memory
   // TMEM columns of a group, and of the CTA (two CTAs share the SM's 512)
   static constexpr uint32_t O = 0, S = D, Q = D + 64 * SBUF, STRIDE = 256, TMEM = 256 * WG;
 };
@@ -130,7 +132,7 @@ struct Shared {
 
 template <class C>
 constexpr int smem_bytes() {
-  return C::NS * C::SLOT + C::QBYTES + 2 * C::P * C::RAW_SLOT + static_cast<int>(sizeof(Shared));
+  return C::PBYTES + C::NS * C::SLOT + C::QBYTES + 2 * C::P * C::RAW_SLOT + static_cast<int>(sizeof(Shared));
 }
 
 // Key tiles of the row tile that starts at row r0 (at least one, so that
@@ -378,7 +380,9 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
   using L = kvf::Layout<FMT, D>;
   constexpr int NSW = 4 * C::WG;  // softmax warps
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint8_t* const qsm = smem + C::NS * C::SLOT;
+  // (products that read the weights there run on into the tiles, for rows that do not exist)
+  uint8_t* const tiles = smem + C::PBYTES;
+  uint8_t* const qsm = tiles + C::NS * C::SLOT;
   uint8_t* const raw = qsm + C::QBYTES;
   Shared& sh = *reinterpret_cast<Shared*>(raw + 2 * C::P * C::RAW_SLOT);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -441,7 +445,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
 
   constexpr uint32_t kIdescQk = idesc_f16(128, kTile, true);
   constexpr uint32_t kIdescPv = idesc_f16(128, D, true) | kIdescBMn;
-  const uint64_t kdesc = sw128_desc(smem_u32(smem)), vdesc = sw128_mn_desc(smem_u32(smem), kTile * 128);
+  const uint64_t kdesc = sw128_desc(smem_u32(tiles)), vdesc = sw128_mn_desc(smem_u32(tiles), kTile * 128), pdesc = sw128_desc(smem_u32(smem));
   const uint64_t qdesc0 = sw128_desc(smem_u32(qsm));
   // The products. Called by a whole warp; the operands come from lane 0, so
   // that the compiler keeps them in uniform registers (issuing a tile's took
@@ -468,9 +472,15 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
     const uint64_t v = vdesc + __shfl_sync(0xffffffffu, at, 0) * (C::SLOT >> 4);
     const uint32_t p = tb + C::S + __shfl_sync(0xffffffffu, buf, 0) * 64;
     if (!elect_one()) return;
+    if constexpr (C::COPIES > 1) {
 #pragma unroll
-    for (int i = 0; i < kTile / 16; ++i)
-      tc_mma_f16_ta(tb + C::O, p + 8 * i, v + ((i * 2048) >> 4), kIdescPv, !first || i > 0);
+      for (int i = 0; i < kTile / 16; ++i)
+        tc_mma_f16(tb + C::O, pdesc + 2 * i, v + ((i * 2048) >> 4), kIdescPv, !first || i > 0);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kTile / 16; ++i)
+        tc_mma_f16_ta(tb + C::O, p + 8 * i, v + ((i * 2048) >> 4), kIdescPv, !first || i > 0);
+    }
     tc_commit(&sh.empty[at]);
     tc_commit(&sh.o_full[wg][buf]);
   };
@@ -491,7 +501,6 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
   } else if (warp < NSW) {
     // ------------------------------------------------------------ softmax
     const int wg = warp >> 2, gw = warp & 3;  // group, and warp of the group
-    const int row = tid;                      // of the unit
     const uint32_t tb = sh.tmem + wg * C::STRIDE;
     const uint32_t lanes = static_cast<uint32_t>(gw * 32) << 16;
     const uint32_t tO = tb + C::O + lanes;
@@ -500,13 +509,30 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
     bool more = it.next(s), run = true;
     int seg = 0, n = 0;   // segments, tiles
     int ns = 0;           // tiles this group has worked on: score buffers and accumulator phases
-    int4 m0 = make_int4(0, 0, 0, 0), m1 = m0;
+    // what the join has to know of this CTA, see join_kernel
+    int* const meta = reinterpret_cast<int*>(a.meta + 2 * cta);
+    if (tid == 0) a.meta[2 * cta] = make_int4(0, 0, 0, 0);
+    // Units of few rows hold each of them four times: a warp takes its copy's
+    // quarter of a tile's scores, and the weights meet in shared memory as the
+    // A operand of the second product. (One warp with all 64 keys of 32 rows
+    // would be most of a tile's time.)
+    const int row = C::COPIES > 1 ? lane : tid, copy = C::COPIES > 1 ? warp : 0;
+    auto query = [&](const Seg& g, int row) {
+      const int r = g.r0 + row;
+      return a.q + static_cast<long long>(g.q0 + r / a.G) * a.qt + static_cast<long long>(g.h * a.G + r % a.G) * a.qh;
+    };
+    // the next unit's queries on their way to L1
+    auto warm = [&](const Seg& g) {
+      if (row < g.rows) {
+        const __nv_bfloat16* q = query(g, row);
+#pragma unroll
+        for (int i = 0; i < C::NBLK; ++i) touch(q + 64 * i);
+      }
+    };
     // the unit's queries, then its first tiles' scores
     auto start_unit = [&](const Seg& g) {
       const bool valid = row < g.rows;
-      const int r = g.r0 + row;
-      const uint4* src = reinterpret_cast<const uint4*>(
-          a.q + (valid ? static_cast<long long>(g.q0 + r / a.G) * a.qt + static_cast<long long>(g.h * a.G + r % a.G) * a.qh : 0));
+      const uint4* src = reinterpret_cast<const uint4*>(valid ? query(g, row) : a.q);
       if constexpr (FORM == kWide) {
         uint8_t* dst = qsm + wg * (128 * D * 2) + (row & 127) * 128;
 #pragma unroll
@@ -546,6 +572,85 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
         advance();
       }
     };
+    // One tile of a unit whose rows have copies: this warp's N of its 64 keys.
+    // The running maximum is the same in all copies of a row: where one finds
+    // its part's maximum more than 2^8 above it, all take the largest.
+    auto spread = [&](auto n_, unsigned long long see, int t, uint32_t tS, bool valid, int qi, const Seg& s, float& m, float& l) {
+      constexpr int N = decltype(n_)::value;
+      const int p0 = t * kTile;
+      const unsigned long long sc = pack2(a.scale2, a.scale2);
+      uint32_t x[N];
+      bool moved = false;
+      while (true) {
+        float mnew = -INFINITY;
+        unsigned long long sum[2] = {0ull, 0ull};
+        if (run) {
+          if (!moved) {
+            tmem_ld_n(tS + copy * N, x);
+            if (!C::SPARSE && valid && p0 + kTile > s.full) see &= row_mask(a, s, qi, p0);
+            const uint32_t bits = static_cast<uint32_t>(see >> (copy * N));
+            tmem_ld_wait_n(x);
+            if (!__all_sync(0xffffffffu, see == ~0ull)) {
+#pragma unroll
+              for (int i = 0; i < N; ++i)
+                if (!((bits >> i) & 1)) x[i] = 0xFF800000u;
+            }
+          }
+          const float sub = m == -INFINITY ? 0.f : m;
+          const unsigned long long sb = pack2(-sub, -sub);
+          float mx[2] = {-INFINITY, -INFINITY};
+          uint32_t p[N / 2];
+#pragma unroll
+          for (int i = 0; i < N / 2; ++i) {
+            const float s0 = __uint_as_float(x[2 * i]), s1 = __uint_as_float(x[2 * i + 1]);
+            mx[i & 1] = fmaxf(mx[i & 1], fmaxf(s0, s1));
+            float e0, e1;
+            unpack2(fma2(pack2(s0, s1), sc, sb), e0, e1);
+            e0 = ex2(e0);
+            e1 = ex2(e1);
+            sum[i & 1] = add2(sum[i & 1], pack2(e0, e1));
+            const __nv_bfloat162 w = __floats2bfloat162_rn(e0, e1);
+            memcpy(&p[i], &w, 4);
+          }
+          mnew = fmaxf(mx[0], mx[1]) * a.scale2;
+#pragma unroll
+          for (int u = 0; u < N / 8; ++u)
+            *reinterpret_cast<uint4*>(smem + row * 128 + (((copy * (N / 8) + u) ^ (row & 7)) << 4)) =
+                make_uint4(p[4 * u], p[4 * u + 1], p[4 * u + 2], p[4 * u + 3]);
+          fence_proxy_async_smem();
+        }
+        const bool grow = !moved && (mnew > m + 8.f || (m == -INFINITY && mnew > m));
+        tc_fence_before();
+        if (named_bar_all(1, 128, run && !grow)) {
+          float l0, l1;
+          unpack2(add2(sum[0], sum[1]), l0, l1);
+          l += l0 + l1;
+          return;
+        }
+        // some row's maximum moves (or a wait ran out): the products with the
+        // old weights are behind, their place serves for the exchange
+        float* const top = reinterpret_cast<float*>(smem);
+        top[tid] = mnew;
+        run = named_bar_all(1, 128, run);
+        if (!run) return;
+#pragma unroll
+        for (int c = 0; c < C::COPIES; ++c) mnew = fmaxf(mnew, top[c * C::ROWS + row]);
+        run = named_bar_all(1, 128, run);
+        const bool up = mnew > m + 8.f || (m == -INFINITY && mnew > m);
+        const float alpha = up ? ex2(m - mnew) : 1.f;
+        if (t > s.t0) {
+          l *= alpha;
+          if (copy == 0 && __any_sync(0xffffffffu, up)) {
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < D / 16; ++c) tmem_scale16(tO + 16 * c, alpha);
+            tmem_st_wait();
+          }
+        }
+        if (up) m = mnew;
+        moved = true;
+      }
+    };
     // the second product of the last tile has completed
     auto wait_product = [&]() { return wait_warp(&sh.o_full[wg][(ns - 1) & (C::SBUF - 1)], ((ns - 1) / C::SBUF) & 1); };
     if (more && has_rows(wg, s)) start_unit(s);
@@ -557,7 +662,12 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
         if (more && has_rows(wg, s)) start_unit(s);
         continue;
       }
-      const bool active = warp * 32 < s.rows;  // some row of this warp is real
+      {
+        Iter<C> peek = it;
+        Seg nx;
+        if (peek.next(nx) && has_rows(wg, nx)) warm(nx);
+      }
+      const bool active = row - lane < s.rows;  // some row of this warp is real
       const bool valid = row < s.rows;
       const int qi = (s.r0 + row) / a.G;       // the row's query in its sequence
       float m = -INFINITY, l = 0.f;
@@ -579,7 +689,9 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
         run = run && wait_warp(&sh.s_full[wg][buf], (ns / C::SBUF) & 1);
         tc_fence_after();
         const uint32_t tS = tb + C::S + 64 * buf + lanes;
-        if (active && run) {
+        if constexpr (C::COPIES > 1) {
+          spread(std::integral_constant<int, kTile / C::COPIES>(), see, t, tS, valid, qi, s, m, l);
+        } else if (active && run) {
           const int p0 = t * kTile;
           if (!C::SPARSE && valid && p0 + kTile > s.full) see &= row_mask(a, s, qi, p0);
           const bool some = !__all_sync(0xffffffffu, see == ~0ull);  // a key that some row does not see
@@ -655,8 +767,10 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
             run = wait_warp(&sh.full[vslot], vround);
             if (run && more_scores) run = wait_warp(&sh.full[slot], round);
           }
-          tmem_st_wait();
-          tc_fence_before();
+          if (C::COPIES == 1) {
+            tmem_st_wait();
+            tc_fence_before();
+          }
           run = named_bar_all(1, 128, run);
           if (gw == 0 && run) {
             tc_fence_after();
@@ -679,15 +793,24 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
       if (!C::SPARSE) run = run && wait_warp(&sh.vdone[seg % kRing], (seg / kRing) & 1);
       tc_fence_after();
       const bool first = done.t0 == 0, last = done.t1 == done.nt;
-      if (!first) {
-        m0.y = 1;
-        m0.z = last;
-      } else if (!last) {
-        m0.x = 1;
-        m0.w = done.rows;
-        m1 = make_int4(done.r0, done.q0, done.h, 0);
+      if (tid == 0 && !first) {
+        meta[1] = 1;
+        meta[2] = last;
+      } else if (tid == 0 && !last) {
+        meta[0] = 1;
+        meta[3] = done.rows;
+        a.meta[2 * cta + 1] = make_int4(done.r0, done.q0, done.h, 0);
       }
-      if (active && run) {
+      if constexpr (C::COPIES > 1) {
+        // the copies' sums of weights, each over its part of the keys
+        float* const sums = reinterpret_cast<float*>(smem);
+        sums[tid] = l;
+        run = named_bar_all(1, 128, run);
+        l = 0.f;
+        for (int c = 0; c < C::COPIES; ++c) l += sums[c * C::ROWS + row];
+        run = named_bar_all(1, 128, run);
+      }
+      if (active && copy == 0 && run) {
         if (!C::SPARSE && *static_cast<volatile int*>(&sh.bad[seg % kRing]) == seg + 1)
           fix_nonfinite<FMT, D>(a, done, max(done.t0, done.full / kTile), done.t1, qi, valid, tO);
         const int r = done.r0 + row;
@@ -732,10 +855,6 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
         tc_fence_before();
       }
       ++seg;
-    }
-    if (tid == 0) {  // the first group has rows in every unit
-      a.meta[2 * cta] = m0;
-      a.meta[2 * cta + 1] = m1;
     }
     if (FORM != kWide && warp == 0) settle_products(0);
   } else if (FORM == kWide && warp >= NSW + 4) {
@@ -813,7 +932,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
     // the segment
     auto hand_over = [&](int info) {
       const int at = info & 15, seg = info >> 8;
-      uint8_t* const tile = smem + at * C::SLOT;
+      uint8_t* const tile = tiles + at * C::SLOT;
       bool found = false;
       if constexpr (C::RAW) {
         const uint8_t* src = ring + (sent % C::P) * C::RAW_SLOT;
@@ -909,7 +1028,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
           cp_async4(dsc + i * 256, head + scale_at + ((off * L::SB) & ~3), ok);
           if (D == 64) odd |= (off & 1) << i;
         } else {
-          cp_async16(smem_u32(place(smem + at * C::SLOT, i, chunk)), head + code_at + off * L::CB + code_off, ok);
+          cp_async16(smem_u32(place(tiles + at * C::SLOT, i, chunk)), head + code_at + off * L::CB + code_off, ok);
         }
       }
       if constexpr (C::RAW && D == 64) reinterpret_cast<uint32_t*>(to + NCH * 64 * 20)[ti] = odd;
@@ -1013,7 +1132,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
             if (lane < 16) {
 #pragma unroll
               for (int c = 0; c < C::NBLK; ++c)
-                tma_gather4(smem + at * C::SLOT + c * (kTile * 128) + lane * 512, &tm, c * 64, y[0], y[1], y[2], y[3], &sh.full[at]);
+                tma_gather4(tiles + at * C::SLOT + c * (kTile * 128) + lane * 512, &tm, c * 64, y[0], y[1], y[2], y[3], &sh.full[at]);
             }
           } else if (run && lane == 0) {
             mbar_arrive(&sh.full[at]);
@@ -1045,7 +1164,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
                 const int y = ((page * a.kv_heads + s.h) * 2 + v) * kTile;
 #pragma unroll
                 for (int c = 0; c < C::NBLK; ++c)
-                  tma_load_2d(smem + at * C::SLOT + c * (kTile * 128), &tm, c * 64, y, &sh.full[at]);
+                  tma_load_2d(tiles + at * C::SLOT + c * (kTile * 128), &tm, c * 64, y, &sh.full[at]);
               }
               if (last) mbar_arrive(&sh.vdone[seg % kRing]);
             }
@@ -1098,15 +1217,21 @@ dsa_status run_one(dsa_ctx* ctx, const CUtensorMap& tm, const AttnArgs& a, int g
   return launch_pdl(kern, dim3(grid), dim3(C::THREADS), bytes, stream, tm, a) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 
+template <int FMT, int D>
+dsa_status run_dim(dsa_ctx* ctx, int form, const CUtensorMap& tm, const AttnArgs& a, int grid, cudaStream_t stream) {
+  switch (form) {
+    case kTree: return run_one<FMT, D, kTree>(ctx, tm, a, grid, stream);
+    case kSparse: return run_one<FMT, D, kSparse>(ctx, tm, a, grid, stream);
+    case kWide: return run_one<FMT, D, kWide>(ctx, tm, a, grid, stream);
+    case kTreeFew: return run_one<FMT, D, kTreeFew>(ctx, tm, a, grid, stream);
+    default: return run_one<FMT, D, kSparseFew>(ctx, tm, a, grid, stream);
+  }
+}
+
 template <int FMT>
 dsa_status run_fmt(dsa_ctx* ctx, int form, int D, const CUtensorMap& tm, const AttnArgs& a, int grid, cudaStream_t stream) {
-  if (D == 128)
-    return form == kSparse ? run_one<FMT, 128, kSparse>(ctx, tm, a, grid, stream)
-           : form == kWide ? run_one<FMT, 128, kWide>(ctx, tm, a, grid, stream)
-                           : run_one<FMT, 128, kTree>(ctx, tm, a, grid, stream);
-  return form == kSparse ? run_one<FMT, 64, kSparse>(ctx, tm, a, grid, stream)
-         : form == kWide ? run_one<FMT, 64, kWide>(ctx, tm, a, grid, stream)
-                         : run_one<FMT, 64, kTree>(ctx, tm, a, grid, stream);
+  if (D == 128) return run_dim<FMT, 128>(ctx, form, tm, a, grid, stream);
+  return run_dim<FMT, 64>(ctx, form, tm, a, grid, stream);
 }
 
 // One cache format's kernels: attn.cu (bf16), attn_fp8.cu, attn_fp4.cu.
