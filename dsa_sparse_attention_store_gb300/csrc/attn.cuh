@@ -1212,7 +1212,11 @@ dsa_status run_one(dsa_ctx* ctx, const CUtensorMap& tm, const AttnArgs& a, int g
   auto kern = attn_kernel<FMT, D, FORM>;
   constexpr int bytes = smem_bytes<C>();
   static_assert(bytes * C::CTAS <= 233472 - 1024 * C::CTAS, "shared memory of an SM");
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return DSA_ERR_CUDA;
+  const uint64_t bit = 1ull << ((FMT * 2 + (D == 128)) * 5 + FORM);  // once a context and kernel
+  if (!(ctx->attn_ready & bit)) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return DSA_ERR_CUDA;
+    ctx->attn_ready |= bit;
+  }
   LaunchScope scope(ctx, DSA_K_ATTN, stream);
   return launch_pdl(kern, dim3(grid), dim3(C::THREADS), bytes, stream, tm, a) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }

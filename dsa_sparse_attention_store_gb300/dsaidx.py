@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 FMT_BF16 = 0
 FMT_FP8 = 1
@@ -40,13 +41,9 @@ class _RopeDesc(ctypes.Structure):  # dsa_rope_desc
                 ("beta_fast", _c_f64), ("mscale", _c_f64)]
 
 
-class _AttnArgs(ctypes.Structure):  # dsa_attn_args
-    _fields_ = [("q", _c_ptr), ("q_stride_t", _c_i64), ("q_stride_h", _c_i64), ("out", _c_ptr),
-                ("out_stride_t", _c_i64), ("out_stride_h", _c_i64), ("lse", _c_ptr), ("cache", _c_ptr),
-                ("num_pages", _c_int), ("fmt", ctypes.c_int), ("heads", _c_int), ("kv_heads", _c_int),
-                ("head_dim", _c_int), ("page_table", _c_ptr), ("max_pages", _c_int), ("seq_lens", _c_ptr),
-                ("cu_q", _c_ptr), ("B", _c_int), ("Tq", _c_int), ("mask", _c_ptr), ("mask_words", _c_int),
-                ("scale", _c_f64), ("workspace", _c_ptr), ("ws_bytes", _c_size)]
+# dsa_attn_args, field by field with the C padding
+_ATTN_PACK = struct.Struct("@PqqPqqPPiiiiiPiPPiiPidPN").pack
+_KV_PAGE_BYTES = {}  # of (kv_heads, head_dim, fmt)
 
 
 class DsaError(RuntimeError):
@@ -106,8 +103,8 @@ def lib() -> ctypes.CDLL:
                                   _c_int, _c_int, _c_int, _c_ptr, _c_ptr, _c_i64, _c_i64, _c_i64, _c_i64, _c_ptr]
         L.dsa_attn_workspace_size.argtypes = [_c_ptr, _c_int]
         L.dsa_attn_workspace_size.restype = _c_size
-        L.dsa_tree_attn.argtypes = [_c_ptr, ctypes.POINTER(_AttnArgs), _c_ptr]
-        L.dsa_sparse_attn.argtypes = [_c_ptr, ctypes.POINTER(_AttnArgs), _c_ptr, _c_int, _c_ptr]
+        L.dsa_tree_attn.argtypes = [_c_ptr, ctypes.c_char_p, _c_ptr]
+        L.dsa_sparse_attn.argtypes = [_c_ptr, ctypes.c_char_p, _c_ptr, _c_int, _c_ptr]
         for f in (L.dsa_rope_create, L.dsa_rope_destroy, L.dsa_rope_apply, L.dsa_kv_store, L.dsa_kv_load,
                   L.dsa_tree_attn, L.dsa_sparse_attn):
             f.restype = ctypes.c_int
@@ -155,22 +152,53 @@ def _dev(t, dtype, shape=None, name="tensor"):
     return _c_ptr(t.data_ptr())
 
 
+# The calls below are made once a layer of a decode step, so their checks are
+# written to cost little where nothing is wrong: plain integers instead of
+# ctypes objects, one comparison per property, messages only on the way out.
+
+def _ptr(t, dtype, shape, name):
+    """data_ptr of a contiguous CUDA tensor of that type and shape (None: any)."""
+    try:
+        if t.dtype is dtype and t.is_cuda and t.is_contiguous() and (shape is None or t.shape == shape):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _dev(t, dtype, shape, name)       # says what is wrong
+    raise ValueError(f"{name} is not usable")
+
+
 def _rows(t, dtype, shape, name):
-    """Pointer and (token, head) strides of a [tokens, heads, dims] tensor whose
-    dims are contiguous."""
+    """Pointer and (token, head) strides of a [tokens, heads, dims] CUDA tensor
+    whose dims are contiguous."""
     import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 3 or tuple(t.shape) != tuple(shape):
+    if t.dim() != 3 or t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.shape[2] > 1 and t.stride(2) != 1:
+    st, sh, sd = t.stride()
+    T, H, D = shape
+    if sd != 1 and D > 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
     # a dimension of one element has no stride to speak of
-    st = 0 if t.shape[0] <= 1 else t.stride(0)
-    sh = 0 if t.shape[1] <= 1 else t.stride(1)
-    return _c_ptr(t.data_ptr()), _c_i64(st), _c_i64(sh)
+    return t.data_ptr(), 0 if T <= 1 else st, 0 if H <= 1 else sh
+
+
+_current_stream = None
+
+
+def _raw_stream(stream):
+    """The stream's address; the current one of the current device for None."""
+    global _current_stream
+    if stream is None:
+        if _current_stream is None:
+            import torch
+            # what torch.cuda.current_stream() asks, without the Stream object around the answer
+            raw, dev = (getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+            _current_stream = (lambda: raw(dev())) if raw and dev else (lambda: torch.cuda.current_stream().cuda_stream)
+        return _current_stream()
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 class Rope:
@@ -312,18 +340,18 @@ class Context:
         """dsa_rope_apply: rotate [T, H, D] rows (bf16, fp16 or fp32) to their
         positions, into `out` or in place. `inverse` turns back (the gradient)."""
         import torch
-        dt = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
-        if not isinstance(x, torch.Tensor) or x.dtype not in dt:
+        dt = x.dtype if isinstance(x, torch.Tensor) else None
+        code = 0 if dt is torch.bfloat16 else 1 if dt is torch.float16 else 2 if dt is torch.float32 else -1
+        if code < 0:
             raise TypeError("x must be a bf16, fp16 or fp32 CUDA tensor")
-        if x.dim() != 3:
-            raise ValueError(f"x must be [T, H, D], got {tuple(x.shape)}")
-        out = x if out is None else out
-        xp, xt, xh = _rows(x, x.dtype, x.shape, "x")
-        yp, yt, yh = _rows(out, x.dtype, x.shape, "out")
-        T, H, D = (int(n) for n in x.shape)
-        st = lib().dsa_rope_apply(self._h, rope.handle, xp, yp, dt[x.dtype], _dev(pos, torch.int32, (T,), "pos"),
-                                  _c_int(T), _c_int(H), _c_int(D), _c_int(rot_start), xt, xh, yt, yh,
-                                  _c_int(1 if inverse else 0), _stream_ptr(stream))
+        shape = x.shape
+        if len(shape) != 3:
+            raise ValueError(f"x must be [T, H, D], got {tuple(shape)}")
+        T, H, D = shape
+        xp, xt, xh = _rows(x, dt, shape, "x")
+        yp, yt, yh = (xp, xt, xh) if out is None else _rows(out, dt, shape, "out")
+        st = lib().dsa_rope_apply(self._h, rope._h, xp, yp, code, _ptr(pos, torch.int32, (T,), "pos"), T, H, D,
+                                  rot_start, xt, xh, yt, yh, 1 if inverse else 0, _raw_stream(stream))
         if st != 0:
             raise DsaError("dsa_rope_apply", st)
 
@@ -332,19 +360,16 @@ class Context:
         """dsa_kv_store: write [T, kv_heads, head_dim] bf16 keys (rotated when a
         plan is given) and values into the paged K/V cache."""
         import torch
-        shape = tuple(k.shape)
+        i32, shape = torch.int32, k.shape
         kp, kt, kh = _rows(k, torch.bfloat16, shape, "k")
         vp, vt, vh = _rows(v, torch.bfloat16, shape, "v")
-        T, n, D = (int(x) for x in shape)
-        B, max_pages = int(page_table.shape[0]), int(page_table.shape[1])
-        self._kv_cache(cache, num_pages, n, D, fmt)
+        T, n, D = shape
+        B, max_pages = page_table.shape
         st = lib().dsa_kv_store(
-            self._h, kp, vp, kt, kh, vt, vh, _dev(cache_pos, torch.int32, (T,), "cache_pos"),
-            _dev(seq_id, torch.int32, (T,), "seq_id"), _dev(page_table, torch.int32, None, "page_table"), _c_int(T),
-            _c_int(B), _c_int(max_pages), _c_int(n), _c_int(D), _dev(cache, torch.uint8, None, "cache"),
-            _c_int(num_pages), int(fmt), None if rope is None else rope.handle,
-            None if rope_pos is None else _dev(rope_pos, torch.int32, (T,), "rope_pos"), _c_int(rot_start),
-            _stream_ptr(stream))
+            self._h, kp, vp, kt, kh, vt, vh, _ptr(cache_pos, i32, (T,), "cache_pos"), _ptr(seq_id, i32, (T,), "seq_id"),
+            _ptr(page_table, i32, None, "page_table"), T, B, max_pages, n, D,
+            self._kv_cache(cache, num_pages, n, D, fmt), num_pages, fmt, None if rope is None else rope._h,
+            None if rope_pos is None else _ptr(rope_pos, i32, (T,), "rope_pos"), rot_start, _raw_stream(stream))
         if st != 0:
             raise DsaError("dsa_kv_store", st)
 
@@ -352,52 +377,58 @@ class Context:
         """dsa_kv_load: read tokens of the K/V cache back into k and v, [T,
         kv_heads, head_dim] bf16."""
         import torch
-        shape = tuple(k.shape)
+        i32, shape = torch.int32, k.shape
         kp, kt, kh = _rows(k, torch.bfloat16, shape, "k")
         vp, vt, vh = _rows(v, torch.bfloat16, shape, "v")
-        T, n, D = (int(x) for x in shape)
-        B, max_pages = int(page_table.shape[0]), int(page_table.shape[1])
-        self._kv_cache(cache, num_pages, n, D, fmt)
+        T, n, D = shape
+        B, max_pages = page_table.shape
         st = lib().dsa_kv_load(
-            self._h, _dev(cache, torch.uint8, None, "cache"), _c_int(num_pages), int(fmt), _c_int(n), _c_int(D),
-            _dev(cache_pos, torch.int32, (T,), "cache_pos"), _dev(seq_id, torch.int32, (T,), "seq_id"),
-            _dev(page_table, torch.int32, None, "page_table"), _c_int(T), _c_int(B), _c_int(max_pages), kp, vp, kt,
-            kh, vt, vh, _stream_ptr(stream))
+            self._h, self._kv_cache(cache, num_pages, n, D, fmt), num_pages, fmt, n, D,
+            _ptr(cache_pos, i32, (T,), "cache_pos"), _ptr(seq_id, i32, (T,), "seq_id"),
+            _ptr(page_table, i32, None, "page_table"), T, B, max_pages, kp, vp, kt, kh, vt, vh, _raw_stream(stream))
         if st != 0:
             raise DsaError("dsa_kv_load", st)
 
     @staticmethod
     def _kv_cache(cache, num_pages, kv_heads, head_dim, fmt):
-        need = int(num_pages) * kv_page_bytes(kv_heads, head_dim, fmt)
-        if need and cache.numel() < need:
-            raise ValueError(f"cache must have at least {need} bytes, got {cache.numel()}")
+        """The cache's pointer, once it is known to hold that many pages."""
+        import torch
+        p = _ptr(cache, torch.uint8, None, "cache")
+        key = (kv_heads, head_dim, fmt)
+        size = _KV_PAGE_BYTES.get(key)
+        if size is None:
+            size = _KV_PAGE_BYTES[key] = kv_page_bytes(*key)
+        if cache.numel() < num_pages * size:
+            raise ValueError(f"cache must have at least {num_pages * size} bytes, got {cache.numel()}")
+        return p
 
     def attn_workspace_size(self, head_dim: int) -> int:
         return int(lib().dsa_attn_workspace_size(self._h, _c_int(head_dim)))
 
     def _attn_args(self, q, cache, num_pages, fmt, kv_heads, page_table, seq_lens, cu_q, out, workspace, mask, lse,
                    scale):
+        """A dsa_attn_args as bytes."""
         import torch
+        i32, bf16 = torch.int32, torch.bfloat16
         if not isinstance(q, torch.Tensor) or q.dim() != 3:
             raise ValueError("q must be a [Tq, heads, head_dim] tensor")
-        Tq, H, D = (int(n) for n in q.shape)
-        qp, qt, qh = _rows(q, torch.bfloat16, q.shape, "q")
-        op, ot, oh = _rows(out, torch.bfloat16, q.shape, "out")
-        B, max_pages = int(page_table.shape[0]), int(page_table.shape[1])
-        self._kv_cache(cache, num_pages, kv_heads, D, fmt)
-        mp, words = None, 0
+        shape = q.shape
+        Tq, H, D = shape
+        qp, qt, qh = _rows(q, bf16, shape, "q")
+        op, ot, oh = _rows(out, bf16, shape, "out")
+        B, max_pages = page_table.shape
+        mp = words = 0
         if mask is not None:
             if mask.dim() != 2:
                 raise ValueError("mask must be [Tq, words]")
-            words = int(mask.shape[1])
-            mp = _dev(mask, torch.int32, (Tq, words), "mask")
-        return _AttnArgs(
-            qp, qt, qh, op, ot, oh, None if lse is None else _dev(lse, torch.float32, (Tq, H), "lse"),
-            _dev(cache, torch.uint8, None, "cache"), _c_int(num_pages), int(fmt), _c_int(H), _c_int(kv_heads),
-            _c_int(D), _dev(page_table, torch.int32, None, "page_table"), _c_int(max_pages),
-            _dev(seq_lens, torch.int32, (B,), "seq_lens"), _dev(cu_q, torch.int32, (B + 1,), "cu_q"), _c_int(B),
-            _c_int(Tq), mp, _c_int(words), D ** -0.5 if scale is None else float(scale),
-            _dev(workspace, torch.uint8, None, "workspace"), _c_size(workspace.numel()))
+            words = mask.shape[1]
+            mp = _ptr(mask, i32, (Tq, words), "mask")
+        return _ATTN_PACK(
+            qp, qt, qh, op, ot, oh, 0 if lse is None else _ptr(lse, torch.float32, (Tq, H), "lse"),
+            self._kv_cache(cache, num_pages, kv_heads, D, fmt), num_pages, fmt, H, kv_heads, D,
+            _ptr(page_table, i32, None, "page_table"), max_pages, _ptr(seq_lens, i32, (B,), "seq_lens"),
+            _ptr(cu_q, i32, (B + 1,), "cu_q"), B, Tq, mp, words, D ** -0.5 if scale is None else scale,
+            _ptr(workspace, torch.uint8, None, "workspace"), workspace.numel())
 
     def tree_attn(self, q, cache, num_pages: int, fmt: int, kv_heads: int, page_table, seq_lens, cu_q, out,
                   workspace, mask=None, lse=None, scale=None, stream=None):
@@ -406,7 +437,7 @@ class Context:
         token; None: token i sees the new tokens up to i."""
         a = self._attn_args(q, cache, num_pages, fmt, kv_heads, page_table, seq_lens, cu_q, out, workspace, mask,
                             lse, scale)
-        st = lib().dsa_tree_attn(self._h, ctypes.byref(a), _stream_ptr(stream))
+        st = lib().dsa_tree_attn(self._h, a, _raw_stream(stream))
         if st != 0:
             raise DsaError("dsa_tree_attn", st)
 
@@ -417,11 +448,10 @@ class Context:
         import torch
         if not isinstance(sel, torch.Tensor) or sel.dim() != 2:
             raise ValueError("sel must be a [Tq, k] tensor")
-        k = int(sel.shape[1])
+        k = sel.shape[1]
         a = self._attn_args(q, cache, num_pages, fmt, kv_heads, page_table, seq_lens, cu_q, out, workspace, mask,
                             lse, scale)
-        st = lib().dsa_sparse_attn(self._h, ctypes.byref(a), _dev(sel, torch.int32, (int(q.shape[0]), k), "sel"),
-                                   _c_int(k), _stream_ptr(stream))
+        st = lib().dsa_sparse_attn(self._h, a, _ptr(sel, torch.int32, (q.shape[0], k), "sel"), k, _raw_stream(stream))
         if st != 0:
             raise DsaError("dsa_sparse_attn", st)
 

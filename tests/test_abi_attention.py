@@ -85,20 +85,20 @@ def test_kv_calls_refuse(L):
 
 
 def _args(**kw):
-    from dsa_sparse_attention_store_gb300.dsaidx import _AttnArgs
+    from dsa_sparse_attention_store_gb300.dsaidx import _ATTN_PACK
     d = dict(q=GOOD, q_stride_t=128, q_stride_h=128, out=GOOD, out_stride_t=128, out_stride_h=128, lse=GOOD, cache=GOOD,
              num_pages=1, fmt=0, heads=8, kv_heads=2, head_dim=128, page_table=GOOD, max_pages=1, seq_lens=GOOD, cu_q=GOOD,
              B=1, Tq=1, mask=None, mask_words=0, scale=0.1, workspace=GOOD, ws_bytes=1 << 40)
     d.update(kw)
-    return _AttnArgs(**d)
+    return _ATTN_PACK(*((v.value or 0) if isinstance(v, P) else 0 if v is None else v for v in d.values()))
 
 
 def test_attention_refuses(L):
     def tree(ctx=FAKE, **kw):
-        return L.dsa_tree_attn(ctx, ctypes.byref(_args(**kw)), None)
+        return L.dsa_tree_attn(ctx, _args(**kw), None)
 
     def sparse(ctx=FAKE, sel=GOOD, k=4, **kw):
-        return L.dsa_sparse_attn(ctx, ctypes.byref(_args(**kw)), sel, k, None)
+        return L.dsa_sparse_attn(ctx, _args(**kw), sel, k, None)
 
     for call in (tree, sparse):
         assert call(ctx=None) == 1
@@ -127,8 +127,8 @@ def test_device_is_checked_before_the_handles_are_read(L):
     assert L.dsa_rope_create(FAKE, ctypes.byref(h), ctypes.byref(_desc())) == 3
     assert L.dsa_rope_apply(FAKE, FAKE, GOOD, GOOD, 0, GOOD, 1, 1, 64, 0, 64, 64, 64, 64, 0, None) == 3
     assert L.dsa_kv_store(FAKE, GOOD, GOOD, 128, 128, 128, 128, GOOD, GOOD, GOOD, 1, 1, 1, 1, 128, GOOD, 1, 0, FAKE, None, 0, None) == 3
-    assert L.dsa_tree_attn(FAKE, ctypes.byref(_args()), None) == 3
-    assert L.dsa_sparse_attn(FAKE, ctypes.byref(_args()), GOOD, 4, None) == 3
+    assert L.dsa_tree_attn(FAKE, _args(), None) == 3
+    assert L.dsa_sparse_attn(FAKE, _args(), GOOD, 4, None) == 3
 
 
 def test_binding_refuses_what_is_not_a_cuda_tensor(L):
