@@ -1,14 +1,17 @@
 // K/V cache: write (rotate keys, quantise, scatter into pages) and read back.
 //
-// One row is one token's key or value of one kv head: D / 8 lanes with 8
-// dimensions each. A key's rotation needs the partner dimensions, which the
-// lane loads itself (the row is in L1 by then), so a row's lanes share
-// nothing but the maximum of a 32-dimension block (4 lanes, two shuffles).
-// The rotation is fp32 with every product and sum rounded separately and the
-// rotated value is rounded once, to the cache's format.
+// A row is one token's key or value of one kv head: D / 8 lanes with 8
+// dimensions each. A thread has its lane's part of the key and the value of
+// up to HPT heads of one token, so that position -> page id -> row, the
+// dependent loads, are walked once for 2 HPT rows and their data loads are in
+// flight together, and the cos/sin of the rotation serve all keys. A row's
+// lanes share the maximum of a 32-dimension block (4 lanes, two shuffles) and,
+// in the half layout, the partner dimensions (a shuffle). The rotation is
+// fp32 with every product and sum rounded separately and the rotated value is
+// rounded once, to the cache's format.
 //
 // Bound: HBM for long batches (each value read once, its code written once),
-// the two dependent loads position -> page id -> row for short ones.
+// the dependent loads for short ones.
 #include <cuda_fp4.h>
 #include <cuda_fp8.h>
 
@@ -40,6 +43,7 @@ struct KvArgs {
   uint8_t* cache;
   unsigned int* status;
   int T, B, max_pages, num_pages, kv_heads;
+  int groups;                   // a token's heads are split among so many threads of a lane
   int R, start, rope_max, half_layout, wide;  // wide: a lane's 8 dimensions pair with 8 others, or among themselves
 };
 
@@ -57,105 +61,30 @@ __device__ __forceinline__ int find_page(const KvArgs& a, int t, int& off, bool 
   return page;
 }
 
-template <int FMT, int D>
-__global__ void __launch_bounds__(128) kv_store_kernel(KvArgs a) {
-  using L = Layout<FMT, D>;
-  constexpr int LANES = D / 8;
-  pdl_wait();
-  pdl_trigger();
-  const long long row = static_cast<long long>(blockIdx.x) * (128 / LANES) + threadIdx.x / LANES;
-  const int l = threadIdx.x % LANES, d0 = 8 * l;
-  const bool live = row < static_cast<long long>(a.T) * a.kv_heads;
-  const int t = live ? static_cast<int>(row / a.kv_heads) : 0;
-  const int h = live ? static_cast<int>(row % a.kv_heads) : 0;
-  const bool is_v = blockIdx.y == 1;
-  const __nv_bfloat16* src = is_v ? a.v + t * a.vt + h * a.vh : a.k + t * a.kt + h * a.kh;
-  float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  int off = 0, page = -1;
-  if (live) {
-    const uint4 raw = __ldg(reinterpret_cast<const uint4*>(src + d0));
-    page = find_page(a, t, off, l == 0 && h == 0);
-    unpack8(raw, x);
-  }
-  int rp = 0;
-  if (a.table && live) {  // a token whose rotary position is out of range is not written
-    rp = a.rope_pos[t];
-    if (rp < 0 || rp >= a.rope_max) {
-      page = -1;
-      rp = 0;
-      if (l == 0 && h == 0) atomicOr(a.status, DSA_DEV_BOUNDS);
-    }
-  }
-  if (a.table && !is_v && live && d0 < a.start + a.R && d0 + 8 > a.start) {
-    const float2* tab = a.table + static_cast<long long>(rp) * (a.R >> 1);
-    const int half = a.R >> 1, p0 = d0 - a.start;
-    if (a.wide) {
-      float c[8], s[8], o[8];
-      if (a.half_layout) {
-        const bool upper = p0 >= half;
-        const int i0 = upper ? p0 - half : p0;
-        const uint4 raw = __ldg(reinterpret_cast<const uint4*>(src + (upper ? d0 - half : d0 + half)));
-#pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-          const float4 w = __ldg(reinterpret_cast<const float4*>(tab + i0 + i));
-          c[i] = w.x;
-          s[i] = upper ? w.y : -w.y;
-          c[i + 1] = w.z;
-          s[i + 1] = upper ? w.w : -w.w;
-        }
-        unpack8(raw, o);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; i += 4) {
-          const float4 w = __ldg(reinterpret_cast<const float4*>(tab + ((p0 + i) >> 1)));
-          c[i] = c[i + 1] = w.x;
-          c[i + 2] = c[i + 3] = w.z;
-          s[i] = -w.y;
-          s[i + 1] = w.y;
-          s[i + 2] = -w.w;
-          s[i + 3] = w.w;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = x[i ^ 1];
-      }
-      // own * c -+ partner * s: x - y and x + (-y) round alike
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = __fadd_rn(__fmul_rn(x[i], c[i]), __fmul_rn(o[i], s[i]));
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int p = p0 + i;
-        if (p < 0 || p >= a.R) continue;
-        const bool upper = a.half_layout ? p >= half : p & 1;
-        const int pair = a.half_layout ? (upper ? p - half : p) : p >> 1;
-        const int other = a.half_layout ? (upper ? p - half : p + half) : p ^ 1;
-        const float2 w = __ldg(tab + pair);
-        const float y = __bfloat162float(src[a.start + other]);
-        x[i] = __fadd_rn(__fmul_rn(x[i], w.x), __fmul_rn(y, upper ? w.y : -w.y));
-      }
-    }
-  }
-  uint8_t* blk = a.cache + (static_cast<long long>(page < 0 ? 0 : page) * a.kv_heads + h) * L::HEAD_BYTES;
-  uint8_t* dst = blk + (is_v ? L::V_CODES : L::K_CODES) + off * L::CB;
+// 8 fp32 values of a row -> the cache (codes at dst for this lane, the block's
+// scale); every lane of the warp calls it, `ok` says whether the row is written
+template <int FMT>
+__device__ __forceinline__ void put_row(const float (&v)[8], bool ok, uint8_t* codes, uint8_t* scale, int l) {
   if constexpr (FMT == DSA_FMT_BF16) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 p = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+      const __nv_bfloat162 p = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
       memcpy(&w[i], &p, 4);
     }
-    if (page >= 0) *reinterpret_cast<uint4*>(dst + 16 * l) = make_uint4(w[0], w[1], w[2], w[3]);
+    if (ok) *reinterpret_cast<uint4*>(codes + 16 * l) = make_uint4(w[0], w[1], w[2], w[3]);
   } else {
     uint32_t amax = 0;  // as bits: above any finite value where a NaN or infinity is among them
 #pragma unroll
-    for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+    for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(v[i]) & 0x7FFFFFFFu);
     amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
     amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
     const bool bad = amax >= 0x7F800000u;
     const int e = Scale<FMT>::exponent(amax);
     const float inv = bad ? 0.f : __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+    float x[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = bad ? 0.f : __fmul_rn(x[i], inv);
+    for (int i = 0; i < 8; ++i) x[i] = bad ? 0.f : __fmul_rn(v[i], inv);
     if constexpr (FMT == DSA_FMT_FP8) {
       uint32_t w[2];
 #pragma unroll
@@ -164,7 +93,7 @@ __global__ void __launch_bounds__(128) kv_store_kernel(KvArgs a) {
         const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i + 2], x[4 * i + 3]), __NV_SATFINITE, __NV_E4M3);
         w[i] = lo | (hi << 16);
       }
-      if (page >= 0) *reinterpret_cast<uint2*>(dst + 8 * l) = make_uint2(w[0], w[1]);
+      if (ok) *reinterpret_cast<uint2*>(codes + 8 * l) = make_uint2(w[0], w[1]);
     } else {
       uint32_t w = 0;
 #pragma unroll
@@ -172,73 +101,219 @@ __global__ void __launch_bounds__(128) kv_store_kernel(KvArgs a) {
         w |= static_cast<uint32_t>(
                  __nv_cvt_float2_to_fp4x2(make_float2(x[2 * i], x[2 * i + 1]), __NV_E2M1, cudaRoundNearest))
              << (8 * i);
-      if (page >= 0) *reinterpret_cast<uint32_t*>(dst + 4 * l) = w;
+      if (ok) *reinterpret_cast<uint32_t*>(codes + 4 * l) = w;
     }
-    if (page >= 0 && (l & 3) == 0)
-      blk[(is_v ? L::V_SCALES : L::K_SCALES) + off * L::SB + (l >> 2)] = bad ? 255 : static_cast<uint8_t>(e + 127);
+    if (ok && (l & 3) == 0) scale[l >> 2] = bad ? 255 : static_cast<uint8_t>(e + 127);
   }
 }
 
-template <int FMT, int D>
-__global__ void __launch_bounds__(128) kv_load_kernel(KvArgs a) {
+// the thread's place: lane of a row, token and first head (heads h, h +
+// groups, ...); a warp's threads are consecutive
+struct Place {
+  int l, t, h;
+  bool live;
+};
+template <int D>
+__device__ __forceinline__ Place place_of(const KvArgs& a) {
+  const long long x = static_cast<long long>(blockIdx.x) * 128 + threadIdx.x;
+  const long long row = x / (D / 8);
+  Place p;
+  p.l = static_cast<int>(x % (D / 8));
+  p.live = row < static_cast<long long>(a.T) * a.groups;
+  p.t = p.live ? static_cast<int>(row / a.groups) : 0;
+  p.h = p.live ? static_cast<int>(row % a.groups) : 0;
+  return p;
+}
+
+template <int FMT, int D, int HPT>
+__global__ void __launch_bounds__(128) kv_store_kernel(KvArgs a) {
   using L = Layout<FMT, D>;
-  constexpr int LANES = D / 8;
   pdl_wait();
   pdl_trigger();
-  const long long row = static_cast<long long>(blockIdx.x) * (128 / LANES) + threadIdx.x / LANES;
-  const int l = threadIdx.x % LANES;
-  if (row >= static_cast<long long>(a.T) * a.kv_heads) return;
-  const int t = static_cast<int>(row / a.kv_heads), h = static_cast<int>(row % a.kv_heads);
-  const bool is_v = blockIdx.y == 1;
-  __nv_bfloat16* out = (is_v ? a.vo + t * a.vt + h * a.vh : a.ko + t * a.kt + h * a.kh) + 8 * l;
-  int off;
-  const int page = find_page(a, t, off, l == 0 && h == 0);
-  uint4 w = make_uint4(0, 0, 0, 0);  // a row that has no page reads as zeros
-  if (page >= 0) {
-    const uint8_t* blk = a.cache + (static_cast<long long>(page) * a.kv_heads + h) * L::HEAD_BYTES;
-    const uint8_t* src = blk + (is_v ? L::V_CODES : L::K_CODES) + off * L::CB;
-    if constexpr (FMT == DSA_FMT_BF16) {
-      w = *reinterpret_cast<const uint4*>(src + 16 * l);
+  const Place p = place_of<D>(a);
+  const int l = p.l, t = p.t, d0 = 8 * l;
+  uint4 rk[HPT], rv[HPT];
+  int rp = 0;
+#pragma unroll
+  for (int j = 0; j < HPT; ++j) {
+    const int h = p.h + j * a.groups;
+    const bool in = p.live && h < a.kv_heads;
+    rk[j] = in ? __ldg(reinterpret_cast<const uint4*>(a.k + t * a.kt + h * a.kh + d0)) : make_uint4(0, 0, 0, 0);
+    rv[j] = in ? __ldg(reinterpret_cast<const uint4*>(a.v + t * a.vt + h * a.vh + d0)) : make_uint4(0, 0, 0, 0);
+  }
+  int off = 0, page = -1;
+  if (p.live) {
+    if (a.table) rp = a.rope_pos[t];
+    page = find_page(a, t, off, l == 0 && p.h == 0);
+    if (a.table && (rp < 0 || rp >= a.rope_max)) {  // a token whose rotary position is out of range is not written
+      page = -1;
+      rp = 0;
+      if (l == 0 && p.h == 0) atomicOr(a.status, DSA_DEV_BOUNDS);
+    }
+  }
+  const bool turns = a.table && d0 < a.start + a.R && d0 + 8 > a.start;  // some of this lane's dimensions do
+  const int half = a.R >> 1, p0 = d0 - a.start;
+  const bool upper = p0 >= half;
+  const float2* tab = a.table + static_cast<long long>(rp) * half;
+  float c[8], s[8];  // own * c + partner * s
+  if (turns && a.wide) {
+    if (a.half_layout) {
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) {
+        const float4 w = __ldg(reinterpret_cast<const float4*>(tab + (upper ? p0 - half : p0) + i));
+        c[i] = w.x;
+        s[i] = upper ? w.y : -w.y;
+        c[i + 1] = w.z;
+        s[i + 1] = upper ? w.w : -w.w;
+      }
     } else {
-      Factor<FMT> f;
-      f.set(blk[(is_v ? L::V_SCALES : L::K_SCALES) + off * L::SB + (l >> 2)]);
-      if constexpr (FMT == DSA_FMT_FP8) {
-        const uint2 v = *reinterpret_cast<const uint2*>(src + 8 * l);
-        const uint32_t c[2] = {v.x, v.y};
-        uint32_t o[4];
-        widen(c, f, o);
-        f.rest(o);
-        w = make_uint4(o[0], o[1], o[2], o[3]);
-      } else {
-        const uint32_t c[1] = {*reinterpret_cast<const uint32_t*>(src + 4 * l)};
-        uint32_t o[4];
-        widen(c, f, o);
-        f.rest(o);
-        w = make_uint4(o[0], o[1], o[2], o[3]);
+#pragma unroll
+      for (int i = 0; i < 8; i += 4) {
+        const float4 w = __ldg(reinterpret_cast<const float4*>(tab + ((p0 + i) >> 1)));
+        c[i] = c[i + 1] = w.x;
+        c[i + 2] = c[i + 3] = w.z;
+        s[i] = -w.y;
+        s[i + 1] = w.y;
+        s[i + 2] = -w.w;
+        s[i + 3] = w.w;
       }
     }
   }
-  *reinterpret_cast<uint4*>(out) = w;
+  // the lane of the row that holds the partners (half layout)
+  const int lane = threadIdx.x & 31;
+  const int mate = turns && a.wide && a.half_layout ? (lane & ~(D / 8 - 1)) | (upper ? l - (half >> 3) : l + (half >> 3)) : lane;
+  uint8_t* const blk = a.cache + static_cast<long long>(page < 0 ? 0 : page) * a.kv_heads * L::HEAD_BYTES;
+#pragma unroll
+  for (int j = 0; j < HPT; ++j) {
+    const int h = p.h + j * a.groups;
+    const bool ok = page >= 0 && h < a.kv_heads;
+    float x[8];
+    unpack8(rk[j], x);
+    if (a.table) {  // uniform
+      if (a.wide) {
+        float o[8];
+        if (a.half_layout) {
+          uint4 m;
+          m.x = __shfl_sync(0xffffffffu, rk[j].x, mate);
+          m.y = __shfl_sync(0xffffffffu, rk[j].y, mate);
+          m.z = __shfl_sync(0xffffffffu, rk[j].z, mate);
+          m.w = __shfl_sync(0xffffffffu, rk[j].w, mate);
+          unpack8(m, o);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o[i] = x[i ^ 1];
+        }
+        if (turns) {
+          // x - y and x + (-y) round alike
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = __fadd_rn(__fmul_rn(x[i], c[i]), __fmul_rn(o[i], s[i]));
+        }
+      } else if (turns && p.live && h < a.kv_heads) {
+        const __nv_bfloat16* src = a.k + t * a.kt + h * a.kh;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int d = p0 + i;
+          if (d < 0 || d >= a.R) continue;
+          const bool up = a.half_layout ? d >= half : d & 1;
+          const int pair = a.half_layout ? (up ? d - half : d) : d >> 1;
+          const int other = a.half_layout ? (up ? d - half : d + half) : d ^ 1;
+          const float2 w = __ldg(tab + pair);
+          const float y = __bfloat162float(src[a.start + other]);
+          x[i] = __fadd_rn(__fmul_rn(x[i], w.x), __fmul_rn(y, up ? w.y : -w.y));
+        }
+      }
+    }
+    uint8_t* const b = blk + static_cast<long long>(ok ? h : 0) * L::HEAD_BYTES;
+    put_row<FMT>(x, ok, b + L::K_CODES + off * L::CB, b + L::K_SCALES + off * L::SB, l);
+    unpack8(rv[j], x);
+    put_row<FMT>(x, ok, b + L::V_CODES + off * L::CB, b + L::V_SCALES + off * L::SB, l);
+  }
 }
 
-template <int D>
-auto store_of(dsa_fmt fmt) {
-  return fmt == DSA_FMT_BF16 ? kv_store_kernel<DSA_FMT_BF16, D>
-         : fmt == DSA_FMT_FP8 ? kv_store_kernel<DSA_FMT_FP8, D> : kv_store_kernel<DSA_FMT_FP4, D>;
-}
-template <int D>
-auto load_of(dsa_fmt fmt) {
-  return fmt == DSA_FMT_BF16 ? kv_load_kernel<DSA_FMT_BF16, D>
-         : fmt == DSA_FMT_FP8 ? kv_load_kernel<DSA_FMT_FP8, D> : kv_load_kernel<DSA_FMT_FP4, D>;
+template <int FMT, int D, int HPT>
+__global__ void __launch_bounds__(128) kv_load_kernel(KvArgs a) {
+  using L = Layout<FMT, D>;
+  constexpr int W = FMT == DSA_FMT_BF16 ? 4 : FMT == DSA_FMT_FP8 ? 2 : 1;  // words of codes a lane has
+  pdl_wait();
+  pdl_trigger();
+  const Place p = place_of<D>(a);
+  if (!p.live) return;
+  const int l = p.l, t = p.t;
+  int off;
+  const int page = find_page(a, t, off, l == 0 && p.h == 0);
+  const uint8_t* const blk = a.cache + static_cast<long long>(page < 0 ? 0 : page) * a.kv_heads * L::HEAD_BYTES;
+  uint32_t c[2 * HPT][W], sc[2 * HPT];
+#pragma unroll
+  for (int j = 0; j < 2 * HPT; ++j) {
+    const int h = p.h + (j >> 1) * a.groups;
+    const uint8_t* b = blk + static_cast<long long>(h) * L::HEAD_BYTES;
+    const uint8_t* src = b + (j & 1 ? L::V_CODES : L::K_CODES) + off * L::CB + 4 * W * l;
+    sc[j] = 0;
+#pragma unroll
+    for (int i = 0; i < W; ++i) c[j][i] = 0;
+    if (page >= 0 && h < a.kv_heads) {
+      if constexpr (W == 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(src);
+        c[j][0] = v.x;
+        c[j][1] = v.y;
+        c[j][2] = v.z;
+        c[j][3] = v.w;
+      } else if constexpr (W == 2) {
+        const uint2 v = *reinterpret_cast<const uint2*>(src);
+        c[j][0] = v.x;
+        c[j][1] = v.y;
+      } else {
+        c[j][0] = *reinterpret_cast<const uint32_t*>(src);
+      }
+      if constexpr (W != 4) sc[j] = b[(j & 1 ? L::V_SCALES : L::K_SCALES) + off * L::SB + (l >> 2)];
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 2 * HPT; ++j) {
+    const int h = p.h + (j >> 1) * a.groups;
+    if (h >= a.kv_heads) continue;
+    uint32_t w[4];
+    if constexpr (W == 4) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = c[j][i];
+    } else {
+      Factor<FMT> f;
+      f.set(sc[j]);
+      widen(c[j], f, w);
+      f.rest(w);
+    }
+    __nv_bfloat16* out = (j & 1 ? a.vo + t * a.vt + h * a.vh : a.ko + t * a.kt + h * a.kh) + 8 * l;
+    // a token that has no page reads as zeros
+    *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
 }
 
-dsa_status launch(dsa_ctx* ctx, int kind, void (*kern)(KvArgs), int D, KvArgs& a, cudaStream_t stream) {
+typedef void (*Kern)(KvArgs);
+template <int D, int HPT>
+Kern store_of(dsa_fmt fmt) {
+  return fmt == DSA_FMT_BF16 ? kv_store_kernel<DSA_FMT_BF16, D, HPT>
+         : fmt == DSA_FMT_FP8 ? kv_store_kernel<DSA_FMT_FP8, D, HPT> : kv_store_kernel<DSA_FMT_FP4, D, HPT>;
+}
+template <int D, int HPT>
+Kern load_of(dsa_fmt fmt) {
+  return fmt == DSA_FMT_BF16 ? kv_load_kernel<DSA_FMT_BF16, D, HPT>
+         : fmt == DSA_FMT_FP8 ? kv_load_kernel<DSA_FMT_FP8, D, HPT> : kv_load_kernel<DSA_FMT_FP4, D, HPT>;
+}
+
+dsa_status launch(dsa_ctx* ctx, bool store, int D, dsa_fmt fmt, KvArgs& a, cudaStream_t stream) {
   a.status = ctx->status;
-  const long long rows = static_cast<long long>(a.T) * a.kv_heads;
-  const long long blocks = (rows * (D / 8) + 127) / 128;
+  // four heads a thread once that still leaves a wave of threads
+  const long long threads = static_cast<long long>(a.T) * a.kv_heads * (D / 8);
+  const bool many = a.kv_heads >= 4 && threads / 4 >= 1024LL * ctx->num_sms;
+  a.groups = many ? (a.kv_heads + 3) / 4 : a.kv_heads;
+  const long long blocks = (static_cast<long long>(a.T) * a.groups * (D / 8) + 127) / 128;
   if (blocks > 0x7FFFFFFFLL) return DSA_ERR_UNSUPPORTED;
-  LaunchScope scope(ctx, kind, stream);
-  const cudaError_t e = launch_pdl(kern, dim3(static_cast<unsigned>(blocks), 2), dim3(128), 0, stream, a);
+  const Kern kern = store ? (D == 128 ? (many ? store_of<128, 4>(fmt) : store_of<128, 1>(fmt))
+                                      : (many ? store_of<64, 4>(fmt) : store_of<64, 1>(fmt)))
+                          : (D == 128 ? (many ? load_of<128, 4>(fmt) : load_of<128, 1>(fmt))
+                                      : (many ? load_of<64, 4>(fmt) : load_of<64, 1>(fmt)));
+  LaunchScope scope(ctx, store ? DSA_K_KV_STORE : DSA_K_KV_LOAD, stream);
+  const cudaError_t e = launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(128), 0, stream, a);
   return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 
@@ -280,7 +355,7 @@ dsa_status launch_kv_store(dsa_ctx* ctx, const void* k, const void* v, long long
     a.half_layout = rope->layout == DSA_ROPE_HALF;
     a.wide = start % 8 == 0 && (a.half_layout ? (a.R / 2) % 8 == 0 : a.R % 8 == 0);
   }
-  return launch(ctx, DSA_K_KV_STORE, head_dim == 128 ? store_of<128>(fmt) : store_of<64>(fmt), head_dim, a, stream);
+  return launch(ctx, true, head_dim, fmt, a, stream);
 }
 
 dsa_status launch_kv_load(dsa_ctx* ctx, const void* cache, int32_t num_pages, dsa_fmt fmt, int32_t kv_heads,
@@ -303,7 +378,7 @@ dsa_status launch_kv_load(dsa_ctx* ctx, const void* cache, int32_t num_pages, ds
   a.max_pages = max_pages;
   a.num_pages = num_pages;
   a.kv_heads = kv_heads;
-  return launch(ctx, DSA_K_KV_LOAD, head_dim == 128 ? load_of<128>(fmt) : load_of<64>(fmt), head_dim, a, stream);
+  return launch(ctx, false, head_dim, fmt, a, stream);
 }
 
 }  // namespace dsa

@@ -39,26 +39,85 @@ __global__ void __launch_bounds__(256) rope_table_kernel(const double* __restric
   }
 }
 
-// element types: 16-byte (or single-element) loads to fp32 and back
+// element types: to fp32 and back, singly and two to a word (one conversion
+// instruction for two values: with one for each, bf16 ran at half the speed)
 struct Bf16 {
   using type = __nv_bfloat16;
+  static constexpr int PER_WORD = 2;
   static __device__ __forceinline__ float up(type v) { return __bfloat162float(v); }
   static __device__ __forceinline__ type down(float v) { return __float2bfloat16_rn(v); }
+  static __device__ __forceinline__ void up2(uint32_t w, float& a, float& b) {
+    a = __uint_as_float(w << 16);
+    b = __uint_as_float(w & 0xFFFF0000u);
+  }
+  static __device__ __forceinline__ uint32_t down2(float a, float b) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
+    uint32_t w;
+    memcpy(&w, &p, 4);
+    return w;
+  }
 };
 struct F16 {
   using type = __half;
+  static constexpr int PER_WORD = 2;
   static __device__ __forceinline__ float up(type v) { return __half2float(v); }
   static __device__ __forceinline__ type down(float v) { return __float2half_rn(v); }
+  static __device__ __forceinline__ void up2(uint32_t w, float& a, float& b) {
+    __half2 p;
+    memcpy(&p, &w, 4);
+    const float2 f = __half22float2(p);
+    a = f.x;
+    b = f.y;
+  }
+  static __device__ __forceinline__ uint32_t down2(float a, float b) {
+    const __half2 p = __floats2half2_rn(a, b);
+    uint32_t w;
+    memcpy(&w, &p, 4);
+    return w;
+  }
 };
 struct F32 {
   using type = float;
+  static constexpr int PER_WORD = 1;
   static __device__ __forceinline__ float up(type v) { return v; }
   static __device__ __forceinline__ type down(float v) { return v; }
 };
 
+// a run of V elements as it lies in memory: one element, or 16 bytes
 template <typename E, int V>
-struct alignas(sizeof(typename E::type) * V) Pack {
-  typename E::type v[V];
+struct Run {
+  uint4 w;
+  __device__ __forceinline__ void load(const typename E::type* p) { w = __ldcs(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void store(typename E::type* p) const { __stcs(reinterpret_cast<uint4*>(p), w); }
+  __device__ __forceinline__ void get(float (&f)[V]) const {
+    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (E::PER_WORD == 2)
+        E::up2(v[i], f[2 * i], f[2 * i + 1]);
+      else
+        f[i] = __uint_as_float(v[i]);
+    }
+  }
+  __device__ __forceinline__ void set(const float (&f)[V]) {
+    uint32_t v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (E::PER_WORD == 2)
+        v[i] = E::down2(f[2 * i], f[2 * i + 1]);
+      else
+        v[i] = __float_as_uint(f[i]);
+    }
+    w = make_uint4(v[0], v[1], v[2], v[3]);
+  }
+};
+template <typename E>
+struct Run<E, 1> {
+  typename E::type w;
+  __device__ __forceinline__ void load(const typename E::type* p) { w = *p; }
+  __device__ __forceinline__ void store(typename E::type* p) const { *p = w; }
+  __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = E::up(w); }
+  __device__ __forceinline__ void set(const float (&f)[1]) { w = E::down(f[0]); }
 };
 
 struct RopeArgs {
@@ -69,21 +128,24 @@ struct RopeArgs {
   unsigned int* status;
   long long xt, xh, yt, yh;  // strides, in elements
   int T, H, D, R, start, max_pos, inverse;
-  int npair;   // items that rotate V pairs of a head
-  int ncopy;   // items that copy 2 V untouched elements of a head (0 in place)
+  int npair;   // items of a head that rotate V pairs
+  int ncopy;   // items that copy 2 V untouched elements (0 in place)
   int groups;  // threads share a token's heads: each takes heads g, g + groups, ...
   int tpb;     // tokens per block (>= 1)
 };
 
-// One thread: V pairs (or 2 V untouched elements) of up to HPT heads of one
-// token, so that the cos/sin it loads serve all of them and 2 HPT loads are
-// in flight. V is 16 bytes' worth of elements where sizes, offsets and
-// addresses allow, else 1.
+// One thread: two runs of V elements of up to HPT heads of one token, so that
+// the cos/sin it loads serve all of them and 2 HPT loads are in flight. The
+// runs are V consecutive elements of the rotated part and those half the part
+// further on (the partners in the half layout; pairs of their own in the
+// interleaved one), or of the untouched part and those half of it further on:
+// neighbouring threads read neighbouring runs either way. V is 16 bytes' worth
+// of elements where sizes, offsets and addresses allow; otherwise a run is one
+// pair's element (V = 1).
 template <typename E, int V, int HPT, bool INTERLEAVED>
 __global__ void __launch_bounds__(256) rope_kernel(RopeArgs a) {
   pdl_wait();
   pdl_trigger();
-  using P = Pack<E, V>;
   using El = typename E::type;
   const int items = a.npair + a.ncopy;
   const int per = items * a.groups;
@@ -99,22 +161,24 @@ __global__ void __launch_bounds__(256) rope_kernel(RopeArgs a) {
   }
   const El* x = static_cast<const El*>(a.x) + t * a.xt;
   El* y = static_cast<El*>(a.y) + t * a.yt;
-  int e0, e1;  // the item's two runs of V elements
+  int e0, e1;  // where the runs begin
   float c[V], s[V];
   const bool rot = item < a.npair;
   if (rot) {
-    const float2* tab = a.table + static_cast<long long>(pos) * (a.R >> 1) + item * V;
+    const float2* tab = a.table + static_cast<long long>(pos) * (a.R >> 1);
     if constexpr (V >= 2) {
+      // interleaved: V / 2 pairs of the first run, then V / 2 of the second
 #pragma unroll
       for (int i = 0; i < V; i += 2) {
-        const float4 w = __ldg(reinterpret_cast<const float4*>(tab + i));
+        const int pair = INTERLEAVED ? (i < V / 2 ? 0 : (a.R >> 2) - V / 2) + item * (V / 2) + i : item * V + i;
+        const float4 w = __ldg(reinterpret_cast<const float4*>(tab + pair));
         c[i] = w.x;
         s[i] = w.y;
         c[i + 1] = w.z;
         s[i + 1] = w.w;
       }
     } else {
-      const float2 w = __ldg(tab);
+      const float2 w = __ldg(tab + item);
       c[0] = w.x;
       s[0] = w.y;
     }
@@ -122,22 +186,22 @@ __global__ void __launch_bounds__(256) rope_kernel(RopeArgs a) {
 #pragma unroll
       for (int i = 0; i < V; ++i) s[i] = -s[i];
     }
-    e0 = a.start + (INTERLEAVED ? 2 : 1) * item * V;
-    e1 = INTERLEAVED ? e0 + V : e0 + (a.R >> 1);
+    e0 = a.start + (INTERLEAVED && V == 1 ? 2 * item : item * V);
+    e1 = INTERLEAVED && V == 1 ? e0 + 1 : e0 + (a.R >> 1);
   } else {
-    e0 = (item - a.npair) * 2 * V;
-    e1 = e0 + V;
+    e0 = (item - a.npair) * V;
+    e1 = e0 + a.ncopy * V;
     if (e0 >= a.start) e0 += a.R;
     if (e1 >= a.start) e1 += a.R;
   }
   for (int h0 = g; h0 < a.H; h0 += a.groups * HPT) {
-    P p0[HPT], p1[HPT];
+    Run<E, V> r0[HPT], r1[HPT];
 #pragma unroll
     for (int j = 0; j < HPT; ++j) {
       const int h = h0 + j * a.groups;
       if (h < a.H) {
-        if (e0 < a.D) p0[j] = *reinterpret_cast<const P*>(x + h * a.xh + e0);
-        if (e1 < a.D) p1[j] = *reinterpret_cast<const P*>(x + h * a.xh + e1);
+        r0[j].load(x + h * a.xh + e0);
+        if (e1 < a.D) r1[j].load(x + h * a.xh + e1);
       }
     }
 #pragma unroll
@@ -145,18 +209,23 @@ __global__ void __launch_bounds__(256) rope_kernel(RopeArgs a) {
       const int h = h0 + j * a.groups;
       if (h >= a.H) continue;
       if (rot) {
+        float f0[V], f1[V];
+        r0[j].get(f0);
+        r1[j].get(f1);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          // interleaved: the two runs hold 2 V consecutive elements, pair i at 2 i
-          El& ea = INTERLEAVED ? (2 * i < V ? p0[j] : p1[j]).v[(2 * i) % V] : p0[j].v[i];
-          El& eb = INTERLEAVED ? (2 * i + 1 < V ? p0[j] : p1[j]).v[(2 * i + 1) % V] : p1[j].v[i];
-          const float u = E::up(ea), w = E::up(eb);
-          ea = E::down(__fsub_rn(__fmul_rn(u, c[i]), __fmul_rn(w, s[i])));
-          eb = E::down(__fadd_rn(__fmul_rn(w, c[i]), __fmul_rn(u, s[i])));
+          // pair i: element i of both runs, or two neighbours of one
+          float& ea = INTERLEAVED && V > 1 ? (2 * i < V ? f0 : f1)[(2 * i) % V] : f0[i];
+          float& eb = INTERLEAVED && V > 1 ? (2 * i < V ? f0 : f1)[(2 * i + 1) % V] : f1[i];
+          const float u = ea, w = eb;
+          ea = __fsub_rn(__fmul_rn(u, c[i]), __fmul_rn(w, s[i]));
+          eb = __fadd_rn(__fmul_rn(w, c[i]), __fmul_rn(u, s[i]));
         }
+        r0[j].set(f0);
+        r1[j].set(f1);
       }
-      if (e0 < a.D) *reinterpret_cast<P*>(y + h * a.yh + e0) = p0[j];
-      if (e1 < a.D) *reinterpret_cast<P*>(y + h * a.yh + e1) = p1[j];
+      r0[j].store(y + h * a.yh + e0);
+      if (e1 < a.D) r1[j].store(y + h * a.yh + e1);
     }
   }
 }
