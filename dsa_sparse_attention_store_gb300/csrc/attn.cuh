@@ -1114,29 +1114,27 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
         mine = at;
         mine_round = rnd;
         if constexpr (C::SPARSE && FMT == DSA_FMT_BF16) {
-          // by TMA, four rows of 64 dimensions an instruction: 16 lanes have
-          // four rows each. A key that is not there is a row outside the cache.
+          // by TMA, four rows of 64 dimensions an instruction. A key that is not
+          // there is a row outside the cache. A warp's lanes issue theirs one
+          // after another (75 cycles each), so both warps of the pair do: half
+          // of the dimensions each, or half of the rows.
           const int y0 = k0 < 0 ? -1 : (((k0 >> 6) * a.kv_heads + s.h) * 2 + v) * kTile + (k0 & 63);
           const int y1 = k1 < 0 ? -1 : (((k1 >> 6) * a.kv_heads + s.h) * 2 + v) * kTile + (k1 & 63);
+          constexpr int LANES = 8 * C::NBLK;  // a warp's instructions
+          const int q = C::NBLK == 2 ? lane & 15 : (lw & 1) * 8 + (lane & 7);  // four rows
+          const int c = C::NBLK == 2 ? lw & 1 : 0;                             // 64 dimensions
           int y[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const int r = 4 * (lane & 15) + j;
+            const int r = 4 * q + j;
             const int p0 = __shfl_sync(0xffffffffu, y0, r & 31), p1 = __shfl_sync(0xffffffffu, y1, r & 31);
             y[j] = r < 32 ? p0 : p1;
           }
           run = acquire(at, rnd);
-          if (run && (lw & 1) == 0) {
-            if (lane == 0) mbar_arrive_expect_tx(&sh.full[at], C::SLOT);
-            __syncwarp();
-            if (lane < 16) {
-#pragma unroll
-              for (int c = 0; c < C::NBLK; ++c)
-                tma_gather4(tiles + at * C::SLOT + c * (kTile * 128) + lane * 512, &tm, c * 64, y[0], y[1], y[2], y[3], &sh.full[at]);
-            }
-          } else if (run && lane == 0) {
-            mbar_arrive(&sh.full[at]);
-          }
+          if (run && lane == 0) mbar_arrive_expect_tx(&sh.full[at], C::SLOT / 2);
+          __syncwarp();
+          if (run && lane < LANES)
+            tma_gather4(tiles + at * C::SLOT + c * (kTile * 128) + q * 512, &tm, c * 64, y[0], y[1], y[2], y[3], &sh.full[at]);
           if (run && last && lane == 0) mbar_arrive(&sh.vdone[seg % kRing]);
           __syncwarp();
         } else if constexpr (C::SPARSE) {

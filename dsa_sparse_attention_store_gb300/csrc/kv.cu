@@ -61,6 +61,13 @@ __device__ __forceinline__ int find_page(const KvArgs& a, int t, int& off, bool 
   return page;
 }
 
+// the larger one; NaN if either is
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
 // 8 fp32 values of a row -> the cache (codes at dst for this lane, the block's
 // scale); every lane of the warp calls it, `ok` says whether the row is written
 template <int FMT>
@@ -74,9 +81,10 @@ __device__ __forceinline__ void put_row(const float (&v)[8], bool ok, uint8_t* c
     }
     if (ok) *reinterpret_cast<uint4*>(codes + 16 * l) = make_uint4(w[0], w[1], w[2], w[3]);
   } else {
-    uint32_t amax = 0;  // as bits: above any finite value where a NaN or infinity is among them
+    float top = fabsf(v[0]);  // a NaN stays one
 #pragma unroll
-    for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+    for (int i = 1; i < 8; ++i) top = max_nan(top, fabsf(v[i]));
+    uint32_t amax = __float_as_uint(top) & 0x7FFFFFFFu;  // as bits: above any finite value for NaN and infinity
     amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
     amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
     const bool bad = amax >= 0x7F800000u;
@@ -84,7 +92,11 @@ __device__ __forceinline__ void put_row(const float (&v)[8], bool ok, uint8_t* c
     const float inv = bad ? 0.f : __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
     float x[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = bad ? 0.f : __fmul_rn(v[i], inv);
+    for (int i = 0; i < 8; ++i) x[i] = __fmul_rn(v[i], inv);
+    if (bad) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = 0.f;
+    }
     if constexpr (FMT == DSA_FMT_FP8) {
       uint32_t w[2];
 #pragma unroll
