@@ -94,6 +94,10 @@ struct Cfg {
   static constexpr int COPIES = FORM == kTreeFew || FORM == kSparseFew ? 4 : 1;  // of a row
   static constexpr int ROWS = 128 * WG / COPIES;       // rows of a unit
   static constexpr int SBUF = FORM == kWide ? 2 : 1;   // score buffers
+  // the next tile's scores are computed before this tile's second product:
+  // where they have a buffer of their own, or the weights are not over them
+  static constexpr bool AHEAD = SBUF == 2 || COPIES > 1;
+  static constexpr int PBUF = AHEAD ? 2 : 1;           // buffers of weights
   static constexpr int THREADS = 128 * WG + 128 + (FORM == kWide ? 64 : 0);
   static constexpr int CTAS = FORM == kWide ? 1 : 2;   // per SM
   static constexpr int NBLK = D / 64;
@@ -110,7 +114,7 @@ struct Cfg {
                             : FORM == kWide ? (!RAW ? 10 : FMT == DSA_FMT_FP8 ? 7 : 8)
                                             : (!RAW ? 6 : 4);
   static constexpr int QBYTES = FORM == kWide ? ROWS * D * 2 : 0;
-  static constexpr int PBYTES = COPIES > 1 ? ROWS * 128 : 0;  // weights, where they meet in shared memory
+  static constexpr int PBYTES = COPIES > 1 ? PBUF * ROWS * 128 : 0;  // weights, where they meet in shared memory
   // TMEM columns of a group, and of the CTA (two CTAs share the SM's 512)
   static constexpr uint32_t O = 0, S = D, Q = D + 64 * SBUF, STRIDE = 256, TMEM = 256 * WG;
 };
@@ -398,6 +402,8 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
       mbar_init(&sh.vdone[i], 2);
       sh.bad[i] = 0;
     }
+    mbar_init(&sh.fin[0], 1);
+    mbar_init(&sh.fin[1], 1);
     for (int i = 0; i < C::WG; ++i) {
       mbar_init(&sh.s_full[i][0], 1);
       mbar_init(&sh.s_full[i][1], 1);
@@ -406,7 +412,6 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
       mbar_init(&sh.q_ready[i], 4);
       mbar_init(&sh.o_full[i][0], 1);
       mbar_init(&sh.o_full[i][1], 1);
-      mbar_init(&sh.fin[i], 1);
     }
     sh.abort = 0;
     fence_mbar_init();
@@ -447,50 +452,56 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
   constexpr uint32_t kIdescPv = idesc_f16(128, D, true) | kIdescBMn;
   const uint64_t kdesc = sw128_desc(smem_u32(tiles)), vdesc = sw128_mn_desc(smem_u32(tiles), kTile * 128), pdesc = sw128_desc(smem_u32(smem));
   const uint64_t qdesc0 = sw128_desc(smem_u32(qsm));
-  // The products. Called by a whole warp; the operands come from lane 0, so
-  // that the compiler keeps them in uniform registers (issuing a tile's took
-  // 1100 cycles without, most of it moving operands; 700 with)
-  auto scores = [&](int wg, int at, int buf) {
-    const uint32_t tb = __shfl_sync(0xffffffffu, sh.tmem + wg * C::STRIDE, 0);
-    const uint64_t qdesc = qdesc0 + __shfl_sync(0xffffffffu, wg, 0) * ((128 * D * 2) >> 4);
-    const uint64_t k = kdesc + __shfl_sync(0xffffffffu, at, 0) * (C::SLOT >> 4);
-    const uint32_t d = tb + C::S + __shfl_sync(0xffffffffu, buf, 0) * 64;
-    if (!elect_one()) return;
+  // The products, called by a whole warp. Their operands are broadcast from
+  // lane 0, so that the compiler keeps them in uniform registers (issuing a
+  // tile's took 1100 cycles without, most of it moving operands).
+  auto uniform = [](auto x) { return __shfl_sync(0xffffffffu, x, 0); };
+  auto scores_of = [&](int at) { return uniform(kdesc + at * (C::SLOT >> 4)); };
+  auto values_of = [&](int at) { return uniform(vdesc + at * (C::SLOT >> 4)); };
+  auto issue_scores = [&](uint32_t tb, uint64_t q, uint64_t k, int at, int wg, int buf) {
+    const uint32_t d = tb + C::S + buf * 64;
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {
       const uint64_t b = k + (((i / 4) * (kTile * 128) + (i % 4) * 32) >> 4);
       if constexpr (FORM == kWide)
-        tc_mma_f16(d, qdesc + (((i / 4) * (128 * 128) + (i % 4) * 32) >> 4), b, kIdescQk, i > 0);
+        tc_mma_f16(d, q + (((i / 4) * (128 * 128) + (i % 4) * 32) >> 4), b, kIdescQk, i > 0);
       else
         tc_mma_f16_ta(d, tb + C::Q + 8 * i, b, kIdescQk, i > 0);
     }
     tc_commit(&sh.empty[at]);
     tc_commit(&sh.s_full[wg][buf]);
   };
-  auto values = [&](int wg, int at, int buf, bool first) {
-    const uint32_t tb = __shfl_sync(0xffffffffu, sh.tmem + wg * C::STRIDE, 0);
-    const uint64_t v = vdesc + __shfl_sync(0xffffffffu, at, 0) * (C::SLOT >> 4);
-    const uint32_t p = tb + C::S + __shfl_sync(0xffffffffu, buf, 0) * 64;
-    if (!elect_one()) return;
-    if constexpr (C::COPIES > 1) {
+  auto issue_values = [&](uint32_t tb, uint64_t v, int at, int wg, int buf, bool first) {
 #pragma unroll
-      for (int i = 0; i < kTile / 16; ++i)
-        tc_mma_f16(tb + C::O, pdesc + 2 * i, v + ((i * 2048) >> 4), kIdescPv, !first || i > 0);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kTile / 16; ++i)
-        tc_mma_f16_ta(tb + C::O, p + 8 * i, v + ((i * 2048) >> 4), kIdescPv, !first || i > 0);
+    for (int i = 0; i < kTile / 16; ++i) {
+      if constexpr (C::COPIES > 1)
+        tc_mma_f16(tb + C::O, pdesc + buf * (C::ROWS * 128 >> 4) + 2 * i, v + ((i * 2048) >> 4), kIdescPv, !first || i > 0);
+      else
+        tc_mma_f16_ta(tb + C::O, tb + C::S + buf * 64 + 8 * i, v + ((i * 2048) >> 4), kIdescPv, !first || i > 0);
     }
     tc_commit(&sh.empty[at]);
     tc_commit(&sh.o_full[wg][buf]);
   };
-
+  auto scores = [&](int wg, int at, int buf) {
+    const uint32_t tb = uniform(sh.tmem + wg * C::STRIDE);
+    const uint64_t q = uniform(qdesc0 + wg * ((128 * D * 2) >> 4)), k = scores_of(at);
+    const int ub = uniform(buf);
+    if (elect_one()) issue_scores(tb, q, k, at, wg, ub);
+    __syncwarp();
+  };
+  auto values = [&](int wg, int at, int buf, bool first) {
+    const uint32_t tb = uniform(sh.tmem + wg * C::STRIDE);
+    const uint64_t v = values_of(at);
+    const int ub = uniform(buf);
+    if (elect_one()) issue_values(tb, v, at, wg, ub, first);
+    __syncwarp();
+  };
   // products in flight end before their TMEM goes back, after an abort too
-  auto settle_products = [&](int wg) {
+  auto settle_products = [&](int i) {
     __syncwarp();
     if (elect_one()) {
-      tc_commit(&sh.fin[wg]);
-      mbar_wait(&sh.fin[wg], 0);
+      tc_commit(&sh.fin[i]);
+      mbar_wait(&sh.fin[i], 0);
     }
     __syncwarp();
   };
@@ -504,6 +515,10 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
     const uint32_t tb = sh.tmem + wg * C::STRIDE;
     const uint32_t lanes = static_cast<uint32_t>(gw * 32) << 16;
     const uint32_t tO = tb + C::O + lanes;
+    const uint32_t utb = uniform(tb);
+    // the warps that issue products: a warp each for scores and values where the
+    // two are independent, since issuing waits for the tensor cores' queue
+    const bool issues = FORM != kWide && (gw == 0 || (C::AHEAD && gw == 1));
     Iter<C> it(a, sh.start, count);
     Seg s;
     bool more = it.next(s), run = true;
@@ -572,6 +587,8 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
         advance();
       }
     };
+    // the second product of the last tile has completed
+    auto wait_product = [&]() { return wait_warp(&sh.o_full[wg][(ns - 1) & (C::PBUF - 1)], ((ns - 1) / C::PBUF) & 1); };
     // One tile of a unit whose rows have copies: this warp's N of its 64 keys.
     // The running maximum is the same in all copies of a row: where one finds
     // its part's maximum more than 2^8 above it, all take the largest.
@@ -613,9 +630,12 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
             memcpy(&p[i], &w, 4);
           }
           mnew = fmaxf(mx[0], mx[1]) * a.scale2;
+          // this buffer's weights of two tiles ago have been read
+          if (!moved && t > s.t0 + 1) run = wait_warp(&sh.o_full[0][ns & 1], ((ns >> 1) - 1) & 1);
+          uint8_t* const weights = smem + (ns & 1) * (C::ROWS * 128);
 #pragma unroll
           for (int u = 0; u < N / 8; ++u)
-            *reinterpret_cast<uint4*>(smem + row * 128 + (((copy * (N / 8) + u) ^ (row & 7)) << 4)) =
+            *reinterpret_cast<uint4*>(weights + row * 128 + (((copy * (N / 8) + u) ^ (row & 7)) << 4)) =
                 make_uint4(p[4 * u], p[4 * u + 1], p[4 * u + 2], p[4 * u + 3]);
           fence_proxy_async_smem();
         }
@@ -627,9 +647,9 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
           l += l0 + l1;
           return;
         }
-        // some row's maximum moves (or a wait ran out): the products with the
-        // old weights are behind, their place serves for the exchange
-        float* const top = reinterpret_cast<float*>(smem);
+        // some row's maximum moves (or a wait ran out): this tile's weights will
+        // be taken again, their place serves for the exchange
+        float* const top = reinterpret_cast<float*>(smem + (ns & 1) * (C::ROWS * 128));
         top[tid] = mnew;
         run = named_bar_all(1, 128, run);
         if (!run) return;
@@ -641,6 +661,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
         if (t > s.t0) {
           l *= alpha;
           if (copy == 0 && __any_sync(0xffffffffu, up)) {
+            run = wait_product();
             tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < D / 16; ++c) tmem_scale16(tO + 16 * c, alpha);
@@ -651,8 +672,6 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
         moved = true;
       }
     };
-    // the second product of the last tile has completed
-    auto wait_product = [&]() { return wait_warp(&sh.o_full[wg][(ns - 1) & (C::SBUF - 1)], ((ns - 1) / C::SBUF) & 1); };
     if (more && has_rows(wg, s)) start_unit(s);
     while (more && run) {
       if (!has_rows(wg, s)) {  // a unit of at most 128 rows: nothing for the second group
@@ -678,13 +697,26 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
         // V of this tile and the next K, usually long there: looked at while
         // the scores are on their way
         const bool more_scores = t + 1 < s.t1;
-        const int vslot = slot, vround = round;
+        int vslot = slot, vround = round, kslot = slot, kround = round;
         bool there = true;
+        uint64_t ku = 0, vu = 0;
         if constexpr (FORM != kWide) {
           advance();
-          if (gw == 0)
+          if (C::AHEAD && more_scores) {
+            vslot = slot;
+            vround = round;
+          } else {
+            kslot = slot;
+            kround = round;
+          }
+          if (more_scores) advance();
+          if (issues) {
+            ku = scores_of(kslot);
+            vu = values_of(vslot);
+          }
+          if (issues)
             there = __all_sync(0xffffffffu, mbar_try_wait(smem_u32(&sh.full[vslot]), vround) &&
-                                                (!more_scores || mbar_try_wait(smem_u32(&sh.full[slot]), round)));
+                                                (!more_scores || mbar_try_wait(smem_u32(&sh.full[kslot]), kround)));
         }
         run = run && wait_warp(&sh.s_full[wg][buf], (ns / C::SBUF) & 1);
         tc_fence_after();
@@ -763,23 +795,28 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
           if (!run) break;
           if (lane == 0) mbar_arrive(&sh.p_ready[wg][buf]);
         } else {
-          if (gw == 0 && run && !there) {
+          if (issues && run && !there) {
             run = wait_warp(&sh.full[vslot], vround);
-            if (run && more_scores) run = wait_warp(&sh.full[slot], round);
+            if (run && more_scores) run = wait_warp(&sh.full[kslot], kround);
           }
           if (C::COPIES == 1) {
             tmem_st_wait();
             tc_fence_before();
           }
           run = named_bar_all(1, 128, run);
-          if (gw == 0 && run) {
+          if (issues && run) {
             tc_fence_after();
-            values(0, vslot, 0, t == s.t0);
-            __syncwarp();
-            if (more_scores) scores(0, slot, 0);
+            if (elect_one()) {
+              if (C::AHEAD) {
+                if (gw == 0 && more_scores) issue_scores(utb, 0, ku, kslot, 0, 0);
+                if (gw == 1) issue_values(utb, vu, vslot, 0, ns & 1, t == s.t0);
+              } else {
+                issue_values(utb, vu, vslot, 0, 0, t == s.t0);
+                if (more_scores) issue_scores(utb, 0, ku, kslot, 0, 0);
+              }
+            }
             __syncwarp();
           }
-          if (more_scores) advance();
           if (!run) break;
         }
       }
@@ -856,7 +893,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
       }
       ++seg;
     }
-    if (FORM != kWide && warp == 0) settle_products(0);
+    if (issues) settle_products(gw);
   } else if (FORM == kWide && warp >= NSW + 4) {
     // ------------------------------------------------------------ products
     const int wg = warp - NSW - 4;
@@ -1084,8 +1121,8 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
       for (int x = 0; run && x < nt; ++x, ++n) {
         const int t = s.t0 + x;
         // the tile's place in the order the products take keys and values:
-        // K0 V0 K1 V1 .., or K0 K1 V0 K2 V1 .. with two score buffers
-        const int order = parts + (C::SBUF == 1 ? 2 * x + v : !v ? (x ? 2 * x - 1 : 0) : x + 1 < nt ? 2 * x + 2 : 2 * nt - 1);
+        // K0 V0 K1 V1 .., or K0 K1 V0 K2 V1 .. with scores ahead
+        const int order = parts + (!C::AHEAD ? 2 * x + v : !v ? (x ? 2 * x - 1 : 0) : x + 1 < nt ? 2 * x + 2 : 2 * nt - 1);
         const int at = order % C::NS, rnd = (order / C::NS) & 1;
         const bool last = v && x + 1 == nt;
         unsigned long long vm;
