@@ -56,7 +56,7 @@ namespace at {
 
 constexpr int kTile = kvf::kPage;  // keys of a tile: a page's, or 64 selected ones
 constexpr int kRing = 16;  // entries of the per-tile and per-segment rings; loaders run at most 9 tiles ahead
-enum Form { kTree = 0, kSparse = 1, kWide = 2, kTreeFew = 3, kSparseFew = 4 };
+enum Form { kTree = 0, kSparse = 1, kWide = 2 };
 
 struct AttnArgs {
   const __nv_bfloat16* q;
@@ -89,15 +89,10 @@ struct Start {
 
 template <int FMT, int D, int FORM>
 struct Cfg {
-  static constexpr bool SPARSE = FORM == kSparse || FORM == kSparseFew;
+  static constexpr bool SPARSE = FORM == kSparse;
   static constexpr int WG = FORM == kWide ? 2 : 1;     // groups of four softmax warps
-  static constexpr int COPIES = FORM == kTreeFew || FORM == kSparseFew ? 4 : 1;  // of a row
-  static constexpr int ROWS = 128 * WG / COPIES;       // rows of a unit
+  static constexpr int ROWS = 128 * WG;                // rows of a unit
   static constexpr int SBUF = FORM == kWide ? 2 : 1;   // score buffers
-  // the next tile's scores are computed before this tile's second product:
-  // where they have a buffer of their own, or the weights are not over them
-  static constexpr bool AHEAD = SBUF == 2 || COPIES > 1;
-  static constexpr int PBUF = AHEAD ? 2 : 1;           // buffers of weights
   static constexpr int THREADS = 128 * WG + 128 + (FORM == kWide ? 64 : 0);
   static constexpr int CTAS = FORM == kWide ? 1 : 2;   // per SM
   static constexpr int NBLK = D / 64;
@@ -109,12 +104,11 @@ struct Cfg {
   static constexpr int RAW_SLOT = RAW ? NCH * 64 * 20 + (D == 64 ? 64 * 4 : 0) : 0;  // codes, a scale word per chunk, flags
   // ring depths that fill the shared memory (113 KB or 227 KB a CTA): operand tiles, and tiles of codes
   // on their way of each loader pair
-  static constexpr int P = !RAW ? 3 : FMT == DSA_FMT_FP8 ? 2 : FORM == kWide ? 3 : 4;
+  static constexpr int P = !RAW ? 3 : FMT == DSA_FMT_FP8 ? 2 : 3;
   static constexpr int NS = D == 64 ? (FORM == kWide ? 12 : 8)
                             : FORM == kWide ? (!RAW ? 10 : FMT == DSA_FMT_FP8 ? 7 : 8)
-                                            : (!RAW ? 6 : 4);
+                                            : (!RAW ? 6 : FMT == DSA_FMT_FP8 ? 4 : 5);
   static constexpr int QBYTES = FORM == kWide ? ROWS * D * 2 : 0;
-  static constexpr int PBYTES = COPIES > 1 ? PBUF * ROWS * 128 : 0;  // weights, where they meet in shared memory
   // TMEM columns of a group, and of the CTA (two CTAs share the SM's 512)
   static constexpr uint32_t O = 0, S = D, Q = D + 64 * SBUF, STRIDE = 256, TMEM = 256 * WG;
 };
@@ -136,7 +130,7 @@ struct Shared {
 
 template <class C>
 constexpr int smem_bytes() {
-  return C::PBYTES + C::NS * C::SLOT + C::QBYTES + 2 * C::P * C::RAW_SLOT + static_cast<int>(sizeof(Shared));
+  return C::NS * C::SLOT + C::QBYTES + 2 * C::P * C::RAW_SLOT + static_cast<int>(sizeof(Shared));
 }
 
 // Key tiles of the row tile that starts at row r0 (at least one, so that
@@ -384,9 +378,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
   using L = kvf::Layout<FMT, D>;
   constexpr int NSW = 4 * C::WG;  // softmax warps
   extern __shared__ __align__(1024) uint8_t smem[];
-  // (products that read the weights there run on into the tiles, for rows that do not exist)
-  uint8_t* const tiles = smem + C::PBYTES;
-  uint8_t* const qsm = tiles + C::NS * C::SLOT;
+  uint8_t* const qsm = smem + C::NS * C::SLOT;
   uint8_t* const raw = qsm + C::QBYTES;
   Shared& sh = *reinterpret_cast<Shared*>(raw + 2 * C::P * C::RAW_SLOT);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -450,7 +442,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
 
   constexpr uint32_t kIdescQk = idesc_f16(128, kTile, true);
   constexpr uint32_t kIdescPv = idesc_f16(128, D, true) | kIdescBMn;
-  const uint64_t kdesc = sw128_desc(smem_u32(tiles)), vdesc = sw128_mn_desc(smem_u32(tiles), kTile * 128), pdesc = sw128_desc(smem_u32(smem));
+  const uint64_t kdesc = sw128_desc(smem_u32(smem)), vdesc = sw128_mn_desc(smem_u32(smem), kTile * 128);
   const uint64_t qdesc0 = sw128_desc(smem_u32(qsm));
   // The products, called by a whole warp. Their operands are broadcast from
   // lane 0, so that the compiler keeps them in uniform registers (issuing a
@@ -473,12 +465,8 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
   };
   auto issue_values = [&](uint32_t tb, uint64_t v, int at, int wg, int buf, bool first) {
 #pragma unroll
-    for (int i = 0; i < kTile / 16; ++i) {
-      if constexpr (C::COPIES > 1)
-        tc_mma_f16(tb + C::O, pdesc + buf * (C::ROWS * 128 >> 4) + 2 * i, v + ((i * 2048) >> 4), kIdescPv, !first || i > 0);
-      else
-        tc_mma_f16_ta(tb + C::O, tb + C::S + buf * 64 + 8 * i, v + ((i * 2048) >> 4), kIdescPv, !first || i > 0);
-    }
+    for (int i = 0; i < kTile / 16; ++i)
+      tc_mma_f16_ta(tb + C::O, tb + C::S + buf * 64 + 8 * i, v + ((i * 2048) >> 4), kIdescPv, !first || i > 0);
     tc_commit(&sh.empty[at]);
     tc_commit(&sh.o_full[wg][buf]);
   };
@@ -516,9 +504,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
     const uint32_t lanes = static_cast<uint32_t>(gw * 32) << 16;
     const uint32_t tO = tb + C::O + lanes;
     const uint32_t utb = uniform(tb);
-    // the warps that issue products: a warp each for scores and values where the
-    // two are independent, since issuing waits for the tensor cores' queue
-    const bool issues = FORM != kWide && (gw == 0 || (C::AHEAD && gw == 1));
+    const bool issues = FORM != kWide && gw == 0;  // this warp issues the products
     Iter<C> it(a, sh.start, count);
     Seg s;
     bool more = it.next(s), run = true;
@@ -527,27 +513,33 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
     // what the join has to know of this CTA, see join_kernel
     int* const meta = reinterpret_cast<int*>(a.meta + 2 * cta);
     if (tid == 0) a.meta[2 * cta] = make_int4(0, 0, 0, 0);
-    // Units of few rows hold each of them four times: a warp takes its copy's
-    // quarter of a tile's scores, and the weights meet in shared memory as the
-    // A operand of the second product. (One warp with all 64 keys of 32 rows
-    // would be most of a tile's time.)
-    const int row = C::COPIES > 1 ? lane : tid, copy = C::COPIES > 1 ? warp : 0;
-    auto query = [&](const Seg& g, int row) {
-      const int r = g.r0 + row;
-      return a.q + static_cast<long long>(g.q0 + r / a.G) * a.qt + static_cast<long long>(g.h * a.G + r % a.G) * a.qh;
+    const int row = tid;  // of the unit
+    // a row's query (in its sequence; 0 of a selection, whose rows are one token's) and head of the group
+    struct Row {
+      int q, g;
+    };
+    auto row_at = [&](const Seg& g) -> Row {
+      if (C::SPARSE) return Row{0, row};
+      const int r = g.r0 + row, q = r / a.G;
+      return Row{q, r - q * a.G};
+    };
+    auto query = [&](const Seg& g, Row r) {
+      return a.q + static_cast<long long>(g.q0 + r.q) * a.qt + static_cast<long long>(g.h * a.G + r.g) * a.qh;
     };
     // the next unit's queries on their way to L1
     auto warm = [&](const Seg& g) {
       if (row < g.rows) {
-        const __nv_bfloat16* q = query(g, row);
+        const __nv_bfloat16* q = query(g, row_at(g));
 #pragma unroll
         for (int i = 0; i < C::NBLK; ++i) touch(q + 64 * i);
       }
     };
+    Row at_row = {0, 0};
     // the unit's queries, then its first tiles' scores
     auto start_unit = [&](const Seg& g) {
       const bool valid = row < g.rows;
-      const uint4* src = reinterpret_cast<const uint4*>(valid ? query(g, row) : a.q);
+      at_row = row_at(g);
+      const uint4* src = reinterpret_cast<const uint4*>(valid ? query(g, at_row) : a.q);
       if constexpr (FORM == kWide) {
         uint8_t* dst = qsm + wg * (128 * D * 2) + (row & 127) * 128;
 #pragma unroll
@@ -588,90 +580,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
       }
     };
     // the second product of the last tile has completed
-    auto wait_product = [&]() { return wait_warp(&sh.o_full[wg][(ns - 1) & (C::PBUF - 1)], ((ns - 1) / C::PBUF) & 1); };
-    // One tile of a unit whose rows have copies: this warp's N of its 64 keys.
-    // The running maximum is the same in all copies of a row: where one finds
-    // its part's maximum more than 2^8 above it, all take the largest.
-    auto spread = [&](auto n_, unsigned long long see, int t, uint32_t tS, bool valid, int qi, const Seg& s, float& m, float& l) {
-      constexpr int N = decltype(n_)::value;
-      const int p0 = t * kTile;
-      const unsigned long long sc = pack2(a.scale2, a.scale2);
-      uint32_t x[N];
-      bool moved = false;
-      while (true) {
-        float mnew = -INFINITY;
-        unsigned long long sum[2] = {0ull, 0ull};
-        if (run) {
-          if (!moved) {
-            tmem_ld_n(tS + copy * N, x);
-            if (!C::SPARSE && valid && p0 + kTile > s.full) see &= row_mask(a, s, qi, p0);
-            const uint32_t bits = static_cast<uint32_t>(see >> (copy * N));
-            tmem_ld_wait_n(x);
-            if (!__all_sync(0xffffffffu, see == ~0ull)) {
-#pragma unroll
-              for (int i = 0; i < N; ++i)
-                if (!((bits >> i) & 1)) x[i] = 0xFF800000u;
-            }
-          }
-          const float sub = m == -INFINITY ? 0.f : m;
-          const unsigned long long sb = pack2(-sub, -sub);
-          float mx[2] = {-INFINITY, -INFINITY};
-          uint32_t p[N / 2];
-#pragma unroll
-          for (int i = 0; i < N / 2; ++i) {
-            const float s0 = __uint_as_float(x[2 * i]), s1 = __uint_as_float(x[2 * i + 1]);
-            mx[i & 1] = fmaxf(mx[i & 1], fmaxf(s0, s1));
-            float e0, e1;
-            unpack2(fma2(pack2(s0, s1), sc, sb), e0, e1);
-            e0 = ex2(e0);
-            e1 = ex2(e1);
-            sum[i & 1] = add2(sum[i & 1], pack2(e0, e1));
-            const __nv_bfloat162 w = __floats2bfloat162_rn(e0, e1);
-            memcpy(&p[i], &w, 4);
-          }
-          mnew = fmaxf(mx[0], mx[1]) * a.scale2;
-          // this buffer's weights of two tiles ago have been read
-          if (!moved && t > s.t0 + 1) run = wait_warp(&sh.o_full[0][ns & 1], ((ns >> 1) - 1) & 1);
-          uint8_t* const weights = smem + (ns & 1) * (C::ROWS * 128);
-#pragma unroll
-          for (int u = 0; u < N / 8; ++u)
-            *reinterpret_cast<uint4*>(weights + row * 128 + (((copy * (N / 8) + u) ^ (row & 7)) << 4)) =
-                make_uint4(p[4 * u], p[4 * u + 1], p[4 * u + 2], p[4 * u + 3]);
-          fence_proxy_async_smem();
-        }
-        const bool grow = !moved && (mnew > m + 8.f || (m == -INFINITY && mnew > m));
-        tc_fence_before();
-        if (named_bar_all(1, 128, run && !grow)) {
-          float l0, l1;
-          unpack2(add2(sum[0], sum[1]), l0, l1);
-          l += l0 + l1;
-          return;
-        }
-        // some row's maximum moves (or a wait ran out): this tile's weights will
-        // be taken again, their place serves for the exchange
-        float* const top = reinterpret_cast<float*>(smem + (ns & 1) * (C::ROWS * 128));
-        top[tid] = mnew;
-        run = named_bar_all(1, 128, run);
-        if (!run) return;
-#pragma unroll
-        for (int c = 0; c < C::COPIES; ++c) mnew = fmaxf(mnew, top[c * C::ROWS + row]);
-        run = named_bar_all(1, 128, run);
-        const bool up = mnew > m + 8.f || (m == -INFINITY && mnew > m);
-        const float alpha = up ? ex2(m - mnew) : 1.f;
-        if (t > s.t0) {
-          l *= alpha;
-          if (copy == 0 && __any_sync(0xffffffffu, up)) {
-            run = wait_product();
-            tc_fence_after();
-#pragma unroll 1
-            for (int c = 0; c < D / 16; ++c) tmem_scale16(tO + 16 * c, alpha);
-            tmem_st_wait();
-          }
-        }
-        if (up) m = mnew;
-        moved = true;
-      }
-    };
+    auto wait_product = [&]() { return wait_warp(&sh.o_full[wg][(ns - 1) & (C::SBUF - 1)], ((ns - 1) / C::SBUF) & 1); };
     if (more && has_rows(wg, s)) start_unit(s);
     while (more && run) {
       if (!has_rows(wg, s)) {  // a unit of at most 128 rows: nothing for the second group
@@ -688,7 +597,8 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
       }
       const bool active = row - lane < s.rows;  // some row of this warp is real
       const bool valid = row < s.rows;
-      const int qi = (s.r0 + row) / a.G;       // the row's query in its sequence
+      const Row mine = at_row;
+      const int qi = mine.q;                   // the row's query in its sequence
       float m = -INFINITY, l = 0.f;
       for (int t = s.t0; t < s.t1; ++t, ++n, ++ns) {
         run = run && wait_warp(&sh.mfull[n % kRing], (n / kRing) & 1);
@@ -697,33 +607,23 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
         // V of this tile and the next K, usually long there: looked at while
         // the scores are on their way
         const bool more_scores = t + 1 < s.t1;
-        int vslot = slot, vround = round, kslot = slot, kround = round;
+        const int vslot = slot, vround = round;
         bool there = true;
         uint64_t ku = 0, vu = 0;
         if constexpr (FORM != kWide) {
           advance();
-          if (C::AHEAD && more_scores) {
-            vslot = slot;
-            vround = round;
-          } else {
-            kslot = slot;
-            kround = round;
-          }
-          if (more_scores) advance();
           if (issues) {
-            ku = scores_of(kslot);
+            ku = scores_of(slot);
             vu = values_of(vslot);
           }
           if (issues)
             there = __all_sync(0xffffffffu, mbar_try_wait(smem_u32(&sh.full[vslot]), vround) &&
-                                                (!more_scores || mbar_try_wait(smem_u32(&sh.full[kslot]), kround)));
+                                                (!more_scores || mbar_try_wait(smem_u32(&sh.full[slot]), round)));
         }
         run = run && wait_warp(&sh.s_full[wg][buf], (ns / C::SBUF) & 1);
         tc_fence_after();
         const uint32_t tS = tb + C::S + 64 * buf + lanes;
-        if constexpr (C::COPIES > 1) {
-          spread(std::integral_constant<int, kTile / C::COPIES>(), see, t, tS, valid, qi, s, m, l);
-        } else if (active && run) {
+        if (active && run) {
           const int p0 = t * kTile;
           if (!C::SPARSE && valid && p0 + kTile > s.full) see &= row_mask(a, s, qi, p0);
           const bool some = !__all_sync(0xffffffffu, see == ~0ull);  // a key that some row does not see
@@ -797,26 +697,20 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
         } else {
           if (issues && run && !there) {
             run = wait_warp(&sh.full[vslot], vround);
-            if (run && more_scores) run = wait_warp(&sh.full[kslot], kround);
+            if (run && more_scores) run = wait_warp(&sh.full[slot], round);
           }
-          if (C::COPIES == 1) {
-            tmem_st_wait();
-            tc_fence_before();
-          }
+          tmem_st_wait();
+          tc_fence_before();
           run = named_bar_all(1, 128, run);
           if (issues && run) {
             tc_fence_after();
             if (elect_one()) {
-              if (C::AHEAD) {
-                if (gw == 0 && more_scores) issue_scores(utb, 0, ku, kslot, 0, 0);
-                if (gw == 1) issue_values(utb, vu, vslot, 0, ns & 1, t == s.t0);
-              } else {
-                issue_values(utb, vu, vslot, 0, 0, t == s.t0);
-                if (more_scores) issue_scores(utb, 0, ku, kslot, 0, 0);
-              }
+              issue_values(utb, vu, vslot, 0, 0, t == s.t0);
+              if (more_scores) issue_scores(utb, 0, ku, slot, 0, 0);
             }
             __syncwarp();
           }
+          if (more_scores) advance();
           if (!run) break;
         }
       }
@@ -838,21 +732,11 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
         meta[3] = done.rows;
         a.meta[2 * cta + 1] = make_int4(done.r0, done.q0, done.h, 0);
       }
-      if constexpr (C::COPIES > 1) {
-        // the copies' sums of weights, each over its part of the keys
-        float* const sums = reinterpret_cast<float*>(smem);
-        sums[tid] = l;
-        run = named_bar_all(1, 128, run);
-        l = 0.f;
-        for (int c = 0; c < C::COPIES; ++c) l += sums[c * C::ROWS + row];
-        run = named_bar_all(1, 128, run);
-      }
-      if (active && copy == 0 && run) {
+      if (active && run) {
         if (!C::SPARSE && *static_cast<volatile int*>(&sh.bad[seg % kRing]) == seg + 1)
           fix_nonfinite<FMT, D>(a, done, max(done.t0, done.full / kTile), done.t1, qi, valid, tO);
-        const int r = done.r0 + row;
-        const long long tok = done.q0 + r / a.G;
-        const int head = done.h * a.G + r % a.G;
+        const long long tok = done.q0 + mine.q;
+        const int head = done.h * a.G + mine.g;
         const int piece = 2 * cta + (first ? 1 : 0);
         const float inv = l > 0.f ? 1.f / l : 0.f;
         __nv_bfloat16* dst = a.out + tok * a.ot + head * a.oh;
@@ -969,7 +853,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
     // the segment
     auto hand_over = [&](int info) {
       const int at = info & 15, seg = info >> 8;
-      uint8_t* const tile = tiles + at * C::SLOT;
+      uint8_t* const tile = smem + at * C::SLOT;
       bool found = false;
       if constexpr (C::RAW) {
         const uint8_t* src = ring + (sent % C::P) * C::RAW_SLOT;
@@ -1065,7 +949,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
           cp_async4(dsc + i * 256, head + scale_at + ((off * L::SB) & ~3), ok);
           if (D == 64) odd |= (off & 1) << i;
         } else {
-          cp_async16(smem_u32(place(tiles + at * C::SLOT, i, chunk)), head + code_at + off * L::CB + code_off, ok);
+          cp_async16(smem_u32(place(smem + at * C::SLOT, i, chunk)), head + code_at + off * L::CB + code_off, ok);
         }
       }
       if constexpr (C::RAW && D == 64) reinterpret_cast<uint32_t*>(to + NCH * 64 * 20)[ti] = odd;
@@ -1121,8 +1005,8 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
       for (int x = 0; run && x < nt; ++x, ++n) {
         const int t = s.t0 + x;
         // the tile's place in the order the products take keys and values:
-        // K0 V0 K1 V1 .., or K0 K1 V0 K2 V1 .. with scores ahead
-        const int order = parts + (!C::AHEAD ? 2 * x + v : !v ? (x ? 2 * x - 1 : 0) : x + 1 < nt ? 2 * x + 2 : 2 * nt - 1);
+        // K0 V0 K1 V1 .., or K0 K1 V0 K2 V1 .. with two score buffers
+        const int order = parts + (C::SBUF == 1 ? 2 * x + v : !v ? (x ? 2 * x - 1 : 0) : x + 1 < nt ? 2 * x + 2 : 2 * nt - 1);
         const int at = order % C::NS, rnd = (order / C::NS) & 1;
         const bool last = v && x + 1 == nt;
         unsigned long long vm;
@@ -1171,7 +1055,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
           if (run && lane == 0) mbar_arrive_expect_tx(&sh.full[at], C::SLOT / 2);
           __syncwarp();
           if (run && lane < LANES)
-            tma_gather4(tiles + at * C::SLOT + c * (kTile * 128) + q * 512, &tm, c * 64, y[0], y[1], y[2], y[3], &sh.full[at]);
+            tma_gather4(smem + at * C::SLOT + c * (kTile * 128) + q * 512, &tm, c * 64, y[0], y[1], y[2], y[3], &sh.full[at]);
           if (run && last && lane == 0) mbar_arrive(&sh.vdone[seg % kRing]);
           __syncwarp();
         } else if constexpr (C::SPARSE) {
@@ -1199,7 +1083,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
                 const int y = ((page * a.kv_heads + s.h) * 2 + v) * kTile;
 #pragma unroll
                 for (int c = 0; c < C::NBLK; ++c)
-                  tma_load_2d(tiles + at * C::SLOT + c * (kTile * 128), &tm, c * 64, y, &sh.full[at]);
+                  tma_load_2d(smem + at * C::SLOT + c * (kTile * 128), &tm, c * 64, y, &sh.full[at]);
               }
               if (last) mbar_arrive(&sh.vdone[seg % kRing]);
             }
@@ -1247,7 +1131,7 @@ dsa_status run_one(dsa_ctx* ctx, const CUtensorMap& tm, const AttnArgs& a, int g
   auto kern = attn_kernel<FMT, D, FORM>;
   constexpr int bytes = smem_bytes<C>();
   static_assert(bytes * C::CTAS <= 233472 - 1024 * C::CTAS, "shared memory of an SM");
-  const uint64_t bit = 1ull << ((FMT * 2 + (D == 128)) * 5 + FORM);  // once a context and kernel
+  const uint64_t bit = 1ull << ((FMT * 2 + (D == 128)) * 3 + FORM);  // once a context and kernel
   if (!(ctx->attn_ready & bit)) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return DSA_ERR_CUDA;
     ctx->attn_ready |= bit;
@@ -1261,9 +1145,7 @@ dsa_status run_dim(dsa_ctx* ctx, int form, const CUtensorMap& tm, const AttnArgs
   switch (form) {
     case kTree: return run_one<FMT, D, kTree>(ctx, tm, a, grid, stream);
     case kSparse: return run_one<FMT, D, kSparse>(ctx, tm, a, grid, stream);
-    case kWide: return run_one<FMT, D, kWide>(ctx, tm, a, grid, stream);
-    case kTreeFew: return run_one<FMT, D, kTreeFew>(ctx, tm, a, grid, stream);
-    default: return run_one<FMT, D, kSparseFew>(ctx, tm, a, grid, stream);
+    default: return run_one<FMT, D, kWide>(ctx, tm, a, grid, stream);
   }
 }
 
