@@ -863,7 +863,8 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
 #pragma unroll
         for (int i0 = 0; i0 < NCH; i0 += BATCH) {
           uint32_t w[BATCH][32 / CPB];
-          kvf::Factor<C::RAW ? FMT : DSA_FMT_FP8> f[BATCH];
+          using F = kvf::Factor<C::RAW ? FMT : DSA_FMT_FP8>;
+          uint32_t byte[BATCH];
           bool two = false;
 #pragma unroll
           for (int b = 0; b < BATCH; ++b) {
@@ -871,13 +872,15 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
             const uint4 c4 = reinterpret_cast<const uint4*>(src)[i * 64 + ti];
             const uint32_t sw = reinterpret_cast<const uint32_t*>(src + NCH * 64 * 16)[i * 64 + ti];
             const uint32_t c[4] = {c4.x, c4.y, c4.z, c4.w};
-            f[b].set((sw >> (8 * (scale_off + (D == 64 ? 2 * ((odd >> i) & 1) : 0)))) & 0xFFu);
-            two |= f[b].two;
-            kvf::widen(c, f[b], w[b]);
+            byte[b] = (sw >> (8 * (scale_off + (D == 64 ? 2 * ((odd >> i) & 1) : 0)))) & 0xFFu;
+            F f;
+            f.set(byte[b]);
+            kvf::widen(c, f, w[b]);
+            two |= F::two(byte[b]);
           }
           if (two) {
 #pragma unroll
-            for (int b = 0; b < BATCH; ++b) f[b].rest(w[b]);
+            for (int b = 0; b < BATCH; ++b) F::rest(byte[b], w[b]);
           }
           if (info & 16) {
 #pragma unroll
@@ -966,32 +969,45 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
       const uint8_t* const heads = a.cache + static_cast<long long>(s.h) * L::HEAD_BYTES;
       const int npg = (s.len + kTile - 1) / kTile, nt = s.t1 - s.t0;
       // A selection's keys go through three steps, a tile apart, so that no
-      // load is waited for: the entry, its page, its cache slot. This lane has
-      // keys `lane` and `lane + 32` of a tile.
-      int e0 = -1, e1 = -1, g0 = -1, g1 = -1, u0 = -1, u1 = -1;  // entries; positions whose pages are on their way; pages
-      auto entry = [&](int t, int j) -> int {  // a position (or cache slot) or -1
+      // load is waited for: the entry, its page, its row in the cache. This
+      // lane has keys `lane` and `lane + 32` of a tile.
+      int e0 = -1, e1 = -1, g0 = -1, g1 = -1, u0 = -1, u1 = -1;  // entries; those whose pages are on their way; pages
+      const int ksel = (a.k + kTile - 1) / kTile;                // tiles of the selection; drafted tokens follow
+      const int32_t* const sel = C::SPARSE ? a.sel + static_cast<long long>(s.q0) * a.k : nullptr;
+      auto entry = [&](int t, int j) -> int {  // a position (or cache slot) or negative
         int x = t * kTile + j;
-        if (t >= s.t1 || s.len == 0) return -1;
-        if (x < a.k) return a.sel[static_cast<long long>(s.q0) * a.k + x];
-        x -= (a.k + kTile - 1) / kTile * kTile;
-        if (x < 0 || !a.mask || x >= s.nd || (x >> 5) >= a.mask_words) return -1;
+        if (t >= s.t1) return -1;
+        if (t < ksel) return x < a.k ? sel[x] : -1;
+        x -= ksel * kTile;
+        if (x >= s.nd || (x >> 5) >= a.mask_words) return -1;
         return (a.mask[static_cast<long long>(s.q0) * a.mask_words + (x >> 5)] >> (x & 31)) & 1 ? s.len - s.nd + x : -1;
       };
-      // the page of tile t's entry e; -2 where e is out of range
-      auto page_of = [&](int e, int t) -> int {
-        if (e < 0) return -1;
-        const bool slot = a.slots && t * kTile < a.k;  // the drafted tokens that follow are positions
-        if (slot ? e < a.num_pages * 64 : e < s.len) return slot ? e >> 6 : table[e >> 6];
-        atomicOr(a.status, DSA_DEV_BOUNDS);
-        return -2;
-      };
-      auto slot_of = [&](int e, int page) -> int {
-        if (e < 0 || page == -2) return -1;
-        if (page < 0 || page >= a.num_pages) {
-          atomicOr(a.status, DSA_DEV_BOUNDS);
-          return -1;
+      // the page of tile t's entry e, as the table (or the slot) has it; e becomes negative where there is none
+      auto page_of = [&](int& e, int t) -> int {
+        const bool slot = a.slots && t < ksel;  // drafted tokens are positions
+        const int limit = s.len == 0 ? 0 : slot ? a.num_pages * kTile : s.len;
+        if (e >= limit) {
+          if (limit > 0) atomicOr(a.status, DSA_DEV_BOUNDS);
+          e = -1;
         }
-        return page * 64 + (e & 63);
+        return e < 0 ? -1 : slot ? e >> 6 : table[e >> 6];
+      };
+      // the row: in bf16 its number in the cache as rows of D elements, -1
+      // where there is no key; else where the page's part of this head begins,
+      // which leaves room for the row's place in it, 0 where there is none
+      constexpr bool GATHER = C::SPARSE && FMT == DSA_FMT_BF16;
+      using RowId = std::conditional_t<GATHER, int, unsigned long long>;
+      constexpr RowId NONE = GATHER ? static_cast<RowId>(-1) : static_cast<RowId>(0);
+      auto row_of = [&](int e, int page) -> RowId {
+        if (e < 0) return NONE;
+        if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.num_pages)) {
+          atomicOr(a.status, DSA_DEV_BOUNDS);
+          return NONE;
+        }
+        if constexpr (GATHER)
+          return ((page * a.kv_heads + s.h) * 2 + v) * kTile + (e & 63);
+        else
+          return reinterpret_cast<unsigned long long>(heads + static_cast<uint64_t>(page) * page_step) | (e & 63);
       };
       int pg = -1;  // page ids of 32 tiles
       if (C::SPARSE) {
@@ -1010,17 +1026,18 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
         const int at = order % C::NS, rnd = (order / C::NS) & 1;
         const bool last = v && x + 1 == nt;
         unsigned long long vm;
-        int page = -1, k0 = -1, k1 = -1;
+        int page = -1;
+        RowId k0 = NONE, k1 = NONE;
         if constexpr (C::SPARSE) {
-          k0 = slot_of(g0, u0);
-          k1 = slot_of(g1, u1);
+          k0 = row_of(g0, u0);
+          k1 = row_of(g1, u1);
           g0 = e0;
           g1 = e1;
           u0 = page_of(g0, t + 1);
           u1 = page_of(g1, t + 1);
           e0 = entry(t + 2, lane);
           e1 = entry(t + 2, lane + 32);
-          vm = __ballot_sync(0xffffffffu, k0 >= 0) | (static_cast<unsigned long long>(__ballot_sync(0xffffffffu, k1 >= 0)) << 32);
+          vm = __ballot_sync(0xffffffffu, k0 != NONE) | (static_cast<unsigned long long>(__ballot_sync(0xffffffffu, k1 != NONE)) << 32);
         } else {
           if ((x & 31) == 0) pg = t + lane < min(s.t1, npg) ? table[t + lane] : -1;
           page = __shfl_sync(0xffffffffu, pg, x & 31);
@@ -1034,13 +1051,11 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
         }
         mine = at;
         mine_round = rnd;
-        if constexpr (C::SPARSE && FMT == DSA_FMT_BF16) {
+        if constexpr (GATHER) {
           // by TMA, four rows of 64 dimensions an instruction. A key that is not
           // there is a row outside the cache. A warp's lanes issue theirs one
           // after another (75 cycles each), so both warps of the pair do: half
           // of the dimensions each, or half of the rows.
-          const int y0 = k0 < 0 ? -1 : (((k0 >> 6) * a.kv_heads + s.h) * 2 + v) * kTile + (k0 & 63);
-          const int y1 = k1 < 0 ? -1 : (((k1 >> 6) * a.kv_heads + s.h) * 2 + v) * kTile + (k1 & 63);
           constexpr int LANES = 8 * C::NBLK;  // a warp's instructions
           const int q = C::NBLK == 2 ? lane & 15 : (lw & 1) * 8 + (lane & 7);  // four rows
           const int c = C::NBLK == 2 ? lw & 1 : 0;                             // 64 dimensions
@@ -1048,7 +1063,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int r = 4 * q + j;
-            const int p0 = __shfl_sync(0xffffffffu, y0, r & 31), p1 = __shfl_sync(0xffffffffu, y1, r & 31);
+            const int p0 = __shfl_sync(0xffffffffu, k0, r & 31), p1 = __shfl_sync(0xffffffffu, k1, r & 31);
             y[j] = r < 32 ? p0 : p1;
           }
           run = acquire(at, rnd);
@@ -1061,12 +1076,11 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
         } else if constexpr (C::SPARSE) {
           run = ask(
               [&](int i, bool& ok, int& off) {
-                const int r = row0 + i * RSTEP;
-                const int p0 = __shfl_sync(0xffffffffu, k0, r & 31), p1 = __shfl_sync(0xffffffffu, k1, r & 31);
-                const int p = r < 32 ? p0 : p1;
-                ok = p >= 0;
-                off = ok ? p & 63 : 0;
-                return heads + static_cast<uint64_t>(ok ? static_cast<uint32_t>(p) >> 6 : 0u) * page_step;
+                // row0 < RSTEP: which of the lane's two keys is known here
+                const unsigned long long k = __shfl_sync(0xffffffffu, i * RSTEP < 32 ? k0 : k1, (row0 + i * RSTEP) & 31);
+                ok = k != 0;
+                off = static_cast<int>(k & 63);
+                return ok ? reinterpret_cast<const uint8_t*>(k - off) : a.cache;
               },
               at, rnd, false, last, seg);
         } else {

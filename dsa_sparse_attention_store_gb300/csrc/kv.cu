@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(128) kv_load_kernel(KvArgs a) {
       Factor<FMT> f;
       f.set(sc[j]);
       widen(c[j], f, w);
-      f.rest(w);
+      f.rest(sc[j], w);
     }
     __nv_bfloat16* out = (j & 1 ? a.vo + t * a.vt + h * a.vh : a.ko + t * a.kt + h * a.kh) + 8 * l;
     // a token that has no page reads as zeros

@@ -65,43 +65,42 @@ template <int FMT>
 struct Factor {
   static constexpr int BIAS = FMT == DSA_FMT_FP8 ? 120 : 126;
   static constexpr uint32_t ONE = 254 - BIAS;  // the largest scale byte one factor covers
-  uint32_t f, g;  // bf16x2 factors; g only where `two`
-  bool two;       // scales above 2^7 (fp8) or 2 (fp4), and NaN: rare
-  __device__ __forceinline__ void set(uint32_t byte) {
-    two = byte > ONE;
-    const uint32_t f1 = min(byte, ONE) + BIAS, g1 = byte + 127 - ONE;  // g: what is left of the exponent
-    f = (f1 << 7) | (f1 << 23);
-    g = byte == 255u ? 0x7FFF7FFFu : (g1 << 7) | (g1 << 23);
-  }
+  uint32_t f;  // bf16x2 factor
+  __device__ __forceinline__ void set(uint32_t byte) { f = (min(byte, ONE) + BIAS) * 0x00800080u; }
+  // scales above 2^7 (fp8) or 2 (fp4), and NaN, take a second factor: rare
+  static __device__ __forceinline__ bool two(uint32_t byte) { return byte > ONE; }
   template <int N>
-  __device__ __forceinline__ void apply(uint32_t (&r)[N]) const {
-#pragma unroll
-    for (int i = 0; i < N; ++i) r[i] = mul_bf16x2(r[i], f);
-  }
-  // the second factor, for the codes of a scale that takes two
-  template <int N>
-  __device__ __forceinline__ void rest(uint32_t (&r)[N]) const {
-    if (two) {
+  static __device__ __forceinline__ void rest(uint32_t byte, uint32_t (&r)[N]) {
+    if (two(byte)) {
+      const uint32_t g = byte == 255u ? 0x7FFF7FFFu : (byte + 127 - ONE) * 0x00800080u;
 #pragma unroll
       for (int i = 0; i < N; ++i) r[i] = mul_bf16x2(r[i], g);
     }
   }
 };
 
-// N words of four e4m3 codes -> bf16 pairs, up to the second factor
+// two bytes of w, each sign-extended to 16 bits: selectors 8 | i stand for
+// eight copies of byte i's sign
+__device__ __forceinline__ uint32_t sext2(uint32_t w, uint32_t sel) {
+  uint32_t d;
+  asm("prmt.b32 %0, %1, %1, %2;" : "=r"(d) : "r"(w), "r"(sel));
+  return d;
+}
+
+// N words of four e4m3 codes -> bf16 pairs, up to the second factor. A code
+// sign-extended to 16 bits and shifted by 4 has its sign, exponent and
+// mantissa where bf16 has them; the bits between are cleared.
 template <int N>
 __device__ __forceinline__ void widen(const uint32_t (&w)[N], const Factor<DSA_FMT_FP8>& s, uint32_t (&o)[2 * N]) {
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const uint32_t a = __byte_perm(w[i], 0, 0x1404), b = __byte_perm(w[i], 0, 0x3424);  // codes in the high bytes
-    o[2 * i] = (a & 0x80008000u) | ((a >> 4) & 0x07F007F0u);
-    o[2 * i + 1] = (b & 0x80008000u) | ((b >> 4) & 0x07F007F0u);
+    o[2 * i] = mul_bf16x2((sext2(w[i], 0x9180) << 4) & 0x87F087F0u, s.f);
+    o[2 * i + 1] = mul_bf16x2((sext2(w[i], 0xB3A2) << 4) & 0x87F087F0u, s.f);
   }
-  s.apply(o);
 }
 
 // N words of eight e2m1 codes (the even dimension in the low nibble) -> bf16
-// pairs, up to the second factor
+// pairs, up to the second factor.
 template <int N>
 __device__ __forceinline__ void widen(const uint32_t (&w)[N], const Factor<DSA_FMT_FP4>& s, uint32_t (&o)[4 * N]) {
 #pragma unroll
@@ -110,9 +109,8 @@ __device__ __forceinline__ void widen(const uint32_t (&w)[N], const Factor<DSA_F
     for (int j = 0; j < 4; ++j) {
       const uint32_t b = w[i] >> (8 * j);
       const uint32_t t = (b & 0xFu) | ((b & 0xF0u) << 12);  // codes in the low nibbles of both halves
-      o[4 * i + j] = ((t & 0x00080008u) << 12) | ((t & 0x00070007u) << 6);
+      o[4 * i + j] = mul_bf16x2(((t & 0x00080008u) << 12) | ((t & 0x00070007u) << 6), s.f);
     }
-  s.apply(o);
 }
 
 // bf16 pairs: what is not finite becomes zero; whether anything did
