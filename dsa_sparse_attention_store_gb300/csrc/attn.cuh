@@ -444,12 +444,9 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
   constexpr uint32_t kIdescPv = idesc_f16(128, D, true) | kIdescBMn;
   const uint64_t kdesc = sw128_desc(smem_u32(smem)), vdesc = sw128_mn_desc(smem_u32(smem), kTile * 128);
   const uint64_t qdesc0 = sw128_desc(smem_u32(qsm));
-  // The products, called by a whole warp. Their operands are broadcast from
-  // lane 0, so that the compiler keeps them in uniform registers (issuing a
-  // tile's took 1100 cycles without, most of it moving operands).
-  auto uniform = [](auto x) { return __shfl_sync(0xffffffffu, x, 0); };
-  auto scores_of = [&](int at) { return uniform(kdesc + at * (C::SLOT >> 4)); };
-  auto values_of = [&](int at) { return uniform(vdesc + at * (C::SLOT >> 4)); };
+  // The products. One thread issues them (elect_one: the compiler then keeps
+  // the operands in uniform registers; issuing a tile's took 1100 cycles
+  // without, most of it moving operands).
   auto issue_scores = [&](uint32_t tb, uint64_t q, uint64_t k, int at, int wg, int buf) {
     const uint32_t d = tb + C::S + buf * 64;
 #pragma unroll
@@ -471,17 +468,11 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
     tc_commit(&sh.o_full[wg][buf]);
   };
   auto scores = [&](int wg, int at, int buf) {
-    const uint32_t tb = uniform(sh.tmem + wg * C::STRIDE);
-    const uint64_t q = uniform(qdesc0 + wg * ((128 * D * 2) >> 4)), k = scores_of(at);
-    const int ub = uniform(buf);
-    if (elect_one()) issue_scores(tb, q, k, at, wg, ub);
+    if (elect_one()) issue_scores(sh.tmem + wg * C::STRIDE, qdesc0 + wg * ((128 * D * 2) >> 4), kdesc + at * (C::SLOT >> 4), at, wg, buf);
     __syncwarp();
   };
   auto values = [&](int wg, int at, int buf, bool first) {
-    const uint32_t tb = uniform(sh.tmem + wg * C::STRIDE);
-    const uint64_t v = values_of(at);
-    const int ub = uniform(buf);
-    if (elect_one()) issue_values(tb, v, at, wg, ub, first);
+    if (elect_one()) issue_values(sh.tmem + wg * C::STRIDE, vdesc + at * (C::SLOT >> 4), at, wg, buf, first);
     __syncwarp();
   };
   // products in flight end before their TMEM goes back, after an abort too
@@ -503,13 +494,14 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
     const uint32_t tb = sh.tmem + wg * C::STRIDE;
     const uint32_t lanes = static_cast<uint32_t>(gw * 32) << 16;
     const uint32_t tO = tb + C::O + lanes;
-    const uint32_t utb = uniform(tb);
     const bool issues = FORM != kWide && gw == 0;  // this warp issues the products
     Iter<C> it(a, sh.start, count);
     Seg s;
     bool more = it.next(s), run = true;
     int seg = 0, n = 0;   // segments, tiles
     int ns = 0;           // tiles this group has worked on: score buffers and accumulator phases
+    bool known = false;   // whether `ahead` holds the next tile's visible keys
+    unsigned long long ahead = 0;
     // what the join has to know of this CTA, see join_kernel
     int* const meta = reinterpret_cast<int*>(a.meta + 2 * cta);
     if (tid == 0) a.meta[2 * cta] = make_int4(0, 0, 0, 0);
@@ -585,6 +577,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
     while (more && run) {
       if (!has_rows(wg, s)) {  // a unit of at most 128 rows: nothing for the second group
         n += s.t1 - s.t0;
+        known = false;
         ++seg;
         more = it.next(s);
         if (more && has_rows(wg, s)) start_unit(s);
@@ -601,25 +594,13 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
       const int qi = mine.q;                   // the row's query in its sequence
       float m = -INFINITY, l = 0.f;
       for (int t = s.t0; t < s.t1; ++t, ++n, ++ns) {
-        run = run && wait_warp(&sh.mfull[n % kRing], (n / kRing) & 1);
-        unsigned long long see = sh.vmask[n % kRing];
-        const int buf = ns & (C::SBUF - 1);
-        // V of this tile and the next K, usually long there: looked at while
-        // the scores are on their way
-        const bool more_scores = t + 1 < s.t1;
-        const int vslot = slot, vround = round;
-        bool there = true;
-        uint64_t ku = 0, vu = 0;
-        if constexpr (FORM != kWide) {
-          advance();
-          if (issues) {
-            ku = scores_of(slot);
-            vu = values_of(vslot);
-          }
-          if (issues)
-            there = __all_sync(0xffffffffu, mbar_try_wait(smem_u32(&sh.full[vslot]), vround) &&
-                                                (!more_scores || mbar_try_wait(smem_u32(&sh.full[slot]), round)));
+        if (!known) {
+          run = run && wait_warp(&sh.mfull[n % kRing], (n / kRing) & 1);
+          ahead = sh.vmask[n % kRing];
         }
+        unsigned long long see = ahead;
+        known = false;
+        const int buf = ns & (C::SBUF - 1);
         run = run && wait_warp(&sh.s_full[wg][buf], (ns / C::SBUF) & 1);
         tc_fence_after();
         const uint32_t tS = tb + C::S + 64 * buf + lanes;
@@ -638,6 +619,10 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
             uint32_t x[2][32];
             tmem_ld32(tS, x[0]);
             tmem_ld32(tS + 32, x[1]);
+            if (!known) {  // the next tile's visible keys, while the scores come: usually there by now
+              known = __all_sync(0xffffffffu, mbar_test(smem_u32(&sh.mfull[(n + 1) % kRing]), ((n + 1) / kRing) & 1));
+              if (known) ahead = sh.vmask[(n + 1) % kRing];
+            }
             const float sub = m == -INFINITY ? 0.f : m;
             const unsigned long long sb = pack2(-sub, -sub);
             unsigned long long sum[2] = {0ull, 0ull};  // pairs of fp32 zeros
@@ -695,26 +680,29 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
           if (!run) break;
           if (lane == 0) mbar_arrive(&sh.p_ready[wg][buf]);
         } else {
-          if (issues && run && !there) {
-            run = wait_warp(&sh.full[vslot], vround);
-            if (run && more_scores) run = wait_warp(&sh.full[slot], round);
-          }
+          const bool more_scores = t + 1 < s.t1;
+          const int vslot = slot, vround = round;
+          advance();
+          const bool there = issues && mbar_test(smem_u32(&sh.full[vslot]), vround);
           tmem_st_wait();
           tc_fence_before();
-          run = named_bar_all(1, 128, run);
-          if (issues && run) {
+          run = named_bar_all(1, 128, run);  // the four warps go on, or stop, together
+          if (!run) break;
+          if (issues) {
             tc_fence_after();
             if (elect_one()) {
-              issue_values(utb, vu, vslot, 0, 0, t == s.t0);
-              if (more_scores) issue_scores(utb, 0, ku, slot, 0, 0);
+              run = there || wait(&sh.full[vslot], vround);
+              if (run) issue_values(tb, vdesc + vslot * (C::SLOT >> 4), vslot, 0, 0, t == s.t0);
+              if (run && more_scores) {
+                run = wait(&sh.full[slot], round);
+                if (run) issue_scores(tb, 0, kdesc + slot * (C::SLOT >> 4), slot, 0, 0);
+              }
             }
-            __syncwarp();
+            run = __all_sync(0xffffffffu, run);  // seen by the other warps at the next barrier
           }
           if (more_scores) advance();
-          if (!run) break;
         }
       }
-      if (!run) break;
       // the next unit's queries go up before this one's sums come down: every
       // product with the old ones has completed (s_full of the last tile)
       const Seg done = s;
@@ -931,7 +919,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
     // an operand tile that copies or TMA will fill; what has landed goes out
     // before this warp waits for one
     auto acquire = [&](int at, int rnd) -> bool {
-      if (__all_sync(0xffffffffu, mbar_try_wait(smem_u32(&sh.empty[at]), rnd ^ 1))) return true;
+      if (__all_sync(0xffffffffu, mbar_test(smem_u32(&sh.empty[at]), rnd ^ 1))) return true;
       hand_over_all();
       return wait_warp(&sh.empty[at], rnd ^ 1);
     };
