@@ -105,9 +105,9 @@ struct Cfg {
   // ring depths that fill the shared memory (113 KB or 227 KB a CTA): operand tiles, and tiles of codes
   // on their way of each loader pair
   static constexpr int P = !RAW ? 3 : FMT == DSA_FMT_FP8 ? 2 : 3;
-  static constexpr int NS = D == 64 ? (FORM == kWide ? 12 : 8)
+  static constexpr int NS = D == 64 ? (FORM == kWide || !RAW ? 12 : 10)
                             : FORM == kWide ? (!RAW ? 10 : FMT == DSA_FMT_FP8 ? 7 : 8)
-                                            : (!RAW ? 6 : FMT == DSA_FMT_FP8 ? 4 : 5);
+                                            : (!RAW ? 7 : FMT == DSA_FMT_FP8 ? 4 : 5);
   static constexpr int QBYTES = FORM == kWide ? ROWS * D * 2 : 0;
   // TMEM columns of a group, and of the CTA (two CTAs share the SM's 512)
   static constexpr uint32_t O = 0, S = D, Q = D + 64 * SBUF, STRIDE = 256, TMEM = 256 * WG;
@@ -619,7 +619,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
             uint32_t x[2][32];
             tmem_ld32(tS, x[0]);
             tmem_ld32(tS + 32, x[1]);
-            if (!known) {  // the next tile's visible keys, while the scores come: usually there by now
+            if (FORM != kWide && !known) {  // the next tile's visible keys, while the scores come: usually there by now
               known = __all_sync(0xffffffffu, mbar_test(smem_u32(&sh.mfull[(n + 1) % kRing]), ((n + 1) / kRing) & 1));
               if (known) ahead = sh.vmask[(n + 1) % kRing];
             }
