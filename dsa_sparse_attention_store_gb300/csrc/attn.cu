@@ -195,7 +195,11 @@ dsa_status launch_attn(dsa_ctx* ctx, const dsa_attn_args& p, const int32_t* sel,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return DSA_ERR_CUDA;
   }
-  // the wide form where the sequences' rows fill more than one 128-row unit on average
+  // the wide form where the sequences' rows fill more than one 128-row unit on
+  // average: 16 sequences of 4509 to 10498 tokens, 8 kv heads, bf16 (fp8), take
+  // with 128 rows 112.7 (143.9) us in the wide form and 115.9 (116.3) in the
+  // other, with 160 rows 128.2 (163.3) and 170.6 (190.9), with 512 248.0 (317.9)
+  // and 325.3 (369.1)
   const bool wide = static_cast<long long>(p.Tq) * a.G > 128LL * p.B;
   const int form = sel ? kSparse : wide ? kWide : kTree;
   const int grid = form == kWide ? ctx->num_sms : 2 * ctx->num_sms, rows = form == kWide ? 256 : 128;

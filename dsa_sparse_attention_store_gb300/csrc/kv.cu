@@ -314,9 +314,10 @@ Kern load_of(dsa_fmt fmt) {
 
 dsa_status launch(dsa_ctx* ctx, bool store, int D, dsa_fmt fmt, KvArgs& a, cudaStream_t stream) {
   a.status = ctx->status;
-  // four heads a thread once that still leaves a wave of threads
+  // four heads a thread once there are many: 8 heads of 512 tokens, fp8, written
+  // and read back 5.6 against 4.9 us, of 1024 6.4 against 7.3, of 4509 12.8 against 15.6
   const long long threads = static_cast<long long>(a.T) * a.kv_heads * (D / 8);
-  const bool many = a.kv_heads >= 4 && threads / 4 >= 1024LL * ctx->num_sms;
+  const bool many = a.kv_heads >= 4 && threads >= 768LL * ctx->num_sms;
   a.groups = many ? (a.kv_heads + 3) / 4 : a.kv_heads;
   const long long blocks = (static_cast<long long>(a.T) * a.groups * (D / 8) + 127) / 128;
   if (blocks > 0x7FFFFFFFLL) return DSA_ERR_UNSUPPORTED;

@@ -311,9 +311,10 @@ dsa_status launch_rope(dsa_ctx* ctx, const dsa_rope* rope, const void* x, void* 
   a.npair = a.R / 2 / V;
   a.ncopy = x == y ? 0 : (D - a.R + 2 * V - 1) / (2 * V);
   const int items = a.npair + a.ncopy;
-  // four heads a thread once that still leaves two waves of threads
+  // four heads a thread once there are many: 64 heads of 128 tokens 2.9 against
+  // 2.7 us, of 256 2.8 against 3.5, of 2048 10.0 against 16.1
   const long long threads = static_cast<long long>(T) * H * items;
-  const bool many = threads / 4 >= 2LL * ctx->num_sms * 2048 && H >= 4;
+  const bool many = threads >= 768LL * ctx->num_sms && H >= 4;
   a.groups = many ? (H + 3) / 4 : H;
   const long long per = static_cast<long long>(items) * a.groups;
   if (per > 0x7FFFFFFFLL - 256) return DSA_ERR_UNSUPPORTED;
