@@ -37,7 +37,7 @@ dsa_status check_attn(const dsa_attn_args& p) {
       p.heads % p.kv_heads || !positive(p.scale) || !(static_cast<float>(p.scale * 1.4426950408889634) > 0.f) ||
       !std::isfinite(static_cast<float>(p.scale * 1.4426950408889634)) || (p.mask && p.mask_words <= 0))
     return DSA_ERR_INVALID_ARG;
-  if (static_cast<long long>(p.num_pages) * 64 > 0x7FFFFFFFLL ||
+  if (static_cast<long long>(p.num_pages) * 64 > 0x7FFFFFFFLL || p.kv_heads > 65536 ||
       static_cast<long long>(p.Tq) * p.heads > 0x7FFFFFFFLL || p.B == 0x7FFFFFFF)
     return DSA_ERR_UNSUPPORTED;
   // a bf16 cache is addressed by rows of one head's key or value

@@ -359,8 +359,8 @@ typedef struct {
   size_t ws_bytes;
 } dsa_attn_args;
 
-/* Workspace of both calls: two partial results per CTA, whatever the sizes
- * of the call. 0 for an unsupported head_dim. */
+/* Workspace of both calls: two partial results of up to 256 rows per SM,
+ * whatever the sizes of the call (40 MB for head_dim 128 on 152 SMs). 0 for an unsupported head_dim. */
 size_t dsa_attn_workspace_size(const dsa_ctx* ctx, int32_t head_dim);
 
 /* Attention of drafted tokens over the cache: query i of sequence b sees the
@@ -372,7 +372,10 @@ size_t dsa_attn_workspace_size(const dsa_ctx* ctx, int32_t head_dim);
  * does not reach it, infinities and NaN included. Keys of a page out of range
  * are left out and DSA_ERR_DEVICE_BOUNDS recorded; so are whole sequences
  * whose lengths are inconsistent (their rows are not written).
- * Tq * heads < 2^31. Results do not depend on timing. */
+ * A row all of whose visible scores are -inf counts as one that sees no key.
+ * Tq * heads < 2^31, kv_heads <= 65536, 64 * num_pages < 2^31 and, in bf16,
+ * 128 * num_pages * kv_heads < 2^31, else DSA_ERR_UNSUPPORTED. Results do not
+ * depend on timing. */
 dsa_status dsa_tree_attn(dsa_ctx* ctx, const dsa_attn_args* args, dsa_stream_t stream);
 
 /* Attention over a selection: query row t sees the keys sel[t][0 .. k-1] of

@@ -102,7 +102,8 @@ def test_attention_refuses(L):
 
     for call in (tree, sparse):
         assert call(ctx=None) == 1
-        for kw in (dict(fmt=5), dict(head_dim=96), dict(num_pages=1 << 26), dict(Tq=1 << 29), dict(num_pages=1 << 24, kv_heads=8)):
+        for kw in (dict(fmt=5), dict(head_dim=96), dict(num_pages=1 << 26), dict(Tq=1 << 29), dict(num_pages=1 << 24, kv_heads=8),
+                   dict(kv_heads=1 << 17, heads=1 << 17, fmt=1)):
             assert call(**kw) == 2, kw
         for kw in (dict(Tq=-1), dict(B=0), dict(heads=0), dict(kv_heads=3), dict(kv_heads=0), dict(max_pages=0), dict(num_pages=0),
                    dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")), dict(scale=1e-60), dict(scale=1e300),
