@@ -500,8 +500,6 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
     bool more = it.next(s), run = true;
     int seg = 0, n = 0;   // segments, tiles
     int ns = 0;           // tiles this group has worked on: score buffers and accumulator phases
-    bool known = false;   // whether `ahead` holds the next tile's visible keys
-    unsigned long long ahead = 0;
     // what the join has to know of this CTA, see join_kernel
     int* const meta = reinterpret_cast<int*>(a.meta + 2 * cta);
     if (tid == 0) a.meta[2 * cta] = make_int4(0, 0, 0, 0);
@@ -577,7 +575,6 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
     while (more && run) {
       if (!has_rows(wg, s)) {  // a unit of at most 128 rows: nothing for the second group
         n += s.t1 - s.t0;
-        known = false;
         ++seg;
         more = it.next(s);
         if (more && has_rows(wg, s)) start_unit(s);
@@ -594,12 +591,8 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
       const int qi = mine.q;                   // the row's query in its sequence
       float m = -INFINITY, l = 0.f;
       for (int t = s.t0; t < s.t1; ++t, ++n, ++ns) {
-        if (!known) {
-          run = run && wait_warp(&sh.mfull[n % kRing], (n / kRing) & 1);
-          ahead = sh.vmask[n % kRing];
-        }
-        unsigned long long see = ahead;
-        known = false;
+        run = run && wait_warp(&sh.mfull[n % kRing], (n / kRing) & 1);
+        unsigned long long see = sh.vmask[n % kRing];
         const int buf = ns & (C::SBUF - 1);
         run = run && wait_warp(&sh.s_full[wg][buf], (ns / C::SBUF) & 1);
         tc_fence_after();
@@ -619,10 +612,6 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
             uint32_t x[2][32];
             tmem_ld32(tS, x[0]);
             tmem_ld32(tS + 32, x[1]);
-            if (FORM != kWide && !known) {  // the next tile's visible keys, while the scores come: usually there by now
-              known = __all_sync(0xffffffffu, mbar_test(smem_u32(&sh.mfull[(n + 1) % kRing]), ((n + 1) / kRing) & 1));
-              if (known) ahead = sh.vmask[(n + 1) % kRing];
-            }
             const float sub = m == -INFINITY ? 0.f : m;
             const unsigned long long sb = pack2(-sub, -sub);
             unsigned long long sum[2] = {0ull, 0ull};  // pairs of fp32 zeros
