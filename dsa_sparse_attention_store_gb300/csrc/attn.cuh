@@ -6,8 +6,9 @@
 //   x_j = s_j log2 e,   lse = (m + log2 sum_j 2^(x_j - m)) / log2 e,
 // in one pass over key tiles with a running m and sum. Statistics and the
 // accumulator are fp32; the weights enter the second product as bf16 (its
-// operands share a type, and a weight's relative error of 2^-9 is that of
-// the output's own rounding); their sum is of the unrounded weights.
+// operands share a type, and a weight's relative error of 2^-8 is that of
+// the output's own rounding); their sum is of the unrounded weights. ex2 is
+// the hardware's, within 2^-22.
 //
 // Layout. A unit is one kv head of one sequence and up to 128 or 256 of its
 // rows (tokens x the G query heads that share the kv head), or, over a
@@ -36,15 +37,29 @@
 // values pass through a ring of 64-key tiles in the 128-byte swizzle: K is
 // read K-major, V MN-major.
 //
-// Loaders: in bf16, tiles that every row sees whole come by TMA; other bf16
-// tiles (selections, the tiles where visibility ends) by 16-byte asynchronous
-// copies straight into the swizzle; fp8 and fp4 codes by asynchronous copies
-// into a ring private to each thread, several tiles ahead, from where the
-// thread widens them into the operand tile. Rows of no visible key are zeros
-// there, never what the page holds: a weight of zero times a stale NaN would
-// be NaN. In tiles that only some rows see, values that are not finite are
-// replaced by zeros too and added afterwards to the rows that do see them
-// (fix_nonfinite).
+// Loaders: a pair of warps brings keys, a pair values. In bf16, tiles that
+// every row sees whole come by TMA boxes and selections by TMA gathers of four
+// rows; tiles where visibility ends by 16-byte asynchronous copies straight
+// into the swizzle. fp8 and fp4 codes come by asynchronous copies into a ring
+// private to each thread, two or three tiles ahead, from where the thread
+// widens them into the operand tile. Rows of no visible key are zeros there,
+// never what the page holds: a weight of zero times a stale NaN would be NaN.
+// In tiles that only some rows see, values that are not finite are replaced by
+// zeros too and added afterwards to the rows that do see them (fix_nonfinite).
+//
+// What bounds it, and what it measures (device time of a call, join included,
+// against a copy rate of 6.79 TB/s and 1909 bf16 TFLOP/s):
+//  - one token of 64 sequences of 2048 to 16384, 8 kv heads, G 8, D 128, bf16:
+//    HBM. 380 us, 6.4 TB/s.
+//  - 2048 tokens behind 8192, the same heads: the softmax of 64 keys takes about
+//    2000 cycles of a group beside the products' 1330 (two groups). 505 us,
+//    1220 TFLOP/s.
+//  - 8 tokens of 8 sequences of 131072, 4 kv heads, G 16, fp8: instruction issue
+//    (0.61 a cycle and scheduler), half of it widening codes for 128 rows. 369
+//    us, 3.0 TB/s, 750 TFLOP/s.
+//  - 2048 queries over 512 keys each, 8 kv heads, G 8, bf16: the loaders' time
+//    to issue gathers and a tile's chain (scores, softmax, values) of about 2300
+//    cycles for 8 rows. 610 us, 7.0 TB/s out of L2.
 #pragma once
 #include <type_traits>
 
@@ -55,7 +70,7 @@ namespace dsa {
 namespace at {
 
 constexpr int kTile = kvf::kPage;  // keys of a tile: a page's, or 64 selected ones
-constexpr int kRing = 16;  // entries of the per-tile and per-segment rings; loaders run at most 9 tiles ahead
+constexpr int kRing = 16;  // entries of the per-tile and per-segment rings; loaders run at most 10 tiles ahead
 enum Form { kTree = 0, kSparse = 1, kWide = 2 };
 
 struct AttnArgs {
@@ -107,7 +122,7 @@ struct Cfg {
   static constexpr int P = !RAW ? 3 : FMT == DSA_FMT_FP8 ? 2 : 3;
   static constexpr int NS = D == 64 ? (FORM == kWide || !RAW ? 12 : 10)
                             : FORM == kWide ? (!RAW ? 10 : FMT == DSA_FMT_FP8 ? 7 : 8)
-                                            : (!RAW ? 7 : FMT == DSA_FMT_FP8 ? 4 : 5);
+                                            : (!RAW ? 6 : FMT == DSA_FMT_FP8 ? 4 : 5);
   static constexpr int QBYTES = FORM == kWide ? ROWS * D * 2 : 0;
   // TMEM columns of a group, and of the CTA (two CTAs share the SM's 512)
   static constexpr uint32_t O = 0, S = D, Q = D + 64 * SBUF, STRIDE = 256, TMEM = 256 * WG;
@@ -905,8 +920,12 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
       hand_over(info);
       return true;
     };
-    // an operand tile that copies or TMA will fill; what has landed goes out
-    // before this warp waits for one
+    // An operand tile that copies or TMA will fill; what has landed goes out
+    // before this warp waits for one. The wait looks at one bit of the slot's
+    // round, so it must not come two rounds early: a pair fills every one of
+    // its tiles, in order and at most three places apart, and to fill the last
+    // one it waited until the tile NS places before that was released, with
+    // all tiles before it; so the tile two rounds back in this slot has been.
     auto acquire = [&](int at, int rnd) -> bool {
       if (__all_sync(0xffffffffu, mbar_test(smem_u32(&sh.empty[at]), rnd ^ 1))) return true;
       hand_over_all();

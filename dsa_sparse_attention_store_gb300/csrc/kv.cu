@@ -10,8 +10,10 @@
 // fp32 with every product and sum rounded separately and the rotated value is
 // rounded once, to the cache's format.
 //
-// Bound: HBM for long batches (each value read once, its code written once),
-// the dependent loads for short ones.
+// Bound: for long batches HBM and, when writing fp8 or fp4, the quantising
+// instructions; the dependent loads for short ones. 22528 tokens x 8 heads x
+// 128: written and read back in 64 us bf16 (floor 54), 63 us fp8 (41), 57 us
+// fp4 (34; store 44, load 22 with launch overhead); 64 tokens 3.7 us.
 #include <cuda_fp4.h>
 #include <cuda_fp8.h>
 
