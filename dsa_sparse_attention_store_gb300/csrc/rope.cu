@@ -22,7 +22,6 @@
 
 #include <cmath>
 #include <new>
-#include <vector>
 
 #include "rope.cuh"
 
@@ -242,7 +241,7 @@ cudaError_t launch(const RopeArgs& a, bool interleaved, bool many, dim3 grid, cu
 
 dsa_status rope_create(dsa_ctx* ctx, dsa_rope** out, const dsa_rope_desc& d) {
   const int half = d.rot_dim / 2;
-  std::vector<double> f(half);
+  double f[512];  // rot_dim is at most 1024
   for (int i = 0; i < half; ++i) {
     const double base = std::pow(d.theta, -(2.0 * i) / d.rot_dim);
     double v = base;
@@ -265,7 +264,7 @@ dsa_status rope_create(dsa_ctx* ctx, dsa_rope** out, const dsa_rope_desc& d) {
   const size_t n = static_cast<size_t>(d.max_pos) * half;
   bool ok = cudaMalloc(&r->table, n * sizeof(float2)) == cudaSuccess &&
             cudaMalloc(&df, half * sizeof(double)) == cudaSuccess &&
-            cudaMemcpy(df, f.data(), half * sizeof(double), cudaMemcpyHostToDevice) == cudaSuccess;
+            cudaMemcpy(df, f, half * sizeof(double), cudaMemcpyHostToDevice) == cudaSuccess;
   if (ok) {
     const size_t blocks = (n + 255) / 256;
     rope_table_kernel<<<static_cast<unsigned>(blocks < 4096 ? blocks : 4096), 256>>>(df, half, d.max_pos, d.mscale,
@@ -275,6 +274,7 @@ dsa_status rope_create(dsa_ctx* ctx, dsa_rope** out, const dsa_rope_desc& d) {
   cudaFree(df);
   if (!ok) {
     cudaFree(r->table);
+    cudaGetLastError();  // a table that does not fit leaves no error behind
     delete r;
     return DSA_ERR_CUDA;
   }

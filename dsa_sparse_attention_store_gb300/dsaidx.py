@@ -231,6 +231,11 @@ class Rope:
     def handle(self):
         return self._h
 
+    def _open(self):
+        if self._h is None:
+            raise ValueError("the rotary plan is closed")
+        return self._h
+
     def close(self):
         if getattr(self, "_h", None):
             lib().dsa_rope_destroy(self._h)
@@ -350,7 +355,7 @@ class Context:
         T, H, D = shape
         xp, xt, xh = _rows(x, dt, shape, "x")
         yp, yt, yh = (xp, xt, xh) if out is None else _rows(out, dt, shape, "out")
-        st = lib().dsa_rope_apply(self._h, rope._h, xp, yp, code, _ptr(pos, torch.int32, (T,), "pos"), T, H, D,
+        st = lib().dsa_rope_apply(self._h, rope._open(), xp, yp, code, _ptr(pos, torch.int32, (T,), "pos"), T, H, D,
                                   rot_start, xt, xh, yt, yh, 1 if inverse else 0, _raw_stream(stream))
         if st != 0:
             raise DsaError("dsa_rope_apply", st)
@@ -368,7 +373,7 @@ class Context:
         st = lib().dsa_kv_store(
             self._h, kp, vp, kt, kh, vt, vh, _ptr(cache_pos, i32, (T,), "cache_pos"), _ptr(seq_id, i32, (T,), "seq_id"),
             _ptr(page_table, i32, None, "page_table"), T, B, max_pages, n, D,
-            self._kv_cache(cache, num_pages, n, D, fmt), num_pages, fmt, None if rope is None else rope._h,
+            self._kv_cache(cache, num_pages, n, D, fmt), num_pages, fmt, None if rope is None else rope._open(),
             None if rope_pos is None else _ptr(rope_pos, i32, (T,), "rope_pos"), rot_start, _raw_stream(stream))
         if st != 0:
             raise DsaError("dsa_kv_store", st)

@@ -366,8 +366,8 @@ size_t dsa_attn_workspace_size(const dsa_ctx* ctx, int32_t head_dim);
 /* Attention of drafted tokens over the cache: query i of sequence b sees the
  * whole committed context and the drafted token j of its own sequence where
  * bit j of its mask row is set (usually its ancestors in the tree and
- * itself), or where j <= i without a mask (a chain: a chunk of a prefill; one
- * token: a decode step). out = softmax(scale q.k) v; a row that sees no key
+ * itself; bits past mask_words count as clear), or where j <= i without a
+ * mask (a chain: a chunk of a prefill; one token: a decode step). out = softmax(scale q.k) v; a row that sees no key
  * gives zeros and lse -inf. What the cache holds in places a row does not see
  * does not reach it, infinities and NaN included. Keys of a page out of range
  * are left out and DSA_ERR_DEVICE_BOUNDS recorded; so are whole sequences

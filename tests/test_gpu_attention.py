@@ -481,3 +481,57 @@ def test_cache_past_32_bits(ctx, fmt):
     at = c.table[0, np.arange(302) // 64].astype(np.int64) * 64 + np.arange(302) % 64
     assert np.array_equal(k.double().cpu().numpy(), K[at]) and np.array_equal(v.double().cpu().numpy(), V[at])
     assert ctx.device_status() == 0
+
+
+def test_binding_refusals(ctx):
+    import torch
+    from dsa_sparse_attention_store_gb300 import Rope, dsaidx
+    c = Case(97, [50], [2], 1, 4, 64, A.BF16, k=16)
+    d = c.device()
+    out, lse = c.run(ctx, d=d)
+    ws = torch.empty(ctx.attn_workspace_size(64), dtype=torch.uint8, device="cuda")
+
+    def tree(**kw):
+        a = dict(q=d["q"], cache=d["cache"], num_pages=c.pages, fmt=c.fmt, kv_heads=1, page_table=d["table"],
+                 seq_lens=d["lens"], cu_q=d["cu"], out=out, workspace=ws, mask=d["mask"], lse=lse)
+        a.update(kw)
+        ctx.tree_attn(**a)
+
+    tree()
+    for kw, err in [(dict(q=d["q"].float()), TypeError), (dict(q=d["q"].cpu()), TypeError), (dict(q=d["q"][0]), ValueError),
+                    (dict(out=out[:1]), ValueError), (dict(cache=d["cache"][:-1]), ValueError), (dict(cache=d["cache"].int()), TypeError),
+                    (dict(lse=lse[:, :2]), ValueError), (dict(mask=d["mask"][:1]), ValueError), (dict(mask=d["mask"].long()), TypeError),
+                    (dict(seq_lens=d["lens"].repeat(2)), ValueError), (dict(cu_q=d["cu"][:1]), ValueError), (dict(kv_heads=3), ValueError),
+                    (dict(q=d["q"].transpose(1, 2).contiguous().transpose(1, 2)), ValueError)]:
+        with pytest.raises(err):
+            tree(**kw)
+    for kw, status in [(dict(workspace=ws[:-1]), 6), (dict(workspace=ws[1:]), 1), (dict(kv_heads=3, num_pages=1), 1), (dict(scale=0.0), 1),
+                       (dict(q=torch.zeros((2, 4, 96), dtype=torch.bfloat16, device="cuda"),
+                             out=torch.zeros((2, 4, 96), dtype=torch.bfloat16, device="cuda")), 2)]:
+        with pytest.raises(dsaidx.DsaError) as e:
+            tree(**kw)
+        assert e.value.status == status, kw
+    with pytest.raises(ValueError):
+        ctx.sparse_attn(d["q"], d["sel"][:1], d["cache"], c.pages, c.fmt, 1, d["table"], d["lens"], d["cu"], out, ws)
+    rope = Rope(ctx, rot_dim=64, max_pos=16)
+    rope.close()
+    k = torch.zeros((1, 1, 64), dtype=torch.bfloat16, device="cuda")
+    at = torch.zeros(1, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError):
+        ctx.kv_store(k, k, at, at, d["table"], d["cache"], c.pages, c.fmt, rope=rope)
+    with pytest.raises(ValueError):
+        ctx.rope_apply(k, at, rope)
+    wide = Rope(ctx, rot_dim=64, max_pos=16)
+    with pytest.raises(dsaidx.DsaError) as e:     # the rotated part passes the end of the head
+        ctx.rope_apply(k, at, wide, rot_start=2)
+    assert e.value.status == 1
+    with pytest.raises(dsaidx.DsaError) as e:
+        ctx.kv_store(k, k, at, at, d["table"], d["cache"], c.pages, c.fmt, rope=wide, rot_start=2)
+    assert e.value.status == 1
+    wide.close()
+    with pytest.raises(dsaidx.DsaError) as e:     # a table that does not fit is refused and leaves no error behind
+        Rope(ctx, rot_dim=1024, max_pos=2 ** 31 - 1)
+    assert e.value.status == 3
+    tree()
+    torch.cuda.synchronize()
+    assert ctx.device_status() == 0
