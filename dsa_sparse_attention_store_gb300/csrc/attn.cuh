@@ -116,7 +116,7 @@ struct Cfg {
   static constexpr int CPB = FMT == DSA_FMT_BF16 ? 8 : FMT == DSA_FMT_FP8 ? 4 : 2;
   static constexpr int NCH = NBLK * CPB;
   static constexpr bool RAW = FMT != DSA_FMT_BF16;
-  static constexpr int RAW_SLOT = RAW ? NCH * 64 * 20 + (D == 64 ? 64 * 4 : 0) : 0;  // codes, a scale word per chunk, flags
+  static constexpr int RAW_SLOT = RAW ? NCH * 64 * 16 + 64 * 4 + (D == 64 ? 64 * 4 : 0) : 0;  // codes, a scale word a row, flags
   // ring depths that fill the shared memory (113 KB or 227 KB a CTA): operand tiles, and tiles of codes
   // on their way of each loader pair
   static constexpr int P = !RAW ? 3 : FMT == DSA_FMT_FP8 ? 2 : 3;
@@ -824,6 +824,10 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
     const int row0 = (ti / (8 * C::NBLK)) * RL + (ti / CPB) % RL;
     const int code_off = (blk * CPB + chunk) * 16;
     const int scale_off = (blk * 64 + chunk * (64 / CPB)) / kvf::kBlock;
+    // A warp's chunks are those of 32 rows. A lane brings the scales of one of
+    // them, so that a thread's NCH rows are neighbours in shared memory.
+    const int scale_row = (lw & 1) * (32 / NCH) + lane / NCH + lane % NCH * RSTEP;
+    const int scale_word = (lw & 1) * 32 + row0 % (32 / NCH) * NCH;  // of this thread's first row
     uint8_t* const ring = raw + v * (C::P * C::RAW_SLOT);
     const uint32_t page_step = static_cast<uint32_t>(a.kv_heads) * L::HEAD_BYTES;
     const int32_t code_at = v ? L::V_CODES : L::K_CODES, scale_at = v ? L::V_SCALES : L::K_SCALES;
@@ -849,22 +853,35 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
       bool found = false;
       if constexpr (C::RAW) {
         const uint8_t* src = ring + (sent % C::P) * C::RAW_SLOT;
+        const uint32_t* const scales = reinterpret_cast<const uint32_t*>(src + NCH * 64 * 16);
+        __syncwarp();  // the other lanes' copies: the scales
         [[maybe_unused]] uint32_t odd = 0;
-        if constexpr (D == 64) odd = reinterpret_cast<const uint32_t*>(src + NCH * 64 * 20)[ti];
+        if constexpr (D == 64) odd = scales[64 + ti];
         constexpr int BATCH = NCH < 4 ? NCH : FMT == DSA_FMT_FP8 ? 4 : 2;  // chunks at a time: enough to overlap their latencies
 #pragma unroll
         for (int i0 = 0; i0 < NCH; i0 += BATCH) {
           uint32_t w[BATCH][32 / CPB];
           using F = kvf::Factor<C::RAW ? FMT : DSA_FMT_FP8>;
-          uint32_t byte[BATCH];
+          uint32_t byte[BATCH], sw[BATCH];
           bool two = false;
+          static_assert(BATCH == 4 || BATCH == 2, "scale words of a batch are one load");
+          if constexpr (BATCH == 4) {
+            const uint4 x = *reinterpret_cast<const uint4*>(scales + scale_word + i0);
+            sw[0] = x.x;
+            sw[1] = x.y;
+            sw[2] = x.z;
+            sw[3] = x.w;
+          } else {
+            const uint2 x = *reinterpret_cast<const uint2*>(scales + scale_word + i0);
+            sw[0] = x.x;
+            sw[1] = x.y;
+          }
 #pragma unroll
           for (int b = 0; b < BATCH; ++b) {
             const int i = i0 + b;
             const uint4 c4 = reinterpret_cast<const uint4*>(src)[i * 64 + ti];
-            const uint32_t sw = reinterpret_cast<const uint32_t*>(src + NCH * 64 * 16)[i * 64 + ti];
             const uint32_t c[4] = {c4.x, c4.y, c4.z, c4.w};
-            byte[b] = (sw >> (8 * (scale_off + (D == 64 ? 2 * ((odd >> i) & 1) : 0)))) & 0xFFu;
+            byte[b] = (sw[b] >> (8 * (scale_off + (D == 64 ? 2 * ((odd >> i) & 1) : 0)))) & 0xFFu;
             F f;
             f.set(byte[b]);
             kvf::widen(c, f, w[b]);
@@ -931,27 +948,39 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
       hand_over_all();
       return wait_warp(&sh.empty[at], rnd ^ 1);
     };
-    // ask for a tile: src(i, ok, off) gives where chunk i's row begins, whether
-    // it is there, and the row's place in its page
-    auto ask = [&](auto src, int at, int rnd, bool clean, bool last, int seg) -> bool {
+    // ask for a tile: src(r, half, ok, off) gives where the head's part of row
+    // r's page begins, whether the row is there, and its place in the page (half
+    // of the tile r lies in; 2: not known in the code). whole: that beginning
+    // for all rows of a page of 64 keys, else null.
+    auto ask = [&](auto src, const uint8_t* whole, int at, int rnd, bool clean, bool last, int seg) -> bool {
       if (!C::RAW && !acquire(at, rnd)) return false;
       uint8_t* const to = ring + (issued % C::P) * C::RAW_SLOT;
-      const uint32_t dst = smem_u32(to) + ti * 16, dsc = smem_u32(to) + NCH * 64 * 16 + ti * 4;
+      auto dst = [&](int i) { return C::RAW ? smem_u32(to) + ti * 16 + i * 1024 : smem_u32(place(smem + at * C::SLOT, i, chunk)); };
+      [[maybe_unused]] const uint32_t scale_dst = smem_u32(to) + NCH * 64 * 16 + (ti << 2);
       [[maybe_unused]] uint32_t odd = 0;
+      if (whole) {
+        const uint8_t* const code = whole + (code_at + row0 * L::CB + code_off);
 #pragma unroll
-      for (int i = 0; i < NCH; ++i) {
+        for (int i = 0; i < NCH; ++i) cp_async16(dst(i), code + i * RSTEP * L::CB, true);
+        if constexpr (C::RAW) {
+          cp_async4(scale_dst, whole + (scale_at + ((scale_row * L::SB) & ~3)), true);
+          if (D == 64) odd = row0 & 1 ? ~0u : 0u;
+        }
+      } else {
         bool ok;
         int off;
-        const uint8_t* head = src(i, ok, off);
+#pragma unroll
+        for (int i = 0; i < NCH; ++i) {
+          const uint8_t* head = src(row0 + i * RSTEP, i * RSTEP >= 32, ok, off);  // row0 < RSTEP
+          cp_async16(dst(i), head + code_at + off * L::CB + code_off, ok);
+          if (C::RAW && D == 64) odd |= (off & 1) << i;
+        }
         if constexpr (C::RAW) {
-          cp_async16(dst + i * 1024, head + code_at + off * L::CB + code_off, ok);
-          cp_async4(dsc + i * 256, head + scale_at + ((off * L::SB) & ~3), ok);
-          if (D == 64) odd |= (off & 1) << i;
-        } else {
-          cp_async16(smem_u32(place(smem + at * C::SLOT, i, chunk)), head + code_at + off * L::CB + code_off, ok);
+          const uint8_t* head = src(scale_row, 2, ok, off);
+          cp_async4(scale_dst, head + scale_at + ((off * L::SB) & ~3), ok);
         }
       }
-      if constexpr (C::RAW && D == 64) reinterpret_cast<uint32_t*>(to + NCH * 64 * 20)[ti] = odd;
+      if constexpr (C::RAW && D == 64) reinterpret_cast<uint32_t*>(to + NCH * 64 * 16)[64 + ti] = odd;
       cp_async_commit();
       if (lane == 0) sh.info[lw][issued & 3] = at | (clean ? 16 : 0) | (last ? 32 : 0) | (rnd << 6) | (seg << 8);
       __syncwarp();
@@ -1071,14 +1100,17 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
           __syncwarp();
         } else if constexpr (C::SPARSE) {
           run = ask(
-              [&](int i, bool& ok, int& off) {
-                // row0 < RSTEP: which of the lane's two keys is known here
-                const unsigned long long k = __shfl_sync(0xffffffffu, i * RSTEP < 32 ? k0 : k1, (row0 + i * RSTEP) & 31);
+              [&](int r, int half, bool& ok, int& off) {
+                RowId k = __shfl_sync(0xffffffffu, half == 1 ? k1 : k0, r & 31);
+                if (half == 2) {
+                  const RowId kk = __shfl_sync(0xffffffffu, k1, r & 31);
+                  if (r >= 32) k = kk;
+                }
                 ok = k != 0;
                 off = static_cast<int>(k & 63);
                 return ok ? reinterpret_cast<const uint8_t*>(k - off) : a.cache;
               },
-              at, rnd, false, last, seg);
+              nullptr, at, rnd, false, last, seg);
         } else {
           const bool whole = vm == ~0ull && (t + 1) * kTile <= s.full;  // every row sees every key
           const uint8_t* const head = heads + static_cast<uint64_t>(vm ? static_cast<uint32_t>(page) : 0u) * page_step;
@@ -1101,12 +1133,12 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
             if (run && sent < issued) hand_over_all();  // copies asked for before go out too
           } else {
             run = ask(
-                [&](int i, bool& ok, int& off) {
-                  off = row0 + i * RSTEP;
-                  ok = (vm >> off) & 1;
+                [&](int r, int, bool& ok, int& off) {
+                  off = r;
+                  ok = (vm >> r) & 1;
                   return head;
                 },
-                at, rnd, v && (t + 1) * kTile > s.full, last, seg);
+                vm == ~0ull ? head : nullptr, at, rnd, v && (t + 1) * kTile > s.full, last, seg);
           }
         }
       }

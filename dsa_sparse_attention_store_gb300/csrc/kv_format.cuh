@@ -79,11 +79,11 @@ struct Factor {
   }
 };
 
-// two bytes of w, each sign-extended to 16 bits: selectors 8 | i stand for
-// eight copies of byte i's sign
-__device__ __forceinline__ uint32_t sext2(uint32_t w, uint32_t sel) {
+// two bytes of a and b (0-3 and 4-7), each sign-extended to 16 bits: selectors
+// 8 | i stand for eight copies of byte i's sign
+__device__ __forceinline__ uint32_t sext2(uint32_t a, uint32_t b, uint32_t sel) {
   uint32_t d;
-  asm("prmt.b32 %0, %1, %1, %2;" : "=r"(d) : "r"(w), "r"(sel));
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
   return d;
 }
 
@@ -94,23 +94,23 @@ template <int N>
 __device__ __forceinline__ void widen(const uint32_t (&w)[N], const Factor<DSA_FMT_FP8>& s, uint32_t (&o)[2 * N]) {
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    o[2 * i] = mul_bf16x2((sext2(w[i], 0x9180) << 4) & 0x87F087F0u, s.f);
-    o[2 * i + 1] = mul_bf16x2((sext2(w[i], 0xB3A2) << 4) & 0x87F087F0u, s.f);
+    o[2 * i] = mul_bf16x2((sext2(w[i], w[i], 0x9180) << 4) & 0x87F087F0u, s.f);
+    o[2 * i + 1] = mul_bf16x2((sext2(w[i], w[i], 0xB3A2) << 4) & 0x87F087F0u, s.f);
   }
 }
 
 // N words of eight e2m1 codes (the even dimension in the low nibble) -> bf16
-// pairs, up to the second factor.
+// pairs, up to the second factor. Likewise, with a code in a byte's high
+// nibble: the odd ones as they are, the even ones in the word shifted by 4.
 template <int N>
 __device__ __forceinline__ void widen(const uint32_t (&w)[N], const Factor<DSA_FMT_FP4>& s, uint32_t (&o)[4 * N]) {
 #pragma unroll
-  for (int i = 0; i < N; ++i)
+  for (int i = 0; i < N; ++i) {
+    const uint32_t even = w[i] << 4;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t b = w[i] >> (8 * j);
-      const uint32_t t = (b & 0xFu) | ((b & 0xF0u) << 12);  // codes in the low nibbles of both halves
-      o[4 * i + j] = mul_bf16x2(((t & 0x00080008u) << 12) | ((t & 0x00070007u) << 6), s.f);
-    }
+    for (int j = 0; j < 4; ++j)
+      o[4 * i + j] = mul_bf16x2((sext2(even, w[i], 0xC480 + 0x1111 * j) << 2) & 0x81C081C0u, s.f);
+  }
 }
 
 // bf16 pairs: what is not finite becomes zero; whether anything did
