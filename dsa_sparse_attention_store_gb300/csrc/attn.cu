@@ -201,8 +201,9 @@ dsa_status launch_attn(dsa_ctx* ctx, const dsa_attn_args& p, const int32_t* sel,
   // other, with 160 rows 128.2 (163.3) and 170.6 (190.9), with 512 248.0 (317.9)
   // and 325.3 (369.1)
   const bool wide = static_cast<long long>(p.Tq) * a.G > 128LL * p.B;
-  const int form = sel ? kSparse : wide ? kWide : kTree;
-  const int grid = form == kWide ? ctx->num_sms : 2 * ctx->num_sms, rows = form == kWide ? 256 : 128;
+  const bool few = sel ? a.G <= kFewRows : static_cast<long long>(p.Tq) * a.G <= static_cast<long long>(kFewRows) * p.B;
+  const int form = sel ? (few ? kSparseFew : kSparse) : wide ? kWide : few ? kTreeFew : kTree;
+  const int grid = form == kWide ? ctx->num_sms : 2 * ctx->num_sms, rows = form == kWide ? 256 : few ? kFewRows : 128;
   const auto run = p.fmt == DSA_FMT_BF16 ? run_bf16 : p.fmt == DSA_FMT_FP8 ? run_fp8 : run_fp4;
   const dsa_status st = run(ctx, form, p.head_dim, tm, a, grid, stream);
   if (st != DSA_OK) return st;

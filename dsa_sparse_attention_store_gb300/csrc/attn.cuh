@@ -17,21 +17,23 @@
 // whatever their lengths. A unit that a cut divides leaves partial sums in the
 // workspace and the join kernel adds them in a fixed order.
 //
-// Forms. Rows up to 128 (a decode step, small trees, selections) are bound by
-// reading the cache: two CTAs per SM, so that one's softmax runs under the
-// other's products, and the queries stay in TMEM as the A operand of the first
-// product, which leaves shared memory to the tiles. Rows beyond that (kWide:
-// large trees, chunks of a prefill) are bound by the tensor cores and by what
-// L2 delivers: one CTA per SM with two groups of four softmax warps that share
-// every tile between 256 rows; queries in shared memory, which leaves TMEM for
-// two score buffers, so that the next tile's scores are there when a tile's
-// softmax ends.
+// Forms. Rows up to 128 (small trees, large groups) are bound by reading the
+// cache: two CTAs per SM, so that one's softmax runs under the other's products,
+// and the queries stay in TMEM as the A operand of the first product, which
+// leaves shared memory to the tiles. Rows beyond that (kWide: large trees, chunks
+// of a prefill) are bound by the tensor cores and by what L2 delivers: one CTA
+// per SM with two groups of four softmax warps that share every tile between 256
+// rows; queries in shared memory, which leaves TMEM for two score buffers, so
+// that the next tile's scores are there when a tile's softmax ends. Up to 32 rows
+// (kTreeFew, kSparseFew: a decode step, selections of usual groups) take one
+// softmax warp and 8 KB of queries in shared memory, so two CTAs per SM have two
+// score buffers as well.
 //
-// A CTA: one or two groups of 4 softmax warps (a row per thread and TMEM lane)
-// and 4 loader warps. One thread issues a group's products: of the group's
-// first warp where scores and softmax take turns anyway (a barrier of the four
-// warps is cheaper than a hop to another warp), of a warp of its own in the
-// wide form, because issuing waits for the tensor cores' queue. TMEM columns
+// A CTA: one or two groups of softmax warps (4, or 1 for few rows; a row per
+// thread and TMEM lane) and 4 loader warps. One thread issues a group's products:
+// of the group's first warp where scores and softmax take turns anyway (a barrier
+// of the four warps is cheaper than a hop to another warp), of a warp of its own
+// with two score buffers, because issuing waits for the tensor cores' queue. TMEM columns
 // of a group: accumulator [0, D), then one or two score buffers of 64 with the
 // bf16 weights over them, then the queries where they are in TMEM. Keys and
 // values pass through a ring of 64-key tiles in the 128-byte swizzle: K is
@@ -71,7 +73,8 @@ namespace at {
 
 constexpr int kTile = kvf::kPage;  // keys of a tile: a page's, or 64 selected ones
 constexpr int kRing = 16;  // entries of the per-tile and per-segment rings; loaders run at most 10 tiles ahead
-enum Form { kTree = 0, kSparse = 1, kWide = 2 };
+enum Form { kTree = 0, kSparse = 1, kWide = 2, kTreeFew = 3, kSparseFew = 4, kForms = 5 };
+constexpr int kFewRows = 32;
 
 struct AttnArgs {
   const __nv_bfloat16* q;
@@ -104,11 +107,15 @@ struct Start {
 
 template <int FMT, int D, int FORM>
 struct Cfg {
-  static constexpr bool SPARSE = FORM == kSparse;
-  static constexpr int WG = FORM == kWide ? 2 : 1;     // groups of four softmax warps
-  static constexpr int ROWS = 128 * WG;                // rows of a unit
-  static constexpr int SBUF = FORM == kWide ? 2 : 1;   // score buffers
-  static constexpr int THREADS = 128 * WG + 128 + (FORM == kWide ? 64 : 0);
+  static constexpr bool SPARSE = FORM == kSparse || FORM == kSparseFew;
+  static constexpr bool FEW = FORM == kTreeFew || FORM == kSparseFew;
+  static constexpr bool TWO = FORM == kWide || FEW;    // two score buffers, queries in shared memory, warps that issue the products
+  static constexpr int WG = FORM == kWide ? 2 : 1;     // groups of softmax warps
+  static constexpr int SW = FEW ? 1 : 4;               // softmax warps of a group
+  static constexpr int QROWS = 32 * SW;                // rows of a group
+  static constexpr int ROWS = QROWS * WG;              // rows of a unit
+  static constexpr int SBUF = TWO ? 2 : 1;             // score buffers
+  static constexpr int THREADS = ROWS + 128 + (TWO ? 32 * WG : 0);
   static constexpr int CTAS = FORM == kWide ? 1 : 2;   // per SM
   static constexpr int NBLK = D / 64;
   static constexpr int SLOT = kTile * D * 2;
@@ -119,11 +126,11 @@ struct Cfg {
   static constexpr int RAW_SLOT = RAW ? NCH * 64 * 16 + 64 * 4 + (D == 64 ? 64 * 4 : 0) : 0;  // codes, a scale word a row, flags
   // ring depths that fill the shared memory (113 KB or 227 KB a CTA): operand tiles, and tiles of codes
   // on their way of each loader pair
-  static constexpr int P = !RAW ? 3 : FMT == DSA_FMT_FP8 ? 2 : 3;
+  static constexpr int P = !RAW ? 3 : FMT == DSA_FMT_FP8 || (FEW && D == 128) ? 2 : 3;
   static constexpr int NS = D == 64 ? (FORM == kWide || !RAW ? 12 : 10)
                             : FORM == kWide ? (!RAW ? 10 : FMT == DSA_FMT_FP8 ? 7 : 8)
                                             : (!RAW ? 6 : FMT == DSA_FMT_FP8 ? 4 : 5);
-  static constexpr int QBYTES = FORM == kWide ? ROWS * D * 2 : 0;
+  static constexpr int QBYTES = TWO ? ROWS * D * 2 : 0;
   // TMEM columns of a group, and of the CTA (two CTAs share the SM's 512)
   static constexpr uint32_t O = 0, S = D, Q = D + 64 * SBUF, STRIDE = 256, TMEM = 256 * WG;
 };
@@ -391,10 +398,15 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
     attn_kernel(const __grid_constant__ CUtensorMap tm, const AttnArgs a) {
   using C = Cfg<FMT, D, FORM>;
   using L = kvf::Layout<FMT, D>;
-  constexpr int NSW = 4 * C::WG;  // softmax warps
+  constexpr int NSW = C::SW * C::WG;  // softmax warps
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint8_t* const qsm = smem + C::NS * C::SLOT;
-  uint8_t* const raw = qsm + C::QBYTES;
+  // Queries first: the first product reads 128 rows of them whatever a group
+  // has, in the few-row forms the ring's bytes beyond 32. What comes of those
+  // stays in accumulator lanes that nothing reads.
+  uint8_t* const qsm = smem;
+  uint8_t* const tiles = smem + C::QBYTES;
+  uint8_t* const raw = tiles + C::NS * C::SLOT;
+  static_assert(C::QBYTES + C::NS * C::SLOT >= 128 * D * 2, "queries that the first product reads");
   Shared& sh = *reinterpret_cast<Shared*>(raw + 2 * C::P * C::RAW_SLOT);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cta = blockIdx.x, grid = gridDim.x;
@@ -414,9 +426,9 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
     for (int i = 0; i < C::WG; ++i) {
       mbar_init(&sh.s_full[i][0], 1);
       mbar_init(&sh.s_full[i][1], 1);
-      mbar_init(&sh.p_ready[i][0], 4);
-      mbar_init(&sh.p_ready[i][1], 4);
-      mbar_init(&sh.q_ready[i], 4);
+      mbar_init(&sh.p_ready[i][0], C::SW);
+      mbar_init(&sh.p_ready[i][1], C::SW);
+      mbar_init(&sh.q_ready[i], C::SW);
       mbar_init(&sh.o_full[i][0], 1);
       mbar_init(&sh.o_full[i][1], 1);
     }
@@ -457,7 +469,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
 
   constexpr uint32_t kIdescQk = idesc_f16(128, kTile, true);
   constexpr uint32_t kIdescPv = idesc_f16(128, D, true) | kIdescBMn;
-  const uint64_t kdesc = sw128_desc(smem_u32(smem)), vdesc = sw128_mn_desc(smem_u32(smem), kTile * 128);
+  const uint64_t kdesc = sw128_desc(smem_u32(tiles)), vdesc = sw128_mn_desc(smem_u32(tiles), kTile * 128);
   const uint64_t qdesc0 = sw128_desc(smem_u32(qsm));
   // The products. One thread issues them (elect_one: the compiler then keeps
   // the operands in uniform registers; issuing a tile's took 1100 cycles
@@ -467,8 +479,8 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {
       const uint64_t b = k + (((i / 4) * (kTile * 128) + (i % 4) * 32) >> 4);
-      if constexpr (FORM == kWide)
-        tc_mma_f16(d, q + (((i / 4) * (128 * 128) + (i % 4) * 32) >> 4), b, kIdescQk, i > 0);
+      if constexpr (C::TWO)
+        tc_mma_f16(d, q + (((i / 4) * (C::QROWS * 128) + (i % 4) * 32) >> 4), b, kIdescQk, i > 0);
       else
         tc_mma_f16_ta(d, tb + C::Q + 8 * i, b, kIdescQk, i > 0);
     }
@@ -483,7 +495,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
     tc_commit(&sh.o_full[wg][buf]);
   };
   auto scores = [&](int wg, int at, int buf) {
-    if (elect_one()) issue_scores(sh.tmem + wg * C::STRIDE, qdesc0 + wg * ((128 * D * 2) >> 4), kdesc + at * (C::SLOT >> 4), at, wg, buf);
+    if (elect_one()) issue_scores(sh.tmem + wg * C::STRIDE, qdesc0 + wg * ((C::QROWS * D * 2) >> 4), kdesc + at * (C::SLOT >> 4), at, wg, buf);
     __syncwarp();
   };
   auto values = [&](int wg, int at, int buf, bool first) {
@@ -499,17 +511,17 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
     }
     __syncwarp();
   };
-  auto has_rows = [&](int wg, const Seg& g) { return wg * 128 < g.rows; };
+  auto has_rows = [&](int wg, const Seg& g) { return wg * C::QROWS < g.rows; };
 
   if (count <= 0) {
     if (tid == 0) a.meta[2 * cta] = make_int4(0, 0, 0, 0);
   } else if (warp < NSW) {
     // ------------------------------------------------------------ softmax
-    const int wg = warp >> 2, gw = warp & 3;  // group, and warp of the group
+    const int wg = warp / C::SW, gw = warp % C::SW;  // group, and warp of the group
     const uint32_t tb = sh.tmem + wg * C::STRIDE;
     const uint32_t lanes = static_cast<uint32_t>(gw * 32) << 16;
     const uint32_t tO = tb + C::O + lanes;
-    const bool issues = FORM != kWide && gw == 0;  // this warp issues the products
+    const bool issues = !C::TWO && gw == 0;  // this warp issues the products
     Iter<C> it(a, sh.start, count);
     Seg s;
     bool more = it.next(s), run = true;
@@ -545,12 +557,12 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
       const bool valid = row < g.rows;
       at_row = row_at(g);
       const uint4* src = reinterpret_cast<const uint4*>(valid ? query(g, at_row) : a.q);
-      if constexpr (FORM == kWide) {
-        uint8_t* dst = qsm + wg * (128 * D * 2) + (row & 127) * 128;
+      if constexpr (C::TWO) {
+        uint8_t* dst = qsm + wg * (C::QROWS * D * 2) + row % C::QROWS * 128;
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) {
           const uint4 v = valid ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-          *reinterpret_cast<uint4*>(dst + (i / 8) * (128 * 128) + (((i & 7) ^ (row & 7)) << 4)) = v;
+          *reinterpret_cast<uint4*>(dst + (i / 8) * (C::QROWS * 128) + (((i & 7) ^ (row & 7)) << 4)) = v;
         }
         fence_proxy_async_smem();
       } else {
@@ -570,7 +582,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
         tmem_st_wait();
         tc_fence_before();
       }
-      if constexpr (FORM == kWide) {
+      if constexpr (C::TWO) {
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.q_ready[wg]);
       } else {
@@ -677,7 +689,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
           }
           tmem_st32(tS, p);  // over scores that are not needed any more
         }
-        if constexpr (FORM == kWide) {
+        if constexpr (C::TWO) {
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
@@ -770,7 +782,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
       ++seg;
     }
     if (issues) settle_products(gw);
-  } else if (FORM == kWide && warp >= NSW + 4) {
+  } else if (C::TWO && warp >= NSW + 4) {
     // ------------------------------------------------------------ products
     const int wg = warp - NSW - 4;
     Iter<C> it(a, sh.start, count);
@@ -849,7 +861,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
     // the segment
     auto hand_over = [&](int info) {
       const int at = info & 15, seg = info >> 8;
-      uint8_t* const tile = smem + at * C::SLOT;
+      uint8_t* const tile = tiles + at * C::SLOT;
       bool found = false;
       if constexpr (C::RAW) {
         const uint8_t* src = ring + (sent % C::P) * C::RAW_SLOT;
@@ -955,7 +967,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
     auto ask = [&](auto src, const uint8_t* whole, int at, int rnd, bool clean, bool last, int seg) -> bool {
       if (!C::RAW && !acquire(at, rnd)) return false;
       uint8_t* const to = ring + (issued % C::P) * C::RAW_SLOT;
-      auto dst = [&](int i) { return C::RAW ? smem_u32(to) + ti * 16 + i * 1024 : smem_u32(place(smem + at * C::SLOT, i, chunk)); };
+      auto dst = [&](int i) { return C::RAW ? smem_u32(to) + ti * 16 + i * 1024 : smem_u32(place(tiles + at * C::SLOT, i, chunk)); };
       [[maybe_unused]] const uint32_t scale_dst = smem_u32(to) + NCH * 64 * 16 + (ti << 2);
       [[maybe_unused]] uint32_t odd = 0;
       if (whole) {
@@ -1095,7 +1107,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
           if (run && lane == 0) mbar_arrive_expect_tx(&sh.full[at], C::SLOT / 2);
           __syncwarp();
           if (run && lane < LANES)
-            tma_gather4(smem + at * C::SLOT + c * (kTile * 128) + q * 512, &tm, c * 64, y[0], y[1], y[2], y[3], &sh.full[at]);
+            tma_gather4(tiles + at * C::SLOT + c * (kTile * 128) + q * 512, &tm, c * 64, y[0], y[1], y[2], y[3], &sh.full[at]);
           if (run && last && lane == 0) mbar_arrive(&sh.vdone[seg % kRing]);
           __syncwarp();
         } else if constexpr (C::SPARSE) {
@@ -1125,7 +1137,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
                 const int y = ((page * a.kv_heads + s.h) * 2 + v) * kTile;
 #pragma unroll
                 for (int c = 0; c < C::NBLK; ++c)
-                  tma_load_2d(smem + at * C::SLOT + c * (kTile * 128), &tm, c * 64, y, &sh.full[at]);
+                  tma_load_2d(tiles + at * C::SLOT + c * (kTile * 128), &tm, c * 64, y, &sh.full[at]);
               }
               if (last) mbar_arrive(&sh.vdone[seg % kRing]);
             }
@@ -1173,7 +1185,7 @@ dsa_status run_one(dsa_ctx* ctx, const CUtensorMap& tm, const AttnArgs& a, int g
   auto kern = attn_kernel<FMT, D, FORM>;
   constexpr int bytes = smem_bytes<C>();
   static_assert(bytes * C::CTAS <= 233472 - 1024 * C::CTAS, "shared memory of an SM");
-  const uint64_t bit = 1ull << ((FMT * 2 + (D == 128)) * 3 + FORM);  // once a context and kernel
+  const uint64_t bit = 1ull << ((FMT * 2 + (D == 128)) * kForms + FORM);  // once a context and kernel
   if (!(ctx->attn_ready & bit)) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return DSA_ERR_CUDA;
     ctx->attn_ready |= bit;
@@ -1187,6 +1199,8 @@ dsa_status run_dim(dsa_ctx* ctx, int form, const CUtensorMap& tm, const AttnArgs
   switch (form) {
     case kTree: return run_one<FMT, D, kTree>(ctx, tm, a, grid, stream);
     case kSparse: return run_one<FMT, D, kSparse>(ctx, tm, a, grid, stream);
+    case kTreeFew: return run_one<FMT, D, kTreeFew>(ctx, tm, a, grid, stream);
+    case kSparseFew: return run_one<FMT, D, kSparseFew>(ctx, tm, a, grid, stream);
     default: return run_one<FMT, D, kWide>(ctx, tm, a, grid, stream);
   }
 }
