@@ -201,6 +201,11 @@ dsa_status launch_attn(dsa_ctx* ctx, const dsa_attn_args& p, const int32_t* sel,
   // other, with 160 rows 128.2 (163.3) and 170.6 (190.9), with 512 248.0 (317.9)
   // and 325.3 (369.1)
   const bool wide = static_cast<long long>(p.Tq) * a.G > 128LL * p.B;
+  // the few-row forms up to 32 rows: 64 sequences of 2048 to 16384 tokens, 8 kv
+  // heads, bf16 (fp8), take with 8 rows 368 (350) us in them and 385 (356) in
+  // the 128-row form, with 32 rows 375 (355) and 389 (363), and with 64 rows,
+  // which read the cache twice there, 729 (682) and 399 (395). 2048 selections of
+  // 512 keys, G 8: 577 (951) and 614 (1006)
   const bool few = sel ? a.G <= kFewRows : static_cast<long long>(p.Tq) * a.G <= static_cast<long long>(kFewRows) * p.B;
   const int form = sel ? (few ? kSparseFew : kSparse) : wide ? kWide : few ? kTreeFew : kTree;
   const int grid = form == kWide ? ctx->num_sms : 2 * ctx->num_sms, rows = form == kWide ? 256 : few ? kFewRows : 128;

@@ -52,16 +52,17 @@
 // What bounds it, and what it measures (device time of a call, join included,
 // against a copy rate of 6.79 TB/s and 1909 bf16 TFLOP/s):
 //  - one token of 64 sequences of 2048 to 16384, 8 kv heads, G 8, D 128, bf16:
-//    HBM. 380 us, 6.4 TB/s.
+//    HBM. 361 to 368 us, 6.6 TB/s. In fp8 350 us: the loaders' work on a tile.
 //  - 2048 tokens behind 8192, the same heads: the softmax of 64 keys takes about
 //    2000 cycles of a group beside the products' 1330 (two groups). 505 us,
 //    1220 TFLOP/s.
-//  - 8 tokens of 8 sequences of 131072, 4 kv heads, G 16, fp8: instruction issue
-//    (0.61 a cycle and scheduler), half of it widening codes for 128 rows. 369
-//    us, 3.0 TB/s, 750 TFLOP/s.
+//  - 8 tokens of 8 sequences of 131072, 4 kv heads, G 16, fp8: the chain of a
+//    tile (scores, softmax, values: 276 us with a bf16 cache out of L2) and the
+//    loaders, which share the issue slots with it (58 % busy; 300 us without the
+//    widening's arithmetic). 344 us, 3.2 TB/s, 800 TFLOP/s.
 //  - 2048 queries over 512 keys each, 8 kv heads, G 8, bf16: the loaders' time
-//    to issue gathers and a tile's chain (scores, softmax, values) of about 2300
-//    cycles for 8 rows. 610 us, 7.0 TB/s out of L2.
+//    to issue gathers (75 cycles each) and the start of a unit every 8 tiles. 578
+//    us, 7.4 TB/s out of L2.
 #pragma once
 #include <type_traits>
 
