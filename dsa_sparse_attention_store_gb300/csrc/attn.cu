@@ -205,7 +205,7 @@ dsa_status launch_attn(dsa_ctx* ctx, const dsa_attn_args& p, const int32_t* sel,
   // heads, bf16 (fp8), take with 8 rows 368 (350) us in them and 385 (356) in
   // the 128-row form, with 32 rows 375 (355) and 389 (363), and with 64 rows,
   // which read the cache twice there, 729 (682) and 399 (395). 2048 selections of
-  // 512 keys, G 8: 577 (951) and 614 (1006)
+  // 512 keys, G 8: 577 (864) and 614 (870), but 796 and 776 in fp4
   const bool few = sel ? a.G <= kFewRows : static_cast<long long>(p.Tq) * a.G <= static_cast<long long>(kFewRows) * p.B;
   const int form = sel ? (few ? kSparseFew : kSparse) : wide ? kWide : few ? kTreeFew : kTree;
   const int grid = form == kWide ? ctx->num_sms : 2 * ctx->num_sms, rows = form == kWide ? 256 : few ? kFewRows : 128;
