@@ -197,9 +197,9 @@ dsa_status launch_attn(dsa_ctx* ctx, const dsa_attn_args& p, const int32_t* sel,
   }
   // the wide form where the sequences' rows fill more than one 128-row unit on
   // average: 16 sequences of 4509 to 10498 tokens, 8 kv heads, bf16 (fp8), take
-  // with 128 rows 112.7 (143.9) us in the wide form and 115.9 (116.3) in the
-  // other, with 160 rows 128.2 (163.3) and 170.6 (190.9), with 512 248.0 (317.9)
-  // and 325.3 (369.1)
+  // with 128 rows 113.7 (135.5) us in the wide form and 113.6 (108.7) in the
+  // other, with 160 rows 130.2 (154.1) and 168.5 (177.6), with 512 250.2 (299.7)
+  // and 318.9 (347.0)
   const bool wide = static_cast<long long>(p.Tq) * a.G > 128LL * p.B;
   // the few-row forms up to 32 rows: 64 sequences of 2048 to 16384 tokens, 8 kv
   // heads, bf16 (fp8), take with 8 rows 368 (350) us in them and 385 (356) in
