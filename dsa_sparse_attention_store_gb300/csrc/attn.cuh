@@ -73,7 +73,16 @@ namespace dsa {
 namespace at {
 
 constexpr int kTile = kvf::kPage;  // keys of a tile: a page's, or 64 selected ones
-constexpr int kRing = 16;  // entries of the per-tile and per-segment rings; loaders run at most 10 tiles ahead
+// Entries of the per-tile and per-segment rings. A wait looks at one bit of an
+// entry's round, so it may come neither a round early nor a round late. Not
+// late: a tile's values are released only after the group's weights, for which
+// it has read the tile's mask, and loaders run at most 10 tiles past a value
+// that is not released. Not early: the second group of the wide form skips
+// units of at most 128 rows without waiting for their tiles, so it may be any
+// number of tiles ahead of the loaders; it looks at the entry of a unit's first
+// tile only when it has that tile's scores, which exist after the loaders
+// announced it, and from there on it goes tile by tile.
+constexpr int kRing = 16;
 enum Form { kTree = 0, kSparse = 1, kWide = 2, kTreeFew = 3, kSparseFew = 4, kForms = 5 };
 constexpr int kFewRows = 32;
 
@@ -619,10 +628,17 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
       const int qi = mine.q;                   // the row's query in its sequence
       float m = -INFINITY, l = 0.f;
       for (int t = s.t0; t < s.t1; ++t, ++n, ++ns) {
+        const int buf = ns & (C::SBUF - 1);
+        auto wait_scores = [&]() { run = run && wait_warp(&sh.s_full[wg][buf], (ns / C::SBUF) & 1); };
+        // A unit's first tile after skipped ones: once its scores are there the
+        // loaders have announced it, so the wait for its mask cannot end a round
+        // early (see kRing). The mask's way to a register is hidden behind the
+        // scores otherwise (a chunk of 2048 tokens takes 505 us so and 516 with
+        // the scores first on every tile).
+        if (C::WG > 1 && t == s.t0) wait_scores();
         run = run && wait_warp(&sh.mfull[n % kRing], (n / kRing) & 1);
         unsigned long long see = sh.vmask[n % kRing];
-        const int buf = ns & (C::SBUF - 1);
-        run = run && wait_warp(&sh.s_full[wg][buf], (ns / C::SBUF) & 1);
+        wait_scores();
         tc_fence_after();
         const uint32_t tS = tb + C::S + 64 * buf + lanes;
         if (active && run) {

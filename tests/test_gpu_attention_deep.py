@@ -1,0 +1,104 @@
+"""Attention on the GPU where a thread block works through dozens of key tiles
+and many units: rings wrap, units of one and of two row groups follow each
+other. Against a 64-bit reference by torch (the definition, whole matrices);
+every case runs twice and gives the same bits."""
+import math
+
+import numpy as np
+import pytest
+
+from oracle import attention as A
+from tests.test_gpu_attention import Case
+
+pytestmark = pytest.mark.gpu
+
+FMTS = [A.BF16, A.FP8, A.FP4]
+
+
+@pytest.fixture(scope="module")
+def ctx():
+    import torch
+    from dsa_sparse_attention_store_gb300 import Context
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    c = Context(max_pos=64)
+    yield c
+    c.close()
+
+
+def _places(c, b, pos):
+    """Rows of the flattened cache of sequence b's positions."""
+    return c.table[b, pos // 64].astype(np.int64) * 64 + pos % 64
+
+
+def reference(c):
+    """As oracle.attention.attend, in whole matrices: (out, lse, sum w|v|,
+    largest visible sum |q||k|) in 64 bits."""
+    import torch
+    up = lambda x: torch.from_numpy(np.ascontiguousarray(x)).cuda()  # noqa: E731
+    K, V = (up(x) for x in A.values(c.cache, c.pages, c.kv, c.D, c.fmt))
+    q = up(c.q.astype(np.float64))
+    out = torch.zeros((c.Tq, c.H, c.D), dtype=torch.float64, device="cuda")
+    wabs, lse = torch.zeros_like(out), torch.full((c.Tq, c.H), -math.inf, dtype=torch.float64, device="cuda")
+    qk = torch.zeros_like(lse)
+    for b in range(c.B):
+        n, r0, ctx_len = c.nds[b], int(c.cu[b]), c.ctx[b]
+        if n == 0:
+            continue
+        if c.mask is None:
+            tree = np.tril(np.ones((n, n), bool))
+        else:
+            tree = np.stack([A.visible(c.mask[r0 + i], n) for i in range(n)])
+        new = _places(c, b, np.arange(ctx_len, ctx_len + n))
+        for rows in [range(n)] if c.sel is None else [[i] for i in range(n)]:
+            if c.sel is None:
+                at = np.concatenate([_places(c, b, np.arange(ctx_len)), new])
+                see = np.concatenate([np.ones((n, ctx_len), bool), tree], 1)
+            else:
+                pos = c.sel[r0 + rows[0]].astype(np.int64)
+                pos = pos[pos >= 0]
+                own = new[tree[rows[0]]] if c.mask is not None else new[:0]
+                at = np.concatenate([_places(c, b, pos), own])
+                see = np.ones((1, len(at)), bool)
+            if len(at) == 0:
+                continue
+            at, hide = up(at), ~up(see).repeat_interleave(c.G, 0)[None]
+            t = slice(r0 + rows[0], r0 + rows[0] + len(rows))
+            m = len(rows)
+            # [kv, rows x G, D] and [kv, keys, D]
+            qq = q[t].view(m, c.kv, c.G, c.D).transpose(0, 1).reshape(c.kv, m * c.G, c.D)
+            k, v = K[at].transpose(0, 1), V[at].transpose(0, 1)
+            z = (qq @ k.transpose(1, 2) * c.scale).masked_fill_(hide, -math.inf)
+            total = torch.logsumexp(z, -1, keepdim=True)
+            w = torch.exp(z - torch.where(torch.isfinite(total), total, torch.zeros_like(total)))
+            back = lambda x: x.view(c.kv, m, c.G, -1).transpose(0, 1).reshape(m, c.H, -1)  # noqa: E731
+            out[t], wabs[t] = back(w @ v), back(w @ v.abs())
+            lse[t] = back(total)[..., 0]
+            qk[t] = back((qq.abs() @ k.abs().transpose(1, 2)).masked_fill_(hide, 0.0).amax(-1, keepdim=True))[..., 0]
+    return tuple(x.cpu().numpy() for x in (out, lse, wabs, qk))
+
+
+def check_twice(c, ctx, ref=None, rows=None):
+    import torch
+    d = c.device()
+    out, lse = c.run(ctx, d=d)
+    again, lse2 = c.run(ctx, d=d)
+    assert ctx.device_status() == 0
+    c.check(out, lse, ref=reference(c) if ref is None else ref, rows=rows)
+    # as bits: NaN compares unequal to itself
+    assert torch.equal(out.view(torch.int16), again.view(torch.int16))
+    assert torch.equal(lse.view(torch.int32), lse2.view(torch.int32))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("ctx_lens,nds,kv,G,D,masked", [
+    # units of 256 and 128 rows, of 31 tiles whose last holds one key
+    ([1873] * 16, [48] * 16, 8, 8, 128, True),
+    # units of 256 and 64 rows
+    ([1930] * 24, [20] * 24, 8, 16, 64, True),
+    # decode steps of about 3000 keys and, among them, chunks of a prefill
+    ([x for i in range(8) for x in (3000 + 70 * i, 3400 - 30 * i, 2900 + i, 700 + 50 * i)], [1, 1, 1, 150 + 9] * 8, 8, 8, 64, False),
+])
+def test_short_units_before_long_ones(ctx, fmt, ctx_lens, nds, kv, G, D, masked):
+    # the second group of rows has nothing to do in units of at most 128 rows
+    # and is far ahead of the loaders when the next unit starts
+    check_twice(Case(len(nds), ctx_lens, nds, kv, G, D, fmt, masked=masked), ctx)
