@@ -76,12 +76,14 @@ constexpr int kTile = kvf::kPage;  // keys of a tile: a page's, or 64 selected o
 // Entries of the per-tile and per-segment rings. A wait looks at one bit of an
 // entry's round, so it may come neither a round early nor a round late. Not
 // late: a tile's values are released only after the group's weights, for which
-// it has read the tile's mask, and loaders run at most 10 tiles past a value
-// that is not released. Not early: the second group of the wide form skips
-// units of at most 128 rows without waiting for their tiles, so it may be any
-// number of tiles ahead of the loaders; it looks at the entry of a unit's first
-// tile only when it has that tile's scores, which exist after the loaders
-// announced it, and from there on it goes tile by tile.
+// it has read the tile's mask, loaders run at most 10 tiles past a value that
+// is not released, and a group that has no rows in a unit releases its tiles
+// only after it has read its last unit's segment entry (u_done). Not early:
+// the second group of the wide form skips units of at most 128 rows without
+// waiting for their tiles, so it may be any number of tiles ahead of the
+// loaders; it looks at the entry of a unit's first tile only when it has that
+// tile's scores, which exist after the loaders announced it, and from there on
+// it goes tile by tile.
 constexpr int kRing = 16;
 enum Form { kTree = 0, kSparse = 1, kWide = 2, kTreeFew = 3, kSparseFew = 4, kForms = 5 };
 constexpr int kFewRows = 32;
@@ -149,8 +151,9 @@ struct Shared {
   uint64_t full[12], empty[12];
   uint64_t mfull[kRing], vdone[kRing];
   // by group and score buffer (a barrier per buffer: no phase can complete twice
-  // before a wait for it): scores there, weights there, their product done
-  uint64_t s_full[2][2], o_full[2][2], p_ready[2][2], q_ready[2], fin[2];
+  // before a wait for it): scores there, weights there, their product done; by
+  // group: queries there, a unit's segment entry read, the end
+  uint64_t s_full[2][2], o_full[2][2], p_ready[2][2], q_ready[2], u_done[2], fin[2];
   unsigned long long vmask[kRing];  // visible keys of a tile, as far as the loader knows
   int bad[kRing];                      // segment number + 1 where a loader replaced a value
   int info[4][4];                      // a loader warp's tiles on their way
@@ -439,6 +442,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
       mbar_init(&sh.p_ready[i][0], C::SW);
       mbar_init(&sh.p_ready[i][1], C::SW);
       mbar_init(&sh.q_ready[i], C::SW);
+      mbar_init(&sh.u_done[i], C::SW);
       mbar_init(&sh.o_full[i][0], 1);
       mbar_init(&sh.o_full[i][1], 1);
     }
@@ -742,7 +746,15 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
       more = it.next(s);
       if (more && has_rows(wg, s)) start_unit(s);
       run = run && wait_product();
-      if (!C::SPARSE) run = run && wait_warp(&sh.vdone[seg % kRing], (seg / kRing) & 1);
+      bool fix = false;  // a loader replaced a value of this segment
+      if (!C::SPARSE) {
+        run = run && wait_warp(&sh.vdone[seg % kRing], (seg / kRing) & 1);
+        fix = *static_cast<volatile int*>(&sh.bad[seg % kRing]) == seg + 1;
+        if constexpr (C::WG > 1) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.u_done[wg]);
+        }
+      }
       tc_fence_after();
       const bool first = done.t0 == 0, last = done.t1 == done.nt;
       if (tid == 0 && !first) {
@@ -754,7 +766,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
         a.meta[2 * cta + 1] = make_int4(done.r0, done.q0, done.h, 0);
       }
       if (active && run) {
-        if (!C::SPARSE && *static_cast<volatile int*>(&sh.bad[seg % kRing]) == seg + 1)
+        if (fix)
           fix_nonfinite<FMT, D>(a, done, max(done.t0, done.full / kTile), done.t1, qi, valid, tO);
         const long long tok = done.q0 + mine.q;
         const int head = done.h * a.G + mine.g;
@@ -805,10 +817,14 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
     Iter<C> it(a, sh.start, count);
     Seg s;
     bool run = true;
-    int ns = 0, units = 0;
+    int ns = 0, units = 0, passed = 0;  // tiles, units, and units known to be read out
     while (run && it.next(s)) {
       if (!has_rows(wg, s)) {
-        // nothing for this group: it only passes the tiles on
+        // Nothing for this group: it only passes the tiles on, once its softmax
+        // has read the last unit's segment entry (see kRing). Of the units before
+        // that one it has: their successor's weights came after.
+        if (units > passed) run = wait_warp(&sh.u_done[wg], (units - 1) & 1);
+        passed = units;
         for (int i = 2 * (s.t1 - s.t0); run && i > 0; --i) {
           run = wait_warp(&sh.full[slot], round);
           if (run && lane == 0) mbar_arrive(&sh.empty[slot]);

@@ -102,3 +102,45 @@ def test_short_units_before_long_ones(ctx, fmt, ctx_lens, nds, kv, G, D, masked)
     # the second group of rows has nothing to do in units of at most 128 rows
     # and is far ahead of the loaders when the next unit starts
     check_twice(Case(len(nds), ctx_lens, nds, kv, G, D, fmt, masked=masked), ctx)
+
+
+def _poison(c, b, j):
+    """Drafted token j of sequence b has values that are NaN in the first 32 dimensions of every kv head."""
+    _, _, vc, vs = A.fields(c.cache, c.pages, c.kv, c.D, c.fmt)
+    pos = c.ctx[b] + j
+    p, o = c.table[b, pos // 64], pos % 64
+    if c.fmt == A.BF16:
+        vc.view(np.uint16)[p, :, o, :32] = 0x7FC1
+    else:
+        vs[p, :, o, 0] = 255
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D", [64, 128])
+def test_runs_of_one_tile_units(ctx, fmt, D):
+    # per kv head 13 units of a long sequence, then runs of 160 units of one
+    # tile and 16 rows, in which the second group has nothing to do. What it
+    # still has to learn about its last unit must not be overwritten meanwhile.
+    ctx_lens, nds = [], []
+    for i in range(12):
+        ctx_lens += [90 + 17 * i] + [(5 * j + i) % 60 for j in range(20)]
+        nds += [200] + [1] * 20
+    c = Case(5 + D, ctx_lens, nds, 8, 16, D, fmt)
+    bits = c.bits.copy()
+    big = [b for b, n in enumerate(nds) if n == 200]
+    for b in big:                               # its last token is seen by itself and token 150 alone
+        bits[c.cu[b]:c.cu[b + 1], 199] = False
+        bits[c.cu[b] + 199, 199] = bits[c.cu[b] + 150, 199] = True
+    c.set_bits(bits)
+    clean = reference(c)
+    check_twice(c, ctx, clean)
+    for b in big:
+        _poison(c, b, 199)
+    hit = sorted(int(c.cu[b]) + i for b in big for i in (150, 199))
+    rows = [t for t in range(c.Tq) if t not in set(hit)]
+    check_twice(c, ctx, clean, rows)
+    out, _ = c.run(ctx)
+    got, want = out.double().cpu().numpy()[hit], clean[0][hit]
+    assert np.all(np.isnan(got[..., :32])) and np.all(np.isfinite(got[..., 32:]))
+    tol = A.tolerance(*clean, c.scale, D, float(c.lens.max()))[0][hit]
+    assert np.all(np.abs(got - want)[..., 32:] <= tol[..., 32:])
