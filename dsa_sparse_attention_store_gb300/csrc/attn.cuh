@@ -400,6 +400,7 @@ __device__ __noinline__ void fix_nonfinite(const AttnArgs& a, const Seg& s, int 
         if ((__float_as_uint(v) & 0x7F800000u) == 0x7F800000u) add += v;
       }
     }
+    __syncwarp();  // the lanes' keys differ; the load takes them together
     const float o = __uint_as_float(tmem_ld1(o_taddr + d));
     __syncwarp();
     tmem_st1(o_taddr + d, __float_as_uint(o + add));
@@ -591,6 +592,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
             w[4 * i + 2] = v.z;
             w[4 * i + 3] = v.w;
           }
+          __syncwarp();  // loads only where the row is real
           tmem_st32(tb + C::Q + lanes + 32 * c, w);
         }
         tmem_st_wait();
@@ -777,6 +779,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
+          __syncwarp();
           tmem_ld32(tO + 32 * c, o);
           tmem_ld_wait32(o);
           if (!valid) {
@@ -797,7 +800,6 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
             for (int i = 0; i < 8; ++i)
               *reinterpret_cast<uint4*>(part + 32 * c + 4 * i) = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
           }
-          __syncwarp();
         }
         if (valid) {
           if (first && last) {

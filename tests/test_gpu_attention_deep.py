@@ -144,3 +144,38 @@ def test_runs_of_one_tile_units(ctx, fmt, D):
     assert np.all(np.isnan(got[..., :32])) and np.all(np.isfinite(got[..., 32:]))
     tol = A.tolerance(*clean, c.scale, D, float(c.lens.max()))[0][hit]
     assert np.all(np.abs(got - want)[..., 32:] <= tol[..., 32:])
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("nd,G", [(9, 3), (19, 5), (70, 4)])   # 27, 95 and 280 rows: each form, warps that are not full
+def test_rows_that_see_different_replaced_values(ctx, fmt, D, nd, G):
+    # a third of the drafted tokens, on both sides of a page's end, hold what is
+    # not finite; every row sees others of them, some none
+    c = Case(77 + nd, [50], [nd], 2, G, D, fmt)
+    rng = np.random.default_rng(nd + D)
+    bits = np.zeros_like(c.bits)
+    bits[:, :nd] = rng.random((nd, nd)) < rng.choice([0.0, 0.1, 0.5], (nd, 1))
+    c.set_bits(bits)
+    clean = c.reference()
+    _, _, vc, vs = A.fields(c.cache, c.pages, c.kv, D, fmt)
+    for j in rng.permutation(nd)[:nd // 3]:
+        pos = 50 + int(j)
+        p, o = c.table[0, pos // 64], pos % 64
+        for h in range(c.kv):
+            if fmt == A.BF16:
+                d = rng.permutation(D)[:9]
+                vc.view(np.uint16)[p, h, o, d] = rng.choice([0x7FC1, 0x7F80, 0xFF80], 9)
+            else:
+                vs[p, h, o, rng.integers(D // 32)] = 255
+    o, z, _, _ = c.reference()
+    assert np.isnan(o).any() and np.isfinite(o).all(axis=(1, 2)).any()
+    out, lse = c.run(ctx)
+    assert ctx.device_status() == 0
+    got = out.double().cpu().numpy()
+    for kind in (np.isnan, np.isposinf, np.isneginf):
+        assert np.array_equal(kind(got), kind(o)), kind
+    fin = np.isfinite(o)
+    tol, tol_lse = A.tolerance(*clean, c.scale, D, float(c.lens.max()))
+    assert np.all(np.abs(got - clean[0])[fin] <= tol[fin])
+    assert np.all(np.abs(lse.double().cpu().numpy() - clean[1]) <= tol_lse)
