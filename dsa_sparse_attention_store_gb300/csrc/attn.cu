@@ -81,7 +81,8 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnArgs a, int grid, i
     for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
     return m;
   };
-  auto weight = [&](float2 v, float m) { return v.x == -INFINITY ? 0.f : v.x == m ? 1.f : ex2(v.x - m); };
+  // a piece's sums hold weights of up to 2^8: denormal factors count
+  auto weight = [&](float2 v, float m) { return v.x == -INFINITY ? 0.f : v.x == m ? 1.f : ex2_denorm(v.x - m); };
   if (n <= kFew) {
     for (int row = blockIdx.y * 8 + warp; row < m0.w; row += gridDim.y * 8) {
       const float m = top(row);

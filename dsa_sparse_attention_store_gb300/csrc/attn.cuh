@@ -699,7 +699,9 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
               l += l0 + l1;
               break;
             }
-            const float alpha = grow ? ex2(m - mnew) : 1.f;
+            // weights of up to 2^8 stand before this factor: flushed to zero below
+            // 2^-126 it would lose weights of 2^-118, which fp32 holds
+            const float alpha = grow ? ex2_denorm(m - mnew) : 1.f;
             if (t > s.t0) {  // after the last tile's second product
               run = run && wait_product();
               tc_fence_after();

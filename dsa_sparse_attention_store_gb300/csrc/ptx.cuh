@@ -380,6 +380,13 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// the same, denormal results kept
+__device__ __forceinline__ float ex2_denorm(float x) {
+  float y;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // ---------------------------------------------------------------- named barriers
 __device__ __forceinline__ void named_bar(int id, int nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");

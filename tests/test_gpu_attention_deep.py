@@ -179,3 +179,63 @@ def test_rows_that_see_different_replaced_values(ctx, fmt, D, nd, G):
     tol, tol_lse = A.tolerance(*clean, c.scale, D, float(c.lens.max()))
     assert np.all(np.abs(got - clean[0])[fin] <= tol[fin])
     assert np.all(np.abs(lse.double().cpu().numpy() - clean[1]) <= tol_lse)
+
+
+# sequences of about so many key tiles: on both sides of what the rings hold
+TILES = [1, 2, 15, 16, 17, 31, 32, 33, 47, 63, 64]
+FORMS = [  # new tokens, kv heads, G, keys selected (0: the tree form): up to 32, up to 128 and more rows
+    (2, 8, 4, 0), (8, 8, 8, 0), (20, 4, 16, 0), (5, 8, 4, 700), (3, 8, 40, 1100)]
+
+
+def _deep(seed, form, fmt, D, copies, masked=True, **kw):
+    nd, kv, G, k = form
+    tiles = TILES * copies
+    return Case(seed, [max(0, 64 * t - nd - (i % 3)) for i, t in enumerate(tiles)], [nd] * len(tiles), kv, G, D, fmt, masked=masked,
+                k=k or None, **kw)
+
+
+def _rise(c):
+    """Keys grow by a power of two every other page of a sequence."""
+    kc, ks, _, _ = A.fields(c.cache, c.pages, c.kv, c.D, c.fmt)
+    for b in range(c.B):
+        for j in range(-(-int(c.lens[b]) // 64)):
+            e, p = min(j // 2, 6), c.table[b, j]
+            if c.fmt == A.BF16:
+                w = kc[p].view(np.uint16)
+                w[...] = np.where(w & 0x7F80, w + (e << 7), w)
+            else:
+                ks[p] += e
+
+
+def _jumps(c, b):
+    """Of sequence b's rows of kv head 0, the share whose running maximum, in
+    tiles of 64 keys in the order the kernel takes them, rises by more than 2^8
+    after the first tile that holds a key."""
+    K, _ = A.values(c.cache, c.pages, c.kv, c.D, c.fmt)
+    hits, rows = 0, 0
+    for i in range(c.nds[b]):
+        t = int(c.cu[b]) + i
+        pos = c.sel[t][c.sel[t] >= 0] if c.sel is not None else np.arange(c.ctx[b])
+        s = c.q[t, :c.G].astype(np.float64) @ K[_places(c, b, pos), 0].T * c.scale / math.log(2)
+        top = np.stack([s[:, x:x + 64].max(1) for x in range(0, s.shape[1], 64)], 1)
+        run = np.maximum.accumulate(top, 1)
+        hits += int((np.diff(run, axis=1) > 8).any(1).sum())
+        rows += c.G
+    return hits / rows
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("form", FORMS)
+def test_maximum_moves_in_later_tiles(ctx, fmt, D, form):
+    # the accumulator and the sums are rescaled between products
+    c = _deep(8, form, fmt, D, 2, q_gain=2.0)
+    _rise(c)
+    if c.sel is not None:
+        for t in range(c.Tq):                   # ascending positions, and a first tile without a key for every third query
+            s = np.sort(c.sel[t][c.sel[t] >= 0])
+            c.sel[t] = -1
+            at = 64 if t % 3 == 0 and len(s) + 64 <= c.sel.shape[1] else 0
+            c.sel[t, at:at + len(s)] = s
+    assert _jumps(c, len(TILES) - 1) > 0.5 and _jumps(c, len(TILES) - 4) > 0.5
+    check_twice(c, ctx)
