@@ -194,6 +194,13 @@ def _deep(seed, form, fmt, D, copies, masked=True, **kw):
                 k=k or None, **kw)
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D,masked", [(64, False), (128, True)])
+@pytest.mark.parametrize("form", FORMS)
+def test_dozens_of_tiles_a_block(ctx, fmt, D, form, masked):
+    check_twice(_deep(7, form, fmt, D, 3 if form[3] == 0 else 2, masked), ctx)
+
+
 def _rise(c):
     """Keys grow by a power of two every other page of a sequence."""
     kc, ks, _, _ = A.fields(c.cache, c.pages, c.kv, c.D, c.fmt)
@@ -238,4 +245,21 @@ def test_maximum_moves_in_later_tiles(ctx, fmt, D, form):
             at = 64 if t % 3 == 0 and len(s) + 64 <= c.sel.shape[1] else 0
             c.sel[t, at:at + len(s)] = s
     assert _jumps(c, len(TILES) - 1) > 0.5 and _jumps(c, len(TILES) - 4) > 0.5
+    check_twice(c, ctx)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("nd,G", [(110, 1), (150, 2)])
+def test_first_tile_hidden_from_some_rows(ctx, fmt, D, nd, G):
+    # no committed context: half of the rows see nothing of the first tile (or
+    # two), which others do, and their maximum begins later
+    c = Case(9, [0] * 40, [nd] * 40, 8, G, D, fmt, q_gain=2.0)
+    bits = c.bits.copy()
+    for b in range(40):
+        for i in range(0, nd, 2):
+            bits[c.cu[b] + i, :64 + 64 * (b % 2 if nd > 128 else 0)] = False
+            bits[c.cu[b] + i, nd - 1 - b % 7] = True
+    c.set_bits(bits)
+    _rise(c)
     check_twice(c, ctx)
