@@ -186,18 +186,22 @@ dsa_status dsa_profile_enable(dsa_ctx* ctx, int on) {
 }
 
 dsa_status dsa_profile_read(dsa_ctx* ctx, float* ms, int32_t* launches) {
-  if (!ctx || !ms || !launches) return DSA_ERR_INVALID_ARG;
+  return dsa_profile_read_kinds(ctx, ms, launches, DSA_K_COUNT);
+}
+
+dsa_status dsa_profile_read_kinds(dsa_ctx* ctx, float* ms, int32_t* launches, int32_t kinds) {
+  if (!ctx || !ms || !launches || kinds < 1) return DSA_ERR_INVALID_ARG;
   if (const dsa_status d = dsa::check_device(ctx)) return d;
-  for (int k = 0; k < DSA_K_COUNT; ++k) {
+  for (int k = 0; k < kinds; ++k) {
     ms[k] = 0.f;
-    launches[k] = static_cast<int32_t>(ctx->launches[k]);
-    ctx->launches[k] = 0;
+    launches[k] = k < DSA_K_ALL ? static_cast<int32_t>(ctx->launches[k]) : 0;
   }
+  for (long long& n : ctx->launches) n = 0;
   if (cudaDeviceSynchronize() != cudaSuccess) return DSA_ERR_CUDA;
   for (int i = 0; i < ctx->prof_n; ++i) {
     float t = 0.f;
     if (cudaEventElapsedTime(&t, ctx->prof[i].ev0, ctx->prof[i].ev1) != cudaSuccess) return DSA_ERR_CUDA;
-    ms[ctx->prof[i].kind] += t;
+    if (ctx->prof[i].kind < kinds) ms[ctx->prof[i].kind] += t;
   }
   ctx->prof_n = 0;
   return DSA_OK;

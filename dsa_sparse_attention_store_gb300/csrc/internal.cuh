@@ -36,7 +36,7 @@ struct dsa_ctx {
   int prof_on;
   int prof_n;                    // records in use
   dsa_prof_rec* prof;            // kProfCap records, events created on enable
-  long long launches[DSA_K_COUNT];
+  long long launches[DSA_K_ALL];
 };
 
 namespace dsa {

@@ -90,6 +90,8 @@ def lib() -> ctypes.CDLL:
         L.dsa_profile_enable.restype = ctypes.c_int
         L.dsa_profile_read.argtypes = [_c_ptr, ctypes.POINTER(ctypes.c_float), ctypes.POINTER(_c_int)]
         L.dsa_profile_read.restype = ctypes.c_int
+        L.dsa_profile_read_kinds.argtypes = [_c_ptr, ctypes.POINTER(ctypes.c_float), ctypes.POINTER(_c_int), _c_int]
+        L.dsa_profile_read_kinds.restype = ctypes.c_int
         L.dsa_rope_create.argtypes = [_c_ptr, ctypes.POINTER(_c_ptr), ctypes.POINTER(_RopeDesc)]
         L.dsa_rope_destroy.argtypes = [_c_ptr]
         L.dsa_rope_apply.argtypes = [_c_ptr, _c_ptr, _c_ptr, _c_ptr, ctypes.c_int, _c_ptr, _c_int, _c_int,
@@ -487,9 +489,9 @@ class Context:
         """{kind: (total ms, launches)} since the previous read (synchronises)."""
         ms = (ctypes.c_float * len(KERNEL_KINDS))()
         n = (_c_int * len(KERNEL_KINDS))()
-        st = lib().dsa_profile_read(self._h, ms, n)
+        st = lib().dsa_profile_read_kinds(self._h, ms, n, len(KERNEL_KINDS))
         if st != 0:
-            raise DsaError("dsa_profile_read", st)
+            raise DsaError("dsa_profile_read_kinds", st)
         return {k: (float(ms[i]), int(n[i])) for i, k in enumerate(KERNEL_KINDS)}
 
     def device_status(self, stream=None) -> int:

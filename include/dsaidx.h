@@ -392,25 +392,31 @@ dsa_status dsa_sparse_attn(dsa_ctx* ctx, const dsa_attn_args* args, const int32_
 /* Kernel timing, for benchmarks and profiling. While enabled, the library
  * records a CUDA event pair on the launch stream around each kernel it
  * launches (at most 8192 pairs between reads; later launches are counted but
- * not timed). dsa_profile_read synchronises the device, writes per-kind total
+ * not timed). Reading synchronises the device, writes per-kind total
  * milliseconds and launch counts since the previous read (launches are
- * counted whether or not timing is on), and resets both. */
+ * counted whether or not timing is on), and resets both, those of kinds that
+ * are not asked for too. dsa_profile_read_kinds writes `kinds` (>= 1) entries,
+ * zeros past the last kind there is. dsa_profile_read writes the indexer's
+ * DSA_K_COUNT, a number that stays: programs have arrays of that length. */
 typedef enum {
   DSA_K_STORE = 0,      /* dsa_index_store */
   DSA_K_PLAN = 1,       /* dsa_index_topk: schedule */
   DSA_K_SCORE_BF16 = 2, /* dsa_index_topk: tensor-core scorer + running top-k, bf16 cache */
   DSA_K_SCORE_FP8 = 3,  /* the same, fp8 cache */
   DSA_K_SCORE_FP4 = 4,  /* the same, fp4 cache */
+  DSA_K_COUNT = 5,      /* kinds that dsa_profile_read reports */
   DSA_K_ROPE = 5,       /* dsa_rope_apply */
   DSA_K_KV_STORE = 6,   /* dsa_kv_store */
   DSA_K_KV_LOAD = 7,    /* dsa_kv_load */
   DSA_K_ATTN = 8,       /* dsa_tree_attn, dsa_sparse_attn: the attention */
   DSA_K_ATTN_JOIN = 9,  /* the same: joining units that were divided */
-  DSA_K_COUNT = 10
+  DSA_K_ALL = 10        /* kinds there are */
 } dsa_kernel_kind;
 dsa_status dsa_profile_enable(dsa_ctx* ctx, int on);
 dsa_status dsa_profile_read(dsa_ctx* ctx, float* ms /* [DSA_K_COUNT] */,
                             int32_t* launches /* [DSA_K_COUNT] */);
+dsa_status dsa_profile_read_kinds(dsa_ctx* ctx, float* ms /* [kinds] */, int32_t* launches /* [kinds] */,
+                                  int32_t kinds);
 
 /* Synchronise `stream`, then read and clear the context's device status
  * word. Returns DSA_OK or the first device-side error recorded. */
