@@ -15,6 +15,24 @@ bool known(dsa_fmt f) { return f == DSA_FMT_BF16 || f == DSA_FMT_FP8 || f == DSA
 
 bool positive(double v) { return v > 0.0 && std::isfinite(v); }
 
+// Whether two of the n0 x n1 rows at element strides s0 and s1 share one of
+// their `width` elements: then the kernel's threads would write it in any
+// order. For outputs; inputs may be expanded.
+bool rows_meet(long long n0, int64_t s0, long long n1, int64_t s1, long long width) {
+  using Wide = __int128;  // products of sizes and strides
+  const Wide t0 = s0 < 0 ? -static_cast<Wide>(s0) : s0, t1 = s1 < 0 ? -static_cast<Wide>(s1) : s1;
+  if ((n0 > 1 && t0 < width) || (n1 > 1 && t1 < width)) return true;
+  if (n0 <= 1 || n1 <= 1) return false;
+  const Wide a = t0 < t1 ? t0 : t1, b = t0 < t1 ? t1 : t0;  // the closer rows and the farther ones
+  const Wide na = t0 < t1 ? n0 : n1, nb = t0 < t1 ? n1 : n0;
+  const Wide reach = (na - 1) * a + width;  // b at least that: none can meet, all usual layouts
+  for (Wide d = 1; d < nb && d * b < reach; ++d) {
+    const Wide e = d * b / a, off = d * b - e * a;  // the closest rows below and above
+    if ((e < na && off < width) || (e + 1 < na && a - off < width) || (e >= na && d * b - (na - 1) * a < width)) return true;
+  }
+  return false;
+}
+
 // what the two directions of the cache share
 dsa_status check_kv(const void* cache, int32_t num_pages, dsa_fmt fmt, int32_t kv_heads, int32_t head_dim, int32_t T,
                     int32_t B, int32_t max_pages, const void* k, const void* v, const int64_t (&strides)[4],
@@ -47,7 +65,8 @@ dsa_status check_attn(const dsa_attn_args& p) {
   if (!p.q || !p.out || !p.cache || !p.page_table || !p.seq_lens || !p.cu_q || !p.workspace) return DSA_ERR_INVALID_ARG;
   if (!aligned(p.q, 16) || !aligned(p.out, 16) || !aligned(p.cache, 256) || !aligned(p.workspace, 256) ||
       !aligned(p.lse, 4) || !aligned(p.mask, 4) || !aligned(p.page_table, 4) || !aligned(p.seq_lens, 4) ||
-      !aligned(p.cu_q, 4) || p.q_stride_t % 8 || p.q_stride_h % 8 || p.out_stride_t % 8 || p.out_stride_h % 8)
+      !aligned(p.cu_q, 4) || p.q_stride_t % 8 || p.q_stride_h % 8 || p.out_stride_t % 8 || p.out_stride_h % 8 ||
+      rows_meet(p.Tq, p.out_stride_t, p.heads, p.out_stride_h, p.head_dim))
     return DSA_ERR_INVALID_ARG;
   return DSA_OK;
 }
@@ -96,8 +115,11 @@ dsa_status dsa_rope_apply(dsa_ctx* ctx, const dsa_rope* rope, const void* x, voi
   const uintptr_t es = dtype == DSA_F32 ? 4 : 2;
   if (!aligned(x, es) || !aligned(y, es) || !aligned(pos, 4)) return DSA_ERR_INVALID_ARG;
   if (x == y && (x_stride_t != y_stride_t || x_stride_h != y_stride_h)) return DSA_ERR_INVALID_ARG;
+  if (y != x && rows_meet(T, y_stride_t, H, y_stride_h, D)) return DSA_ERR_INVALID_ARG;
   if (const dsa_status s = dsa::check_device(ctx)) return s;
   if (rope->device != ctx->device || static_cast<long long>(rot_start) + rope->rot_dim > D) return DSA_ERR_INVALID_ARG;
+  // in place only the rotated part is written
+  if (y == x && rows_meet(T, y_stride_t, H, y_stride_h, rope->rot_dim)) return DSA_ERR_INVALID_ARG;
   return dsa::launch_rope(ctx, rope, x, y, dtype, pos, T, H, D, rot_start, x_stride_t, x_stride_h, y_stride_t,
                           y_stride_h, inverse ? 1 : 0, as_stream(stream));
 }
@@ -137,6 +159,8 @@ dsa_status dsa_kv_load(dsa_ctx* ctx, const void* cache, int32_t num_pages, dsa_f
                                     cache_pos, seq_id, page_table))
     return s;
   if (T == 0) return DSA_OK;
+  if (rows_meet(T, k_stride_t, kv_heads, k_stride_h, head_dim) || rows_meet(T, v_stride_t, kv_heads, v_stride_h, head_dim))
+    return DSA_ERR_INVALID_ARG;
   if (const dsa_status s = dsa::check_device(ctx)) return s;
   return dsa::launch_kv_load(ctx, cache, num_pages, fmt, kv_heads, head_dim, cache_pos, seq_id, page_table, T, B,
                              max_pages, k, v, k_stride_t, k_stride_h, v_stride_t, v_stride_h, as_stream(stream));

@@ -276,6 +276,8 @@ dsa_status dsa_rope_destroy(dsa_rope* rope);
  * the type.
  *  x, y   (device) [T][H][D] of dtype, any strides of tokens and heads. y == x
  *         with the same strides rotates in place; otherwise they must not overlap.
+ *         Rows of y that share elements are refused (those of x may, unless in
+ *         place).
  *  pos    (device) [T] int32. A token whose position is out of range is not
  *         written and DSA_ERR_DEVICE_BOUNDS is recorded.
  * Any D, H and alignment of the type's own size; 16-byte aligned rows and
@@ -324,7 +326,8 @@ dsa_status dsa_kv_store(dsa_ctx* ctx, const void* k, const void* v, int64_t k_st
                         int32_t rot_start, dsa_stream_t stream);
 
 /* Read tokens back as bf16 (exact: the values the cache stands for) into k
- * and v, laid out and aligned as dsa_kv_store's. A token whose sequence,
+ * and v, laid out and aligned as dsa_kv_store's; rows that share elements are
+ * refused, and k and v must not overlap. A token whose sequence,
  * place or page is out of range reads as zeros, and DSA_ERR_DEVICE_BOUNDS is
  * recorded. */
 dsa_status dsa_kv_load(dsa_ctx* ctx, const void* cache, int32_t num_pages, dsa_fmt fmt, int32_t kv_heads,
@@ -341,7 +344,7 @@ typedef struct {
   const void* q;            /* (device) [Tq][heads][head_dim] bf16, 16-byte aligned */
   int64_t q_stride_t, q_stride_h;      /* multiples of 8 */
   void* out;                /* (device) [Tq][heads][head_dim] bf16, 16-byte aligned */
-  int64_t out_stride_t, out_stride_h;  /* multiples of 8 */
+  int64_t out_stride_t, out_stride_h;  /* multiples of 8; no two rows may share elements */
   float* lse;               /* (device) [Tq][heads] log of the sum of exp(score), or NULL */
   const void* cache;        /* (device) as written by dsa_kv_store, 256-byte aligned */
   int32_t num_pages;
