@@ -158,23 +158,39 @@ def _dev(t, dtype, shape=None, name="tensor"):
 # written to cost little where nothing is wrong: plain integers instead of
 # ctypes objects, one comparison per property, messages only on the way out.
 
-def _ptr(t, dtype, shape, name):
-    """data_ptr of a contiguous CUDA tensor of that type and shape (None: any)."""
+_current_device = None
+
+
+def _device():
+    """The current device's index: the calls enqueue there, and the library
+    compares it with the context's."""
+    global _current_device
+    if _current_device is None:
+        import torch
+        _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    return _current_device()
+
+
+def _ptr(t, dtype, shape, name, dev):
+    """data_ptr of a contiguous tensor of that type and shape (None: any) on
+    device `dev`."""
     try:
-        if t.dtype is dtype and t.is_cuda and t.is_contiguous() and (shape is None or t.shape == shape):
+        if t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and (shape is None or t.shape == shape):
             return t.data_ptr()
     except AttributeError:
         pass
     _dev(t, dtype, shape, name)       # says what is wrong
-    raise ValueError(f"{name} is not usable")
+    raise ValueError(f"{name} is on another device than the current one")
 
 
-def _rows(t, dtype, shape, name):
-    """Pointer and (token, head) strides of a [tokens, heads, dims] CUDA tensor
-    whose dims are contiguous."""
+def _rows(t, dtype, shape, name, dev):
+    """Pointer and (token, head) strides of a [tokens, heads, dims] tensor on
+    device `dev` whose dims are contiguous."""
     import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on another device than the current one")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.dim() != 3 or t.shape != shape:
@@ -355,9 +371,10 @@ class Context:
         if len(shape) != 3:
             raise ValueError(f"x must be [T, H, D], got {tuple(shape)}")
         T, H, D = shape
-        xp, xt, xh = _rows(x, dt, shape, "x")
-        yp, yt, yh = (xp, xt, xh) if out is None else _rows(out, dt, shape, "out")
-        st = lib().dsa_rope_apply(self._h, rope._open(), xp, yp, code, _ptr(pos, torch.int32, (T,), "pos"), T, H, D,
+        dev = _device()
+        xp, xt, xh = _rows(x, dt, shape, "x", dev)
+        yp, yt, yh = (xp, xt, xh) if out is None else _rows(out, dt, shape, "out", dev)
+        st = lib().dsa_rope_apply(self._h, rope._open(), xp, yp, code, _ptr(pos, torch.int32, (T,), "pos", dev), T, H, D,
                                   rot_start, xt, xh, yt, yh, 1 if inverse else 0, _raw_stream(stream))
         if st != 0:
             raise DsaError("dsa_rope_apply", st)
@@ -367,16 +384,16 @@ class Context:
         """dsa_kv_store: write [T, kv_heads, head_dim] bf16 keys (rotated when a
         plan is given) and values into the paged K/V cache."""
         import torch
-        i32, shape = torch.int32, k.shape
-        kp, kt, kh = _rows(k, torch.bfloat16, shape, "k")
-        vp, vt, vh = _rows(v, torch.bfloat16, shape, "v")
+        i32, shape, dev = torch.int32, k.shape, _device()
+        kp, kt, kh = _rows(k, torch.bfloat16, shape, "k", dev)
+        vp, vt, vh = _rows(v, torch.bfloat16, shape, "v", dev)
         T, n, D = shape
         B, max_pages = page_table.shape
         st = lib().dsa_kv_store(
-            self._h, kp, vp, kt, kh, vt, vh, _ptr(cache_pos, i32, (T,), "cache_pos"), _ptr(seq_id, i32, (T,), "seq_id"),
-            _ptr(page_table, i32, None, "page_table"), T, B, max_pages, n, D,
-            self._kv_cache(cache, num_pages, n, D, fmt), num_pages, fmt, None if rope is None else rope._open(),
-            None if rope_pos is None else _ptr(rope_pos, i32, (T,), "rope_pos"), rot_start, _raw_stream(stream))
+            self._h, kp, vp, kt, kh, vt, vh, _ptr(cache_pos, i32, (T,), "cache_pos", dev), _ptr(seq_id, i32, (T,), "seq_id", dev),
+            _ptr(page_table, i32, None, "page_table", dev), T, B, max_pages, n, D,
+            self._kv_cache(cache, num_pages, n, D, fmt, dev), num_pages, fmt, None if rope is None else rope._open(),
+            None if rope_pos is None else _ptr(rope_pos, i32, (T,), "rope_pos", dev), rot_start, _raw_stream(stream))
         if st != 0:
             raise DsaError("dsa_kv_store", st)
 
@@ -384,23 +401,23 @@ class Context:
         """dsa_kv_load: read tokens of the K/V cache back into k and v, [T,
         kv_heads, head_dim] bf16."""
         import torch
-        i32, shape = torch.int32, k.shape
-        kp, kt, kh = _rows(k, torch.bfloat16, shape, "k")
-        vp, vt, vh = _rows(v, torch.bfloat16, shape, "v")
+        i32, shape, dev = torch.int32, k.shape, _device()
+        kp, kt, kh = _rows(k, torch.bfloat16, shape, "k", dev)
+        vp, vt, vh = _rows(v, torch.bfloat16, shape, "v", dev)
         T, n, D = shape
         B, max_pages = page_table.shape
         st = lib().dsa_kv_load(
-            self._h, self._kv_cache(cache, num_pages, n, D, fmt), num_pages, fmt, n, D,
-            _ptr(cache_pos, i32, (T,), "cache_pos"), _ptr(seq_id, i32, (T,), "seq_id"),
-            _ptr(page_table, i32, None, "page_table"), T, B, max_pages, kp, vp, kt, kh, vt, vh, _raw_stream(stream))
+            self._h, self._kv_cache(cache, num_pages, n, D, fmt, dev), num_pages, fmt, n, D,
+            _ptr(cache_pos, i32, (T,), "cache_pos", dev), _ptr(seq_id, i32, (T,), "seq_id", dev),
+            _ptr(page_table, i32, None, "page_table", dev), T, B, max_pages, kp, vp, kt, kh, vt, vh, _raw_stream(stream))
         if st != 0:
             raise DsaError("dsa_kv_load", st)
 
     @staticmethod
-    def _kv_cache(cache, num_pages, kv_heads, head_dim, fmt):
+    def _kv_cache(cache, num_pages, kv_heads, head_dim, fmt, dev):
         """The cache's pointer, once it is known to hold that many pages."""
         import torch
-        p = _ptr(cache, torch.uint8, None, "cache")
+        p = _ptr(cache, torch.uint8, None, "cache", dev)
         key = (kv_heads, head_dim, fmt)
         size = _KV_PAGE_BYTES.get(key)
         if size is None:
@@ -421,21 +438,22 @@ class Context:
             raise ValueError("q must be a [Tq, heads, head_dim] tensor")
         shape = q.shape
         Tq, H, D = shape
-        qp, qt, qh = _rows(q, bf16, shape, "q")
-        op, ot, oh = _rows(out, bf16, shape, "out")
+        dev = _device()
+        qp, qt, qh = _rows(q, bf16, shape, "q", dev)
+        op, ot, oh = _rows(out, bf16, shape, "out", dev)
         B, max_pages = page_table.shape
         mp = words = 0
         if mask is not None:
             if mask.dim() != 2:
                 raise ValueError("mask must be [Tq, words]")
             words = mask.shape[1]
-            mp = _ptr(mask, i32, (Tq, words), "mask")
+            mp = _ptr(mask, i32, (Tq, words), "mask", dev)
         return _ATTN_PACK(
-            qp, qt, qh, op, ot, oh, 0 if lse is None else _ptr(lse, torch.float32, (Tq, H), "lse"),
-            self._kv_cache(cache, num_pages, kv_heads, D, fmt), num_pages, fmt, H, kv_heads, D,
-            _ptr(page_table, i32, None, "page_table"), max_pages, _ptr(seq_lens, i32, (B,), "seq_lens"),
-            _ptr(cu_q, i32, (B + 1,), "cu_q"), B, Tq, mp, words, D ** -0.5 if scale is None else scale,
-            _ptr(workspace, torch.uint8, None, "workspace"), workspace.numel())
+            qp, qt, qh, op, ot, oh, 0 if lse is None else _ptr(lse, torch.float32, (Tq, H), "lse", dev),
+            self._kv_cache(cache, num_pages, kv_heads, D, fmt, dev), num_pages, fmt, H, kv_heads, D,
+            _ptr(page_table, i32, None, "page_table", dev), max_pages, _ptr(seq_lens, i32, (B,), "seq_lens", dev),
+            _ptr(cu_q, i32, (B + 1,), "cu_q", dev), B, Tq, mp, words, D ** -0.5 if scale is None else scale,
+            _ptr(workspace, torch.uint8, None, "workspace", dev), workspace.numel())
 
     def tree_attn(self, q, cache, num_pages: int, fmt: int, kv_heads: int, page_table, seq_lens, cu_q, out,
                   workspace, mask=None, lse=None, scale=None, stream=None):
@@ -458,7 +476,7 @@ class Context:
         k = sel.shape[1]
         a = self._attn_args(q, cache, num_pages, fmt, kv_heads, page_table, seq_lens, cu_q, out, workspace, mask,
                             lse, scale)
-        st = lib().dsa_sparse_attn(self._h, a, _ptr(sel, torch.int32, (q.shape[0], k), "sel"), k, _raw_stream(stream))
+        st = lib().dsa_sparse_attn(self._h, a, _ptr(sel, torch.int32, (q.shape[0], k), "sel", q.get_device()), k, _raw_stream(stream))
         if st != 0:
             raise DsaError("dsa_sparse_attn", st)
 
