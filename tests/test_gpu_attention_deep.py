@@ -263,3 +263,17 @@ def test_first_tile_hidden_from_some_rows(ctx, fmt, D, nd, G):
     c.set_bits(bits)
     _rise(c)
     check_twice(c, ctx)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("steps,chunk,kv,G,D", [
+    (63, 1100, 2, 8, 128),      # the mean chooses 256 rows: the steps have 8 of them
+    (255, 512, 1, 8, 64),       # the mean chooses 32 rows: the chunk is 128 units
+    (40, 300, 2, 12, 64),       # the mean chooses 128 rows
+])
+def test_decode_steps_beside_a_chunk(ctx, fmt, steps, chunk, kv, G, D):
+    # a serving batch: one chunk of a prefill among decode steps, no mask
+    ctx_lens, nds = [(97 * i) % 1500 for i in range(steps)], [1] * steps
+    ctx_lens.insert(steps // 3, 700)
+    nds.insert(steps // 3, chunk)
+    check_twice(Case(steps, ctx_lens, nds, kv, G, D, fmt, masked=False), ctx)
