@@ -173,7 +173,14 @@ constexpr int smem_bytes() {
 template <class C>
 __device__ __forceinline__ int tiles_of(const AttnArgs& a, int nd, int len, int r) {
   int end = len;
-  if (!a.mask) end = len - nd + min(nd, static_cast<int>((static_cast<long long>(r + 1) * C::ROWS - 1) / a.G) + 1);
+  // Rows are below 2^31, so the tile's last one has 32 bits. In 64 the plan's
+  // divisions, one a row tile in one thread, and those of every unit's start
+  // took 26 of 440 us of a chunk of 4096 tokens (8 kv heads, G 8), 108 of 828
+  // with one kv head of 64 query heads.
+  if (!a.mask) {
+    const uint32_t seen = (static_cast<uint32_t>(r + 1) * C::ROWS - 1) / static_cast<uint32_t>(a.G) + 1;
+    end = len - nd + static_cast<int>(min(static_cast<uint32_t>(nd), seen));
+  }
   return max(1, (end + kTile - 1) / kTile);
 }
 

@@ -277,3 +277,15 @@ def test_decode_steps_beside_a_chunk(ctx, fmt, steps, chunk, kv, G, D):
     ctx_lens.insert(steps // 3, 700)
     nds.insert(steps // 3, chunk)
     check_twice(Case(steps, ctx_lens, nds, kv, G, D, fmt, masked=False), ctx)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("ctx_lens,nds,kv,G", [
+    ([0], [1500], 1, 64),                       # 375 row tiles of four tokens
+    ([100, 64, 3], [700, 513, 1], 2, 40),       # a token ends inside a row tile
+    ([0, 63, 2000, 5], [400, 0, 900, 64], 3, 1),    # 256 tokens a row tile
+    ([31, 0, 65], [257, 255, 256], 1, 7),
+])
+def test_chunks_of_many_row_tiles(ctx, fmt, ctx_lens, nds, kv, G):
+    # the plan counts row tiles by their number of key tiles; cuts fall anywhere in them
+    check_twice(Case(3 + G, ctx_lens, nds, kv, G, 64, fmt, masked=False), ctx)
