@@ -5,10 +5,11 @@
 // (no scales in bf16), so one head's keys of a page are one contiguous tile.
 // In fp8 (e4m3) and fp4 (e2m1) 32 dimensions share a power-of-two scale, a
 // byte holding its exponent + 127: the OCP microscaling formats MXFP8 and
-// MXFP4, with the exponent rounded up so that no value saturates. A stored
-// value is then a bf16 number exactly: a code has at most 4 significant bits
-// and the scale moves only the exponent. Reading back loses nothing, and the
-// attention's bf16 tensor-core operands are the stored values themselves.
+// MXFP4, with the exponent rounded up so that no value saturates below the
+// largest scale (448 * 2^119, 6 * 2^125). A stored value is then a bf16 number
+// exactly: a code has at most 4 significant bits and the scale moves only the
+// exponent. Reading back loses nothing, and the attention's bf16 tensor-core
+// operands are the stored values themselves.
 #pragma once
 #include <cuda_bf16.h>
 

@@ -297,9 +297,10 @@ dsa_status dsa_rope_apply(dsa_ctx* ctx, const dsa_rope* rope, const void* x, voi
  *                 nibble), SB = head_dim / 32
  * In fp8 and fp4, 32 dimensions share the power of two 2^e, stored as the
  * byte e + 127: e is the smallest integer with max|y| <= 448 * 2^e (fp8) or
- * 6 * 2^e (fp4), within -117 .. 119 or -125 .. 125, so a code never saturates
- * and a stored value is a bf16 number exactly (OCP microscaling layouts with
- * the exponent rounded up). 32 dimensions of which one is not finite get the
+ * 6 * 2^e (fp4), within -117 .. 119 or -125 .. 125, so a stored value is a
+ * bf16 number exactly and a code saturates only beyond 448 * 2^119 (2.98e38)
+ * or 6 * 2^125 (2.55e38) (OCP microscaling layouts with the exponent rounded
+ * up). 32 dimensions of which one is not finite get the
  * byte 255 and read as NaN. Not the index cache's scales: those are one fp32
  * per token. Returns 0 for unsupported arguments. */
 size_t dsa_kv_page_bytes(int32_t kv_heads, int32_t head_dim, dsa_fmt fmt);
