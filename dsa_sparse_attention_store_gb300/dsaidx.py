@@ -493,7 +493,8 @@ class Context:
             raise DsaError("dsa_selftest_bounded_wait", st)
 
     def set_slot_output(self, on: bool = True):
-        """Top-k returns cache slots (page * 64 + offset) instead of positions."""
+        """Top-k returns cache slots (page * 64 + offset) instead of positions, and
+        sparse_attn() reads its selection as slots."""
         st = lib().dsa_ctx_set_slot_output(self._h, 1 if on else 0)
         if st != 0:
             raise DsaError("dsa_ctx_set_slot_output", st)

@@ -152,7 +152,10 @@ dsa_status dsa_ctx_set_hadamard(dsa_ctx* ctx, int32_t on);
  * sparse attention gathers), instead of its position pos; padding stays -1.
  * The pages feed the selected tokens to the attention ("The Crash That
  * Changed Direction", section "The Experiment: Why fp32?"); the slot is what
- * a paged gather needs. Off by default; applies to the calls made after it. */
+ * a paged gather needs. dsa_sparse_attn reads its selection by the same
+ * setting: a top-k and the attention over its answer are called under one
+ * setting, and a caller that changes it in between changes how the other's
+ * selection is read. Off by default; applies to the calls made after it. */
 dsa_status dsa_ctx_set_slot_output(dsa_ctx* ctx, int32_t on);
 
 /* Upper bound of the workspace bytes dsa_index_topk needs for these sizes.
@@ -377,6 +380,9 @@ size_t dsa_attn_workspace_size(const dsa_ctx* ctx, int32_t head_dim);
  * are left out and DSA_ERR_DEVICE_BOUNDS recorded; so are whole sequences
  * whose lengths are inconsistent (their rows are not written).
  * A row all of whose visible scores are -inf counts as one that sees no key.
+ * Sums over the keys are fp32, taken before the division by the weights' sum
+ * with weights of up to 2^8: they stay finite where the visible |v| add up to
+ * less than 2^119.
  * Tq * heads < 2^31, kv_heads <= 65536, 64 * num_pages < 2^31 and, in bf16,
  * 128 * num_pages * kv_heads < 2^31, else DSA_ERR_UNSUPPORTED. Results do not
  * depend on timing. */
