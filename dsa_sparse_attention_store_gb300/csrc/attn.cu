@@ -205,8 +205,12 @@ dsa_status launch_attn(dsa_ctx* ctx, const dsa_attn_args& p, const int32_t* sel,
   // the few-row forms up to 32 rows: 64 sequences of 2048 to 16384 tokens, 8 kv
   // heads, bf16 (fp8), take with 8 rows 368 (350) us in them and 385 (356) in
   // the 128-row form, with 32 rows 375 (355) and 389 (363), and with 64 rows,
-  // which read the cache twice there, 729 (682) and 399 (395). 2048 selections of
-  // 512 keys, G 8: 577 (864) and 614 (870), but 796 and 776 in fp4
+  // which read the cache twice there, 729 (682) and 399 (395). Selections, 8 kv
+  // heads, G 8, D 128: 2048 of 512 keys in bf16 575 and 616; 512 of 2048 keys in
+  // fp8 (fp4) 804 (738) and 824 (741), 8192 of 128 keys 1051 (949) and 1177
+  // (1099), but 2048 of 512 keys 874 (809) and 863 (772), 3495 of 300 keys 1047
+  // (967) and 979 (882). In fp8 and fp4 the 128-row form is ahead for units of 5
+  // to 8 tiles alone (and not for D 64 in fp4): the rule does not follow that dip
   const bool few = sel ? a.G <= kFewRows : static_cast<long long>(p.Tq) * a.G <= static_cast<long long>(kFewRows) * p.B;
   const int form = sel ? (few ? kSparseFew : kSparse) : wide ? kWide : few ? kTreeFew : kTree;
   const int grid = form == kWide ? ctx->num_sms : 2 * ctx->num_sms, rows = form == kWide ? 256 : few ? kFewRows : 128;

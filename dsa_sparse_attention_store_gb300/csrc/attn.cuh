@@ -52,17 +52,21 @@
 // What bounds it, and what it measures (device time of a call, join included,
 // against a copy rate of 6.79 TB/s and 1909 bf16 TFLOP/s):
 //  - one token of 64 sequences of 2048 to 16384, 8 kv heads, G 8, D 128, bf16:
-//    HBM. 361 to 368 us, 6.6 TB/s. In fp8 350 us: the loaders' work on a tile.
+//    HBM. 361 to 368 us, 6.6 TB/s. In fp8 350 us, fp4 335: the loaders' work on
+//    a tile.
 //  - 2048 tokens behind 8192, the same heads: the softmax of 64 keys takes about
-//    2000 cycles of a group beside the products' 1330 (two groups). 505 us,
-//    1220 TFLOP/s.
+//    2000 cycles of a group beside the products' 1330 (two groups; tensor pipe
+//    52 %, issue slots 47 % busy). 508 us, 1220 TFLOP/s. In fp8 and fp4 675:
+//    widening joins the chain.
 //  - 8 tokens of 8 sequences of 131072, 4 kv heads, G 16, fp8: the chain of a
 //    tile (scores, softmax, values: 276 us with a bf16 cache out of L2) and the
 //    loaders, which share the issue slots with it (58 % busy; 300 us without the
-//    widening's arithmetic). 344 us, 3.2 TB/s, 800 TFLOP/s.
+//    widening's arithmetic). 347 us, 3.2 TB/s, 790 TFLOP/s.
 //  - 2048 queries over 512 keys each, 8 kv heads, G 8, bf16: the loaders' time
-//    to issue gathers (75 cycles each) and the start of a unit every 8 tiles. 578
-//    us, 7.4 TB/s out of L2.
+//    to issue gathers (75 cycles each) and the start of a unit every 8 tiles;
+//    nothing is saturated (issue slots 42 %, tensor pipe 39 % for 128 rows of
+//    which 8 are real, L2 31 %). 575 us, 7.4 TB/s out of L2. In fp8 880, fp4 810:
+//    widening 64 keys and values for 8 rows.
 #pragma once
 #include <type_traits>
 
@@ -175,7 +179,7 @@ __device__ __forceinline__ int tiles_of(const AttnArgs& a, int nd, int len, int 
   int end = len;
   // Rows are below 2^31, so the tile's last one has 32 bits. In 64 the plan's
   // divisions, one a row tile in one thread, and those of every unit's start
-  // took 26 of 440 us of a chunk of 4096 tokens (8 kv heads, G 8), 108 of 828
+  // took 23 of 440 us of a chunk of 4096 tokens (8 kv heads, G 8), 114 of 828
   // with one kv head of 64 query heads.
   if (!a.mask) {
     const uint32_t seen = (static_cast<uint32_t>(r + 1) * C::ROWS - 1) / static_cast<uint32_t>(a.G) + 1;

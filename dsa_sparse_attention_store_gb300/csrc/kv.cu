@@ -10,10 +10,11 @@
 // fp32 with every product and sum rounded separately and the rotated value is
 // rounded once, to the cache's format.
 //
-// Bound: for long batches HBM and, when writing fp8 or fp4, the quantising
-// instructions; the dependent loads for short ones. 22528 tokens x 8 heads x
-// 128: written and read back in 64 us bf16 (floor 54), 63 us fp8 (41), 57 us
-// fp4 (34; store 44, load 22 with launch overhead); 64 tokens 3.7 us.
+// Bound: for long batches HBM in bf16; writing fp8 or fp4, the quantising
+// instructions and the loads they wait for (fp4: issue slots 57 % busy, integer
+// pipe 46 %, DRAM 36 %); the dependent loads for short ones. 22528 tokens x 8
+// heads x 128: written and read back in 63 us bf16 (floor 54), 60 us fp8 (41),
+// 56 us fp4 (34; store 38 to 44, load 22 with launch overhead); 64 tokens 3.9 us.
 #include <cuda_fp4.h>
 #include <cuda_fp8.h>
 
