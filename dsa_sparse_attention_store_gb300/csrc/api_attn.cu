@@ -71,6 +71,26 @@ dsa_status check_attn(const dsa_attn_args& p) {
   return DSA_OK;
 }
 
+// sequences (and groups) of the calls that list their units
+constexpr int32_t kMaxListed = 1 << 20;
+
+bool listable(int32_t Tq, int32_t B, int32_t heads, int32_t kv_heads, int32_t head_dim) {
+  return Tq >= 0 && B > 0 && B <= kMaxListed && heads > 0 && kv_heads > 0 && heads % kv_heads == 0 &&
+         static_cast<long long>(Tq) * heads <= 0x7FFFFFFFLL && (head_dim == 64 || head_dim == 128);
+}
+
+dsa_status check_span(const dsa_attn_args& p, const dsa_span& s) {
+  if (const dsa_status st = check_attn(p)) return st;
+  if (s.window < 0 || !(s.cap >= 0.0) || !aligned(s.first, 4) || !aligned(s.last, 4) || !aligned(s.slopes, 4))
+    return DSA_ERR_INVALID_ARG;
+  if (s.cap != 0.0) {  // as the kernels have them: cap log2 e, 2 log2 e scale / cap
+    const float c = static_cast<float>(s.cap * 1.4426950408889634), x = static_cast<float>(p.scale / s.cap * 2.8853900817779268);
+    if (!(c >= 1.17549435e-38f) || !std::isfinite(c) || !(x >= 1.17549435e-38f) || !std::isfinite(x)) return DSA_ERR_INVALID_ARG;
+  }
+  if (p.B > kMaxListed || (s.slopes && p.mask)) return DSA_ERR_UNSUPPORTED;
+  return DSA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -190,6 +210,77 @@ dsa_status dsa_sparse_attn(dsa_ctx* ctx, const dsa_attn_args* args, const int32_
   if (const dsa_status s = dsa::check_device(ctx)) return s;
   if (args->ws_bytes < dsa::attn_workspace(ctx, args->head_dim)) return DSA_ERR_WORKSPACE;
   return dsa::launch_attn(ctx, *args, sel, k, as_stream(stream));
+}
+
+size_t dsa_span_attn_workspace_size(const dsa_ctx* ctx, int32_t Tq, int32_t B, int32_t heads, int32_t kv_heads,
+                                    int32_t head_dim) {
+  if (!ctx || !listable(Tq, B, heads, kv_heads, head_dim)) return 0;
+  return dsa::span_workspace(ctx, Tq, B, 0, heads, kv_heads, head_dim);
+}
+
+dsa_status dsa_span_attn(dsa_ctx* ctx, const dsa_attn_args* args, const dsa_span* span, dsa_stream_t stream) {
+  if (!ctx || !args) return DSA_ERR_INVALID_ARG;
+  const dsa_span none = {};
+  if (!span) span = &none;
+  if (const dsa_status s = check_span(*args, *span)) return s;
+  if (args->Tq == 0) return DSA_OK;
+  if (const dsa_status s = dsa::check_device(ctx)) return s;
+  if (args->ws_bytes < dsa::span_workspace(ctx, args->Tq, args->B, 0, args->heads, args->kv_heads, args->head_dim))
+    return DSA_ERR_WORKSPACE;
+  return dsa::launch_span(ctx, *args, *span, nullptr, nullptr, 0, as_stream(stream));
+}
+
+size_t dsa_shared_attn_workspace_size(const dsa_ctx* ctx, int32_t Tq, int32_t B, int32_t n_groups, int32_t heads,
+                                      int32_t kv_heads, int32_t head_dim) {
+  if (!ctx || !listable(Tq, B, heads, kv_heads, head_dim) || n_groups <= 0 || n_groups > kMaxListed) return 0;
+  return dsa::span_workspace(ctx, Tq, B, n_groups, heads, kv_heads, head_dim);
+}
+
+dsa_status dsa_shared_attn(dsa_ctx* ctx, const dsa_attn_args* args, const dsa_span* span, const int32_t* cu_groups,
+                           const int32_t* shared_lens, int32_t n_groups, dsa_stream_t stream) {
+  if (!ctx || !args) return DSA_ERR_INVALID_ARG;
+  const dsa_span none = {};
+  if (!span) span = &none;
+  if (const dsa_status s = check_span(*args, *span)) return s;
+  if (n_groups <= 0) return DSA_ERR_INVALID_ARG;
+  if (n_groups > kMaxListed) return DSA_ERR_UNSUPPORTED;
+  if (args->Tq == 0) return DSA_OK;
+  if (!cu_groups || !shared_lens || !aligned(cu_groups, 4) || !aligned(shared_lens, 4)) return DSA_ERR_INVALID_ARG;
+  if (const dsa_status s = dsa::check_device(ctx)) return s;
+  if (args->ws_bytes < dsa::span_workspace(ctx, args->Tq, args->B, n_groups, args->heads, args->kv_heads, args->head_dim))
+    return DSA_ERR_WORKSPACE;
+  return dsa::launch_span(ctx, *args, *span, cu_groups, shared_lens, n_groups, as_stream(stream));
+}
+
+dsa_status dsa_batch_plan(dsa_ctx* ctx, const int32_t* old_lens, const int32_t* new_lens, const int32_t* own_from, int32_t B,
+                          int32_t* page_table, int32_t max_pages, int32_t num_pages, int32_t* free_pages, int32_t free_cap,
+                          const int32_t* free_count, int32_t* free_left, int32_t* seq_lens, int32_t* cu_q, int32_t* seq_id,
+                          int32_t* cache_pos, int32_t* slots, int32_t T, dsa_stream_t stream) {
+  if (!ctx || B <= 0 || T < 0 || max_pages <= 0 || num_pages <= 0 || free_cap < 0) return DSA_ERR_INVALID_ARG;
+  if (B > 65536 || max_pages > 0x7FFFFFFF / 64 || num_pages > 0x7FFFFFFF / 64) return DSA_ERR_UNSUPPORTED;
+  if (!old_lens || !new_lens || !page_table || (!free_pages && free_cap) || !free_count || !free_left || !seq_lens || !cu_q ||
+      (T && (!seq_id || !cache_pos)))
+    return DSA_ERR_INVALID_ARG;
+  struct Span {
+    const int32_t* p;
+    long long n;
+  };
+  // what is written comes first
+  const Span spans[] = {{page_table, static_cast<long long>(B) * max_pages}, {free_pages, free_cap}, {free_left, 1},
+                        {seq_lens, B}, {cu_q, B + 1LL}, {seq_id, T}, {cache_pos, T}, {slots, T},
+                        {old_lens, B}, {new_lens, B}, {own_from, B}, {free_count, 1}};
+  constexpr int kAll = sizeof(spans) / sizeof(spans[0]), kWritten = 8;
+  for (int i = 0; i < kAll; ++i) {
+    if (!aligned(spans[i].p, 4)) return DSA_ERR_INVALID_ARG;
+    for (int j = 0; j < i && j < kWritten; ++j)
+      if (spans[i].p && spans[j].p && spans[i].p < spans[j].p + spans[j].n && spans[j].p < spans[i].p + spans[i].n)
+        return DSA_ERR_INVALID_ARG;
+  }
+  if (const dsa_status s = dsa::check_device(ctx)) return s;
+  dsa::BatchPlanArgs a = {old_lens, new_lens, own_from, free_count, page_table, free_pages, free_left, seq_lens,
+                          cu_q,     seq_id,   cache_pos, slots,     ctx->status, B,         T,         max_pages,
+                          num_pages, free_cap};
+  return dsa::launch_batch_plan(ctx, a, as_stream(stream));
 }
 
 }  // extern "C"

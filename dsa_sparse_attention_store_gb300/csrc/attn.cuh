@@ -108,21 +108,53 @@ struct AttnArgs {
   int B, Tq, max_pages, num_pages, kv_heads, G, k, mask_words, slots;
 };
 
+// Units of the span form come from a list that its plan kernel writes (attn_span.cu):
+// up to 128 or 256 rows of neighbouring tokens and the tiles that one of them sees.
+struct Unit {
+  int b, q0, nd, len;     // row of the page table; first query, queries and keys of the rows' sequence (or group)
+  int r0, t0, t1, base;   // first row among those queries' rows; tiles; whether the rows have sums over a shared prefix
+  int lo, full, pad0, pad1;  // every row sees the places from lo to before full
+};
+
+// What a token sees: the places [lo, hi) of its sequence, and where it lies
+// itself. ctx: places from there on are the new tokens, which a mask may hide.
+struct Token {
+  int lo, hi, place, ctx;
+};
+
+struct SpanArgs : AttnArgs {
+  const int4* units;   // [slots][3], the words of a Unit
+  const int* tiles;    // [slots] tiles of a unit, 0 where there is none
+  const int4* tokens;  // [Tq]
+  const float* slopes; // [heads] or null
+  float cap2, to_cap;  // cap log2 e, scale / cap; 0: no cap
+  int units_n;
+  int base_mode;       // rows' sums over a shared prefix: 1 these are they, 2 join them where the unit has some
+  float2* base_ml;     // [Tq][heads]
+  float* base;         // [Tq][heads][D]
+};
+
 // One stretch of a unit's key tiles.
 struct Seg {
   int b, h;
   int r0, rows;       // first row of the unit among its sequence's rows, and how many
   int q0, nd, len;    // the sequence's first query, its queries, its keys (a selection: the query itself, ...)
-  int t0, t1, nt;     // tiles [t0, t1) of nt
+  int t0, t1, nt;     // tiles [t0, t1) of the unit's, which end before nt
   int full;           // keys before this position are visible to every row
+};
+struct SpanSeg : Seg {
+  int tb, lo, base;   // the unit's first tile; `full` holds from this position on; Unit::base
 };
 
 struct Start {
   int b, h, r, tile;
 };
 
-template <int FMT, int D, int FORM>
+template <int FMT, int D, int FORM, bool LISTED = false>
 struct Cfg {
+  static constexpr bool SPAN = LISTED;
+  using Args = std::conditional_t<LISTED, SpanArgs, AttnArgs>;
+  using Segment = std::conditional_t<LISTED, SpanSeg, Seg>;
   static constexpr bool SPARSE = FORM == kSparse || FORM == kSparseFew;
   static constexpr bool FEW = FORM == kTreeFew || FORM == kSparseFew;
   static constexpr bool TWO = FORM == kWide || FEW;    // two score buffers, queries in shared memory, warps that issue the products
@@ -203,18 +235,45 @@ __device__ __forceinline__ bool read_seq(const AttnArgs& a, int b, int& q0, int&
 
 template <class C>
 struct Iter {
-  const AttnArgs& a;
+  const typename C::Args& a;
   long long left;
-  int b, h, r, tile;
+  int b, h, r, tile;  // span form: b is the unit's place in the list
   int q0, nd, len, nrt;
   bool ok;
-  __device__ Iter(const AttnArgs& a_, const Start& s, long long n) : a(a_), left(n), b(s.b), h(s.h), r(s.r), tile(s.tile) {
+  __device__ Iter(const typename C::Args& a_, const Start& s, long long n) : a(a_), left(n), b(s.b), h(s.h), r(s.r), tile(s.tile) {
+    if constexpr (!C::SPAN) start();
+  }
+  __device__ void start() {
     ok = read_seq(a, b, q0, nd, len);
     nrt = static_cast<int>((static_cast<long long>(nd) * a.G + C::ROWS - 1) / C::ROWS);
   }
   // the next stretch; a selection's r is its query
-  __device__ bool next(Seg& s) {
+  __device__ bool next(typename C::Segment& s) {
     if (left <= 0) return false;
+    if constexpr (C::SPAN) {
+      int n;
+      while ((n = a.tiles[b]) == 0) advance();
+      const int4 x = a.units[3 * b], y = a.units[3 * b + 1], z = a.units[3 * b + 2];
+      s.b = x.x;
+      s.q0 = x.y;
+      s.nd = x.z;
+      s.len = x.w;
+      s.r0 = y.x;
+      s.tb = y.y;
+      s.nt = y.z;
+      s.base = y.w;
+      s.lo = z.x;
+      s.full = z.y;
+      s.rows = static_cast<int>(min(static_cast<long long>(C::ROWS), static_cast<long long>(s.nd) * a.G - s.r0));
+      s.h = h;
+      s.t0 = s.tb + tile;
+      const long long room = s.nt - s.t0;
+      s.t1 = left < room ? s.t0 + static_cast<int>(left) : s.nt;
+      left -= s.t1 - s.t0;
+      tile = 0;
+      advance();
+      return true;
+    }
     if constexpr (C::SPARSE) {
       while (b + 1 < a.B && a.cu_q[b + 1] <= r) {
         ++b;
@@ -266,12 +325,20 @@ struct Iter {
     }
     return true;
   }
+  // span form: the next place of the list, then the next kv head's turn at it
+  __device__ void advance() {
+    if constexpr (C::SPAN)
+      if (++b == a.units_n) {
+        b = 0;
+        ++h;
+      }
+  }
 };
 
 // The launch's tiles, and where this CTA's range begins. Every thread of
 // the block calls it; the result is in sh.
 template <class C>
-__device__ __forceinline__ void make_plan(const AttnArgs& a, Shared& sh, int cta, int grid, long long& begin, long long& count) {
+__device__ __forceinline__ void make_plan(const typename C::Args& a, Shared& sh, int cta, int grid, long long& begin, long long& count) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   long long total;
   constexpr int kThreads = C::THREADS;
@@ -297,10 +364,13 @@ __device__ __forceinline__ void make_plan(const AttnArgs& a, Shared& sh, int cta
     __syncthreads();
     return;
   }
-  // each thread adds up a run of sequences; a scan over the threads places them
-  const int per = (a.B + kThreads - 1) / kThreads;
-  const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
+  // each thread adds up a run of sequences (or of the list); a scan over the threads places them
+  int N = a.B;
+  if constexpr (C::SPAN) N = a.units_n;
+  const int per = (N + kThreads - 1) / kThreads;
+  const int b0 = min(N, tid * per), b1 = min(N, b0 + per);
   auto weigh = [&](int b) -> long long {
+    if constexpr (C::SPAN) return a.tiles[b];
     int q0, nd, len;
     if (!read_seq(a, b, q0, nd, len)) {
       if (cta == 0) atomicOr(a.status, DSA_DEV_BOUNDS);
@@ -332,9 +402,24 @@ __device__ __forceinline__ void make_plan(const AttnArgs& a, Shared& sh, int cta
     total += sh.scan[w];
   }
   const long long ex = before + inc - sum;
+  [[maybe_unused]] const long long head = total;  // span form: the list's tiles, which every kv head has
+  if constexpr (C::SPAN) total *= a.kv_heads;
   const long long n = total < grid ? total : grid;
   begin = cta < n ? total * cta / n : total;
   count = cta < n ? total * (cta + 1) / n - begin : 0;
+  if constexpr (C::SPAN) {
+    if (count > 0) {
+      const long long h = begin / head;
+      long long x = begin - h * head - ex;
+      if (0 <= x && x < sum) {
+        int b = b0;
+        for (long long w; x >= (w = weigh(b)); ++b) x -= w;
+        sh.start = Start{b, static_cast<int>(h), 0, static_cast<int>(x)};
+      }
+    }
+    __syncthreads();
+    return;
+  }
   if (count > 0 && ex <= begin && begin < ex + sum) {
     long long x = begin - ex;
     int b = b0;
@@ -367,6 +452,24 @@ __device__ __forceinline__ unsigned long long low_bits(int n) {
   return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1;
 }
 
+// Of the 64 keys from position p0 on, those that token `token`, which sees `y`, may see.
+__device__ __forceinline__ unsigned long long span_mask(const AttnArgs& a, long long token, const Token& y, int p0) {
+  unsigned long long m = low_bits(y.hi - p0) & ~low_bits(y.lo - p0);
+  if (a.mask && p0 + 64 > y.ctx) {
+    const uint32_t* w = a.mask + token * a.mask_words;
+    auto word = [&](int j) -> uint32_t { return j < a.mask_words ? w[j] : 0u; };
+    const int n = y.ctx - p0;  // committed keys of the tile, if positive
+    if (n > 0) {
+      m &= low_bits(n) | ((word(0) | (static_cast<unsigned long long>(word(1)) << 32)) << n);
+    } else {
+      const int j = -n >> 5, sh = -n & 31;
+      const uint32_t w0 = word(j), w1 = word(j + 1), w2 = word(j + 2);
+      m &= __funnelshift_r(w0, w1, sh) | (static_cast<unsigned long long>(__funnelshift_r(w1, w2, sh)) << 32);
+    }
+  }
+  return m;
+}
+
 // Of the 64 keys from position p0 on, those that a row of query i may see (tree form).
 __device__ __forceinline__ unsigned long long row_mask(const AttnArgs& a, const Seg& s, int i, int p0) {
   const int ctx = s.len - s.nd;
@@ -384,22 +487,63 @@ __device__ __forceinline__ unsigned long long row_mask(const AttnArgs& a, const 
   return low_bits(n) | ((word(0) | (static_cast<unsigned long long>(word(1)) << 32)) << n);
 }
 
+// The place a token measures its keys' distance from: its own, or the nearest
+// that it sees. Softmax takes no notice of the difference; exponents stay small
+// for the keys that matter where all of them are far away. away(): how far that
+// place is, for lse.
+__device__ __forceinline__ int nearest(const Token& y) { return max(y.lo, min(y.place, y.hi - 1)); }
+__device__ __forceinline__ float away(const Token& y) { return fabsf(static_cast<float>(y.place - nearest(y))); }
+
+// Capped and biased scores of 64 keys, as exponents of 2: q.k -> cap tanh(scale
+// q.k / cap) - slope |from - j|, or as they are where there is neither.
+// tanh y = 1 - 2 / (1 + e^2y): within 2^-22 of 1, for infinities too.
+__device__ __forceinline__ void change_scores(const SpanArgs& a, uint32_t (&x)[2][32], float slope2, int from) {
+  if (a.cap2 != 0.f) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const float e = ex2(__uint_as_float(x[c][i]) * (a.to_cap * 2.8853900817779268f));
+        x[c][i] = __float_as_uint(fmaf(-2.f * a.cap2, rcp(1.f + e), a.cap2));
+      }
+  } else if (a.slopes) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int i = 0; i < 32; ++i) x[c][i] = __float_as_uint(__uint_as_float(x[c][i]) * a.scale2);
+  }
+  if (a.slopes) {
+    const float f = static_cast<float>(from);
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        x[c][i] = __float_as_uint(fmaf(-slope2, fabsf(f - static_cast<float>(32 * c + i)), __uint_as_float(x[c][i])));
+  }
+}
+
 __device__ __forceinline__ float widen_one(uint32_t bits) { return __uint_as_float(bits << 16); }
 
 // Adds the values that are not finite, of the pages [t0, t1) that hold keys
 // only some rows see, to the rows that see them. Only reached where a loader
 // found one.
-template <int FMT, int D>
-__device__ __noinline__ void fix_nonfinite(const AttnArgs& a, const Seg& s, int t0, int t1, int i, bool valid, uint32_t o_taddr) {
+template <int FMT, int D, class Segment>
+__device__ __noinline__ void fix_nonfinite(const AttnArgs& a, const Segment& s, int t0, int t1, int i, bool valid, uint32_t o_taddr,
+                                           const Token tok = Token{}) {
   using L = kvf::Layout<FMT, D>;
   for (int d = 0; d < D; ++d) {
     float add = 0.f;
     for (int t = t0; t < t1; ++t) {
       if (t * kTile >= s.len) break;
+      constexpr bool SPAN = std::is_same_v<Segment, SpanSeg>;
+      if constexpr (SPAN) {
+        if (t * kTile >= s.lo && (t + 1) * kTile <= s.full) continue;  // tiles that every row sees kept theirs
+      }
       const int page = a.page_table[static_cast<long long>(s.b) * a.max_pages + t];
       if (page < 0 || page >= a.num_pages) continue;
       const uint8_t* blk = a.cache + (static_cast<long long>(page) * a.kv_heads + s.h) * L::HEAD_BYTES;
-      unsigned long long m = valid ? row_mask(a, s, i, t * kTile) & low_bits(s.len - t * kTile) : 0ull;
+      unsigned long long m = !valid ? 0ull : SPAN ? span_mask(a, s.q0 + i, tok, t * kTile) : row_mask(a, s, i, t * kTile);
+      m &= low_bits(s.len - t * kTile);
       while (m) {
         const int j = __ffsll(static_cast<long long>(m)) - 1;
         m &= m - 1;
@@ -418,10 +562,11 @@ __device__ __noinline__ void fix_nonfinite(const AttnArgs& a, const Seg& s, int 
   }
 }
 
-template <int FMT, int D, int FORM>
-__global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>::CTAS)
-    attn_kernel(const __grid_constant__ CUtensorMap tm, const AttnArgs a) {
-  using C = Cfg<FMT, D, FORM>;
+template <int FMT, int D, int FORM, bool LISTED>
+__global__ void __launch_bounds__(Cfg<FMT, D, FORM, LISTED>::THREADS, Cfg<FMT, D, FORM, LISTED>::CTAS)
+    attn_kernel(const __grid_constant__ CUtensorMap tm, const typename Cfg<FMT, D, FORM, LISTED>::Args a) {
+  using C = Cfg<FMT, D, FORM, LISTED>;
+  using Segment = typename C::Segment;
   using L = kvf::Layout<FMT, D>;
   constexpr int NSW = C::SW * C::WG;  // softmax warps
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -537,7 +682,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
     }
     __syncwarp();
   };
-  auto has_rows = [&](int wg, const Seg& g) { return wg * C::QROWS < g.rows; };
+  auto has_rows = [&](int wg, const Segment& g) { return wg * C::QROWS < g.rows; };
 
   if (count <= 0) {
     if (tid == 0) a.meta[2 * cta] = make_int4(0, 0, 0, 0);
@@ -549,7 +694,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
     const uint32_t tO = tb + C::O + lanes;
     const bool issues = !C::TWO && gw == 0;  // this warp issues the products
     Iter<C> it(a, sh.start, count);
-    Seg s;
+    Segment s;
     bool more = it.next(s), run = true;
     int seg = 0, n = 0;   // segments, tiles
     int ns = 0;           // tiles this group has worked on: score buffers and accumulator phases
@@ -558,30 +703,44 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
     if (tid == 0) a.meta[2 * cta] = make_int4(0, 0, 0, 0);
     const int row = tid;  // of the unit
     // a row's query (in its sequence; 0 of a selection, whose rows are one token's) and head of the group
-    struct Row {
+    struct Plain {
       int q, g;
     };
-    auto row_at = [&](const Seg& g) -> Row {
-      if (C::SPARSE) return Row{0, row};
-      const int r = g.r0 + row, q = r / a.G;
-      return Row{q, r - q * a.G};
+    struct Listed {  // what it sees, too, and the slope of its bias
+      int q, g;
+      Token tok;
+      float slope2;
     };
-    auto query = [&](const Seg& g, Row r) {
+    using Row = std::conditional_t<C::SPAN, Listed, Plain>;
+    auto row_at = [&](const Segment& g) -> Row {
+      Row x = {0, row};
+      if (C::SPARSE) return x;
+      const int r = g.r0 + row;
+      x.q = r / a.G;
+      x.g = r - x.q * a.G;
+      return x;
+    };
+    auto query = [&](const Segment& g, Row r) {
       return a.q + static_cast<long long>(g.q0 + r.q) * a.qt + static_cast<long long>(g.h * a.G + r.g) * a.qh;
     };
     // the next unit's queries on their way to L1
-    auto warm = [&](const Seg& g) {
+    auto warm = [&](const Segment& g) {
       if (row < g.rows) {
         const __nv_bfloat16* q = query(g, row_at(g));
 #pragma unroll
         for (int i = 0; i < C::NBLK; ++i) touch(q + 64 * i);
       }
     };
-    Row at_row = {0, 0};
+    Row at_row = {};
     // the unit's queries, then its first tiles' scores
-    auto start_unit = [&](const Seg& g) {
+    auto start_unit = [&](const Segment& g) {
       const bool valid = row < g.rows;
       at_row = row_at(g);
+      if constexpr (C::SPAN) {
+        const int4 y = valid ? a.tokens[g.q0 + at_row.q] : make_int4(0, 0, 0, 0);
+        at_row.tok = Token{y.x, y.y, y.z, y.w};
+        at_row.slope2 = valid && a.slopes ? a.slopes[g.h * a.G + at_row.g] * 1.4426950408889634f : 0.f;
+      }
       const uint4* src = reinterpret_cast<const uint4*>(valid ? query(g, at_row) : a.q);
       if constexpr (C::TWO) {
         uint8_t* dst = qsm + wg * (C::QROWS * D * 2) + row % C::QROWS * 128;
@@ -636,7 +795,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
       }
       {
         Iter<C> peek = it;
-        Seg nx;
+        Segment nx;
         if (peek.next(nx) && has_rows(wg, nx)) warm(nx);
       }
       const bool active = row - lane < s.rows;  // some row of this warp is real
@@ -660,9 +819,20 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
         const uint32_t tS = tb + C::S + 64 * buf + lanes;
         if (active && run) {
           const int p0 = t * kTile;
-          if (!C::SPARSE && valid && p0 + kTile > s.full) see &= row_mask(a, s, qi, p0);
+          if constexpr (C::SPAN) {
+            if (valid && (p0 + kTile > s.full || p0 < s.lo)) see &= span_mask(a, s.q0 + qi, mine.tok, p0);
+          } else if (!C::SPARSE && valid && p0 + kTile > s.full) {
+            see &= row_mask(a, s, qi, p0);
+          }
           const bool some = !__all_sync(0xffffffffu, see == ~0ull);  // a key that some row does not see
-          const unsigned long long sc = pack2(a.scale2, a.scale2);
+          float scale2 = a.scale2;
+          // the place from which a row measures distance: its own, or of what it sees the nearest
+          [[maybe_unused]] int from = 0;
+          if constexpr (C::SPAN) {
+            from = nearest(mine.tok) - p0;
+            if (a.cap2 != 0.f || a.slopes) scale2 = 1.f;  // the scores become exponents of 2 as they are changed
+          }
+          const unsigned long long sc = pack2(scale2, scale2);
           uint32_t p[32];
           // The weights are taken under the running maximum while the tile's
           // own is found. Only if that is more than 2^8 above it (a unit's
@@ -679,6 +849,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
             float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
             tmem_ld_wait32(x[0]);
             tmem_ld_wait32(x[1]);
+            if constexpr (C::SPAN) change_scores(a, x, mine.slope2, from);
             if (some) {
 #pragma unroll
               for (int c = 0; c < 2; ++c) {
@@ -702,7 +873,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
                 const __nv_bfloat162 w = __floats2bfloat162_rn(e0, e1);
                 memcpy(&p[16 * c + i], &w, 4);
               }
-            const float mnew = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale2;
+            const float mnew = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale2;
             const bool grow = mnew > m + 8.f || (m == -INFINITY && mnew > m);
             if (!__any_sync(0xffffffffu, grow)) {
               float l0, l1;
@@ -757,7 +928,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
       }
       // the next unit's queries go up before this one's sums come down: every
       // product with the old ones has completed (s_full of the last tile)
-      const Seg done = s;
+      const Segment done = s;
       more = it.next(s);
       if (more && has_rows(wg, s)) start_unit(s);
       run = run && wait_product();
@@ -771,32 +942,71 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
         }
       }
       tc_fence_after();
-      const bool first = done.t0 == 0, last = done.t1 == done.nt;
+      int unit = 0;  // the unit's first tile
+      if constexpr (C::SPAN) unit = done.tb;
+      const bool first = done.t0 == unit, last = done.t1 == done.nt;
       if (tid == 0 && !first) {
         meta[1] = 1;
         meta[2] = last;
       } else if (tid == 0 && !last) {
         meta[0] = 1;
         meta[3] = done.rows;
-        a.meta[2 * cta + 1] = make_int4(done.r0, done.q0, done.h, 0);
+        int base = 0;
+        if constexpr (C::SPAN) base = done.base;
+        a.meta[2 * cta + 1] = make_int4(done.r0, done.q0, done.h, base);
       }
       if (active && run) {
-        if (fix)
-          fix_nonfinite<FMT, D>(a, done, max(done.t0, done.full / kTile), done.t1, qi, valid, tO);
+        if (fix) {
+          if constexpr (C::SPAN)
+            fix_nonfinite<FMT, D>(a, done, done.t0, done.t1, qi, valid, tO, mine.tok);
+          else
+            fix_nonfinite<FMT, D>(a, done, max(done.t0, done.full / kTile), done.t1, qi, valid, tO);
+        }
         const long long tok = done.q0 + mine.q;
         const int head = done.h * a.G + mine.g;
         const int piece = 2 * cta + (first ? 1 : 0);
-        const float inv = l > 0.f ? 1.f / l : 0.f;
         __nv_bfloat16* dst = a.out + tok * a.ot + head * a.oh;
         float* part = a.part + (static_cast<long long>(piece) * C::ROWS + row) * D;
+        // span form: a whole unit's sums join those over the shared prefix, or are those
+        [[maybe_unused]] const float* base = nullptr;
+        [[maybe_unused]] float wm = 1.f, wb = 0.f;  // weights of the unit's sums and of the others
+        bool whole = first && last;
+        if constexpr (C::SPAN) {
+          const long long at = tok * a.kv_heads * a.G + head;
+          if (whole && a.base_mode == 1) {
+            whole = false;
+            part = a.base + at * D;
+          }
+          if (whole && done.base && valid) {
+            const float2 y = __ldcg(a.base_ml + at);
+            const float top = fmaxf(m, y.x);
+            base = a.base + at * D;
+            wm = m == top ? 1.f : ex2_denorm(m - top);
+            wb = y.x == top ? 1.f : ex2_denorm(y.x - top);
+            l = l * wm + y.y * wb;
+            m = top;
+          }
+        }
+        const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
           __syncwarp();
           tmem_ld32(tO + 32 * c, o);
           tmem_ld_wait32(o);
+          if constexpr (C::SPAN) {
+            if (valid && base) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float4 y = __ldcg(reinterpret_cast<const float4*>(base + 32 * c + 4 * i));
+                const float z[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[4 * i + e] = __float_as_uint(fmaf(z[e], wb, __uint_as_float(o[4 * i + e]) * wm));
+              }
+            }
+          }
           if (!valid) {
-          } else if (first && last) {
+          } else if (whole) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               uint32_t w[4];
@@ -815,8 +1025,12 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
           }
         }
         if (valid) {
-          if (first && last) {
-            if (a.lse) a.lse[tok * a.kv_heads * a.G + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+          if (whole) {
+            float top = m;
+            if constexpr (C::SPAN) top -= mine.slope2 * away(mine.tok);
+            if (a.lse) a.lse[tok * a.kv_heads * a.G + head] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
+          } else if (C::SPAN && first && last) {
+            if constexpr (C::SPAN) a.base_ml[tok * a.kv_heads * a.G + head] = make_float2(m, l);
           } else {
             a.ml[static_cast<long long>(piece) * C::ROWS + row] = make_float2(m, l);
           }
@@ -830,7 +1044,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
     // ------------------------------------------------------------ products
     const int wg = warp - NSW - 4;
     Iter<C> it(a, sh.start, count);
-    Seg s;
+    Segment s;
     bool run = true;
     int ns = 0, units = 0, passed = 0;  // tiles, units, and units known to be read out
     while (run && it.next(s)) {
@@ -898,7 +1112,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
     };
 
     Iter<C> it(a, sh.start, count);
-    Seg s;
+    Segment s;
     int n = 0, parts = 0;             // tiles; operand tiles of both kinds before this segment
     int issued = 0, sent = 0;         // tiles asked for by copies, and handed over
     int mine = -1, mine_round = 0;    // the last operand tile asked for, and its round
@@ -1174,7 +1388,9 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
               },
               nullptr, at, rnd, false, last, seg);
         } else {
-          const bool whole = vm == ~0ull && (t + 1) * kTile <= s.full;  // every row sees every key
+          bool all = (t + 1) * kTile <= s.full;
+          if constexpr (C::SPAN) all = all && t * kTile >= s.lo;
+          const bool whole = vm == ~0ull && all;  // every row sees every key
           const uint8_t* const head = heads + static_cast<uint64_t>(vm ? static_cast<uint32_t>(page) : 0u) * page_step;
           if (FMT == DSA_FMT_BF16 && whole) {
             // by TMA: 64 keys of 64 dimensions a box
@@ -1200,7 +1416,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
                   ok = (vm >> r) & 1;
                   return head;
                 },
-                vm == ~0ull ? head : nullptr, at, rnd, v && (t + 1) * kTile > s.full, last, seg);
+                vm == ~0ull ? head : nullptr, at, rnd, v && !all, last, seg);
           }
         }
       }
@@ -1229,13 +1445,14 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM>::THREADS, Cfg<FMT, D, FORM>:
   }
 }
 
-template <int FMT, int D, int FORM>
-dsa_status run_one(dsa_ctx* ctx, const CUtensorMap& tm, const AttnArgs& a, int grid, cudaStream_t stream) {
-  using C = Cfg<FMT, D, FORM>;
-  auto kern = attn_kernel<FMT, D, FORM>;
+template <int FMT, int D, int FORM, class Args>
+dsa_status run_one(dsa_ctx* ctx, const CUtensorMap& tm, const Args& a, int grid, cudaStream_t stream) {
+  constexpr bool LISTED = std::is_same_v<Args, SpanArgs>;
+  using C = Cfg<FMT, D, FORM, LISTED>;
+  auto kern = attn_kernel<FMT, D, FORM, LISTED>;
   constexpr int bytes = smem_bytes<C>();
   static_assert(bytes * C::CTAS <= 233472 - 1024 * C::CTAS, "shared memory of an SM");
-  const uint64_t bit = 1ull << ((FMT * 2 + (D == 128)) * kForms + FORM);  // once a context and kernel
+  const uint64_t bit = 1ull << (((LISTED ? 3 + FMT : FMT) * 2 + (D == 128)) * kForms + FORM);  // once a context and kernel
   if (!(ctx->attn_ready & bit)) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return DSA_ERR_CUDA;
     ctx->attn_ready |= bit;
@@ -1244,27 +1461,45 @@ dsa_status run_one(dsa_ctx* ctx, const CUtensorMap& tm, const AttnArgs& a, int g
   return launch_pdl(kern, dim3(grid), dim3(C::THREADS), bytes, stream, tm, a) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 
-template <int FMT, int D>
-dsa_status run_dim(dsa_ctx* ctx, int form, const CUtensorMap& tm, const AttnArgs& a, int grid, cudaStream_t stream) {
+template <int FMT, int D, class Args>
+dsa_status run_dim(dsa_ctx* ctx, int form, const CUtensorMap& tm, const Args& a, int grid, cudaStream_t stream) {
+  if constexpr (!std::is_same_v<Args, SpanArgs>) {
+    if (form == kSparse) return run_one<FMT, D, kSparse>(ctx, tm, a, grid, stream);
+    if (form == kSparseFew) return run_one<FMT, D, kSparseFew>(ctx, tm, a, grid, stream);
+  }
   switch (form) {
     case kTree: return run_one<FMT, D, kTree>(ctx, tm, a, grid, stream);
-    case kSparse: return run_one<FMT, D, kSparse>(ctx, tm, a, grid, stream);
     case kTreeFew: return run_one<FMT, D, kTreeFew>(ctx, tm, a, grid, stream);
-    case kSparseFew: return run_one<FMT, D, kSparseFew>(ctx, tm, a, grid, stream);
     default: return run_one<FMT, D, kWide>(ctx, tm, a, grid, stream);
   }
 }
 
-template <int FMT>
-dsa_status run_fmt(dsa_ctx* ctx, int form, int D, const CUtensorMap& tm, const AttnArgs& a, int grid, cudaStream_t stream) {
+template <int FMT, class Args>
+dsa_status run_fmt(dsa_ctx* ctx, int form, int D, const CUtensorMap& tm, const Args& a, int grid, cudaStream_t stream) {
   if (D == 128) return run_dim<FMT, 128>(ctx, form, tm, a, grid, stream);
   return run_dim<FMT, 64>(ctx, form, tm, a, grid, stream);
 }
 
-// One cache format's kernels: attn.cu (bf16), attn_fp8.cu, attn_fp4.cu.
+// Where the parts of the workspace begin: two pieces a CTA, 256 rows on each SM
+// whatever the form.
+struct Workspace {
+  size_t ml, part, bytes;
+};
+Workspace layout(const dsa_ctx* ctx, int D);
+
+// What a call's arguments and workspace say, and a bf16 cache as rows of D
+// elements (a page's K or V of one head is 64 of them). In attn.cu.
+void fill_args(const dsa_ctx* ctx, const dsa_attn_args& p, AttnArgs& a);
+bool cache_map(const dsa_ctx* ctx, const dsa_attn_args& p, int box_rows, CUtensorMap& tm);
+
+// One cache format's kernels: attn.cu (bf16), attn_fp8.cu, attn_fp4.cu; of
+// listed units attn_span.cu, attn_span_fp8.cu, attn_span_fp4.cu.
 dsa_status run_bf16(dsa_ctx* ctx, int form, int D, const CUtensorMap& tm, const AttnArgs& a, int grid, cudaStream_t stream);
 dsa_status run_fp8(dsa_ctx* ctx, int form, int D, const CUtensorMap& tm, const AttnArgs& a, int grid, cudaStream_t stream);
 dsa_status run_fp4(dsa_ctx* ctx, int form, int D, const CUtensorMap& tm, const AttnArgs& a, int grid, cudaStream_t stream);
+dsa_status run_span_bf16(dsa_ctx* ctx, int form, int D, const CUtensorMap& tm, const SpanArgs& a, int grid, cudaStream_t stream);
+dsa_status run_span_fp8(dsa_ctx* ctx, int form, int D, const CUtensorMap& tm, const SpanArgs& a, int grid, cudaStream_t stream);
+dsa_status run_span_fp4(dsa_ctx* ctx, int form, int D, const CUtensorMap& tm, const SpanArgs& a, int grid, cudaStream_t stream);
 
 }  // namespace at
 }  // namespace dsa

@@ -1,0 +1,301 @@
+// Attention of spans and behind shared prefixes: the plan of the units, the
+// bf16 kernels and the launches. The attention itself is attn.cuh's span form.
+//
+// The plan lists units of up to 32, 128 or 256 rows (tokens x the G query heads
+// of a kv head; one list for all kv heads) with the 64-key tiles that one of
+// their tokens sees. It says of each token which places it sees, and of each
+// unit which places all of its tokens see, where no masks are needed. A unit of
+// sequence b that begins at its row r0 = r rows has the place
+//   floor(cu_q[b] G / rows) + b + r
+// in the list: different for all units, in order, and with at most one gap a
+// sequence, so no scan over the sequences comes first.
+//
+// Behind shared prefixes there are two lists. The first takes a group's
+// sequences for one, with all of their tokens, and the whole pages that they
+// share; its sums go to the workspace, 32 bits each. The second takes each
+// sequence alone and the keys behind those pages, and joins both.
+#include "attn_join.cuh"
+
+namespace dsa {
+namespace at {
+
+struct SpanPlan {
+  const int32_t *first, *last;
+  const int32_t *cu_groups, *shared;  // or null
+  int4* tokens;
+  int4 *units, *group_units;    // of sequences, of groups
+  int *tiles, *group_tiles;
+  int n, group_n, rows, group_rows, groups, window;
+};
+
+// The last i < N with before(i) <= u, before not decreasing (0 if there is
+// none). A warp's lanes look at 32 places at a time.
+template <class F>
+__device__ __forceinline__ int last_at(int N, long long u, F before) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = N;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32, i = lo + (lane + 1) * step;
+    const int c = __popc(__ballot_sync(0xffffffffu, i < hi && before(i) <= u));
+    lo += c * step;
+    hi = min(hi, lo + step);
+  }
+  return lo;
+}
+
+// the last i of [lo, hi) with x[i] <= u, by one thread
+__device__ __forceinline__ int last_of(const int32_t* x, int lo, int hi, int u) {
+  while (hi - lo > 1) {
+    const int i = lo + (hi - lo) / 2;
+    if (x[i] <= u)
+      lo = i;
+    else
+      hi = i;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ bool read_group(const AttnArgs& a, const SpanPlan& p, int g, int& b0, int& b1) {
+  b0 = p.cu_groups[g];
+  b1 = p.cu_groups[g + 1];
+  return b0 >= 0 && b0 <= b1 && b1 <= a.B;
+}
+
+// Whole pages that group g's sequences read from the first one's row; one
+// sequence alone has none to share.
+__device__ __forceinline__ int shared_pages(const AttnArgs& a, const SpanPlan& p, int g) {
+  int b0, b1, q0, nd, len;
+  if (!read_group(a, p, g, b0, b1) || b1 - b0 < 2 || !read_seq(a, b0, q0, nd, len)) return 0;
+  return max(0, min(p.shared[g], len)) / kTile;
+}
+
+// What token i of sequence b sees.
+__device__ __forceinline__ Token token_of(const AttnArgs& a, const SpanPlan& p, int q0, int nd, int len, int i) {
+  Token y;
+  y.ctx = len - nd;
+  y.place = y.ctx + i;
+  y.lo = p.first ? p.first[q0 + i] : 0;
+  if (p.window) y.lo = max(y.lo, y.place - p.window + 1);
+  y.lo = max(y.lo, 0);
+  y.hi = min(len, p.last ? p.last[q0 + i] : a.mask ? len : y.place + 1);
+  if (y.hi <= y.lo) y.lo = y.hi = 0;
+  return y;
+}
+
+// A warp a place of the lists.
+__global__ void __launch_bounds__(256) span_plan_kernel(const AttnArgs a, const SpanPlan p) {
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31;
+  const long long at = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) >> 5, self = at * 32 + lane;
+  int q0, nd, len;
+  if (self < a.B && !read_seq(a, static_cast<int>(self), q0, nd, len)) atomicOr(a.status, DSA_DEV_BOUNDS);
+  if (self < p.groups) {
+    int b0, b1;
+    if (!read_group(a, p, static_cast<int>(self), b0, b1) || p.shared[self] < 0) atomicOr(a.status, DSA_DEV_BOUNDS);
+  }
+  if (at >= static_cast<long long>(p.n) + p.group_n) return;
+  const bool group = at >= p.n;
+  const int u = static_cast<int>(group ? at - p.n : at), rows = group ? p.group_rows : p.rows;
+  int* const tiles = (group ? p.group_tiles : p.tiles) + u;
+  // the sequences' first row of the page table, queries and keys; t0, t1: tiles they may have
+  int b, b1, r, t0, t1;
+  bool ok;
+  if (!group) {
+    auto before = [&](int i) -> long long { return static_cast<long long>(a.cu_q[i]) * a.G / rows + i; };
+    b = last_at(a.B, u, before);
+    b1 = b + 1;
+    ok = read_seq(a, b, q0, nd, len);
+    const long long from = u - before(b);
+    r = static_cast<int>(from);
+    ok = ok && from >= 0;
+    t0 = 0;
+    t1 = 0x7FFFFFFF;
+    if (p.groups) {
+      const int g = last_of(p.cu_groups, 0, p.groups, b);
+      int g0, g1;
+      if (read_group(a, p, g, g0, g1) && g0 <= b && b < g1) t0 = shared_pages(a, p, g);
+    }
+  } else {
+    auto before = [&](int i) -> long long {
+      return static_cast<long long>(a.cu_q[min(max(p.cu_groups[i], 0), a.B)]) * a.G / rows + i;
+    };
+    const int g = last_at(p.groups, u, before);
+    ok = read_group(a, p, g, b, b1);
+    t0 = 0;
+    t1 = ok ? shared_pages(a, p, g) : 0;
+    ok = ok && t1 > 0;
+    q0 = ok ? a.cu_q[b] : 0;
+    const int q1 = ok ? a.cu_q[b1] : 0;
+    nd = q1 - q0;
+    len = t1 * kTile;
+    ok = ok && q0 >= 0 && q1 >= q0 && q1 <= a.Tq;
+    const long long from = u - before(g);
+    r = static_cast<int>(from);
+    ok = ok && from >= 0;
+  }
+  if (!ok || static_cast<long long>(r) * rows >= static_cast<long long>(nd) * a.G) {
+    if (lane == 0) *tiles = 0;
+    return;
+  }
+  const int r0 = r * rows;
+  const int i0 = r0 / a.G, i1 = static_cast<int>((min(static_cast<long long>(r0) + rows, static_cast<long long>(nd) * a.G) - 1) / a.G);
+  int min_lo = 0x7FFFFFFF, max_lo = 0, min_hi = len, max_hi = 0;
+  for (int i = i0 + lane; i <= i1; i += 32) {
+    Token y;
+    if (!group) {
+      y = token_of(a, p, q0, nd, len, i);
+    } else {
+      int s0, sn, sl;
+      const int t = q0 + i, s = last_of(a.cu_q, b, b1, t);
+      y = Token{0, 0, 0, 0};
+      if (read_seq(a, s, s0, sn, sl) && s0 <= t && t < s0 + sn) y = token_of(a, p, s0, sn, sl, t - s0);
+    }
+    p.tokens[q0 + i] = make_int4(y.lo, y.hi, y.place, y.ctx);  // the same from every warp that has the token
+    if (y.hi > 0) min_lo = min(min_lo, y.lo);
+    max_lo = max(max_lo, y.lo);
+    max_hi = max(max_hi, y.hi);
+    min_hi = min(min_hi, a.mask ? min(y.hi, y.ctx) : y.hi);
+  }
+  min_lo = __reduce_min_sync(0xffffffffu, min_lo);
+  max_lo = __reduce_max_sync(0xffffffffu, max_lo);
+  min_hi = __reduce_min_sync(0xffffffffu, min_hi);
+  max_hi = __reduce_max_sync(0xffffffffu, max_hi);
+  if (lane == 0) {
+    const int base = !group && t0 > 0;
+    int e0 = max(t0, min_lo / kTile), e1 = min(t1, (max_hi + kTile - 1) / kTile);
+    if (e1 <= e0) {  // nothing to see: one tile, so that the rows are written
+      e0 = t0;
+      e1 = t0 + 1;
+    }
+    int4* const x = (group ? p.group_units : p.units) + 3LL * u;
+    x[0] = make_int4(b, q0, nd, len);
+    x[1] = make_int4(r0, e0, e1, base);
+    x[2] = make_int4(max_lo, min_hi, 0, 0);
+    *tiles = e1 - e0;
+  }
+}
+
+dsa_status run_span_bf16(dsa_ctx* ctx, int form, int D, const CUtensorMap& tm, const SpanArgs& a, int grid, cudaStream_t stream) {
+  return run_fmt<DSA_FMT_BF16>(ctx, form, D, tm, a, grid, stream);
+}
+
+// The form for n sequences (or groups) with these rows in all; the rule is launch_attn's.
+struct Shape {
+  int form, rows, grid, places;  // rows of a unit, CTAs, places of the list
+};
+
+Shape shape_of(const dsa_ctx* ctx, long long rows, int n) {
+  Shape f;
+  f.form = rows > 128LL * n ? kWide : rows <= static_cast<long long>(kFewRows) * n ? kTreeFew : kTree;
+  f.rows = f.form == kWide ? 256 : f.form == kTreeFew ? kFewRows : 128;
+  f.grid = f.form == kWide ? ctx->num_sms : 2 * ctx->num_sms;
+  f.places = static_cast<int>(rows / f.rows) + n + 1;
+  return f;
+}
+
+// What follows the attention's own workspace.
+struct SpanWorkspace {
+  size_t tokens, units, tiles, group_units, group_tiles, base_ml, base, bytes;
+};
+
+SpanWorkspace span_layout(const dsa_ctx* ctx, long long Tq, int B, int groups, long long heads, long long kv_heads, int D) {
+  const long long G = heads / kv_heads;
+  size_t at = layout(ctx, D).bytes;
+  auto take = [&](size_t bytes) {
+    const size_t here = (at + 255) / 256 * 256;
+    at = here + bytes;
+    return here;
+  };
+  SpanWorkspace w = {};
+  const size_t places = shape_of(ctx, Tq * G, B).places;
+  w.tokens = take(Tq * sizeof(int4));
+  w.units = take(places * 3 * sizeof(int4));
+  w.tiles = take(places * sizeof(int));
+  if (groups) {
+    const size_t more = shape_of(ctx, Tq * G, groups).places;
+    w.group_units = take(more * 3 * sizeof(int4));
+    w.group_tiles = take(more * sizeof(int));
+    w.base_ml = take(static_cast<size_t>(Tq) * heads * sizeof(float2));
+    w.base = take(static_cast<size_t>(Tq) * heads * D * sizeof(float));
+  }
+  w.bytes = at;
+  return w;
+}
+
+}  // namespace at
+
+size_t span_workspace(const dsa_ctx* ctx, int32_t Tq, int32_t B, int32_t groups, int32_t heads, int32_t kv_heads, int32_t head_dim) {
+  return at::span_layout(ctx, Tq, B, groups, heads, kv_heads, head_dim).bytes;
+}
+
+dsa_status launch_span(dsa_ctx* ctx, const dsa_attn_args& p, const dsa_span& span, const int32_t* cu_groups,
+                       const int32_t* shared, int32_t groups, cudaStream_t stream) {
+  using namespace at;
+  const SpanWorkspace w = span_layout(ctx, p.Tq, p.B, groups, p.heads, p.kv_heads, p.head_dim);
+  uint8_t* ws = static_cast<uint8_t*>(p.workspace);
+  SpanArgs a = {};
+  fill_args(ctx, p, a);
+  a.slopes = span.slopes;
+  if (span.cap != 0.0) {
+    a.cap2 = static_cast<float>(span.cap * 1.4426950408889634);
+    a.to_cap = static_cast<float>(p.scale / span.cap);
+  }
+  a.tokens = reinterpret_cast<int4*>(ws + w.tokens);
+  if (groups) {
+    a.base_ml = reinterpret_cast<float2*>(ws + w.base_ml);
+    a.base = reinterpret_cast<float*>(ws + w.base);
+  }
+  CUtensorMap tm = {};
+  if (!cache_map(ctx, p, kTile, tm)) return DSA_ERR_CUDA;
+
+  const long long rows = static_cast<long long>(p.Tq) * a.G;
+  const Shape own = shape_of(ctx, rows, p.B), all = groups ? shape_of(ctx, rows, groups) : Shape{};
+  SpanPlan plan = {};
+  plan.first = span.first;
+  plan.last = span.last;
+  plan.window = span.window;
+  plan.cu_groups = cu_groups;
+  plan.shared = shared;
+  plan.groups = groups;
+  plan.tokens = reinterpret_cast<int4*>(ws + w.tokens);
+  plan.units = reinterpret_cast<int4*>(ws + w.units);
+  plan.tiles = reinterpret_cast<int*>(ws + w.tiles);
+  plan.group_units = reinterpret_cast<int4*>(ws + w.group_units);
+  plan.group_tiles = reinterpret_cast<int*>(ws + w.group_tiles);
+  plan.n = own.places;
+  plan.rows = own.rows;
+  plan.group_n = all.places;
+  plan.group_rows = all.rows;
+  {
+    LaunchScope scope(ctx, DSA_K_SPAN_PLAN, stream);
+    const long long warps = static_cast<long long>(plan.n) + plan.group_n;
+    if (launch_pdl(span_plan_kernel, dim3(static_cast<unsigned>((warps + 7) / 8)), dim3(256), 0, stream,
+                   static_cast<const AttnArgs&>(a), plan) != cudaSuccess)
+      return DSA_ERR_CUDA;
+  }
+  const auto run = p.fmt == DSA_FMT_BF16 ? run_span_bf16 : p.fmt == DSA_FMT_FP8 ? run_span_fp8 : run_span_fp4;
+  auto pass = [&](const Shape& f) {
+    const dsa_status st = run(ctx, f.form, p.head_dim, tm, a, f.grid, stream);
+    if (st != DSA_OK) return st;
+    LaunchScope scope(ctx, DSA_K_ATTN_JOIN, stream);
+    const cudaError_t e = launch_pdl(p.head_dim == 128 ? join_kernel<128, SpanArgs> : join_kernel<64, SpanArgs>,
+                                     dim3(f.grid, 8), dim3(256), 0, stream, a, f.grid, f.rows);
+    return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+  };
+  if (groups) {
+    a.units = plan.group_units;
+    a.tiles = plan.group_tiles;
+    a.units_n = plan.group_n;
+    a.base_mode = 1;
+    const dsa_status st = pass(all);
+    if (st != DSA_OK) return st;
+    a.base_mode = 2;
+  }
+  a.units = plan.units;
+  a.tiles = plan.tiles;
+  a.units_n = plan.n;
+  return pass(own);
+}
+
+}  // namespace dsa

@@ -387,6 +387,13 @@ __device__ __forceinline__ float ex2_denorm(float x) {
   return y;
 }
 
+// 1 / x (the hardware's approximation, within 1 ulp)
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // ---------------------------------------------------------------- named barriers
 __device__ __forceinline__ void named_bar(int id, int nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");

@@ -16,7 +16,7 @@ FMT_BF16 = 0
 FMT_FP8 = 1
 FMT_FP4 = 2
 KERNEL_KINDS = ("store", "plan", "score_bf16", "score_fp8", "score_fp4", "rope", "kv_store", "kv_load",
-                "attn", "attn_join")
+                "attn", "attn_join", "span_plan", "batch_plan")
 HEADS = 64
 HEAD_DIM = 128
 PAGE_SIZE = 64
@@ -43,6 +43,7 @@ class _RopeDesc(ctypes.Structure):  # dsa_rope_desc
 
 # dsa_attn_args, field by field with the C padding
 _ATTN_PACK = struct.Struct("@PqqPqqPPiiiiiPiPPiiPidPN").pack
+_SPAN_PACK = struct.Struct("@PPPdi4x").pack  # dsa_span
 _KV_PAGE_BYTES = {}  # of (kv_heads, head_dim, fmt)
 
 
@@ -107,8 +108,16 @@ def lib() -> ctypes.CDLL:
         L.dsa_attn_workspace_size.restype = _c_size
         L.dsa_tree_attn.argtypes = [_c_ptr, ctypes.c_char_p, _c_ptr]
         L.dsa_sparse_attn.argtypes = [_c_ptr, ctypes.c_char_p, _c_ptr, _c_int, _c_ptr]
+        L.dsa_span_attn_workspace_size.argtypes = [_c_ptr] + [_c_int] * 5
+        L.dsa_span_attn_workspace_size.restype = _c_size
+        L.dsa_shared_attn_workspace_size.argtypes = [_c_ptr] + [_c_int] * 6
+        L.dsa_shared_attn_workspace_size.restype = _c_size
+        L.dsa_span_attn.argtypes = [_c_ptr, ctypes.c_char_p, ctypes.c_char_p, _c_ptr]
+        L.dsa_shared_attn.argtypes = [_c_ptr, ctypes.c_char_p, ctypes.c_char_p, _c_ptr, _c_ptr, _c_int, _c_ptr]
+        L.dsa_batch_plan.argtypes = [_c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_int, _c_ptr, _c_int, _c_int, _c_ptr, _c_int,
+                                     _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_int, _c_ptr]
         for f in (L.dsa_rope_create, L.dsa_rope_destroy, L.dsa_rope_apply, L.dsa_kv_store, L.dsa_kv_load,
-                  L.dsa_tree_attn, L.dsa_sparse_attn):
+                  L.dsa_tree_attn, L.dsa_sparse_attn, L.dsa_span_attn, L.dsa_shared_attn, L.dsa_batch_plan):
             f.restype = ctypes.c_int
         L.dsa_status_str.argtypes = [ctypes.c_int]
         L.dsa_status_str.restype = ctypes.c_char_p
@@ -479,6 +488,76 @@ class Context:
         st = lib().dsa_sparse_attn(self._h, a, _ptr(sel, torch.int32, (q.shape[0], k), "sel", q.get_device()), k, _raw_stream(stream))
         if st != 0:
             raise DsaError("dsa_sparse_attn", st)
+
+    def span_attn_workspace_size(self, Tq: int, B: int, heads: int, kv_heads: int, head_dim: int) -> int:
+        return int(lib().dsa_span_attn_workspace_size(self._h, Tq, B, heads, kv_heads, head_dim))
+
+    def shared_attn_workspace_size(self, Tq: int, B: int, n_groups: int, heads: int, kv_heads: int, head_dim: int) -> int:
+        return int(lib().dsa_shared_attn_workspace_size(self._h, Tq, B, n_groups, heads, kv_heads, head_dim))
+
+    @staticmethod
+    def _span(q, cap, slopes, window, first, last):
+        """A dsa_span as bytes."""
+        import torch
+        Tq, H, _ = q.shape
+        dev = q.get_device()
+        return _SPAN_PACK(0 if first is None else _ptr(first, torch.int32, (Tq,), "first", dev),
+                          0 if last is None else _ptr(last, torch.int32, (Tq,), "last", dev),
+                          0 if slopes is None else _ptr(slopes, torch.float32, (H,), "slopes", dev), cap, window)
+
+    def span_attn(self, q, cache, num_pages: int, fmt: int, kv_heads: int, page_table, seq_lens, cu_q, out, workspace,
+                  mask=None, lse=None, scale=None, cap: float = 0.0, slopes=None, window: int = 0, first=None, last=None,
+                  stream=None):
+        """dsa_span_attn: as tree_attn(), each new token over a span of places.
+        first, last: int32 [Tq], the first place and one past the last one that
+        a token sees; window: how many places it looks back over, itself
+        included; cap: scores become cap * tanh(score / cap); slopes: fp32
+        [heads], times the distance in places, taken off the scores."""
+        a = self._attn_args(q, cache, num_pages, fmt, kv_heads, page_table, seq_lens, cu_q, out, workspace, mask,
+                            lse, scale)
+        st = lib().dsa_span_attn(self._h, a, self._span(q, cap, slopes, window, first, last), _raw_stream(stream))
+        if st != 0:
+            raise DsaError("dsa_span_attn", st)
+
+    def shared_attn(self, q, cache, num_pages: int, fmt: int, kv_heads: int, page_table, seq_lens, cu_q, out, workspace,
+                    cu_groups, shared_lens, mask=None, lse=None, scale=None, cap: float = 0.0, slopes=None,
+                    window: int = 0, first=None, last=None, stream=None):
+        """dsa_shared_attn: span_attn() for a batch whose sequences cu_groups[g] ..
+        cu_groups[g+1]-1 have their first shared_lens[g] tokens in common, in the
+        same pages: those are read once a group."""
+        import torch
+        a = self._attn_args(q, cache, num_pages, fmt, kv_heads, page_table, seq_lens, cu_q, out, workspace, mask,
+                            lse, scale)
+        n, dev = shared_lens.shape[0], q.get_device()
+        st = lib().dsa_shared_attn(self._h, a, self._span(q, cap, slopes, window, first, last),
+                                   _ptr(cu_groups, torch.int32, (n + 1,), "cu_groups", dev),
+                                   _ptr(shared_lens, torch.int32, (n,), "shared_lens", dev), n, _raw_stream(stream))
+        if st != 0:
+            raise DsaError("dsa_shared_attn", st)
+
+    def batch_plan(self, old_lens, new_lens, page_table, num_pages: int, free_pages, free_count, free_left, seq_lens,
+                   cu_q, seq_id, cache_pos, slots=None, own_from=None, stream=None):
+        """dsa_batch_plan: a step's page tables and slot maps from its requests'
+        lengths. Sequence b's new_lens[b] tokens follow the old_lens[b] in the
+        cache (negative: it ends and its pages from own_from[b] on come back);
+        pages come off the stack free_pages[:free_count]. Writes page_table,
+        free_pages, free_left [1], seq_lens [B], cu_q [B+1] and seq_id,
+        cache_pos, slots [T], which are -1 past the last token."""
+        import torch
+        i32, dev = torch.int32, _device()
+        B, max_pages = page_table.shape
+        T = seq_id.shape[0]
+        st = lib().dsa_batch_plan(
+            self._h, _ptr(old_lens, i32, (B,), "old_lens", dev), _ptr(new_lens, i32, (B,), "new_lens", dev),
+            None if own_from is None else _ptr(own_from, i32, (B,), "own_from", dev), B,
+            _ptr(page_table, i32, None, "page_table", dev), max_pages, num_pages,
+            _ptr(free_pages, i32, None, "free_pages", dev), free_pages.numel(), _ptr(free_count, i32, (1,), "free_count", dev),
+            _ptr(free_left, i32, (1,), "free_left", dev), _ptr(seq_lens, i32, (B,), "seq_lens", dev),
+            _ptr(cu_q, i32, (B + 1,), "cu_q", dev), _ptr(seq_id, i32, (T,), "seq_id", dev),
+            _ptr(cache_pos, i32, (T,), "cache_pos", dev), None if slots is None else _ptr(slots, i32, (T,), "slots", dev),
+            T, _raw_stream(stream))
+        if st != 0:
+            raise DsaError("dsa_batch_plan", st)
 
     def set_hadamard(self, on: bool = True):
         """Store keys (and rotate queries) with the 128-point Walsh-Hadamard transform."""

@@ -2,7 +2,8 @@
  * libdsaidx -- the DeepSeek Sparse Attention (DSA) indexer hot path on one
  * GB300 GPU: the index-key store and the score + top-k selection; and the
  * attention it serves: rotary positions, the K/V cache, attention of drafted
- * tokens over it and over the selection.
+ * tokens over it and over the selection, of spans and behind shared prefixes,
+ * and the page tables and slot maps of a step.
  *
  * Sources (web pages on the bf16 index-K fix in the DSA indexer):
  *  [VAL] "The Moment of Validation: Diagnosing an OOM Crash in the bf16 Index-K
@@ -399,6 +400,105 @@ dsa_status dsa_tree_attn(dsa_ctx* ctx, const dsa_attn_args* args, dsa_stream_t s
 dsa_status dsa_sparse_attn(dsa_ctx* ctx, const dsa_attn_args* args, const int32_t* sel, int32_t k,
                            dsa_stream_t stream);
 
+/* What a query token sees and how its scores are changed. A token is the i-th
+ * query of its sequence b and lies at place p = seq_lens[b] - n_b + i; it sees
+ * the keys at places j of its own sequence with
+ *   first[t] <= j < last[t]   (first NULL: 0; last NULL: p + 1, or seq_lens[b]
+ *                             where dsa_attn_args has a mask)
+ *   j > p - window            (window 0: no limit)
+ *   j < seq_lens[b], and its mask bit where j is a new token and there is a mask.
+ * So first cuts a packed prompt into documents, last lets the tokens of a
+ * prefix see each other both ways (the larger of p + 1 and the prefix's
+ * length), window looks back over so many places, itself included.
+ * Scores are s = scale q.k; with cap > 0 they become cap tanh(s / cap), then
+ * with slopes s - slopes[head] |p - j|. Distances are of places, so slopes
+ * and a mask of drafted tokens (whose depth is not their place) together are
+ * DSA_ERR_UNSUPPORTED. */
+typedef struct {
+  const int32_t* first;  /* (device) [Tq] or NULL */
+  const int32_t* last;   /* (device) [Tq] or NULL */
+  const float* slopes;   /* (device) [heads] or NULL */
+  double cap;            /* 0: none */
+  int32_t window;        /* 0: none */
+} dsa_span;
+
+/* dsa_tree_attn over spans (span NULL: none of it). Tiles of 64 keys that no
+ * row of a unit (up to 256 rows of neighbouring tokens) sees are neither read
+ * nor computed. Everything else is as in dsa_tree_attn: layouts, formats,
+ * strides, rows that see no key, infinities and NaN in hidden places, bad
+ * pages and lengths, limits; B <= 2^20. The workspace holds the list of units
+ * and 16 bytes a token besides dsa_attn_workspace_size's. A row measures its
+ * distances from its own place or, where it lies outside its span, from the
+ * nearest place in it, and adds the rest to lse. */
+size_t dsa_span_attn_workspace_size(const dsa_ctx* ctx, int32_t Tq, int32_t B, int32_t heads,
+                                    int32_t kv_heads, int32_t head_dim);
+dsa_status dsa_span_attn(dsa_ctx* ctx, const dsa_attn_args* args, const dsa_span* span,
+                         dsa_stream_t stream);
+
+/* dsa_span_attn for batches whose sequences share prefixes: group g is the
+ * sequences cu_groups[g] .. cu_groups[g+1]-1, and their first shared_lens[g]
+ * places hold the same tokens. The whole pages of those (shared_lens[g] / 64)
+ * are read from the first sequence's row of the page table, once for all rows
+ * of the group; the rest, a page that is shared in part too, from each
+ * sequence's own row. The result is dsa_span_attn's of the same batch, up to
+ * the order of fp32 sums. Sequences of no group, of a group of one, or of a
+ * group with fewer than 64 shared places read all their keys themselves.
+ *  cu_groups    (device) [n_groups+1] int32, non-decreasing, within 0 .. B. A
+ *               group out of range shares nothing and DSA_ERR_DEVICE_BOUNDS is
+ *               recorded, as it is for a negative shared_lens[g]; one that is
+ *               longer than the first sequence counts as that long.
+ *  n_groups     1 .. 2^20.
+ * The workspace also holds each row's fp32 sums over the prefix (Tq * heads *
+ * (head_dim + 2) * 4 bytes). */
+size_t dsa_shared_attn_workspace_size(const dsa_ctx* ctx, int32_t Tq, int32_t B, int32_t n_groups,
+                                      int32_t heads, int32_t kv_heads, int32_t head_dim);
+dsa_status dsa_shared_attn(dsa_ctx* ctx, const dsa_attn_args* args, const dsa_span* span,
+                           const int32_t* cu_groups, const int32_t* shared_lens, int32_t n_groups,
+                           dsa_stream_t stream);
+
+/* A step's page tables and slot maps, from the lengths of its requests. For
+ * each sequence b, in order, with p(n) = ceil(n / 64) pages for n tokens:
+ *   new_lens[b] >= 0  new_lens[b] tokens follow the old_lens[b] in the cache;
+ *                     pages p(old) .. p(old + new) - 1 of its row are taken
+ *                     from the pool.
+ *   new_lens[b] < 0   the sequence ends: pages own_from[b] .. p(old) - 1 of its
+ *                     row go back to the pool, and seq_lens[b] = 0.
+ * The pool is a stack: free_pages[0 .. *free_count - 1], then the pages that
+ * come back, by sequence and place. Pages are taken from its end, by sequence
+ * and place; what is left of it stays free, *free_left pages, and those that
+ * came back are written behind the others. With too few pages the last places
+ * get -1 (in the page table and in slots) and DSA_ERR_DEVICE_BOUNDS is recorded.
+ * free_count and old_lens are only read, so a call can be made again with the
+ * same result; the next step takes free_left and seq_lens for them.
+ * Out, besides page_table and free_pages: seq_lens[b] = old + new, cu_q
+ * (cu_q[0] = 0, sums of the new tokens), and for each new token t its
+ * sequence, its place, and its slot page * 64 + place % 64; -1 in all three for
+ * t >= cu_q[B] (a padded batch).
+ *  old_lens, new_lens  (device) [B] int32. A sequence with a negative old
+ *              length or own_from, or more than 64 * max_pages tokens, counts as
+ *              empty (no tokens, seq_lens 0, no pages either way) and
+ *              DSA_ERR_DEVICE_BOUNDS is recorded.
+ *  own_from    (device) [B] int32, or NULL for zeros: pages at the front of the
+ *              row that belong to another sequence (a shared prefix).
+ *  page_table  (device) [B][max_pages] int32, in and out.
+ *  free_pages  (device) [free_cap] int32, in and out; pages that would land
+ *              past it are dropped, a count out of 0 .. free_cap is taken for
+ *              the nearest, DSA_ERR_DEVICE_BOUNDS recorded in both cases, and
+ *              for page ids not in 0 .. num_pages-1 that a token would use
+ *              (its slot is -1).
+ *  free_count, free_left  (device) one int32 each.
+ *  seq_lens    (device) [B];  cu_q (device) [B+1];  seq_id, cache_pos, slots
+ *              (device) [T], slots NULL if not wanted. Tokens past T are left
+ *              out and DSA_ERR_DEVICE_BOUNDS recorded; their pages are taken.
+ * Arrays that are written must not overlap others. B <= 65536, 64 * max_pages
+ * and 64 * num_pages < 2^31, else DSA_ERR_UNSUPPORTED. */
+dsa_status dsa_batch_plan(dsa_ctx* ctx, const int32_t* old_lens, const int32_t* new_lens,
+                          const int32_t* own_from, int32_t B, int32_t* page_table, int32_t max_pages,
+                          int32_t num_pages, int32_t* free_pages, int32_t free_cap,
+                          const int32_t* free_count, int32_t* free_left, int32_t* seq_lens,
+                          int32_t* cu_q, int32_t* seq_id, int32_t* cache_pos, int32_t* slots, int32_t T,
+                          dsa_stream_t stream);
+
 /* Kernel timing, for benchmarks and profiling. While enabled, the library
  * records a CUDA event pair on the launch stream around each kernel it
  * launches (at most 8192 pairs between reads; later launches are counted but
@@ -418,9 +518,11 @@ typedef enum {
   DSA_K_ROPE = 5,       /* dsa_rope_apply */
   DSA_K_KV_STORE = 6,   /* dsa_kv_store */
   DSA_K_KV_LOAD = 7,    /* dsa_kv_load */
-  DSA_K_ATTN = 8,       /* dsa_tree_attn, dsa_sparse_attn: the attention */
+  DSA_K_ATTN = 8,       /* the attention calls: the attention */
   DSA_K_ATTN_JOIN = 9,  /* the same: joining units that were divided */
-  DSA_K_ALL = 10        /* kinds there are */
+  DSA_K_SPAN_PLAN = 10, /* dsa_span_attn, dsa_shared_attn: listing the units */
+  DSA_K_BATCH_PLAN = 11, /* dsa_batch_plan */
+  DSA_K_ALL = 12        /* kinds there are */
 } dsa_kernel_kind;
 dsa_status dsa_profile_enable(dsa_ctx* ctx, int on);
 dsa_status dsa_profile_read(dsa_ctx* ctx, float* ms /* [DSA_K_COUNT] */,
