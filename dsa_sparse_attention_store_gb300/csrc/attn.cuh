@@ -127,7 +127,8 @@ struct SpanArgs : AttnArgs {
   const int* tiles;    // [slots] tiles of a unit, 0 where there is none
   const int4* tokens;  // [Tq]
   const float* slopes; // [heads] or null
-  float cap2, to_cap;  // cap log2 e, scale / cap; 0: no cap
+  float cap2, to_cap;  // cap log2 e, 2 log2 e scale / cap; 0: no cap
+  float poly[5], poly_most;  // capped score log2 e / q.k in powers of (q.k)^2, and where that holds
   int units_n;
   int base_mode;       // rows' sums over a shared prefix: 1 these are they, 2 join them where the unit has some
   float2* base_ml;     // [Tq][heads]
@@ -487,6 +488,29 @@ __device__ __forceinline__ unsigned long long row_mask(const AttnArgs& a, const 
   return low_bits(n) | ((word(0) | (static_cast<unsigned long long>(word(1)) << 32)) << n);
 }
 
+__device__ __forceinline__ Token token_at(const SpanArgs& a, long long t) {
+  const int4 y = a.tokens[t];
+  return Token{y.x, y.y, y.z, y.w};
+}
+
+// One step of turning four lanes' four 16-byte runs around: lanes that differ in
+// bit N exchange the runs that differ in it.
+template <int N>
+__device__ __forceinline__ void swap_runs(uint32_t (&w)[4][4], bool upper) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (i & N) continue;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? w[i][e] : w[i | N][e], N);
+      if (upper)
+        w[i][e] = got;
+      else
+        w[i | N][e] = got;
+    }
+  }
+}
+
 // The place a token measures its keys' distance from: its own, or the nearest
 // that it sees. Softmax takes no notice of the difference; exponents stay small
 // for the keys that matter where all of them are far away. away(): how far that
@@ -494,32 +518,68 @@ __device__ __forceinline__ unsigned long long row_mask(const AttnArgs& a, const 
 __device__ __forceinline__ int nearest(const Token& y) { return max(y.lo, min(y.place, y.hi - 1)); }
 __device__ __forceinline__ float away(const Token& y) { return fabsf(static_cast<float>(y.place - nearest(y))); }
 
-// Capped and biased scores of 64 keys, as exponents of 2: q.k -> cap tanh(scale
-// q.k / cap) - slope |from - j|, or as they are where there is neither.
-// tanh y = 1 - 2 / (1 + e^2y): within 2^-22 of 1, for infinities too.
-__device__ __forceinline__ void change_scores(const SpanArgs& a, uint32_t (&x)[2][32], float slope2, int from) {
-  if (a.cap2 != 0.f) {
+// cap tanh(scale q.k / cap) of 64 keys, times log2 e. tanh y = 1 - 2 / (1 + e^2y),
+// within 2^-22, for infinities too: two more of the special-function unit's
+// operations a score, which a tile takes only where some |y| is above kCapPoly.
+// Below, y P(y^2) with a minimax polynomial (within 2^-23) on the fp32 pipe; its
+// coefficients are the host's, with scale and cap in them.
+constexpr int kCapTerms = 5;
+constexpr double kCapPoly = 0.625;
+
+__device__ __forceinline__ bool cap_near(const SpanArgs& a, uint32_t (&x)[2][32]) {
+  float most = 0.f;
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
+  for (int c = 0; c < 2; ++c)
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const float e = ex2(__uint_as_float(x[c][i]) * (a.to_cap * 2.8853900817779268f));
-        x[c][i] = __float_as_uint(fmaf(-2.f * a.cap2, rcp(1.f + e), a.cap2));
-      }
-  } else if (a.slopes) {
+    for (int i = 0; i < 16; ++i) {
+      const unsigned long long s = pack2(__uint_as_float(x[c][2 * i]), __uint_as_float(x[c][2 * i + 1]));
+      const unsigned long long u = mul2(s, s);
+      unsigned long long p = pack2(a.poly[kCapTerms - 1], a.poly[kCapTerms - 1]);
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
+      for (int k = kCapTerms - 2; k >= 0; --k) p = fma2(p, u, pack2(a.poly[k], a.poly[k]));
+      float u0, u1, y0, y1;
+      unpack2(u, u0, u1);
+      unpack2(mul2(p, s), y0, y1);
+      most = fmaxf(most, fmaxf(u0, u1));
+      x[c][2 * i] = __float_as_uint(y0);
+      x[c][2 * i + 1] = __float_as_uint(y1);
+    }
+  return most <= a.poly_most;
+}
+
+// in TMEM, where a tile's scores stay capped: in registers the 64 chains spill
+__device__ __forceinline__ void cap_any(const SpanArgs& a, uint32_t taddr) {
+#pragma unroll 1
+  for (int c = 0; c < 2; ++c) {
+    uint32_t x[32];
+    tmem_ld32(taddr + 32 * c, x);
+    tmem_ld_wait32(x);
 #pragma unroll
-      for (int i = 0; i < 32; ++i) x[c][i] = __float_as_uint(__uint_as_float(x[c][i]) * a.scale2);
+    for (int i = 0; i < 32; ++i)
+      x[i] = __float_as_uint(fmaf(-2.f * a.cap2, rcp(1.f + ex2(__uint_as_float(x[i]) * a.to_cap)), a.cap2));
+    tmem_st32(taddr + 32 * c, x);
   }
-  if (a.slopes) {
-    const float f = static_cast<float>(from);
+  tmem_st_wait();
+}
+
+// Takes slope |from - j| off 64 exponents of 2; `from` counts from the first
+// key. Where no key lies past it in any of the warp's rows the bias is slope (j -
+// from), of which slope from is left to the caller: one operation a score.
+__device__ __forceinline__ float bias_scores(uint32_t (&x)[2][32], float slope2, float from) {
+  asm volatile("" : "+f"(slope2), "+f"(from));  // or the 64 products move out of the loop around, into registers there are not
+  if (__all_sync(0xffffffffu, from >= 63.f)) {
 #pragma unroll
     for (int c = 0; c < 2; ++c)
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        x[c][i] = __float_as_uint(fmaf(-slope2, fabsf(f - static_cast<float>(32 * c + i)), __uint_as_float(x[c][i])));
+      for (int i = 0; i < 32; ++i) x[c][i] = __float_as_uint(fmaf(slope2, static_cast<float>(32 * c + i), __uint_as_float(x[c][i])));
+    return -slope2 * from;
   }
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      x[c][i] = __float_as_uint(fmaf(-slope2, fabsf(from - static_cast<float>(32 * c + i)), __uint_as_float(x[c][i])));
+  return 0.f;
 }
 
 __device__ __forceinline__ float widen_one(uint32_t bits) { return __uint_as_float(bits << 16); }
@@ -703,22 +763,13 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM, LISTED>::THREADS, Cfg<FMT, D
     if (tid == 0) a.meta[2 * cta] = make_int4(0, 0, 0, 0);
     const int row = tid;  // of the unit
     // a row's query (in its sequence; 0 of a selection, whose rows are one token's) and head of the group
-    struct Plain {
+    struct Row {
       int q, g;
     };
-    struct Listed {  // what it sees, too, and the slope of its bias
-      int q, g;
-      Token tok;
-      float slope2;
-    };
-    using Row = std::conditional_t<C::SPAN, Listed, Plain>;
     auto row_at = [&](const Segment& g) -> Row {
-      Row x = {0, row};
-      if (C::SPARSE) return x;
-      const int r = g.r0 + row;
-      x.q = r / a.G;
-      x.g = r - x.q * a.G;
-      return x;
+      if (C::SPARSE) return Row{0, row};
+      const int r = g.r0 + row, q = r / a.G;
+      return Row{q, r - q * a.G};
     };
     auto query = [&](const Segment& g, Row r) {
       return a.q + static_cast<long long>(g.q0 + r.q) * a.qt + static_cast<long long>(g.h * a.G + r.g) * a.qh;
@@ -731,18 +782,28 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM, LISTED>::THREADS, Cfg<FMT, D
         for (int i = 0; i < C::NBLK; ++i) touch(q + 64 * i);
       }
     };
-    Row at_row = {};
+    Row at_row = {0, 0};
     // the unit's queries, then its first tiles' scores
     auto start_unit = [&](const Segment& g) {
       const bool valid = row < g.rows;
       at_row = row_at(g);
-      if constexpr (C::SPAN) {
-        const int4 y = valid ? a.tokens[g.q0 + at_row.q] : make_int4(0, 0, 0, 0);
-        at_row.tok = Token{y.x, y.y, y.z, y.w};
-        at_row.slope2 = valid && a.slopes ? a.slopes[g.h * a.G + at_row.g] * 1.4426950408889634f : 0.f;
-      }
       const uint4* src = reinterpret_cast<const uint4*>(valid ? query(g, at_row) : a.q);
-      if constexpr (C::TWO) {
+      if constexpr (C::TWO && C::SPAN) {
+        // a row's 16-byte runs by neighbouring lanes, two or four rows at a time: a
+        // load of a row a lane takes the L1 32 steps, and 16 of them a unit
+        constexpr int RUNS = D / 8, AT_ONCE = 32 / RUNS;
+        const unsigned long long from = valid ? reinterpret_cast<unsigned long long>(src) : 0ull;
+        uint8_t* dst = qsm + wg * (C::QROWS * D * 2) + gw * (32 * 128);
+        const int run = lane % RUNS;
+#pragma unroll
+        for (int i = 0; i < RUNS; ++i) {
+          const int r = i * AT_ONCE + lane / RUNS;
+          const unsigned long long p = __shfl_sync(0xffffffffu, from, r);
+          const uint4 v = p ? __ldg(reinterpret_cast<const uint4*>(p) + run) : make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(dst + (run / 8) * (C::QROWS * 128) + r * 128 + (((run & 7) ^ (r & 7)) << 4)) = v;
+        }
+        fence_proxy_async_smem();
+      } else if constexpr (C::TWO) {
         uint8_t* dst = qsm + wg * (C::QROWS * D * 2) + row % C::QROWS * 128;
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) {
@@ -820,17 +881,22 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM, LISTED>::THREADS, Cfg<FMT, D
         if (active && run) {
           const int p0 = t * kTile;
           if constexpr (C::SPAN) {
-            if (valid && (p0 + kTile > s.full || p0 < s.lo)) see &= span_mask(a, s.q0 + qi, mine.tok, p0);
+            // read again where it is needed: kept in registers they would spill
+            if (valid && (p0 + kTile > s.full || p0 < s.lo)) see &= span_mask(a, s.q0 + qi, token_at(a, s.q0 + qi), p0);
           } else if (!C::SPARSE && valid && p0 + kTile > s.full) {
             see &= row_mask(a, s, qi, p0);
           }
           const bool some = !__all_sync(0xffffffffu, see == ~0ull);  // a key that some row does not see
           float scale2 = a.scale2;
           // the place from which a row measures distance: its own, or of what it sees the nearest
-          [[maybe_unused]] int from = 0;
+          [[maybe_unused]] float from = 0.f, slope2 = 0.f;
+          [[maybe_unused]] bool capped = false;  // in TMEM
           if constexpr (C::SPAN) {
-            from = nearest(mine.tok) - p0;
             if (a.cap2 != 0.f || a.slopes) scale2 = 1.f;  // the scores become exponents of 2 as they are changed
+            if (a.slopes && valid) {
+              from = static_cast<float>(nearest(token_at(a, s.q0 + qi)) - p0);
+              slope2 = a.slopes[s.h * a.G + mine.g] * 1.4426950408889634f;
+            }
           }
           const unsigned long long sc = pack2(scale2, scale2);
           uint32_t p[32];
@@ -843,13 +909,30 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM, LISTED>::THREADS, Cfg<FMT, D
             uint32_t x[2][32];
             tmem_ld32(tS, x[0]);
             tmem_ld32(tS + 32, x[1]);
-            const float sub = m == -INFINITY ? 0.f : m;
-            const unsigned long long sb = pack2(-sub, -sub);
+            float sub = m == -INFINITY ? 0.f : m;
             unsigned long long sum[2] = {0ull, 0ull};  // pairs of fp32 zeros
             float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
             tmem_ld_wait32(x[0]);
             tmem_ld_wait32(x[1]);
-            if constexpr (C::SPAN) change_scores(a, x, mine.slope2, from);
+            [[maybe_unused]] float shift = 0.f;  // of all of the tile's exponents
+            if constexpr (C::SPAN) {
+              if (a.cap2 != 0.f && !capped && !__all_sync(0xffffffffu, cap_near(a, x))) {
+                cap_any(a, tS);
+                capped = true;
+                continue;
+              }
+              if (a.slopes) {
+                if (a.cap2 == 0.f) {
+#pragma unroll
+                  for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) x[c][i] = __float_as_uint(__uint_as_float(x[c][i]) * a.scale2);
+                }
+                shift = bias_scores(x, slope2, from);
+                sub -= shift;
+              }
+            }
+            const unsigned long long sb = pack2(-sub, -sub);
             if (some) {
 #pragma unroll
               for (int c = 0; c < 2; ++c) {
@@ -873,7 +956,8 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM, LISTED>::THREADS, Cfg<FMT, D
                 const __nv_bfloat162 w = __floats2bfloat162_rn(e0, e1);
                 memcpy(&p[16 * c + i], &w, 4);
               }
-            const float mnew = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale2;
+            float mnew = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale2;
+            if constexpr (C::SPAN) mnew += shift;
             const bool grow = mnew > m + 8.f || (m == -INFINITY && mnew > m);
             if (!__any_sync(0xffffffffu, grow)) {
               float l0, l1;
@@ -958,7 +1042,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM, LISTED>::THREADS, Cfg<FMT, D
       if (active && run) {
         if (fix) {
           if constexpr (C::SPAN)
-            fix_nonfinite<FMT, D>(a, done, done.t0, done.t1, qi, valid, tO, mine.tok);
+            fix_nonfinite<FMT, D>(a, done, done.t0, done.t1, qi, valid, tO, token_at(a, min(done.q0 + qi, a.Tq - 1)));
           else
             fix_nonfinite<FMT, D>(a, done, max(done.t0, done.full / kTile), done.t1, qi, valid, tO);
         }
@@ -1005,6 +1089,29 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM, LISTED>::THREADS, Cfg<FMT, D
               }
             }
           }
+          if constexpr (C::SPAN) {
+            if (whole) {
+              // four lanes exchange their rows' 16-byte runs, so that a store's
+              // lanes have 64 bytes of a row each four
+              uint32_t w[4][4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const float u = __uint_as_float(o[8 * i + 2 * e]) * inv, v = __uint_as_float(o[8 * i + 2 * e + 1]) * inv;
+                  const __nv_bfloat162 p = l == 0.f ? __floats2bfloat162_rn(0.f, 0.f) : __floats2bfloat162_rn(u, v);
+                  memcpy(&w[i][e], &p, 4);
+                }
+              swap_runs<1>(w, lane & 1);
+              swap_runs<2>(w, lane & 2);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const unsigned long long to = __shfl_sync(0xffffffffu, valid ? reinterpret_cast<unsigned long long>(dst) : 0ull, (lane & 28) + i);
+                if (to) reinterpret_cast<uint4*>(to)[4 * c + (lane & 3)] = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
+              }
+              continue;
+            }
+          }
           if (!valid) {
           } else if (whole) {
 #pragma unroll
@@ -1027,7 +1134,9 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM, LISTED>::THREADS, Cfg<FMT, D
         if (valid) {
           if (whole) {
             float top = m;
-            if constexpr (C::SPAN) top -= mine.slope2 * away(mine.tok);
+            if constexpr (C::SPAN) {
+              if (a.slopes) top -= a.slopes[head] * 1.4426950408889634f * away(token_at(a, tok));
+            }
             if (a.lse) a.lse[tok * a.kv_heads * a.G + head] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
           } else if (C::SPAN && first && last) {
             if constexpr (C::SPAN) a.base_ml[tok * a.kv_heads * a.G + head] = make_float2(m, l);

@@ -66,10 +66,7 @@ __global__ void __launch_bounds__(256) join_kernel(const Args a, int grid, int r
 #pragma unroll
         for (int i = 0; i < E; ++i) o[i] = fmaf(__ldcg(base + i), wb, o[i] * wm);
       }
-      if (a.slopes && a.lse && lane == 0) {
-        const int4 y = a.tokens[tok];
-        top -= a.slopes[head] * 1.4426950408889634f * away(Token{y.x, y.y, y.z, y.w});
-      }
+      if (a.slopes && a.lse && lane == 0) top -= a.slopes[head] * 1.4426950408889634f * away(token_at(a, tok));
     }
     const float inv = l > 0.f ? 1.f / l : 0.f;
     uint32_t w[E / 2];

@@ -14,6 +14,8 @@
 // sequences for one, with all of their tokens, and the whole pages that they
 // share; its sums go to the workspace, 32 bits each. The second takes each
 // sequence alone and the keys behind those pages, and joins both.
+#include <cmath>
+
 #include "attn_join.cuh"
 
 namespace dsa {
@@ -194,6 +196,27 @@ Shape shape_of(const dsa_ctx* ctx, long long rows, int n) {
   return f;
 }
 
+// The cap as the kernels have it. tanh(y) / y in powers of y^2, for |y| up to
+// 0.625: minimax in tanh's absolute error (2^-25; evaluated in fp32, 2^-23.5), by
+// least squares with weights raised where the error was largest until it was
+// level. y = scale q.k / cap.
+void cap_args(double scale, double cap, SpanArgs& a) {
+  constexpr double kTanh[kCapTerms] = {0.999999463558197, -0.33330482244491577, 0.13291031122207642, -0.05136286839842796,
+                                       0.014530066400766373};
+  const double log2e = 1.4426950408889634, k = scale / cap;
+  a.cap2 = static_cast<float>(cap * log2e);
+  a.to_cap = static_cast<float>(2 * log2e * k);
+  double power = k * cap * log2e;
+  bool fits = true;
+  for (int i = 0; i < kCapTerms; ++i, power *= k * k) {
+    a.poly[i] = static_cast<float>(kTanh[i] * power);
+    fits = fits && std::isfinite(a.poly[i]) && std::fabs(a.poly[i]) >= 1.17549435e-38f;
+  }
+  a.poly_most = static_cast<float>(kCapPoly / k * (kCapPoly / k));
+  // caps thousands of times their usual size: never by the polynomial
+  if (!fits || !std::isfinite(a.poly_most)) a.poly_most = -1.f;
+}
+
 // What follows the attention's own workspace.
 struct SpanWorkspace {
   size_t tokens, units, tiles, group_units, group_tiles, base_ml, base, bytes;
@@ -237,10 +260,7 @@ dsa_status launch_span(dsa_ctx* ctx, const dsa_attn_args& p, const dsa_span& spa
   SpanArgs a = {};
   fill_args(ctx, p, a);
   a.slopes = span.slopes;
-  if (span.cap != 0.0) {
-    a.cap2 = static_cast<float>(span.cap * 1.4426950408889634);
-    a.to_cap = static_cast<float>(p.scale / span.cap);
-  }
+  if (span.cap != 0.0) cap_args(p.scale, span.cap, a);
   a.tokens = reinterpret_cast<int4*>(ws + w.tokens);
   if (groups) {
     a.base_ml = reinterpret_cast<float2*>(ws + w.base_ml);
