@@ -134,6 +134,7 @@ struct SpanArgs : AttnArgs {
   const float* slopes; // [heads] or null
   float cap2, to_cap;  // cap log2 e, 2 log2 e scale / cap; 0: no cap
   float poly[5], poly_most;  // capped score log2 e / q.k in powers of (q.k)^2, and where that holds
+  float fixed;               // what every row is weighed under where capped scores allow it, else -inf
   int units_n;
   int base_mode;       // rows' sums over a shared prefix: 1 these are they, 2 join them where the unit has some
   float2* base_ml;     // [Tq][heads]
@@ -156,11 +157,24 @@ struct Start {
   int b, h, r, tile;
 };
 
-template <int FMT, int D, int FORM, bool LISTED = false>
+// What a kernel does to the scores. Not listed: the tree and the selection
+// forms. The listed units' kernels are apart, because one with all of their code
+// spilled (a chunk of 2048 tokens without a cap took 611 us in it, 568 alone):
+// scores as they are; capped ones, all weighed under one exponent; biased ones,
+// capped or not, and caps too wide for that.
+enum Scores { kUnlisted = 0, kAsTheyAre = 1, kCapped = 2, kBiased = 3, kScores = 4 };
+
+template <int FMT, int D, int FORM, int SCORES = kUnlisted>
 struct Cfg {
-  static constexpr bool SPAN = LISTED;
-  using Args = std::conditional_t<LISTED, SpanArgs, AttnArgs>;
-  using Segment = std::conditional_t<LISTED, SpanSeg, Seg>;
+  static constexpr bool SPAN = SCORES != kUnlisted;
+  // A segment's tiles from the last to the first: a bias makes the nearest keys'
+  // weights the largest, so the maximum is known after the first tile and does
+  // not move in every one (2048 tokens behind 8192 1176 -> 634 us). Without a
+  // bias the first tile would be the one in which rows see the fewest keys
+  // (packed documents 394 -> 429).
+  static constexpr bool BACKWARDS = SCORES == kBiased;
+  using Args = std::conditional_t<SPAN, SpanArgs, AttnArgs>;
+  using Segment = std::conditional_t<SPAN, SpanSeg, Seg>;
   static constexpr bool SPARSE = FORM == kSparse || FORM == kSparseFew;
   static constexpr bool FEW = FORM == kTreeFew || FORM == kSparseFew;
   static constexpr bool TWO = FORM == kWide || FEW;    // two score buffers, queries in shared memory, warps that issue the products
@@ -531,25 +545,12 @@ __device__ __forceinline__ float away(const Token& y) { return fabsf(static_cast
 constexpr int kCapTerms = 5;
 constexpr double kCapPoly = 0.625;
 
-__device__ __forceinline__ bool cap_near(const SpanArgs& a, uint32_t (&x)[2][32]) {
-  float most = 0.f;
+// capped score log2 e / q.k of two scores whose squares are u
+__device__ __forceinline__ unsigned long long cap_factor(const SpanArgs& a, unsigned long long u) {
+  unsigned long long y = pack2(a.poly[kCapTerms - 1], a.poly[kCapTerms - 1]);
 #pragma unroll
-  for (int c = 0; c < 2; ++c)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const unsigned long long s = pack2(__uint_as_float(x[c][2 * i]), __uint_as_float(x[c][2 * i + 1]));
-      const unsigned long long u = mul2(s, s);
-      unsigned long long p = pack2(a.poly[kCapTerms - 1], a.poly[kCapTerms - 1]);
-#pragma unroll
-      for (int k = kCapTerms - 2; k >= 0; --k) p = fma2(p, u, pack2(a.poly[k], a.poly[k]));
-      float u0, u1, y0, y1;
-      unpack2(u, u0, u1);
-      unpack2(mul2(p, s), y0, y1);
-      most = fmaxf(most, fmaxf(u0, u1));
-      x[c][2 * i] = __float_as_uint(y0);
-      x[c][2 * i + 1] = __float_as_uint(y1);
-    }
-  return most <= a.poly_most;
+  for (int k = kCapTerms - 2; k >= 0; --k) y = fma2(y, u, pack2(a.poly[k], a.poly[k]));
+  return y;
 }
 
 // in TMEM, where a tile's scores stay capped: in registers the 64 chains spill
@@ -567,12 +568,32 @@ __device__ __forceinline__ void cap_any(const SpanArgs& a, uint32_t taddr) {
   tmem_st_wait();
 }
 
+// 64 scores capped by the polynomial, in place; whether all of a row's were
+// small enough for it.
+__device__ __forceinline__ bool cap_near(const SpanArgs& a, uint32_t (&x)[2][32]) {
+  float most = 0.f;
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const unsigned long long s = pack2(__uint_as_float(x[c][2 * i]), __uint_as_float(x[c][2 * i + 1]));
+      const unsigned long long u = mul2(s, s);
+      float u0, u1, y0, y1;
+      unpack2(u, u0, u1);
+      unpack2(mul2(cap_factor(a, u), s), y0, y1);
+      most = fmaxf(most, fmaxf(u0, u1));
+      x[c][2 * i] = __float_as_uint(y0);
+      x[c][2 * i + 1] = __float_as_uint(y1);
+    }
+  return most <= a.poly_most;
+}
+
 // Takes slope |from - j| off 64 exponents of 2; `from` counts from the first
 // key. Where no key lies past it in any of the warp's rows the bias is slope (j -
 // from), of which slope from is left to the caller: one operation a score.
-__device__ __forceinline__ float bias_scores(uint32_t (&x)[2][32], float slope2, float from) {
+__device__ __forceinline__ float bias_scores(uint32_t (&x)[2][32], float slope2, float from, bool edge) {
   asm volatile("" : "+f"(slope2), "+f"(from));  // or the 64 products move out of the loop around, into registers there are not
-  if (__all_sync(0xffffffffu, from >= 63.f)) {
+  if (!edge) {
 #pragma unroll
     for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -585,6 +606,42 @@ __device__ __forceinline__ float bias_scores(uint32_t (&x)[2][32], float slope2,
     for (int i = 0; i < 32; ++i)
       x[c][i] = __float_as_uint(fmaf(-slope2, fabsf(from - static_cast<float>(32 * c + i)), __uint_as_float(x[c][i])));
   return 0.f;
+}
+
+// The weights 2^(x - sub) of a row's 64 keys, as bf16 pairs, their sum, and the
+// largest exponent x. x = mul score; or, CAP, the score capped by the
+// polynomial, and instead of the largest exponent, which nobody asks for, the
+// largest (q.k)^2.
+struct Weighed {
+  float most, sum;
+};
+
+template <bool CAP>
+__device__ __forceinline__ Weighed weigh(const SpanArgs& a, const uint32_t (&x)[2][32], uint32_t (&p)[32], float mul, float sub) {
+  const unsigned long long sc = pack2(mul, mul), sb = pack2(-sub, -sub);
+  unsigned long long sum[2] = {0ull, 0ull};  // pairs of fp32 zeros
+  constexpr float kLeast = CAP ? 0.f : -INFINITY;
+  float mx[4] = {kLeast, kLeast, kLeast, kLeast};
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const unsigned long long s = pack2(__uint_as_float(x[c][2 * i]), __uint_as_float(x[c][2 * i + 1]));
+      const unsigned long long u = CAP ? mul2(s, s) : s;
+      float e0, e1;
+      unpack2(u, e0, e1);
+      mx[i & 3] = fmaxf(mx[i & 3], fmaxf(e0, e1));
+      unpack2(CAP ? fma2(s, cap_factor(a, u), sb) : fma2(s, sc, sb), e0, e1);
+      e0 = ex2(e0);
+      e1 = ex2(e1);
+      sum[i & 1] = add2(sum[i & 1], pack2(e0, e1));
+      const __nv_bfloat162 w = __floats2bfloat162_rn(e0, e1);
+      memcpy(&p[16 * c + i], &w, 4);
+    }
+  float l0, l1;
+  unpack2(add2(sum[0], sum[1]), l0, l1);
+  const float most = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+  return Weighed{CAP ? most : most * mul, l0 + l1};
 }
 
 __device__ __forceinline__ float widen_one(uint32_t bits) { return __uint_as_float(bits << 16); }
@@ -627,10 +684,10 @@ __device__ __noinline__ void fix_nonfinite(const AttnArgs& a, const Segment& s, 
   }
 }
 
-template <int FMT, int D, int FORM, bool LISTED>
-__global__ void __launch_bounds__(Cfg<FMT, D, FORM, LISTED>::THREADS, Cfg<FMT, D, FORM, LISTED>::CTAS)
-    attn_kernel(const __grid_constant__ CUtensorMap tm, const typename Cfg<FMT, D, FORM, LISTED>::Args a) {
-  using C = Cfg<FMT, D, FORM, LISTED>;
+template <int FMT, int D, int FORM, int SCORES>
+__global__ void __launch_bounds__(Cfg<FMT, D, FORM, SCORES>::THREADS, Cfg<FMT, D, FORM, SCORES>::CTAS)
+    attn_kernel(const __grid_constant__ CUtensorMap tm, const typename Cfg<FMT, D, FORM, SCORES>::Args a) {
+  using C = Cfg<FMT, D, FORM, SCORES>;
   using Segment = typename C::Segment;
   using L = kvf::Layout<FMT, D>;
   constexpr int NSW = C::SW * C::WG;  // softmax warps
@@ -836,6 +893,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM, LISTED>::THREADS, Cfg<FMT, D
       }
     };
     // the second product of the last tile has completed
+    auto tile_at = [&](int t) { return C::BACKWARDS ? s.t0 + s.t1 - 1 - t : t; };
     auto wait_product = [&]() { return wait_warp(&sh.o_full[wg][(ns - 1) & (C::SBUF - 1)], ((ns - 1) / C::SBUF) & 1); };
     if (more && has_rows(wg, s)) start_unit(s);
     while (more && run) {
@@ -856,6 +914,16 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM, LISTED>::THREADS, Cfg<FMT, D
       const Row mine = at_row;
       const int qi = mine.q;                   // the row's query in its sequence
       float m = -INFINITY, l = 0.f;
+      // the place that a row measures distance from, and its head's slope
+      [[maybe_unused]] int near = 0;
+      [[maybe_unused]] float slope2 = 0.f;
+      if constexpr (C::SPAN) {
+        if constexpr (SCORES == kCapped) m = a.fixed;
+        if (SCORES == kBiased && a.slopes && valid) {
+          near = nearest(token_at(a, s.q0 + qi));
+          slope2 = a.slopes[s.h * a.G + mine.g] * 1.4426950408889634f;
+        }
+      }
       for (int t = s.t0; t < s.t1; ++t, ++n, ++ns) {
         const int buf = ns & (C::SBUF - 1);
         auto wait_scores = [&]() { run = run && wait_warp(&sh.s_full[wg][buf], (ns / C::SBUF) & 1); };
@@ -871,104 +939,143 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM, LISTED>::THREADS, Cfg<FMT, D
         tc_fence_after();
         const uint32_t tS = tb + C::S + 64 * buf + lanes;
         if (active && run) {
-          const int p0 = t * kTile;
-          if constexpr (C::SPAN) {
-            // read again where it is needed: kept in registers they would spill
-            if (valid && (p0 + kTile > s.full || p0 < s.lo)) see &= span_mask(a, s.q0 + qi, token_at(a, s.q0 + qi), p0);
-          } else if (!C::SPARSE && valid && p0 + kTile > s.full) {
-            see &= row_mask(a, s, qi, p0);
-          }
-          const bool some = !__all_sync(0xffffffffu, see == ~0ull);  // a key that some row does not see
-          float scale2 = a.scale2;
-          // the place from which a row measures distance: its own, or of what it sees the nearest
-          [[maybe_unused]] float from = 0.f, slope2 = 0.f;
-          [[maybe_unused]] bool capped = false;  // in TMEM
-          if constexpr (C::SPAN) {
-            if (a.cap2 != 0.f || a.slopes) scale2 = 1.f;  // the scores become exponents of 2 as they are changed
-            if (a.slopes && valid) {
-              from = static_cast<float>(nearest(token_at(a, s.q0 + qi)) - p0);
-              slope2 = a.slopes[s.h * a.G + mine.g] * 1.4426950408889634f;
-            }
-          }
-          const unsigned long long sc = pack2(scale2, scale2);
+          const int p0 = tile_at(t) * kTile;
+          if (!C::SPAN && !C::SPARSE && valid && p0 + kTile > s.full) see &= row_mask(a, s, qi, p0);
           uint32_t p[32];
-          // The weights are taken under the running maximum while the tile's
-          // own is found. Only if that is more than 2^8 above it (a unit's
-          // first tile, rarely later) does the maximum move, are the sums
-          // rescaled and the tile's weights taken again; the weights stay
-          // below 2^8 otherwise.
-          while (true) {
-            uint32_t x[2][32];
-            tmem_ld32(tS, x[0]);
-            tmem_ld32(tS + 32, x[1]);
-            float sub = m == -INFINITY ? 0.f : m;
-            unsigned long long sum[2] = {0ull, 0ull};  // pairs of fp32 zeros
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-            tmem_ld_wait32(x[0]);
-            tmem_ld_wait32(x[1]);
-            [[maybe_unused]] float shift = 0.f;  // of all of the tile's exponents
-            if constexpr (C::SPAN) {
-              if (a.cap2 != 0.f && !capped && !__all_sync(0xffffffffu, cap_near(a, x))) {
+          if constexpr (!C::SPAN) {
+            const bool some = !__all_sync(0xffffffffu, see == ~0ull);  // a key that some row does not see
+            const unsigned long long sc = pack2(a.scale2, a.scale2);
+            // The weights are taken under the running maximum while the tile's
+            // own is found. Only if that is more than 2^8 above it (a unit's
+            // first tile, rarely later) does the maximum move, are the sums
+            // rescaled and the tile's weights taken again; the weights stay
+            // below 2^8 otherwise.
+            while (true) {
+              uint32_t x[2][32];
+              tmem_ld32(tS, x[0]);
+              tmem_ld32(tS + 32, x[1]);
+              const float sub = m == -INFINITY ? 0.f : m;
+              unsigned long long sum[2] = {0ull, 0ull};  // pairs of fp32 zeros
+              float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+              tmem_ld_wait32(x[0]);
+              tmem_ld_wait32(x[1]);
+              const unsigned long long sb = pack2(-sub, -sub);
+              if (some) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                  const uint32_t bits = static_cast<uint32_t>(see >> (32 * c));
+#pragma unroll
+                  for (int i = 0; i < 32; ++i)
+                    if (!((bits >> i) & 1)) x[c][i] = 0xFF800000u;
+                }
+              }
+#pragma unroll
+              for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  const float s0 = __uint_as_float(x[c][2 * i]), s1 = __uint_as_float(x[c][2 * i + 1]);
+                  mx[i & 3] = fmaxf(mx[i & 3], fmaxf(s0, s1));
+                  float e0, e1;
+                  unpack2(fma2(pack2(s0, s1), sc, sb), e0, e1);
+                  e0 = ex2(e0);
+                  e1 = ex2(e1);
+                  sum[i & 1] = add2(sum[i & 1], pack2(e0, e1));
+                  const __nv_bfloat162 w = __floats2bfloat162_rn(e0, e1);
+                  memcpy(&p[16 * c + i], &w, 4);
+                }
+              const float mnew = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale2;
+              const bool grow = mnew > m + 8.f || (m == -INFINITY && mnew > m);
+              if (!__any_sync(0xffffffffu, grow)) {
+                float l0, l1;
+                unpack2(add2(sum[0], sum[1]), l0, l1);
+                l += l0 + l1;
+                break;
+              }
+              // weights of up to 2^8 stand before this factor: flushed to zero below
+              // 2^-126 it would lose weights of 2^-118, which fp32 holds
+              const float alpha = grow ? ex2_denorm(m - mnew) : 1.f;
+              if (t > s.t0) {  // after the last tile's second product
+                run = run && wait_product();
+                tc_fence_after();
+                l *= alpha;
+#pragma unroll 1
+                for (int c = 0; c < D / 16; ++c) tmem_scale16(tO + 16 * c, alpha);
+                tmem_st_wait();
+              }
+              if (grow) m = mnew;
+            }
+          } else {
+            if (valid && (p0 + kTile > s.full || p0 < s.lo)) see &= span_mask(a, s.q0 + qi, token_at(a, s.q0 + qi), p0);
+            [[maybe_unused]] const float from = static_cast<float>(near - p0);
+            const bool some = !__all_sync(0xffffffffu, see == ~0ull);  // a key that some row does not see
+            constexpr bool CAP = SCORES == kCapped, BIAS = SCORES == kBiased;
+            [[maybe_unused]] bool capped = !CAP && !(BIAS && a.cap2 != 0.f);  // in TMEM, or not to be
+            if constexpr (CAP) {
+              if (some) {  // masks come after the cap, and few tiles have one
+                cap_any(a, tS);
+                capped = true;
+              }
+            }
+            while (true) {
+              uint32_t x[2][32];
+              tmem_ld32(tS, x[0]);
+              tmem_ld32(tS + 32, x[1]);
+              tmem_ld_wait32(x[0]);
+              tmem_ld_wait32(x[1]);
+              Weighed w;
+              if (CAP && !capped) {
+                w = weigh<true>(a, x, p, 1.f, m);
+                if (__all_sync(0xffffffffu, w.most <= a.poly_most)) {
+                  l += w.sum;
+                  break;
+                }
                 cap_any(a, tS);
                 capped = true;
                 continue;
               }
-              if (a.slopes) {
+              float shift = 0.f;  // of all of the tile's exponents
+              if constexpr (BIAS) {
+                if (!capped && !__all_sync(0xffffffffu, cap_near(a, x))) {
+                  cap_any(a, tS);
+                  capped = true;
+                  continue;
+                }
                 if (a.cap2 == 0.f) {
 #pragma unroll
                   for (int c = 0; c < 2; ++c)
 #pragma unroll
                     for (int i = 0; i < 32; ++i) x[c][i] = __float_as_uint(__uint_as_float(x[c][i]) * a.scale2);
                 }
-                shift = bias_scores(x, slope2, from);
-                sub -= shift;
+                shift = bias_scores(x, slope2, from, !__all_sync(0xffffffffu, from >= 63.f || !valid));
               }
-            }
-            const unsigned long long sb = pack2(-sub, -sub);
-            if (some) {
+              if (some) {
 #pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                const uint32_t bits = static_cast<uint32_t>(see >> (32 * c));
+                for (int c = 0; c < 2; ++c) {
+                  const uint32_t bits = static_cast<uint32_t>(see >> (32 * c));
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  if (!((bits >> i) & 1)) x[c][i] = 0xFF800000u;
+                  for (int i = 0; i < 32; ++i)
+                    if (!((bits >> i) & 1)) x[c][i] = 0xFF800000u;
+                }
               }
-            }
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const float s0 = __uint_as_float(x[c][2 * i]), s1 = __uint_as_float(x[c][2 * i + 1]);
-                mx[i & 3] = fmaxf(mx[i & 3], fmaxf(s0, s1));
-                float e0, e1;
-                unpack2(fma2(pack2(s0, s1), sc, sb), e0, e1);
-                e0 = ex2(e0);
-                e1 = ex2(e1);
-                sum[i & 1] = add2(sum[i & 1], pack2(e0, e1));
-                const __nv_bfloat162 w = __floats2bfloat162_rn(e0, e1);
-                memcpy(&p[16 * c + i], &w, 4);
+              w = weigh<false>(a, x, p, CAP || BIAS ? 1.f : a.scale2, (m == -INFINITY ? 0.f : m) - shift);
+              w.most += shift;
+              const bool grow = !CAP && (w.most > m + kSpanStep || (m == -INFINITY && w.most > m));
+              if (!__any_sync(0xffffffffu, grow)) {
+                l += w.sum;
+                break;
               }
-            float mnew = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale2;
-            if constexpr (C::SPAN) mnew += shift;
-            const bool grow = mnew > m + (C::SPAN ? kSpanStep : 8.f) || (m == -INFINITY && mnew > m);
-            if (!__any_sync(0xffffffffu, grow)) {
-              float l0, l1;
-              unpack2(add2(sum[0], sum[1]), l0, l1);
-              l += l0 + l1;
-              break;
-            }
-            // weights of up to 2^8 stand before this factor: flushed to zero below
-            // 2^-126 it would lose weights of 2^-118, which fp32 holds
-            const float alpha = grow ? ex2_denorm(m - mnew) : 1.f;
-            if (t > s.t0) {  // after the last tile's second product
-              run = run && wait_product();
-              tc_fence_after();
-              l *= alpha;
+              const float mnew = w.most;
+              const float alpha = grow ? ex2_denorm(m - mnew) : 1.f;
+              if (t > s.t0) {  // after the last tile's second product
+                run = run && wait_product();
+                tc_fence_after();
+                l *= alpha;
 #pragma unroll 1
-              for (int c = 0; c < D / 16; ++c) tmem_scale16(tO + 16 * c, alpha);
-              tmem_st_wait();
+                for (int c = 0; c < D / 16; ++c) tmem_scale16(tO + 16 * c, alpha);
+                tmem_st_wait();
+              }
+              if (grow) m = mnew;
             }
-            if (grow) m = mnew;
           }
           tmem_st32(tS, p);  // over scores that are not needed any more
         }
@@ -1477,7 +1584,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM, LISTED>::THREADS, Cfg<FMT, D
         u1 = page_of(g1, s.t0);
       }
       for (int x = 0; run && x < nt; ++x, ++n) {
-        const int t = s.t0 + x;
+        const int t = C::BACKWARDS ? s.t1 - 1 - x : s.t0 + x;
         // the tile's place in the order the products take keys and values:
         // K0 V0 K1 V1 .., or K0 K1 V0 K2 V1 .. with two score buffers
         const int order = parts + (C::SBUF == 1 ? 2 * x + v : !v ? (x ? 2 * x - 1 : 0) : x + 1 < nt ? 2 * x + 2 : 2 * nt - 1);
@@ -1497,7 +1604,10 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM, LISTED>::THREADS, Cfg<FMT, D
           e1 = entry(t + 2, lane + 32);
           vm = __ballot_sync(0xffffffffu, k0 != NONE) | (static_cast<unsigned long long>(__ballot_sync(0xffffffffu, k1 != NONE)) << 32);
         } else {
-          if ((x & 31) == 0) pg = t + lane < min(s.t1, npg) ? table[t + lane] : -1;
+          if ((x & 31) == 0) {
+            const int mine_at = C::BACKWARDS ? t - lane : t + lane;
+            pg = mine_at < min(s.t1, npg) && (!C::BACKWARDS || mine_at >= s.t0) ? table[mine_at] : -1;
+          }
           page = __shfl_sync(0xffffffffu, pg, x & 31);
           const bool ok = page >= 0 && page < a.num_pages;
           if (!ok && t < npg && lw == 0 && lane == 0) atomicOr(a.status, DSA_DEV_BOUNDS);
@@ -1602,39 +1712,39 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM, LISTED>::THREADS, Cfg<FMT, D
   }
 }
 
-template <int FMT, int D, int FORM, class Args>
+template <int FMT, int D, int FORM, int SCORES, class Args>
 dsa_status run_one(dsa_ctx* ctx, const CUtensorMap& tm, const Args& a, int grid, cudaStream_t stream) {
-  constexpr bool LISTED = std::is_same_v<Args, SpanArgs>;
-  using C = Cfg<FMT, D, FORM, LISTED>;
-  auto kern = attn_kernel<FMT, D, FORM, LISTED>;
+  using C = Cfg<FMT, D, FORM, SCORES>;
+  auto kern = attn_kernel<FMT, D, FORM, SCORES>;
   constexpr int bytes = smem_bytes<C>();
   static_assert(bytes * C::CTAS <= 233472 - 1024 * C::CTAS, "shared memory of an SM");
-  const uint64_t bit = 1ull << (((LISTED ? 3 + FMT : FMT) * 2 + (D == 128)) * kForms + FORM);  // once a context and kernel
-  if (!(ctx->attn_ready & bit)) {
+  constexpr int at = ((SCORES * 3 + FMT) * 2 + (D == 128)) * kForms + FORM;  // once a context and kernel
+  static_assert(at < 64 * static_cast<int>(sizeof(ctx->attn_ready) / sizeof(uint64_t)), "a bit for each kernel");
+  if (!(ctx->attn_ready[at / 64] >> (at % 64) & 1)) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return DSA_ERR_CUDA;
-    ctx->attn_ready |= bit;
+    ctx->attn_ready[at / 64] |= 1ull << (at % 64);
   }
   LaunchScope scope(ctx, DSA_K_ATTN, stream);
   return launch_pdl(kern, dim3(grid), dim3(C::THREADS), bytes, stream, tm, a) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 
-template <int FMT, int D, class Args>
+template <int FMT, int D, int SCORES, class Args>
 dsa_status run_dim(dsa_ctx* ctx, int form, const CUtensorMap& tm, const Args& a, int grid, cudaStream_t stream) {
-  if constexpr (!std::is_same_v<Args, SpanArgs>) {
-    if (form == kSparse) return run_one<FMT, D, kSparse>(ctx, tm, a, grid, stream);
-    if (form == kSparseFew) return run_one<FMT, D, kSparseFew>(ctx, tm, a, grid, stream);
+  if constexpr (SCORES == kUnlisted) {
+    if (form == kSparse) return run_one<FMT, D, kSparse, SCORES>(ctx, tm, a, grid, stream);
+    if (form == kSparseFew) return run_one<FMT, D, kSparseFew, SCORES>(ctx, tm, a, grid, stream);
   }
   switch (form) {
-    case kTree: return run_one<FMT, D, kTree>(ctx, tm, a, grid, stream);
-    case kTreeFew: return run_one<FMT, D, kTreeFew>(ctx, tm, a, grid, stream);
-    default: return run_one<FMT, D, kWide>(ctx, tm, a, grid, stream);
+    case kTree: return run_one<FMT, D, kTree, SCORES>(ctx, tm, a, grid, stream);
+    case kTreeFew: return run_one<FMT, D, kTreeFew, SCORES>(ctx, tm, a, grid, stream);
+    default: return run_one<FMT, D, kWide, SCORES>(ctx, tm, a, grid, stream);
   }
 }
 
-template <int FMT, class Args>
+template <int FMT, int SCORES = kUnlisted, class Args>
 dsa_status run_fmt(dsa_ctx* ctx, int form, int D, const CUtensorMap& tm, const Args& a, int grid, cudaStream_t stream) {
-  if (D == 128) return run_dim<FMT, 128>(ctx, form, tm, a, grid, stream);
-  return run_dim<FMT, 64>(ctx, form, tm, a, grid, stream);
+  if (D == 128) return run_dim<FMT, 128, SCORES>(ctx, form, tm, a, grid, stream);
+  return run_dim<FMT, 64, SCORES>(ctx, form, tm, a, grid, stream);
 }
 
 // Where the parts of the workspace begin: two pieces a CTA, 256 rows on each SM
@@ -1649,14 +1759,16 @@ Workspace layout(const dsa_ctx* ctx, int D);
 void fill_args(const dsa_ctx* ctx, const dsa_attn_args& p, AttnArgs& a);
 bool cache_map(const dsa_ctx* ctx, const dsa_attn_args& p, int box_rows, CUtensorMap& tm);
 
-// One cache format's kernels: attn.cu (bf16), attn_fp8.cu, attn_fp4.cu; of
-// listed units attn_span.cu, attn_span_fp8.cu, attn_span_fp4.cu.
+// One cache format's kernels: attn.cu (bf16), attn_fp8.cu, attn_fp4.cu.
 dsa_status run_bf16(dsa_ctx* ctx, int form, int D, const CUtensorMap& tm, const AttnArgs& a, int grid, cudaStream_t stream);
 dsa_status run_fp8(dsa_ctx* ctx, int form, int D, const CUtensorMap& tm, const AttnArgs& a, int grid, cudaStream_t stream);
 dsa_status run_fp4(dsa_ctx* ctx, int form, int D, const CUtensorMap& tm, const AttnArgs& a, int grid, cudaStream_t stream);
-dsa_status run_span_bf16(dsa_ctx* ctx, int form, int D, const CUtensorMap& tm, const SpanArgs& a, int grid, cudaStream_t stream);
-dsa_status run_span_fp8(dsa_ctx* ctx, int form, int D, const CUtensorMap& tm, const SpanArgs& a, int grid, cudaStream_t stream);
-dsa_status run_span_fp4(dsa_ctx* ctx, int form, int D, const CUtensorMap& tm, const SpanArgs& a, int grid, cudaStream_t stream);
+
+// Listed units' kernels of one cache format and treatment of the scores:
+// span_*.cu, span_cap_*.cu, span_bias_*.cu, so that they compile in parallel.
+using RunSpan = dsa_status(dsa_ctx* ctx, int form, int D, const CUtensorMap& tm, const SpanArgs& a, int grid, cudaStream_t stream);
+RunSpan run_span_bf16, run_span_fp8, run_span_fp4, run_span_cap_bf16, run_span_cap_fp8, run_span_cap_fp4, run_span_bias_bf16,
+    run_span_bias_fp8, run_span_bias_fp4;
 
 }  // namespace at
 }  // namespace dsa

@@ -1,5 +1,5 @@
-// Attention of spans and behind shared prefixes: the plan of the units, the
-// bf16 kernels and the launches. The attention itself is attn.cuh's span form.
+// Attention of spans and behind shared prefixes: the plan of the units and the
+// launches. The attention itself is attn.cuh's span form.
 //
 // The plan lists units of up to 32, 128 or 256 rows (tokens x the G query heads
 // of a kv head; one list for all kv heads) with the 64-key tiles that one of
@@ -178,10 +178,6 @@ __global__ void __launch_bounds__(256) span_plan_kernel(const AttnArgs a, const 
   }
 }
 
-dsa_status run_span_bf16(dsa_ctx* ctx, int form, int D, const CUtensorMap& tm, const SpanArgs& a, int grid, cudaStream_t stream) {
-  return run_fmt<DSA_FMT_BF16>(ctx, form, D, tm, a, grid, stream);
-}
-
 // The form for n sequences (or groups) with these rows in all; the rule is launch_attn's.
 struct Shape {
   int form, rows, grid, places;  // rows of a unit, CTAs, places of the list
@@ -215,6 +211,11 @@ void cap_args(double scale, double cap, SpanArgs& a) {
   a.poly_most = static_cast<float>(kCapPoly / k * (kCapPoly / k));
   // caps thousands of times their usual size: never by the polynomial
   if (!fits || !std::isfinite(a.poly_most)) a.poly_most = -1.f;
+  // Capped scores lie within cap of zero, so all rows can be weighed under the
+  // same exponent and no maximum is looked for: 2^H for the largest possible
+  // weight, H 8 or as much as keeps the smallest at 2^-120. Up to cap 62.
+  const double range = cap * log2e, room = std::fmax(8.0, 2 * range - 120);
+  if (range <= 90 && !a.slopes) a.fixed = static_cast<float>(range - room);
 }
 
 // What follows the attention's own workspace.
@@ -260,6 +261,7 @@ dsa_status launch_span(dsa_ctx* ctx, const dsa_attn_args& p, const dsa_span& spa
   SpanArgs a = {};
   fill_args(ctx, p, a);
   a.slopes = span.slopes;
+  a.fixed = -INFINITY;
   if (span.cap != 0.0) cap_args(p.scale, span.cap, a);
   a.tokens = reinterpret_cast<int4*>(ws + w.tokens);
   if (groups) {
@@ -294,7 +296,11 @@ dsa_status launch_span(dsa_ctx* ctx, const dsa_attn_args& p, const dsa_span& spa
                    static_cast<const AttnArgs&>(a), plan) != cudaSuccess)
       return DSA_ERR_CUDA;
   }
-  const auto run = p.fmt == DSA_FMT_BF16 ? run_span_bf16 : p.fmt == DSA_FMT_FP8 ? run_span_fp8 : run_span_fp4;
+  static constexpr RunSpan* kRun[3][3] = {{run_span_bf16, run_span_fp8, run_span_fp4},
+                                          {run_span_cap_bf16, run_span_cap_fp8, run_span_cap_fp4},
+                                          {run_span_bias_bf16, run_span_bias_fp8, run_span_bias_fp4}};
+  // a cap too wide to weigh all rows under one exponent goes with slopes of zero
+  RunSpan* const run = kRun[a.slopes || (a.cap2 != 0.f && a.fixed == -INFINITY) ? 2 : a.cap2 != 0.f ? 1 : 0][p.fmt];
   auto pass = [&](const Shape& f) {
     const dsa_status st = run(ctx, f.form, p.head_dim, tm, a, f.grid, stream);
     if (st != DSA_OK) return st;

@@ -31,7 +31,7 @@ struct dsa_ctx {
   float* gamma;          // [128]
   unsigned int* status;  // device status word
   void* encode_tiled;    // cuTensorMapEncodeTiled entry point
-  uint64_t attn_ready;   // attention kernels whose shared memory limit is raised
+  uint64_t attn_ready[2];  // attention kernels whose shared memory limit is raised
   // kernel timing (dsa_profile_*)
   int prof_on;
   int prof_n;                    // records in use
