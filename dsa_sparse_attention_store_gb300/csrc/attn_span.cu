@@ -306,7 +306,7 @@ dsa_status launch_span(dsa_ctx* ctx, const dsa_attn_args& p, const dsa_span& spa
     if (st != DSA_OK) return st;
     LaunchScope scope(ctx, DSA_K_ATTN_JOIN, stream);
     const cudaError_t e = launch_pdl(p.head_dim == 128 ? join_kernel<128, SpanArgs> : join_kernel<64, SpanArgs>,
-                                     dim3(f.grid, 8), dim3(256), 0, stream, a, f.grid, f.rows);
+                                     dim3(f.grid, f.rows < 64 ? 8 : f.rows / 8), dim3(256), 0, stream, a, f.grid, f.rows);
     return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
   };
   if (groups) {
