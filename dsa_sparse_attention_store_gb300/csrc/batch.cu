@@ -1,24 +1,33 @@
 // Page tables and slot maps of a step, from the lengths of its requests.
 //
-// Every block adds up all sequences' tokens, new pages and returned pages (a
-// run of sequences a thread, then a scan over the threads), so that one launch
-// does and no block waits for another; then the blocks divide the tokens and
-// the returned pages. The pool is never moved: the i-th page that is taken is
-// entry count + returned - 1 - i of the free pages followed by the returned
-// ones, and the returned ones are found through the same sums. No entry that is
-// read is written: pages are read from the free stack only where all returned
-// ones are taken too, and then none is written to it; a row that is read for
-// its returned pages gets no new ones.
+// Every block adds up all sequences' tokens, new pages and returned pages into
+// shared memory, so that one launch does and no block waits for another; then
+// the blocks divide the tokens, the new pages and the returned ones, and find
+// each one's sequence by bisection there. The pool is never moved: the i-th page
+// that is taken is entry count + returned - 1 - i of the free pages followed by
+// the returned ones, and a returned one is found through the same sums. No entry
+// that is read is written: pages are read from the free stack only where all
+// returned ones are taken too, and then none is written to it; a row that is
+// read for its returned pages gets no new ones.
 //
-// What bounds it: one launch and the chain lengths -> sums -> token for small
-// steps, 12 bytes a token for large ones.
+// What bounds it: a step of 64 tokens one launch and the chain of loads lengths
+// -> page -> slot, 3.2 us. 16384 sequences with a million tokens, of which a ninth
+// end, 27 us (12.6 MB, 1.9 us at the copy rate): the sums over all sequences,
+// which every block makes for itself (about 10), the bisections and dependent
+// loads of a thread's tokens (8), and of the pages that come back (5). With a walk
+// along 16 sequences for each token it took 57.
+#include <algorithm>
+
 #include "internal.cuh"
 
 namespace dsa {
 namespace {
 
-constexpr int kThreads = 1024;
 constexpr int kPage = 64;
+constexpr int kMost = 0x7FFFFFFF;
+// Sums that shared memory has room for: of a sequence each up to 16384, of a run
+// of neighbours beyond.
+constexpr int kSums = 16384;
 
 struct Request {
   int old, n, pages, fresh, ended, keep;  // tokens there and to come; pages there, to take, to return; first page to return
@@ -27,19 +36,21 @@ struct Request {
 
 __device__ __forceinline__ Request request(const BatchPlanArgs& a, int b) {
   Request x = {};
-  const int o = a.old_lens[b], n = a.new_lens[b], keep = a.own_from ? a.own_from[b] : 0;
-  const long long most = static_cast<long long>(a.max_pages) * kPage;
-  x.ok = o >= 0 && keep >= 0 && static_cast<long long>(o) + max(n, 0) <= most;
+  // 64 max_pages and so all that is not refused is below 2^31
+  const uint32_t o = a.old_lens[b], keep = a.own_from ? a.own_from[b] : 0, most = a.max_pages * kPage;
+  const int n = a.new_lens[b];
   x.ends = n < 0;
+  const uint32_t len = o + max(n, 0), pages = (o + kPage - 1) / kPage;
+  x.ok = o <= most && len <= most && keep < 0x80000000u;
   if (!x.ok) return x;
   x.old = o;
-  x.pages = (o + kPage - 1) / kPage;
+  x.pages = pages;
   x.keep = keep;
   if (x.ends) {
-    x.ended = max(0, x.pages - keep);
+    x.ended = max(0, x.pages - x.keep);
   } else {
     x.n = n;
-    x.fresh = static_cast<int>((static_cast<long long>(o) + n + kPage - 1) / kPage) - x.pages;
+    x.fresh = (len + kPage - 1) / kPage - pages;
   }
   return x;
 }
@@ -48,23 +59,60 @@ struct Sums {
   long long tokens, fresh, ended;
 };
 
-__global__ void __launch_bounds__(kThreads) batch_plan_kernel(const BatchPlanArgs a) {
-  __shared__ Sums s_before[kThreads + 1];  // of a thread's run of sequences: what came before it
-  __shared__ Sums s_warp[32];
+__device__ __forceinline__ int clamp_sum(long long x) { return static_cast<int>(min(x, static_cast<long long>(kMost))); }
+
+// per: sequences of a run; runs of them; own: neighbouring runs a thread adds
+// up, an odd number, so that a warp's accesses fall into different banks. A
+// thread has EACH neighbouring tokens: four look up their sequence and page once
+// where they are the same.
+template <int THREADS, int EACH>
+__global__ void __launch_bounds__(THREADS) batch_plan_kernel(const BatchPlanArgs a, int per, int runs, int own) {
+  extern __shared__ int s_sums[];  // of each run, then before it: tokens, new pages, returned pages
+  __shared__ Sums s_warp[THREADS / 32];
+  __shared__ int s_bad;
+  int *const s_tokens = s_sums, *const s_fresh = s_sums + runs, *const s_ended = s_sums + 2 * runs;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, grid = gridDim.x, cta = blockIdx.x;
+  if (tid == 0) s_bad = 0;
   pdl_wait();
   pdl_trigger();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, grid = gridDim.x, cta = blockIdx.x;
-  const int per = (a.B + kThreads - 1) / kThreads;
-  const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
-  Sums sum = {0, 0, 0};
   bool bad = false;
-  for (int b = b0; b < b1; ++b) {
-    const Request x = request(a, b);
-    sum.tokens += x.n;
-    sum.fresh += x.fresh;
-    sum.ended += x.ended;
-    bad |= !x.ok;
+  if (per == 1) {
+#pragma unroll 4
+    for (int r = tid; r < runs; r += THREADS) {
+      const Request x = request(a, r);
+      s_tokens[r] = x.n;
+      s_fresh[r] = x.fresh;
+      s_ended[r] = x.ended;
+      bad |= !x.ok;
+    }
+  } else {
+    for (int r = tid; r < runs; r += THREADS) {
+      long long t = 0, f = 0, e = 0;
+      for (int b = r * per; b < min(a.B, r * per + per); ++b) {
+        const Request x = request(a, b);
+        t += x.n;
+        f += x.fresh;
+        e += x.ended;
+        bad |= !x.ok;
+      }
+      s_tokens[r] = clamp_sum(t);
+      s_fresh[r] = clamp_sum(f);
+      s_ended[r] = clamp_sum(e);
+    }
   }
+  const int given = *a.free_count, count = min(max(given, 0), a.cap);
+  __syncthreads();
+  const int r0 = min(runs, tid * own), r1 = min(runs, r0 + own);
+  // pages: of up to 4 sequences of below 2^25 in up to 17 runs
+  long long sum_tokens = 0;
+  uint32_t sum_fresh = 0, sum_ended = 0;
+#pragma unroll 4
+  for (int r = r0; r < r1; ++r) {
+    sum_tokens += s_tokens[r];
+    sum_fresh += s_fresh[r];
+    sum_ended += s_ended[r];
+  }
+  const Sums sum = {sum_tokens, sum_fresh, sum_ended};
   Sums inc = sum;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -78,54 +126,62 @@ __global__ void __launch_bounds__(kThreads) batch_plan_kernel(const BatchPlanArg
   }
   if (lane == 31) s_warp[warp] = inc;
   __syncthreads();
-  Sums before = {0, 0, 0};
-  for (int w = 0; w < warp; ++w) {
-    before.tokens += s_warp[w].tokens;
-    before.fresh += s_warp[w].fresh;
-    before.ended += s_warp[w].ended;
+  Sums all = {0, 0, 0}, before = {inc.tokens - sum.tokens, inc.fresh - sum.fresh, inc.ended - sum.ended};
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    const Sums x = s_warp[w];
+    if (w < warp) {
+      before.tokens += x.tokens;
+      before.fresh += x.fresh;
+      before.ended += x.ended;
+    }
+    all.tokens += x.tokens;
+    all.fresh += x.fresh;
+    all.ended += x.ended;
   }
-  before.tokens += inc.tokens - sum.tokens;
-  before.fresh += inc.fresh - sum.fresh;
-  before.ended += inc.ended - sum.ended;
-  s_before[tid] = before;
-  if (tid == kThreads - 1) s_before[kThreads] = Sums{before.tokens + sum.tokens, before.fresh + sum.fresh, before.ended + sum.ended};
+#pragma unroll 4
+  for (int r = r0; r < r1; ++r) {
+    const int t = s_tokens[r], f = s_fresh[r], e = s_ended[r];
+    s_tokens[r] = clamp_sum(before.tokens);
+    s_fresh[r] = clamp_sum(before.fresh);
+    s_ended[r] = clamp_sum(before.ended);
+    before.tokens += t;
+    before.fresh += f;
+    before.ended += e;
+  }
   __syncthreads();
-  const Sums all = s_before[kThreads];
-  const int given = *a.free_count, count = min(max(given, 0), a.cap);
   const long long pool = count + all.ended, left = pool - all.fresh;
+  const int step = grid * THREADS, first = cta * THREADS + tid;
 
-  // lengths, by this block's share of the threads' runs
-  if (tid % grid == cta) {
-    long long t = before.tokens;
-    for (int b = b0; b < b1; ++b) {
+  for (int r = first; r < runs; r += step) {  // lengths
+    long long t = s_tokens[r];
+    for (int b = r * per; b < min(a.B, r * per + per); ++b) {
       const Request x = request(a, b);
-      a.cu_q[b] = static_cast<int>(min(t, 0x7FFFFFFFLL));
+      a.cu_q[b] = clamp_sum(t);
       a.lens[b] = x.ok && !x.ends ? x.old + x.n : 0;
       t += x.n;
     }
   }
-  if (cta == 0 && tid == 0) {
-    a.cu_q[a.B] = static_cast<int>(min(all.tokens, 0x7FFFFFFFLL));
+  if (first == 0) {
+    a.cu_q[a.B] = clamp_sum(all.tokens);
     *a.left = static_cast<int>(min(max(left, 0LL), static_cast<long long>(a.cap)));
     bad |= given != count || left < 0 || left > a.cap || all.tokens > a.T;
   }
 
-  // the run of sequences in which sum `f` of those before passes i
-  auto run_of = [&](auto f, long long i) {
-    int lo = 0, hi = kThreads;
-    while (hi - lo > 1) {
-      const int m = (lo + hi) / 2;
-      if (f(s_before[m]) <= i)
-        lo = m;
-      else
-        hi = m;
+  // the last run with sums[run] <= i
+  auto run_of = [&](const int* sums, int i) {
+    int lo = 0, n = runs;
+    while (n > 1) {
+      const int half = n / 2;
+      if (sums[lo + half] <= i) lo += half;
+      n -= half;
     }
     return lo;
   };
   // returned page j
-  auto returned = [&](long long j) -> int {
-    const int run = run_of([](const Sums& s) { return s.ended; }, j);
-    j -= s_before[run].ended;
+  auto returned = [&](int j) -> int {
+    const int run = run_of(s_ended, j);
+    j -= s_ended[run];
     for (int b = run * per; b < min(a.B, run * per + per); ++b) {
       const Request x = request(a, b);
       if (j < x.ended) return a.table[static_cast<long long>(b) * a.max_pages + x.keep + j];
@@ -136,49 +192,113 @@ __global__ void __launch_bounds__(kThreads) batch_plan_kernel(const BatchPlanArg
   // the i-th page that is taken
   auto taken = [&](long long i) -> int {
     const long long v = pool - 1 - i;
-    return v < 0 ? -1 : v < count ? a.stack[v] : returned(v - count);
+    return v < 0 ? -1 : v < count ? a.stack[v] : returned(clamp_sum(v - count));
   };
-  const long long step = static_cast<long long>(grid) * kThreads;
-  for (long long t = static_cast<long long>(cta) * kThreads + tid; t < max(all.tokens, static_cast<long long>(a.T)); t += step) {
-    int seq = -1, pos = -1, slot = -1;
-    if (t < all.tokens) {
-      const int run = run_of([](const Sums& s) { return s.tokens; }, t);
-      Sums s = s_before[run];
-      seq = run * per;
-      Request x = request(a, seq);
-      while (t >= s.tokens + x.n) {
-        s.tokens += x.n;
-        s.fresh += x.fresh;
-        x = request(a, ++seq);
+  const long long tokens = min(all.tokens, static_cast<long long>(a.T));
+  const bool wide = EACH == 4 && !((reinterpret_cast<uintptr_t>(a.seq) | reinterpret_cast<uintptr_t>(a.pos) |
+                                     reinterpret_cast<uintptr_t>(a.slots)) & 15);
+  for (long long t0 = static_cast<long long>(first) * EACH; t0 < a.T; t0 += static_cast<long long>(step) * EACH) {
+    int seq[EACH], pos[EACH], slot[EACH];
+    Request x = {};
+    long long at = 0, end = -1, fresh = 0;  // the sequence's first token and one past its last, new pages before it
+    int b = 0, p = -1, page = -1;           // the sequence, the last token's place in its row, its page
+#pragma unroll
+    for (int k = 0; k < EACH; ++k) {
+      const long long t = t0 + k;
+      seq[k] = pos[k] = slot[k] = -1;
+      if (t >= tokens) continue;
+      if (t >= end) {
+        const int run = run_of(s_tokens, static_cast<int>(t));
+        at = s_tokens[run];
+        fresh = s_fresh[run];
+        b = run * per;
+        x = request(a, b);
+        while (t >= at + x.n) {
+          at += x.n;
+          fresh += x.fresh;
+          x = request(a, ++b);
+        }
+        end = at + x.n;
+        p = -1;
       }
-      pos = x.old + static_cast<int>(t - s.tokens);
-      const int p = pos / kPage;
-      int32_t* const entry = a.table + static_cast<long long>(seq) * a.max_pages + p;
-      const int page = p < x.pages ? *entry : taken(s.fresh + p - x.pages);
+      seq[k] = b;
+      pos[k] = x.old + static_cast<int>(t - at);
+      if (pos[k] / kPage != p) {
+        p = pos[k] / kPage;
+        page = p < x.pages ? a.table[static_cast<long long>(b) * a.max_pages + p] : taken(fresh + p - x.pages);
+      }
       const bool there = page >= 0 && page < a.num_pages;
-      if (p >= x.pages && pos % kPage == 0) *entry = page;  // a new page's first token
       bad |= !there;
-      if (there) slot = page * kPage + pos % kPage;
+      if (there) slot[k] = page * kPage + pos[k] % kPage;
     }
-    if (t < a.T) {
-      a.seq[t] = seq;
-      a.pos[t] = pos;
-      if (a.slots) a.slots[t] = slot;
+    if (wide && t0 + EACH <= a.T) {
+      if constexpr (EACH == 4) {
+        *reinterpret_cast<int4*>(a.seq + t0) = make_int4(seq[0], seq[1], seq[2], seq[3]);
+        *reinterpret_cast<int4*>(a.pos + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+        if (a.slots) *reinterpret_cast<int4*>(a.slots + t0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < EACH; ++k)
+        if (t0 + k < a.T) {
+          a.seq[t0 + k] = seq[k];
+          a.pos[t0 + k] = pos[k];
+          if (a.slots) a.slots[t0 + k] = slot[k];
+        }
     }
   }
+  const long long fresh_pages = min(all.fresh, static_cast<long long>(kMost));
+  for (long long i = first; i < fresh_pages; i += step) {
+    const int run = run_of(s_fresh, static_cast<int>(i));
+    long long at = s_fresh[run];
+    int seq = run * per;
+    Request x = request(a, seq);
+    while (i >= at + x.fresh) {
+      at += x.fresh;
+      x = request(a, ++seq);
+    }
+    a.table[static_cast<long long>(seq) * a.max_pages + x.pages + (i - at)] = taken(i);
+  }
   // pages that came back and were not taken again
-  for (long long j = static_cast<long long>(cta) * kThreads + tid; j < min(left, static_cast<long long>(a.cap)) - count; j += step)
-    a.stack[count + j] = returned(j);
-  if (bad) atomicOr(a.status, DSA_DEV_BOUNDS);
+  for (long long j = first; j < min(left, static_cast<long long>(a.cap)) - count; j += step)
+    a.stack[count + j] = returned(static_cast<int>(j));
+  if (bad) s_bad = 1;
+  __syncthreads();
+  if (tid == 0 && s_bad) atomicOr(a.status, DSA_DEV_BOUNDS);
+}
+
+constexpr int kSmallThreads = 128, kThreads = 1024;
+
+template <int THREADS, int EACH>
+cudaError_t launch(const BatchPlanArgs& a, int grid, cudaStream_t stream) {
+  const int per = (a.B + kSums - 1) / kSums, runs = (a.B + per - 1) / per, own = ((runs + THREADS - 1) / THREADS) | 1;
+  return launch_pdl(batch_plan_kernel<THREADS, EACH>, dim3(grid), dim3(THREADS), 12 * static_cast<size_t>(runs), stream, a, per,
+                    runs, own);
 }
 
 }  // namespace
 
 dsa_status launch_batch_plan(dsa_ctx* ctx, const BatchPlanArgs& a, cudaStream_t stream) {
+  if (!ctx->batch_ready) {
+    for (auto kern : {batch_plan_kernel<kThreads, 1>, batch_plan_kernel<kThreads, 4>})
+      if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 12 * kSums) != cudaSuccess) return DSA_ERR_CUDA;
+    ctx->batch_ready = 1;
+  }
   LaunchScope scope(ctx, DSA_K_BATCH_PLAN, stream);
-  const int most = (max(a.T, a.B) + 2 * kThreads - 1) / (2 * kThreads);
-  const int grid = max(1, min(most, ctx->num_sms));
-  return launch_pdl(batch_plan_kernel, dim3(grid), dim3(kThreads), 0, stream, a) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+  const int most = std::max(a.T, a.B);
+  // One small block for a decode step: fewer warps to meet. Four tokens a thread
+  // where sequences have as many. A block on each SM, or as many as
+  // have two sequences or tokens a thread, or eight pages that may come back.
+  const long long pages = static_cast<long long>(a.B) * a.max_pages;
+  auto blocks = [&](int threads) {
+    return static_cast<int>(std::min(std::max({1LL, (most + 2LL * threads - 1) / (2 * threads), pages / (8 * threads)}),
+                                     static_cast<long long>(ctx->num_sms)));
+  };
+  const int grid = blocks(kThreads);
+  const cudaError_t e = most <= 2 * kSmallThreads         ? launch<kSmallThreads, 1>(a, blocks(kSmallThreads), stream)
+                        : a.T / 8 >= a.B && a.T >= 16384 ? launch<kThreads, 4>(a, grid, stream)
+                                                          : launch<kThreads, 1>(a, grid, stream);
+  return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 
 }  // namespace dsa
