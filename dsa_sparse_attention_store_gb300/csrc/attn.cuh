@@ -117,8 +117,9 @@ struct AttnArgs {
 // up to 128 or 256 rows of neighbouring tokens and the tiles that one of them sees.
 struct Unit {
   int b, q0, nd, len;     // row of the page table; first query, queries and keys of the rows' sequence (or group)
-  int r0, t0, t1, base;   // first row among those queries' rows; tiles; whether the rows have sums over a shared prefix
-  int lo, full, pad0, pad1;  // every row sees the places from lo to before full
+  int r0, t0, t1, base;   // first row among those queries' rows; tiles; whether the rows have keys in a shared prefix too
+  int lo, full;           // every row sees the places from lo to before full
+  int group_q0, group_at; // base: the group's first query, and the place of its first unit in the groups' list
 };
 
 // What a token sees: the places [lo, hi) of its sequence, and where it lies
@@ -136,9 +137,10 @@ struct SpanArgs : AttnArgs {
   float poly[5], poly_most;  // capped score log2 e / q.k in powers of (q.k)^2, and where that holds
   float fixed;               // what every row is weighed under where capped scores allow it, else -inf
   int units_n;
-  int base_mode;       // rows' sums over a shared prefix: 1 these are they, 2 join them where the unit has some
-  float2* base_ml;     // [Tq][heads]
-  float* base;         // [Tq][heads][D]
+  int raw_mode;        // whole units' sums go to `raw`, for rows_join_kernel: 1 all, 2 those with Unit::base
+  float2* raw_ml;      // [Tq][heads] maximum and sum of weights
+  float* raw;          // [Tq][heads][D]
+  int2* ends;          // [slots][kv_heads] the CTAs that have a unit's first and last tile, if raw_mode
 };
 
 // One stretch of a unit's key tiles.
@@ -151,6 +153,7 @@ struct Seg {
 };
 struct SpanSeg : Seg {
   int tb, lo, base;   // the unit's first tile; `full` holds from this position on; Unit::base
+  int place;          // of the unit in the list
 };
 
 struct Start {
@@ -284,6 +287,7 @@ struct Iter {
       s.base = y.w;
       s.lo = z.x;
       s.full = z.y;
+      s.place = b;
       s.rows = static_cast<int>(min(static_cast<long long>(C::ROWS), static_cast<long long>(s.nd) * a.G - s.r0));
       s.h = h;
       s.t0 = s.tb + tile;
@@ -355,6 +359,15 @@ struct Iter {
   }
 };
 
+// Where CTA c's share of total tiles begins, of n CTAs.
+__device__ __forceinline__ long long share(long long total, int c, int n) {
+  if (total < 0x7FFFFFFFLL) {  // by divisions of 32 bits
+    const uint32_t t = static_cast<uint32_t>(total), q = t / n;
+    return static_cast<long long>(q) * c + (t - q * n) * static_cast<uint32_t>(c) / n;
+  }
+  return total / n * c + total % n * c / n;
+}
+
 // The launch's tiles, and where this CTA's range begins. Every thread of
 // the block calls it; the result is in sh.
 template <class C>
@@ -425,11 +438,11 @@ __device__ __forceinline__ void make_plan(const typename C::Args& a, Shared& sh,
   [[maybe_unused]] const long long head = total;  // span form: the list's tiles, which every kv head has
   if constexpr (C::SPAN) total *= a.kv_heads;
   const long long n = total < grid ? total : grid;
-  begin = cta < n ? total * cta / n : total;
-  count = cta < n ? total * (cta + 1) / n - begin : 0;
   if constexpr (C::SPAN) {
+    begin = cta < n ? share(total, cta, static_cast<int>(n)) : total;
+    count = cta < n ? share(total, cta + 1, static_cast<int>(n)) - begin : 0;
     if (count > 0) {
-      const long long h = begin / head;
+      const long long h = total < 0x7FFFFFFFLL ? static_cast<uint32_t>(begin) / static_cast<uint32_t>(head) : begin / head;
       long long x = begin - h * head - ex;
       if (0 <= x && x < sum) {
         int b = b0;
@@ -440,6 +453,8 @@ __device__ __forceinline__ void make_plan(const typename C::Args& a, Shared& sh,
     __syncthreads();
     return;
   }
+  begin = cta < n ? total * cta / n : total;
+  count = cta < n ? total * (cta + 1) / n - begin : 0;
   if (count > 0 && ex <= begin && begin < ex + sum) {
     long long x = begin - ex;
     int b = b0;
@@ -512,6 +527,21 @@ __device__ __forceinline__ Token token_at(const SpanArgs& a, long long t) {
   return Token{y.x, y.y, y.z, y.w};
 }
 
+// The place a token measures its keys' distance from: its own, or the nearest
+// that it sees. Softmax takes no notice of the difference; exponents stay small
+// for the keys that matter where all of them are far away. away(): how far that
+// place is, for lse.
+__device__ __forceinline__ int nearest(const Token& y) { return max(y.lo, min(y.place, y.hi - 1)); }
+__device__ __forceinline__ float away(const Token& y) { return fabsf(static_cast<float>(y.place - nearest(y))); }
+
+// cap tanh(scale q.k / cap) of 64 keys, times log2 e. tanh y = 1 - 2 / (1 + e^2y),
+// within 2^-22, for infinities too: two more of the special-function unit's
+// operations a score, which a tile takes only where some |y| is above kCapPoly.
+// Below, y P(y^2) with a minimax polynomial (within 2^-23) on the fp32 pipe; its
+// coefficients are the host's, with scale and cap in them.
+constexpr int kCapTerms = 5;
+constexpr double kCapPoly = 0.625;
+
 // One step of turning four lanes' four 16-byte runs around: lanes that differ in
 // bit N exchange the runs that differ in it.
 template <int N>
@@ -530,20 +560,17 @@ __device__ __forceinline__ void swap_runs(uint32_t (&w)[4][4], bool upper) {
   }
 }
 
-// The place a token measures its keys' distance from: its own, or the nearest
-// that it sees. Softmax takes no notice of the difference; exponents stay small
-// for the keys that matter where all of them are far away. away(): how far that
-// place is, for lse.
-__device__ __forceinline__ int nearest(const Token& y) { return max(y.lo, min(y.place, y.hi - 1)); }
-__device__ __forceinline__ float away(const Token& y) { return fabsf(static_cast<float>(y.place - nearest(y))); }
-
-// cap tanh(scale q.k / cap) of 64 keys, times log2 e. tanh y = 1 - 2 / (1 + e^2y),
-// within 2^-22, for infinities too: two more of the special-function unit's
-// operations a score, which a tile takes only where some |y| is above kCapPoly.
-// Below, y P(y^2) with a minimax polynomial (within 2^-23) on the fp32 pipe; its
-// coefficients are the host's, with scale and cap in them.
-constexpr int kCapTerms = 5;
-constexpr double kCapPoly = 0.625;
+// 64 bytes of each lane's row to `to`, null for none
+__device__ __forceinline__ void store_runs(uint32_t (&w)[4][4], void* to) {
+  const int lane = threadIdx.x & 31;
+  swap_runs<1>(w, lane & 1);
+  swap_runs<2>(w, lane & 2);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const unsigned long long p = __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(to), (lane & 28) + i);
+    if (p) reinterpret_cast<uint4*>(p)[lane & 3] = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
+  }
+}
 
 // capped score log2 e / q.k of two scores whose squares are u
 __device__ __forceinline__ unsigned long long cap_factor(const SpanArgs& a, unsigned long long u) {
@@ -1128,15 +1155,20 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM, SCORES>::THREADS, Cfg<FMT, D
       int unit = 0;  // the unit's first tile
       if constexpr (C::SPAN) unit = done.tb;
       const bool first = done.t0 == unit, last = done.t1 == done.nt;
+      if constexpr (C::SPAN) {
+        if (tid == 0 && a.raw_mode) {
+          int2* const ends = a.ends + static_cast<long long>(done.place) * a.kv_heads + done.h;
+          if (first) ends->x = cta;
+          if (last) ends->y = cta;
+        }
+      }
       if (tid == 0 && !first) {
         meta[1] = 1;
         meta[2] = last;
       } else if (tid == 0 && !last) {
         meta[0] = 1;
         meta[3] = done.rows;
-        int base = 0;
-        if constexpr (C::SPAN) base = done.base;
-        a.meta[2 * cta + 1] = make_int4(done.r0, done.q0, done.h, base);
+        a.meta[2 * cta + 1] = make_int4(done.r0, done.q0, done.h, 0);
       }
       if (active && run) {
         if (fix) {
@@ -1150,24 +1182,11 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM, SCORES>::THREADS, Cfg<FMT, D
         const int piece = 2 * cta + (first ? 1 : 0);
         __nv_bfloat16* dst = a.out + tok * a.ot + head * a.oh;
         float* part = a.part + (static_cast<long long>(piece) * C::ROWS + row) * D;
-        // span form: a whole unit's sums join those over the shared prefix, or are those
-        [[maybe_unused]] const float* base = nullptr;
-        [[maybe_unused]] float wm = 1.f, wb = 0.f;  // weights of the unit's sums and of the others
         bool whole = first && last;
         if constexpr (C::SPAN) {
-          const long long at = tok * a.kv_heads * a.G + head;
-          if (whole && a.base_mode == 1) {
+          if (whole && (a.raw_mode == 1 || (a.raw_mode == 2 && done.base))) {
             whole = false;
-            part = a.base + at * D;
-          }
-          if (whole && done.base && valid) {
-            const float2 y = __ldcg(a.base_ml + at);
-            const float top = fmaxf(m, y.x);
-            base = a.base + at * D;
-            wm = m == top ? 1.f : ex2_denorm(m - top);
-            wb = y.x == top ? 1.f : ex2_denorm(y.x - top);
-            l = l * wm + y.y * wb;
-            m = top;
+            part = a.raw + (tok * a.kv_heads * a.G + head) * D;
           }
         }
         const float inv = l > 0.f ? 1.f / l : 0.f;
@@ -1178,21 +1197,10 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM, SCORES>::THREADS, Cfg<FMT, D
           tmem_ld32(tO + 32 * c, o);
           tmem_ld_wait32(o);
           if constexpr (C::SPAN) {
-            if (valid && base) {
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float4 y = __ldcg(reinterpret_cast<const float4*>(base + 32 * c + 4 * i));
-                const float z[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[4 * i + e] = __float_as_uint(fmaf(z[e], wb, __uint_as_float(o[4 * i + e]) * wm));
-              }
-            }
-          }
-          if constexpr (C::SPAN) {
+            // Four lanes exchange their rows' 16-byte runs, so that a store's lanes
+            // have 64 bytes of a row each four; by rows it takes the L1 32 steps.
+            uint32_t w[4][4];
             if (whole) {
-              // four lanes exchange their rows' 16-byte runs, so that a store's
-              // lanes have 64 bytes of a row each four
-              uint32_t w[4][4];
 #pragma unroll
               for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -1201,15 +1209,16 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM, SCORES>::THREADS, Cfg<FMT, D
                   const __nv_bfloat162 p = l == 0.f ? __floats2bfloat162_rn(0.f, 0.f) : __floats2bfloat162_rn(u, v);
                   memcpy(&w[i][e], &p, 4);
                 }
-              swap_runs<1>(w, lane & 1);
-              swap_runs<2>(w, lane & 2);
+              store_runs(w, valid ? dst + 32 * c : nullptr);
+            } else {
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const unsigned long long to = __shfl_sync(0xffffffffu, valid ? reinterpret_cast<unsigned long long>(dst) : 0ull, (lane & 28) + i);
-                if (to) reinterpret_cast<uint4*>(to)[4 * c + (lane & 3)] = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
+              for (int half = 0; half < 2; ++half) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) w[i / 4][i % 4] = o[16 * half + i];
+                store_runs(w, valid ? part + 32 * c + 16 * half : nullptr);
               }
-              continue;
             }
+            continue;
           }
           if (!valid) {
           } else if (whole) {
@@ -1238,7 +1247,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM, SCORES>::THREADS, Cfg<FMT, D
             }
             if (a.lse) a.lse[tok * a.kv_heads * a.G + head] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
           } else if (C::SPAN && first && last) {
-            if constexpr (C::SPAN) a.base_ml[tok * a.kv_heads * a.G + head] = make_float2(m, l);
+            if constexpr (C::SPAN) a.raw_ml[tok * a.kv_heads * a.G + head] = make_float2(m, l);
           } else {
             a.ml[static_cast<long long>(piece) * C::ROWS + row] = make_float2(m, l);
           }

@@ -14,9 +14,6 @@ namespace at {
 //
 // Few pieces (the usual case): a warp per row. Many (a long context and few
 // rows): the block's warps share a row's pieces.
-//
-// Units of the span form: sums over a shared prefix go to their rows as they
-// are, the others take their rows' in as one more piece.
 // 20 pieces of 256 rows (32 sequences behind 131072 tokens) took 83 us by the
 // block and 15 by warps.
 template <class Args>
@@ -45,30 +42,12 @@ __global__ void __launch_bounds__(256) join_kernel(const Args a, int grid, int r
   __syncthreads();
   const int n = s_end - c + 1;  // pieces
   auto slot = [&](int p) -> long long { return p == 0 ? 2 * c + 1 : 2 * (c + p); };
-  auto finish = [&](int row, float m, float l, float (&o)[E]) {
+  auto finish = [&](int row, float m, float l, const float (&o)[E]) {
     const int r = m1.x + row;
     const long long tok = m1.y + r / a.G;
     const int head = m1.z * a.G + r % a.G;
     float top = m;  // for lse
     if constexpr (std::is_same_v<Args, SpanArgs>) {
-      const long long at = tok * a.kv_heads * a.G + head;
-      float* base = a.base + at * D + lane * E;
-      if (a.base_mode == 1) {
-        if constexpr (E == 4)
-          *reinterpret_cast<float4*>(base) = make_float4(o[0], o[1], o[2], o[3]);
-        else
-          *reinterpret_cast<float2*>(base) = make_float2(o[0], o[1]);
-        if (lane == 0) a.base_ml[at] = make_float2(m, l);
-        return;
-      }
-      if (m1.w) {
-        const float2 y = __ldcg(a.base_ml + at);
-        top = fmaxf(m, y.x);
-        const float wm = m == top ? 1.f : ex2_denorm(m - top), wb = y.x == top ? 1.f : ex2_denorm(y.x - top);
-        l = l * wm + y.y * wb;
-#pragma unroll
-        for (int i = 0; i < E; ++i) o[i] = fmaf(__ldcg(base + i), wb, o[i] * wm);
-      }
       if (a.slopes && a.lse && lane == 0) top -= a.slopes[head] * 1.4426950408889634f * away(token_at(a, tok));
     }
     const float inv = l > 0.f ? 1.f / l : 0.f;

@@ -12,8 +12,9 @@
 //
 // Behind shared prefixes there are two lists. The first takes a group's
 // sequences for one, with all of their tokens, and the whole pages that they
-// share; its sums go to the workspace, 32 bits each. The second takes each
-// sequence alone and the keys behind those pages, and joins both.
+// share. The second takes each sequence alone and the keys behind those pages.
+// The sums of both go to the workspace, 32 bits each, and are joined row by row.
+#include <algorithm>
 #include <cmath>
 
 #include "attn_join.cuh"
@@ -165,6 +166,12 @@ __global__ void __launch_bounds__(256) span_plan_kernel(const AttnArgs a, const 
   max_hi = __reduce_max_sync(0xffffffffu, max_hi);
   if (lane == 0) {
     const int base = !group && t0 > 0;
+    int group_q0 = 0, group_at = 0;
+    if (base) {
+      const int g = last_of(p.cu_groups, 0, p.groups, b);
+      group_q0 = a.cu_q[p.cu_groups[g]];
+      group_at = static_cast<int>(static_cast<long long>(group_q0) * a.G / p.group_rows + g);
+    }
     int e0 = max(t0, min_lo / kTile), e1 = min(t1, (max_hi + kTile - 1) / kTile);
     if (e1 <= e0) {  // nothing to see: one tile, so that the rows are written
       e0 = t0;
@@ -173,8 +180,104 @@ __global__ void __launch_bounds__(256) span_plan_kernel(const AttnArgs a, const 
     int4* const x = (group ? p.group_units : p.units) + 3LL * u;
     x[0] = make_int4(b, q0, nd, len);
     x[1] = make_int4(r0, e0, e1, base);
-    x[2] = make_int4(max_lo, min_hi, 0, 0);
+    x[2] = make_int4(max_lo, min_hi, group_q0, group_at);
     *tiles = e1 - e0;
+  }
+}
+
+// The join behind shared prefixes: of each row's sums over the prefix and over
+// its sequence's own keys, each whole or in the pieces of the CTAs that the cuts
+// gave a part to. A row a warp; in the order of the keys, so the result does not
+// depend on timing.
+struct RowsJoin {
+  SpanArgs group, own;  // the two passes
+  int group_rows, own_rows;
+};
+
+template <int D>
+__global__ void __launch_bounds__(256) rows_join_kernel(const RowsJoin j) {
+  constexpr int E = D / 32;  // dimensions a lane holds
+  pdl_wait();
+  pdl_trigger();
+  const SpanArgs &a = j.own, &b = j.group;
+  const int u = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = blockIdx.z * 8 + warp;  // of the unit
+  if (a.tiles[u] == 0) return;
+  const int4 x = a.units[3 * u], y = a.units[3 * u + 1], z = a.units[3 * u + 2];
+  if (y.x + static_cast<long long>(row) >= static_cast<long long>(x.z) * a.G) return;
+  const bool base = y.w;
+  const int i = (y.x + row) / a.G, g = y.x + row - i * a.G;
+  const long long tok = x.y + i, r = base ? (tok - z.z) * a.G + g : 0;  // and the row of the group
+  const int place = z.w + static_cast<int>(r / j.group_rows);
+  for (int h = blockIdx.y; h < a.kv_heads; h += gridDim.y) {
+    const int2 own = a.ends[static_cast<long long>(u) * a.kv_heads + h];
+    const int2 all = base ? b.ends[static_cast<long long>(place) * a.kv_heads + h] : make_int2(0, -1);
+    if (!base && own.x == own.y) continue;  // written as it is
+    const int head = h * a.G + g, before = all.y - all.x + 1, n = before + own.y - own.x + 1;
+    const long long at = tok * a.kv_heads * a.G + head;
+    // where piece p is, the prefix's first: maximum and sum, and sums
+    auto piece = [&](int p, const float2*& ml, const float*& o) {
+      const bool of_group = p < before;
+      const SpanArgs& q = of_group ? b : a;
+      const int2 e = of_group ? all : own;
+      const int rows = of_group ? j.group_rows : j.own_rows, k = of_group ? p : p - before;
+      const long long slot = (2LL * (e.x + k) + (k == 0)) * rows + (of_group ? static_cast<int>(r % j.group_rows) : row);
+      ml = e.x == e.y ? q.raw_ml + at : q.ml + slot;
+      o = e.x == e.y ? q.raw + at * D : q.part + slot * D;
+    };
+    float m = -INFINITY, l = 0.f, o[E] = {};
+    for (int p0 = 0; p0 < n; p0 += 32) {  // a lane a piece: the maxima
+      const float2* ml;
+      const float* src = a.raw;
+      float2 v = make_float2(-INFINITY, 0.f);
+      if (p0 + lane < n) {
+        piece(p0 + lane, ml, src);
+        v = __ldcg(ml);
+      }
+      float top = v.x;
+#pragma unroll
+      for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      top = fmaxf(top, m);
+      // sums hold weights of more than 1: denormal factors count
+      const float old = m == top ? 1.f : ex2_denorm(m - top), now = v.x == top ? 1.f : ex2_denorm(v.x - top);
+      l *= old;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] *= old;
+      m = top;
+#pragma unroll 8
+      for (int p = 0; p < min(32, n - p0); ++p) {
+        const float w = __shfl_sync(0xffffffffu, now, p);
+        const float* at_p = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), p));
+        l = fmaf(__shfl_sync(0xffffffffu, v.y, p), w, l);
+        if constexpr (E == 4) {
+          const float4 f = __ldcg(reinterpret_cast<const float4*>(at_p) + lane);
+          o[0] = fmaf(f.x, w, o[0]);
+          o[1] = fmaf(f.y, w, o[1]);
+          o[2] = fmaf(f.z, w, o[2]);
+          o[3] = fmaf(f.w, w, o[3]);
+        } else {
+          const float2 f = __ldcg(reinterpret_cast<const float2*>(at_p) + lane);
+          o[0] = fmaf(f.x, w, o[0]);
+          o[1] = fmaf(f.y, w, o[1]);
+        }
+      }
+    }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    uint32_t w[E / 2];
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) {
+      const __nv_bfloat162 v = l == 0.f ? __floats2bfloat162_rn(0.f, 0.f) : __floats2bfloat162_rn(o[2 * e] * inv, o[2 * e + 1] * inv);
+      memcpy(&w[e], &v, 4);
+    }
+    __nv_bfloat16* dst = a.out + tok * a.ot + head * a.oh + lane * E;
+    if constexpr (E == 4)
+      *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+    else
+      *reinterpret_cast<uint32_t*>(dst) = w[0];
+    if (a.lse && lane == 0) {
+      if (a.slopes) m -= a.slopes[head] * 1.4426950408889634f * away(token_at(a, tok));
+      a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+    }
   }
 }
 
@@ -220,7 +323,8 @@ void cap_args(double scale, double cap, SpanArgs& a) {
 
 // What follows the attention's own workspace.
 struct SpanWorkspace {
-  size_t tokens, units, tiles, group_units, group_tiles, base_ml, base, bytes;
+  size_t tokens, units, tiles, group_units, group_tiles, ends, group_ends, group_ml, group_part, raw_ml, raw, group_raw_ml,
+      group_raw, bytes;
 };
 
 SpanWorkspace span_layout(const dsa_ctx* ctx, long long Tq, int B, int groups, long long heads, long long kv_heads, int D) {
@@ -240,8 +344,17 @@ SpanWorkspace span_layout(const dsa_ctx* ctx, long long Tq, int B, int groups, l
     const size_t more = shape_of(ctx, Tq * G, groups).places;
     w.group_units = take(more * 3 * sizeof(int4));
     w.group_tiles = take(more * sizeof(int));
-    w.base_ml = take(static_cast<size_t>(Tq) * heads * sizeof(float2));
-    w.base = take(static_cast<size_t>(Tq) * heads * D * sizeof(float));
+    w.ends = take(places * kv_heads * sizeof(int2));
+    w.group_ends = take(more * kv_heads * sizeof(int2));
+    // the first pass's pieces; the second's are where dsa_tree_attn has them
+    const Workspace pieces = layout(ctx, D);
+    w.group_ml = take(pieces.part - pieces.ml);
+    w.group_part = take(pieces.bytes - pieces.part);
+    const size_t rows = static_cast<size_t>(Tq) * heads;
+    w.raw_ml = take(rows * sizeof(float2));
+    w.raw = take(rows * D * sizeof(float));
+    w.group_raw_ml = take(rows * sizeof(float2));
+    w.group_raw = take(rows * D * sizeof(float));
   }
   w.bytes = at;
   return w;
@@ -264,10 +377,6 @@ dsa_status launch_span(dsa_ctx* ctx, const dsa_attn_args& p, const dsa_span& spa
   a.fixed = -INFINITY;
   if (span.cap != 0.0) cap_args(p.scale, span.cap, a);
   a.tokens = reinterpret_cast<int4*>(ws + w.tokens);
-  if (groups) {
-    a.base_ml = reinterpret_cast<float2*>(ws + w.base_ml);
-    a.base = reinterpret_cast<float*>(ws + w.base);
-  }
   CUtensorMap tm = {};
   if (!cache_map(ctx, p, kTile, tm)) return DSA_ERR_CUDA;
 
@@ -301,27 +410,39 @@ dsa_status launch_span(dsa_ctx* ctx, const dsa_attn_args& p, const dsa_span& spa
                                           {run_span_bias_bf16, run_span_bias_fp8, run_span_bias_fp4}};
   // a cap too wide to weigh all rows under one exponent goes with slopes of zero
   RunSpan* const run = kRun[a.slopes || (a.cap2 != 0.f && a.fixed == -INFINITY) ? 2 : a.cap2 != 0.f ? 1 : 0][p.fmt];
-  auto pass = [&](const Shape& f) {
-    const dsa_status st = run(ctx, f.form, p.head_dim, tm, a, f.grid, stream);
-    if (st != DSA_OK) return st;
-    LaunchScope scope(ctx, DSA_K_ATTN_JOIN, stream);
-    const cudaError_t e = launch_pdl(p.head_dim == 128 ? join_kernel<128, SpanArgs> : join_kernel<64, SpanArgs>,
-                                     dim3(f.grid, f.rows < 64 ? 8 : f.rows / 8), dim3(256), 0, stream, a, f.grid, f.rows);
-    return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
-  };
-  if (groups) {
-    a.units = plan.group_units;
-    a.tiles = plan.group_tiles;
-    a.units_n = plan.group_n;
-    a.base_mode = 1;
-    const dsa_status st = pass(all);
-    if (st != DSA_OK) return st;
-    a.base_mode = 2;
-  }
   a.units = plan.units;
   a.tiles = plan.tiles;
   a.units_n = plan.n;
-  return pass(own);
+  if (!groups) {
+    const dsa_status st = run(ctx, own.form, p.head_dim, tm, a, own.grid, stream);
+    if (st != DSA_OK) return st;
+    LaunchScope scope(ctx, DSA_K_ATTN_JOIN, stream);
+    const cudaError_t e = launch_pdl(p.head_dim == 128 ? join_kernel<128, SpanArgs> : join_kernel<64, SpanArgs>,
+                                     dim3(own.grid, own.rows < 64 ? 8 : own.rows / 8), dim3(256), 0, stream, a, own.grid, own.rows);
+    return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+  }
+  a.raw_mode = 2;
+  a.ends = reinterpret_cast<int2*>(ws + w.ends);
+  a.raw_ml = reinterpret_cast<float2*>(ws + w.raw_ml);
+  a.raw = reinterpret_cast<float*>(ws + w.raw);
+  SpanArgs b = a;
+  b.raw_mode = 1;
+  b.units = plan.group_units;
+  b.tiles = plan.group_tiles;
+  b.units_n = plan.group_n;
+  b.ends = reinterpret_cast<int2*>(ws + w.group_ends);
+  b.ml = reinterpret_cast<float2*>(ws + w.group_ml);
+  b.part = reinterpret_cast<float*>(ws + w.group_part);
+  b.raw_ml = reinterpret_cast<float2*>(ws + w.group_raw_ml);
+  b.raw = reinterpret_cast<float*>(ws + w.group_raw);
+  dsa_status st = run(ctx, all.form, p.head_dim, tm, b, all.grid, stream);
+  if (st == DSA_OK) st = run(ctx, own.form, p.head_dim, tm, a, own.grid, stream);
+  if (st != DSA_OK) return st;
+  LaunchScope scope(ctx, DSA_K_ATTN_JOIN, stream);
+  const RowsJoin join = {b, a, all.rows, own.rows};
+  const cudaError_t e = launch_pdl(p.head_dim == 128 ? rows_join_kernel<128> : rows_join_kernel<64>,
+                                   dim3(own.places, std::min(p.kv_heads, 32768), own.rows / 8), dim3(256), 0, stream, join);
+  return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 
 }  // namespace dsa
