@@ -191,8 +191,11 @@ __global__ void __launch_bounds__(256) span_plan_kernel(const AttnArgs a, const 
 // depend on timing.
 struct RowsJoin {
   SpanArgs group, own;  // the two passes
-  int group_rows, own_rows;
+  int group_rows, own_rows, group_grid, own_grid;
 };
+
+// Whether a pass left a unit's ends: not after a wait that ran out.
+__device__ __forceinline__ bool ends_there(int2 e, int grid) { return e.x >= 0 && e.x <= e.y && e.y < grid; }
 
 template <int D>
 __global__ void __launch_bounds__(256) rows_join_kernel(const RowsJoin j) {
@@ -211,8 +214,14 @@ __global__ void __launch_bounds__(256) rows_join_kernel(const RowsJoin j) {
   const int place = z.w + static_cast<int>(r / j.group_rows);
   for (int h = blockIdx.y; h < a.kv_heads; h += gridDim.y) {
     const int2 own = a.ends[static_cast<long long>(u) * a.kv_heads + h];
-    const int2 all = base ? b.ends[static_cast<long long>(place) * a.kv_heads + h] : make_int2(0, -1);
-    if (!base && own.x == own.y) continue;  // written as it is
+    if (!ends_there(own, j.own_grid) || (!base && own.x == own.y)) continue;  // nothing there, or written as it is
+    int2 all = make_int2(0, -1);
+    if (base) {
+      // a group's queries that do not hang together (reported by the plan) may have no units
+      if (r < 0 || place < 0 || place >= b.units_n || b.tiles[place] == 0) continue;
+      all = b.ends[static_cast<long long>(place) * a.kv_heads + h];
+      if (!ends_there(all, j.group_grid)) continue;
+    }
     const int head = h * a.G + g, before = all.y - all.x + 1, n = before + own.y - own.x + 1;
     const long long at = tok * a.kv_heads * a.G + head;
     // where piece p is, the prefix's first: maximum and sum, and sums
@@ -441,7 +450,7 @@ dsa_status launch_span(dsa_ctx* ctx, const dsa_attn_args& p, const dsa_span& spa
   if (st == DSA_OK) st = run(ctx, own.form, p.head_dim, tm, a, own.grid, stream);
   if (st != DSA_OK) return st;
   LaunchScope scope(ctx, DSA_K_ATTN_JOIN, stream);
-  const RowsJoin join = {b, a, all.rows, own.rows};
+  const RowsJoin join = {b, a, all.rows, own.rows, all.grid, own.grid};
   const cudaError_t e = launch_pdl(p.head_dim == 128 ? rows_join_kernel<128> : rows_join_kernel<64>,
                                    dim3(own.places, std::min(p.kv_heads, 32768), own.rows / 8), dim3(256), 0, stream, join);
   return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;

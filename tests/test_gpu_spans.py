@@ -85,6 +85,17 @@ def test_extremes_of_caps_and_slopes(ctx, fmt):
     assert ctx.device_status() == 0
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("size", ["few", "tree", "wide"])
+@pytest.mark.parametrize("cap", [8.0, 45.0, 57.0, 62.0, 63.0, 90.0, 2000.0, 1e5])
+def test_every_treatment_of_caps(ctx, fmt, size, cap):
+    # weighed under one exponent (to 62), under a running maximum; scores for the polynomial, and beyond it
+    for q_gain in (1.0, 12.0):
+        c = SpanCase(int(cap) + int(q_gain), *SIZES[size], 64, fmt, cap=cap, q_gain=q_gain)
+        c.check(*c.run(ctx))
+    assert ctx.device_status() == 0
+
+
 def test_far_keys_alone(ctx):
     # a bias of thousands that every visible key has: weights depend on their differences
     c = SpanCase(18, [20000], [4], 1, 2, 64, A.BF16, slopes=np.array([0.5, 0.07]), first=[100, 0, 300, 64], last=[230, 64, 310, 65])
