@@ -177,6 +177,13 @@ struct Cfg {
   // bias the first tile would be the one in which rows see the fewest keys
   // (packed documents 394 -> 429).
   static constexpr bool BACKWARDS = SCORES == kBiased;
+  // Whether results are over the sum of the weights as the product has them,
+  // rounded to bf16, which leaves out the rounding of a weight that outdoes the
+  // others: in all tiles where the tiles' bytes or their chain set the time; of
+  // 256-row units, whose time is the softmax's (687 -> 747 us), in capped ones'
+  // tiles that some row does not see whole. Rows of fewer than 64 keys have no
+  // others, and without a running maximum even one key's weight is not 1.
+  static constexpr bool ROUND_ALL = SPAN && FORM != kWide, ROUND = ROUND_ALL || SCORES == kCapped;
   using Args = std::conditional_t<SPAN, SpanArgs, AttnArgs>;
   using Segment = std::conditional_t<SPAN, SpanSeg, Seg>;
   static constexpr bool SPARSE = FORM == kSparse || FORM == kSparseFew;
@@ -641,15 +648,15 @@ __device__ __forceinline__ float bias_scores(uint32_t (&x)[2][32], float slope2,
 // polynomial, and instead of the largest exponent, which nobody asks for, the
 // largest (q.k)^2.
 struct Weighed {
-  float most, sum;
+  float most, sum, rounded;  // ROUNDED: the sum of the weights as they go into the product, too (else the same sum)
 };
 
-template <bool CAP>
+template <bool CAP, bool ROUNDED = false>
 __device__ __forceinline__ Weighed weigh(const SpanArgs& a, const uint32_t (&x)[2][32], uint32_t (&p)[32], float mul, float sub) {
   const unsigned long long sc = pack2(mul, mul), sb = pack2(-sub, -sub);
   unsigned long long sum[2] = {0ull, 0ull};  // pairs of fp32 zeros
   constexpr float kLeast = CAP ? 0.f : -INFINITY;
-  float mx[4] = {kLeast, kLeast, kLeast, kLeast};
+  float mx[4] = {kLeast, kLeast, kLeast, kLeast}, rounded[2] = {0.f, 0.f};
 #pragma unroll
   for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -665,11 +672,15 @@ __device__ __forceinline__ Weighed weigh(const SpanArgs& a, const uint32_t (&x)[
       sum[i & 1] = add2(sum[i & 1], pack2(e0, e1));
       const __nv_bfloat162 w = __floats2bfloat162_rn(e0, e1);
       memcpy(&p[16 * c + i], &w, 4);
+      if constexpr (ROUNDED) {
+        rounded[0] = add_bf16(rounded[0], __bfloat16_as_ushort(w.x));
+        rounded[1] = add_bf16(rounded[1], __bfloat16_as_ushort(w.y));
+      }
     }
   float l0, l1;
   unpack2(add2(sum[0], sum[1]), l0, l1);
   const float most = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-  return Weighed{CAP ? most : most * mul, l0 + l1};
+  return Weighed{CAP ? most : most * mul, l0 + l1, ROUNDED ? rounded[0] + rounded[1] : l0 + l1};
 }
 
 __device__ __forceinline__ float widen_one(uint32_t bits) { return __uint_as_float(bits << 16); }
@@ -949,6 +960,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM, SCORES>::THREADS, Cfg<FMT, D
       const Row mine = at_row;
       const int qi = mine.q;                   // the row's query in its sequence
       float m = -INFINITY, l = 0.f;
+      [[maybe_unused]] float lr = 0.f;  // the sum of the rounded weights, see Cfg::ROUND
       // the place that a row measures distance from, and its head's slope
       [[maybe_unused]] int near = 0;
       [[maybe_unused]] float slope2 = 0.f;
@@ -1059,9 +1071,10 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM, SCORES>::THREADS, Cfg<FMT, D
               tmem_ld_wait32(x[1]);
               Weighed w;
               if (CAP && !capped) {
-                w = weigh<true>(a, x, p, 1.f, m);
+                w = weigh<true, C::ROUND_ALL>(a, x, p, 1.f, m);
                 if (__all_sync(0xffffffffu, w.most <= a.poly_most)) {
                   l += w.sum;
+                  lr += w.rounded;
                   break;
                 }
                 cap_any(a, tS);
@@ -1092,11 +1105,12 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM, SCORES>::THREADS, Cfg<FMT, D
                     if (!((bits >> i) & 1)) x[c][i] = 0xFF800000u;
                 }
               }
-              w = weigh<false>(a, x, p, CAP || BIAS ? 1.f : a.scale2, (m == -INFINITY ? 0.f : m) - shift);
+              w = weigh<false, C::ROUND>(a, x, p, CAP || BIAS ? 1.f : a.scale2, (m == -INFINITY ? 0.f : m) - shift);
               w.most += shift;
               const bool grow = !CAP && (w.most > m + kSpanStep || (m == -INFINITY && w.most > m));
               if (!__any_sync(0xffffffffu, grow)) {
                 l += w.sum;
+                lr += w.rounded;
                 break;
               }
               const float mnew = w.most;
@@ -1105,6 +1119,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM, SCORES>::THREADS, Cfg<FMT, D
                 run = run && wait_product();
                 tc_fence_after();
                 l *= alpha;
+                lr *= alpha;
 #pragma unroll 1
                 for (int c = 0; c < D / 16; ++c) tmem_scale16(tO + 16 * c, alpha);
                 tmem_st_wait();
@@ -1197,7 +1212,14 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM, SCORES>::THREADS, Cfg<FMT, D
             part = a.raw + (tok * a.kv_heads * a.G + head) * D;
           }
         }
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        float inv = l > 0.f ? 1.f / l : 0.f;
+        // lse is of the exact weights; sums for a join are brought to them by the
+        // two sums' ratio
+        [[maybe_unused]] float ratio = 1.f;
+        if constexpr (C::ROUND) {
+          inv = lr > 0.f ? 1.f / lr : 0.f;
+          if (lr > 0.f) ratio = l * inv;
+        }
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
@@ -1222,7 +1244,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM, SCORES>::THREADS, Cfg<FMT, D
 #pragma unroll
               for (int half = 0; half < 2; ++half) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) w[i / 4][i % 4] = o[16 * half + i];
+                for (int i = 0; i < 16; ++i) w[i / 4][i % 4] = C::ROUND ? __float_as_uint(__uint_as_float(o[16 * half + i]) * ratio) : o[16 * half + i];
                 store_runs(w, valid ? part + 32 * c + 16 * half : nullptr);
               }
             }

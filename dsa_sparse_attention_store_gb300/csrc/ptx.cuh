@@ -392,6 +392,13 @@ __device__ __forceinline__ float ex2_denorm(float x) {
   return y;
 }
 
+// c + the bf16 of a pair's lower or upper half
+__device__ __forceinline__ float add_bf16(float c, unsigned short a) {
+  float d;
+  asm("add.f32.bf16 %0, %1, %2;" : "=f"(d) : "h"(a), "f"(c));
+  return d;
+}
+
 // 1 / x (the hardware's approximation, within 1 ulp)
 __device__ __forceinline__ float rcp(float x) {
   float y;

@@ -74,10 +74,14 @@ def tolerance(out, lse, wabs, qk, far, away, scale, D, keys, cap=0.0):
     most half and |z| 2^z / (1 + 2^z)^2 < 0.65 of the rest arrive, and a
     reciprocal and two roundings within 2^-23 each: below cap 2^-21. Bias: a
     rounded slope, product and sum, 3 2^-24 of the bias of a key with weight
-    (one below 1e-12 has none). lse takes the nearest key's bias off at its end."""
+    (one below 1e-12 has none). lse takes the nearest key's bias off at its end.
+    The results are over the sum of the rounded weights w_i (1 + e_i), |e_i| <=
+    2^-8: out = sum w_i (1 + e_i) v_i / (1 + sum w_i e_i), which is off by at most
+    sum w_i |e_i| |v_i| <= 2^-8 wabs, as counted there, and by |out| |sum w_i e_i|
+    <= 2^-8 |out| (1 + 2^-7) besides."""
     extra = cap * 2.0 ** -21 + far * 3 * 2.0 ** -24 + (cap + far) * 2.0 ** -23
     to, tl = plain_tolerance(out, lse, wabs, qk, scale, D, keys)
-    return to + wabs * (2.02 * extra)[..., None], tl + 2 * extra + away * 2.0 ** -22
+    return to + wabs * (2.02 * extra)[..., None] + np.abs(out) * (1.01 * 2.0 ** -8), tl + 2 * extra + away * 2.0 ** -22
 
 
 def batch_plan(old, new, table, num_pages, stack, count, T, own_from=None):
