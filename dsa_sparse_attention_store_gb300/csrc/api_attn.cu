@@ -252,35 +252,31 @@ dsa_status dsa_shared_attn(dsa_ctx* ctx, const dsa_attn_args* args, const dsa_sp
   return dsa::launch_span(ctx, *args, *span, cu_groups, shared_lens, n_groups, as_stream(stream));
 }
 
-dsa_status dsa_batch_plan(dsa_ctx* ctx, const int32_t* old_lens, const int32_t* new_lens, const int32_t* own_from, int32_t B,
-                          int32_t* page_table, int32_t max_pages, int32_t num_pages, int32_t* free_pages, int32_t free_cap,
-                          const int32_t* free_count, int32_t* free_left, int32_t* seq_lens, int32_t* cu_q, int32_t* seq_id,
-                          int32_t* cache_pos, int32_t* slots, int32_t T, dsa_stream_t stream) {
-  if (!ctx || B <= 0 || T < 0 || max_pages <= 0 || num_pages <= 0 || free_cap < 0) return DSA_ERR_INVALID_ARG;
-  if (B > 65536 || max_pages > 0x7FFFFFFF / 64 || num_pages > 0x7FFFFFFF / 64) return DSA_ERR_UNSUPPORTED;
-  if (!old_lens || !new_lens || !page_table || (!free_pages && free_cap) || !free_count || !free_left || !seq_lens || !cu_q ||
-      (T && (!seq_id || !cache_pos)))
+dsa_status dsa_batch_plan(dsa_ctx* ctx, const dsa_batch_args* args, dsa_stream_t stream) {
+  if (!ctx || !args) return DSA_ERR_INVALID_ARG;
+  const dsa_batch_args& p = *args;
+  if (p.B <= 0 || p.T < 0 || p.max_pages <= 0 || p.num_pages <= 0 || p.free_cap < 0) return DSA_ERR_INVALID_ARG;
+  if (p.B > 65536 || p.max_pages > 0x7FFFFFFF / 64 || p.num_pages > 0x7FFFFFFF / 64) return DSA_ERR_UNSUPPORTED;
+  if (!p.old_lens || !p.new_lens || !p.page_table || (!p.free_pages && p.free_cap) || !p.free_count || !p.free_left || !p.seq_lens ||
+      !p.cu_q || (p.T && (!p.seq_id || !p.cache_pos)))
     return DSA_ERR_INVALID_ARG;
-  struct Span {
+  struct Array {
     const int32_t* p;
     long long n;
   };
   // what is written comes first
-  const Span spans[] = {{page_table, static_cast<long long>(B) * max_pages}, {free_pages, free_cap}, {free_left, 1},
-                        {seq_lens, B}, {cu_q, B + 1LL}, {seq_id, T}, {cache_pos, T}, {slots, T},
-                        {old_lens, B}, {new_lens, B}, {own_from, B}, {free_count, 1}};
-  constexpr int kAll = sizeof(spans) / sizeof(spans[0]), kWritten = 8;
+  const Array arrays[] = {{p.page_table, static_cast<long long>(p.B) * p.max_pages}, {p.free_pages, p.free_cap}, {p.free_left, 1},
+                          {p.seq_lens, p.B}, {p.cu_q, p.B + 1LL}, {p.seq_id, p.T}, {p.cache_pos, p.T}, {p.slots, p.T},
+                          {p.old_lens, p.B}, {p.new_lens, p.B}, {p.own_from, p.B}, {p.free_count, 1}};
+  constexpr int kAll = sizeof(arrays) / sizeof(arrays[0]), kWritten = 8;
   for (int i = 0; i < kAll; ++i) {
-    if (!aligned(spans[i].p, 4)) return DSA_ERR_INVALID_ARG;
+    if (!aligned(arrays[i].p, 4)) return DSA_ERR_INVALID_ARG;
     for (int j = 0; j < i && j < kWritten; ++j)
-      if (spans[i].p && spans[j].p && spans[i].p < spans[j].p + spans[j].n && spans[j].p < spans[i].p + spans[i].n)
+      if (arrays[i].p && arrays[j].p && arrays[i].p < arrays[j].p + arrays[j].n && arrays[j].p < arrays[i].p + arrays[i].n)
         return DSA_ERR_INVALID_ARG;
   }
   if (const dsa_status s = dsa::check_device(ctx)) return s;
-  dsa::BatchPlanArgs a = {old_lens, new_lens, own_from, free_count, page_table, free_pages, free_left, seq_lens,
-                          cu_q,     seq_id,   cache_pos, slots,     ctx->status, B,         T,         max_pages,
-                          num_pages, free_cap};
-  return dsa::launch_batch_plan(ctx, a, as_stream(stream));
+  return dsa::launch_batch_plan(ctx, p, as_stream(stream));
 }
 
 }  // extern "C"

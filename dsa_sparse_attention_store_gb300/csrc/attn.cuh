@@ -129,7 +129,7 @@ struct Token {
 };
 
 struct SpanArgs : AttnArgs {
-  const int4* units;   // [slots][3], the words of a Unit
+  const int4* units;   // [slots][3], the words of a Unit; without one t0 = t1 = 0
   const int* tiles;    // [slots] tiles of a unit, 0 where there is none
   const int4* tokens;  // [Tq]
   const float* slopes; // [heads] or null
@@ -177,13 +177,12 @@ struct Cfg {
   // bias the first tile would be the one in which rows see the fewest keys
   // (packed documents 394 -> 429).
   static constexpr bool BACKWARDS = SCORES == kBiased;
-  // Whether results are over the sum of the weights as the product has them,
-  // rounded to bf16, which leaves out the rounding of a weight that outdoes the
-  // others: in all tiles where the tiles' bytes or their chain set the time; of
-  // 256-row units, whose time is the softmax's (687 -> 747 us), in capped ones'
-  // tiles that some row does not see whole. Rows of fewer than 64 keys have no
-  // others, and without a running maximum even one key's weight is not 1.
-  static constexpr bool ROUND_ALL = SPAN && FORM != kWide, ROUND = ROUND_ALL || SCORES == kCapped;
+  // Results over the sum of the weights as the product has them, rounded to bf16:
+  // without a running maximum even the weight of a row's only key is not 1, and
+  // its rounding would come on top of the result's. In tiles that some row does
+  // not see whole; rows of fewer than 64 keys have no others. (In all tiles, and
+  // without a cap too, it cost 3 % of a decode step and 9 to 11 % of a chunk.)
+  static constexpr bool ROUND = SCORES == kCapped;
   using Args = std::conditional_t<SPAN, SpanArgs, AttnArgs>;
   using Segment = std::conditional_t<SPAN, SpanSeg, Seg>;
   static constexpr bool SPARSE = FORM == kSparse || FORM == kSparseFew;
@@ -282,9 +281,14 @@ struct Iter {
   __device__ bool next(typename C::Segment& s) {
     if (left <= 0) return false;
     if constexpr (C::SPAN) {
-      int n;
-      while ((n = a.tiles[b]) == 0) advance();
-      const int4 x = a.units[3 * b], y = a.units[3 * b + 1], z = a.units[3 * b + 2];
+      int4 x, y, z;
+      while (true) {
+        x = a.units[3 * b];
+        y = a.units[3 * b + 1];
+        z = a.units[3 * b + 2];
+        if (y.y < y.z) break;  // a gap of the list has no tiles
+        advance();
+      }
       s.b = x.x;
       s.q0 = x.y;
       s.nd = x.z;
@@ -1071,7 +1075,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM, SCORES>::THREADS, Cfg<FMT, D
               tmem_ld_wait32(x[1]);
               Weighed w;
               if (CAP && !capped) {
-                w = weigh<true, C::ROUND_ALL>(a, x, p, 1.f, m);
+                w = weigh<true>(a, x, p, 1.f, m);
                 if (__all_sync(0xffffffffu, w.most <= a.poly_most)) {
                   l += w.sum;
                   lr += w.rounded;

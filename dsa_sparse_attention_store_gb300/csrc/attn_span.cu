@@ -138,7 +138,10 @@ __global__ void __launch_bounds__(256) span_plan_kernel(const AttnArgs a, const 
     ok = ok && from >= 0;
   }
   if (!ok || static_cast<long long>(r) * rows >= static_cast<long long>(nd) * a.G) {
-    if (lane == 0) *tiles = 0;
+    if (lane == 0) {
+      *tiles = 0;
+      (group ? p.group_units : p.units)[3LL * u + 1] = make_int4(0, 0, 0, 0);
+    }
     return;
   }
   const int r0 = r * rows;
@@ -426,8 +429,12 @@ dsa_status launch_span(dsa_ctx* ctx, const dsa_attn_args& p, const dsa_span& spa
     const dsa_status st = run(ctx, own.form, p.head_dim, tm, a, own.grid, stream);
     if (st != DSA_OK) return st;
     LaunchScope scope(ctx, DSA_K_ATTN_JOIN, stream);
+    // a row a warp, or, with so few units that they may have dozens of pieces, a
+    // few a block (64 decode steps 363 us with 4 rows of blocks and 372 with 8; one
+    // of 131072 keys and one kv head 43 and 32)
+    const bool many = static_cast<long long>(own.places) * p.kv_heads * 16 < own.grid;
     const cudaError_t e = launch_pdl(p.head_dim == 128 ? join_kernel<128, SpanArgs> : join_kernel<64, SpanArgs>,
-                                     dim3(own.grid, own.rows < 64 ? 8 : own.rows / 8), dim3(256), 0, stream, a, own.grid, own.rows);
+                                     dim3(own.grid, many ? 8 : own.rows / 8), dim3(256), 0, stream, a, own.grid, own.rows);
     return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
   }
   a.raw_mode = 2;

@@ -23,6 +23,10 @@
 namespace dsa {
 namespace {
 
+struct BatchPlanArgs : dsa_batch_args {
+  unsigned int* status;
+};
+
 constexpr int kPage = 64;
 constexpr int kMost = 0x7FFFFFFF;
 // Sums that shared memory has room for: of a sequence each up to 16384, of a run
@@ -100,7 +104,7 @@ __global__ void __launch_bounds__(THREADS) batch_plan_kernel(const BatchPlanArgs
       s_ended[r] = clamp_sum(e);
     }
   }
-  const int given = *a.free_count, count = min(max(given, 0), a.cap);
+  const int given = *a.free_count, count = min(max(given, 0), a.free_cap);
   __syncthreads();
   const int r0 = min(runs, tid * own), r1 = min(runs, r0 + own);
   // pages: of up to 4 sequences of below 2^25 in up to 17 runs
@@ -158,14 +162,14 @@ __global__ void __launch_bounds__(THREADS) batch_plan_kernel(const BatchPlanArgs
     for (int b = r * per; b < min(a.B, r * per + per); ++b) {
       const Request x = request(a, b);
       a.cu_q[b] = clamp_sum(t);
-      a.lens[b] = x.ok && !x.ends ? x.old + x.n : 0;
+      a.seq_lens[b] = x.ok && !x.ends ? x.old + x.n : 0;
       t += x.n;
     }
   }
   if (first == 0) {
     a.cu_q[a.B] = clamp_sum(all.tokens);
-    *a.left = static_cast<int>(min(max(left, 0LL), static_cast<long long>(a.cap)));
-    bad |= given != count || left < 0 || left > a.cap || all.tokens > a.T;
+    *a.free_left = static_cast<int>(min(max(left, 0LL), static_cast<long long>(a.free_cap)));
+    bad |= given != count || left < 0 || left > a.free_cap || all.tokens > a.T;
   }
 
   // the last run with sums[run] <= i
@@ -184,7 +188,7 @@ __global__ void __launch_bounds__(THREADS) batch_plan_kernel(const BatchPlanArgs
     j -= s_ended[run];
     for (int b = run * per; b < min(a.B, run * per + per); ++b) {
       const Request x = request(a, b);
-      if (j < x.ended) return a.table[static_cast<long long>(b) * a.max_pages + x.keep + j];
+      if (j < x.ended) return a.page_table[static_cast<long long>(b) * a.max_pages + x.keep + j];
       j -= x.ended;
     }
     return -1;
@@ -192,10 +196,10 @@ __global__ void __launch_bounds__(THREADS) batch_plan_kernel(const BatchPlanArgs
   // the i-th page that is taken
   auto taken = [&](long long i) -> int {
     const long long v = pool - 1 - i;
-    return v < 0 ? -1 : v < count ? a.stack[v] : returned(clamp_sum(v - count));
+    return v < 0 ? -1 : v < count ? a.free_pages[v] : returned(clamp_sum(v - count));
   };
   const long long tokens = min(all.tokens, static_cast<long long>(a.T));
-  const bool wide = EACH == 4 && !((reinterpret_cast<uintptr_t>(a.seq) | reinterpret_cast<uintptr_t>(a.pos) |
+  const bool wide = EACH == 4 && !((reinterpret_cast<uintptr_t>(a.seq_id) | reinterpret_cast<uintptr_t>(a.cache_pos) |
                                      reinterpret_cast<uintptr_t>(a.slots)) & 15);
   for (long long t0 = static_cast<long long>(first) * EACH; t0 < a.T; t0 += static_cast<long long>(step) * EACH) {
     int seq[EACH], pos[EACH], slot[EACH];
@@ -225,7 +229,7 @@ __global__ void __launch_bounds__(THREADS) batch_plan_kernel(const BatchPlanArgs
       pos[k] = x.old + static_cast<int>(t - at);
       if (pos[k] / kPage != p) {
         p = pos[k] / kPage;
-        page = p < x.pages ? a.table[static_cast<long long>(b) * a.max_pages + p] : taken(fresh + p - x.pages);
+        page = p < x.pages ? a.page_table[static_cast<long long>(b) * a.max_pages + p] : taken(fresh + p - x.pages);
       }
       const bool there = page >= 0 && page < a.num_pages;
       bad |= !there;
@@ -233,16 +237,16 @@ __global__ void __launch_bounds__(THREADS) batch_plan_kernel(const BatchPlanArgs
     }
     if (wide && t0 + EACH <= a.T) {
       if constexpr (EACH == 4) {
-        *reinterpret_cast<int4*>(a.seq + t0) = make_int4(seq[0], seq[1], seq[2], seq[3]);
-        *reinterpret_cast<int4*>(a.pos + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+        *reinterpret_cast<int4*>(a.seq_id + t0) = make_int4(seq[0], seq[1], seq[2], seq[3]);
+        *reinterpret_cast<int4*>(a.cache_pos + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
         if (a.slots) *reinterpret_cast<int4*>(a.slots + t0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
       }
     } else {
 #pragma unroll
       for (int k = 0; k < EACH; ++k)
         if (t0 + k < a.T) {
-          a.seq[t0 + k] = seq[k];
-          a.pos[t0 + k] = pos[k];
+          a.seq_id[t0 + k] = seq[k];
+          a.cache_pos[t0 + k] = pos[k];
           if (a.slots) a.slots[t0 + k] = slot[k];
         }
     }
@@ -257,11 +261,11 @@ __global__ void __launch_bounds__(THREADS) batch_plan_kernel(const BatchPlanArgs
       at += x.fresh;
       x = request(a, ++seq);
     }
-    a.table[static_cast<long long>(seq) * a.max_pages + x.pages + (i - at)] = taken(i);
+    a.page_table[static_cast<long long>(seq) * a.max_pages + x.pages + (i - at)] = taken(i);
   }
   // pages that came back and were not taken again
-  for (long long j = first; j < min(left, static_cast<long long>(a.cap)) - count; j += step)
-    a.stack[count + j] = returned(static_cast<int>(j));
+  for (long long j = first; j < min(left, static_cast<long long>(a.free_cap)) - count; j += step)
+    a.free_pages[count + j] = returned(static_cast<int>(j));
   if (bad) s_bad = 1;
   __syncthreads();
   if (tid == 0 && s_bad) atomicOr(a.status, DSA_DEV_BOUNDS);
@@ -278,7 +282,8 @@ cudaError_t launch(const BatchPlanArgs& a, int grid, cudaStream_t stream) {
 
 }  // namespace
 
-dsa_status launch_batch_plan(dsa_ctx* ctx, const BatchPlanArgs& a, cudaStream_t stream) {
+dsa_status launch_batch_plan(dsa_ctx* ctx, const dsa_batch_args& args, cudaStream_t stream) {
+  BatchPlanArgs a = {args, ctx->status};
   if (!ctx->batch_ready) {
     for (auto kern : {batch_plan_kernel<kThreads, 1>, batch_plan_kernel<kThreads, 4>})
       if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 12 * kSums) != cudaSuccess) return DSA_ERR_CUDA;

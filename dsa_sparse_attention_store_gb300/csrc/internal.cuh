@@ -142,12 +142,6 @@ size_t span_workspace(const dsa_ctx* ctx, int32_t Tq, int32_t B, int32_t groups,
 dsa_status launch_span(dsa_ctx* ctx, const dsa_attn_args& args, const dsa_span& span, const int32_t* cu_groups,
                        const int32_t* shared, int32_t groups, cudaStream_t stream);
 
-struct BatchPlanArgs {
-  const int32_t *old_lens, *new_lens, *own_from, *free_count;
-  int32_t *table, *stack, *left, *lens, *cu_q, *seq, *pos, *slots;
-  unsigned int* status;
-  int B, T, max_pages, num_pages, cap;
-};
-dsa_status launch_batch_plan(dsa_ctx* ctx, const BatchPlanArgs& a, cudaStream_t stream);
+dsa_status launch_batch_plan(dsa_ctx* ctx, const dsa_batch_args& args, cudaStream_t stream);
 
 }  // namespace dsa

@@ -44,6 +44,7 @@ class _RopeDesc(ctypes.Structure):  # dsa_rope_desc
 # dsa_attn_args, field by field with the C padding
 _ATTN_PACK = struct.Struct("@PqqPqqPPiiiiiPiPPiiPidPN").pack
 _SPAN_PACK = struct.Struct("@PPPdi4x").pack  # dsa_span
+_BATCH_PACK = struct.Struct("@12P5i4x").pack   # dsa_batch_args
 _KV_PAGE_BYTES = {}  # of (kv_heads, head_dim, fmt)
 
 
@@ -114,8 +115,7 @@ def lib() -> ctypes.CDLL:
         L.dsa_shared_attn_workspace_size.restype = _c_size
         L.dsa_span_attn.argtypes = [_c_ptr, ctypes.c_char_p, ctypes.c_char_p, _c_ptr]
         L.dsa_shared_attn.argtypes = [_c_ptr, ctypes.c_char_p, ctypes.c_char_p, _c_ptr, _c_ptr, _c_int, _c_ptr]
-        L.dsa_batch_plan.argtypes = [_c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_int, _c_ptr, _c_int, _c_int, _c_ptr, _c_int,
-                                     _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_int, _c_ptr]
+        L.dsa_batch_plan.argtypes = [_c_ptr, ctypes.c_char_p, _c_ptr]
         for f in (L.dsa_rope_create, L.dsa_rope_destroy, L.dsa_rope_apply, L.dsa_kv_store, L.dsa_kv_load,
                   L.dsa_tree_attn, L.dsa_sparse_attn, L.dsa_span_attn, L.dsa_shared_attn, L.dsa_batch_plan):
             f.restype = ctypes.c_int
@@ -547,15 +547,15 @@ class Context:
         i32, dev = torch.int32, _device()
         B, max_pages = page_table.shape
         T = seq_id.shape[0]
-        st = lib().dsa_batch_plan(
-            self._h, _ptr(old_lens, i32, (B,), "old_lens", dev), _ptr(new_lens, i32, (B,), "new_lens", dev),
-            None if own_from is None else _ptr(own_from, i32, (B,), "own_from", dev), B,
-            _ptr(page_table, i32, None, "page_table", dev), max_pages, num_pages,
-            _ptr(free_pages, i32, None, "free_pages", dev), free_pages.numel(), _ptr(free_count, i32, (1,), "free_count", dev),
+        a = _BATCH_PACK(
+            _ptr(old_lens, i32, (B,), "old_lens", dev), _ptr(new_lens, i32, (B,), "new_lens", dev),
+            0 if own_from is None else _ptr(own_from, i32, (B,), "own_from", dev), _ptr(free_count, i32, (1,), "free_count", dev),
+            _ptr(page_table, i32, None, "page_table", dev), _ptr(free_pages, i32, None, "free_pages", dev),
             _ptr(free_left, i32, (1,), "free_left", dev), _ptr(seq_lens, i32, (B,), "seq_lens", dev),
             _ptr(cu_q, i32, (B + 1,), "cu_q", dev), _ptr(seq_id, i32, (T,), "seq_id", dev),
-            _ptr(cache_pos, i32, (T,), "cache_pos", dev), None if slots is None else _ptr(slots, i32, (T,), "slots", dev),
-            T, _raw_stream(stream))
+            _ptr(cache_pos, i32, (T,), "cache_pos", dev), 0 if slots is None else _ptr(slots, i32, (T,), "slots", dev),
+            B, T, max_pages, num_pages, free_pages.numel())
+        st = lib().dsa_batch_plan(self._h, a, _raw_stream(stream))
         if st != 0:
             raise DsaError("dsa_batch_plan", st)
 

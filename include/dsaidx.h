@@ -426,10 +426,16 @@ typedef struct {
  * row of a unit (up to 256 rows of neighbouring tokens) sees are neither read
  * nor computed. Everything else is as in dsa_tree_attn: layouts, formats,
  * strides, rows that see no key, infinities and NaN in hidden places, bad
- * pages and lengths, limits; B <= 2^20. The workspace holds the list of units
- * and 16 bytes a token besides dsa_attn_workspace_size's. A row measures its
- * distances from its own place or, where it lies outside its span, from the
- * nearest place in it, and adds the rest to lse. */
+ * pages and lengths, limits; B <= 2^20. cu_q[B] may be less than Tq (a padded
+ * batch): the rows behind are left as they are. The workspace holds the list of
+ * units and 16 bytes a token besides dsa_attn_workspace_size's. A row measures
+ * its distances from its own place or, where it lies outside its span, from the
+ * nearest place in it, and adds the rest to lse.
+ * Sums over the keys stay finite where the visible |v| add up to less than
+ * 2^111, and with a cap of 44 to 62, whose weights are taken under one exponent
+ * and reach 2^(2.89 cap - 120), where they add up to less than 2^(247 - 2.89
+ * cap). cap and scale / cap (times 3) have to be normal fp32 numbers, else
+ * DSA_ERR_INVALID_ARG. */
 size_t dsa_span_attn_workspace_size(const dsa_ctx* ctx, int32_t Tq, int32_t B, int32_t heads,
                                     int32_t kv_heads, int32_t head_dim);
 dsa_status dsa_span_attn(dsa_ctx* ctx, const dsa_attn_args* args, const dsa_span* span,
@@ -448,8 +454,9 @@ dsa_status dsa_span_attn(dsa_ctx* ctx, const dsa_attn_args* args, const dsa_span
  *               recorded, as it is for a negative shared_lens[g]; one that is
  *               longer than the first sequence counts as that long.
  *  n_groups     1 .. 2^20.
- * The workspace also holds each row's fp32 sums over the prefix (Tq * heads *
- * (head_dim + 2) * 4 bytes). */
+ * The workspace also holds each row's fp32 sums over the prefix and over its own
+ * keys (2 * Tq * heads * (head_dim + 2) * 4 bytes) and a second
+ * dsa_attn_workspace_size. */
 size_t dsa_shared_attn_workspace_size(const dsa_ctx* ctx, int32_t Tq, int32_t B, int32_t n_groups,
                                       int32_t heads, int32_t kv_heads, int32_t head_dim);
 dsa_status dsa_shared_attn(dsa_ctx* ctx, const dsa_attn_args* args, const dsa_span* span,
@@ -468,36 +475,40 @@ dsa_status dsa_shared_attn(dsa_ctx* ctx, const dsa_attn_args* args, const dsa_sp
  * and place; what is left of it stays free, *free_left pages, and those that
  * came back are written behind the others. With too few pages the last places
  * get -1 (in the page table and in slots) and DSA_ERR_DEVICE_BOUNDS is recorded.
- * free_count and old_lens are only read, so a call can be made again with the
- * same result; the next step takes free_left and seq_lens for them.
+ * free_count and old_lens are only read, and page table entries of old tokens
+ * stay, so a call can be made again with the same result, or with fewer tokens
+ * after a shortage (a row's -1 would come back to the pool as they are); the next
+ * step takes free_left and seq_lens for them.
  * Out, besides page_table and free_pages: seq_lens[b] = old + new, cu_q
  * (cu_q[0] = 0, sums of the new tokens), and for each new token t its
  * sequence, its place, and its slot page * 64 + place % 64; -1 in all three for
- * t >= cu_q[B] (a padded batch).
- *  old_lens, new_lens  (device) [B] int32. A sequence with a negative old
- *              length or own_from, or more than 64 * max_pages tokens, counts as
- *              empty (no tokens, seq_lens 0, no pages either way) and
- *              DSA_ERR_DEVICE_BOUNDS is recorded.
- *  own_from    (device) [B] int32, or NULL for zeros: pages at the front of the
- *              row that belong to another sequence (a shared prefix).
- *  page_table  (device) [B][max_pages] int32, in and out.
- *  free_pages  (device) [free_cap] int32, in and out; pages that would land
- *              past it are dropped, a count out of 0 .. free_cap is taken for
- *              the nearest, DSA_ERR_DEVICE_BOUNDS recorded in both cases, and
- *              for page ids not in 0 .. num_pages-1 that a token would use
- *              (its slot is -1).
- *  free_count, free_left  (device) one int32 each.
- *  seq_lens    (device) [B];  cu_q (device) [B+1];  seq_id, cache_pos, slots
- *              (device) [T], slots NULL if not wanted. Tokens past T are left
- *              out and DSA_ERR_DEVICE_BOUNDS recorded; their pages are taken.
+ * t >= cu_q[B] (a padded batch: dsa_kv_store skips such tokens, and reports
+ * them as out of range).
+ * A sequence with a negative old length or own_from, or more than 64 * max_pages
+ * tokens, counts as empty (no tokens, seq_lens 0, no pages either way); a
+ * free_count out of 0 .. free_cap is taken for the nearest; pages that would
+ * land past free_cap are dropped; a page id not in 0 .. num_pages-1 that a token
+ * would use gives it the slot -1; tokens past T are left out, though their pages
+ * are taken. DSA_ERR_DEVICE_BOUNDS is recorded in each case.
  * Arrays that are written must not overlap others. B <= 65536, 64 * max_pages
  * and 64 * num_pages < 2^31, else DSA_ERR_UNSUPPORTED. */
-dsa_status dsa_batch_plan(dsa_ctx* ctx, const int32_t* old_lens, const int32_t* new_lens,
-                          const int32_t* own_from, int32_t B, int32_t* page_table, int32_t max_pages,
-                          int32_t num_pages, int32_t* free_pages, int32_t free_cap,
-                          const int32_t* free_count, int32_t* free_left, int32_t* seq_lens,
-                          int32_t* cu_q, int32_t* seq_id, int32_t* cache_pos, int32_t* slots, int32_t T,
-                          dsa_stream_t stream);
+typedef struct {
+  const int32_t* old_lens;    /* (device) [B] tokens in the cache */
+  const int32_t* new_lens;    /* (device) [B] tokens to come, negative where a sequence ends */
+  const int32_t* own_from;    /* (device) [B], or NULL for zeros: pages at the front of the row that
+                                 belong to another sequence (a shared prefix) */
+  const int32_t* free_count;  /* (device) one int32 */
+  int32_t* page_table;        /* (device) [B][max_pages], in and out */
+  int32_t* free_pages;        /* (device) [free_cap], in and out */
+  int32_t* free_left;         /* (device) one int32 */
+  int32_t* seq_lens;          /* (device) [B] */
+  int32_t* cu_q;              /* (device) [B+1] */
+  int32_t* seq_id;            /* (device) [T] */
+  int32_t* cache_pos;         /* (device) [T] */
+  int32_t* slots;             /* (device) [T] or NULL */
+  int32_t B, T, max_pages, num_pages, free_cap;
+} dsa_batch_args;
+dsa_status dsa_batch_plan(dsa_ctx* ctx, const dsa_batch_args* args, dsa_stream_t stream);
 
 /* Kernel timing, for benchmarks and profiling. While enabled, the library
  * records a CUDA event pair on the launch stream around each kernel it

@@ -66,15 +66,17 @@ def test_batch_plan_refuses(L):
         return at
 
     def call(c=FAKE, B=2, mp=3, pages=9, cap=9, T=5, **kw):
+        from dsa_sparse_attention_store_gb300.dsaidx import _BATCH_PACK
         a = arrays(**kw)
-        return L.dsa_batch_plan(c, a["old"], a["new"], a["own"], B, a["table"], mp, pages, a["free"], cap, a["count"], a["left"],
-                                a["lens"], a["cu"], a["seq"], a["pos"], a["slot"], T, None)
+        v = [(a[k].value or 0) if a[k] is not None else 0 for k in ("old", "new", "own", "count", "table", "free", "left", "lens", "cu", "seq",
+                                                                    "pos", "slot")]
+        return L.dsa_batch_plan(c, _BATCH_PACK(*v, B, T, mp, pages, cap), None)
 
     import torch
     fine = 3                                    # got as far as asking for the device, where there is none
     if not torch.cuda.is_available():
         assert call() == fine and call(own=None, slot=None) == fine and call(T=0, seq=None, pos=None, slot=None) == fine
-    assert call(c=None) == 1
+    assert call(c=None) == 1 and L.dsa_batch_plan(FAKE, None, None) == 1
     for kw in (dict(B=0), dict(B=-1), dict(T=-1), dict(mp=0), dict(pages=0), dict(cap=-1), dict(seq=None), dict(pos=None)):
         assert call(**kw) == 1, kw
     for k in ("old", "new", "table", "free", "count", "left", "lens", "cu"):
@@ -122,6 +124,8 @@ def test_arguments_are_packed_as_the_header_has_them(L, tmp_path):
     src.write_text('#include "dsaidx.h"\n'
                    f"_Static_assert(sizeof(dsa_span) == {len(_span())} && offsetof(dsa_span, slopes) == 16 && "
                    "offsetof(dsa_span, cap) == 24 && offsetof(dsa_span, window) == 32, \"dsa_span\");\n"
+                   "_Static_assert(sizeof(dsa_batch_args) == 120 && offsetof(dsa_batch_args, slots) == 88 && offsetof(dsa_batch_args, B) == 96 && "
+                   "offsetof(dsa_batch_args, free_cap) == 112, \"dsa_batch_args\");\n"
                    f"_Static_assert(DSA_K_ALL == {len(dsaidx.KERNEL_KINDS)}, \"kinds\");\n")
     subprocess.run([cc, "-fsyntax-only", "-I", os.path.join(root, "include"), str(src)], check=True)
     assert ctypes.sizeof(ctypes.c_void_p) == 8

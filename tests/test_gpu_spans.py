@@ -327,6 +327,45 @@ def test_no_prefix_is_span_attn_and_no_span_is_tree_attn(ctx):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("groups", [None, [(2, 192)]])
+def test_padded_batches_leave_the_rows_behind_as_they_were(ctx, fmt, groups):
+    # more rows of q than the sequences have
+    import torch
+    c = SpanCase(93, [300, 200], [3, 40], 2, 4, 64, fmt, groups=groups, cap=30.0, window=120)
+    d = c.device()
+    pad = 37
+    d["q"] = torch.cat([d["q"], torch.full((pad, c.H, c.D), float("nan"), dtype=torch.bfloat16, device="cuda")])
+    rows, c.Tq = c.Tq, c.Tq + pad
+    out, lse = c.run(ctx, d=d)
+    c.Tq = rows
+    c.check(out[:rows], lse[:rows])
+    assert (out[rows:] == 77.0).all() and (lse[rows:] == 77.0).all()
+    assert ctx.device_status() == 0
+
+
+@pytest.mark.parametrize("groups", [None, [(4, 640)]])
+def test_calls_on_two_streams_at_once(ctx, groups):
+    # each with a workspace of its own
+    import torch
+    cs = [SpanCase(94 + i, [700 + 100 * i, 900, 650, 800], [5, 1, 30, 2], 2, 8, 128, A.FP8, groups=groups, cap=[0.0, 40.0][i]) for i in range(2)]
+    ds = [c.device() for c in cs]
+    wants = [c.run(ctx, d=d) for c, d in zip(cs, ds)]
+    outs = [[torch.empty_like(x) for x in w] for w in wants]
+    wss = [torch.empty(c.workspace_size(ctx), dtype=torch.uint8, device="cuda") for c in cs]
+    streams = [torch.cuda.Stream() for _ in cs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, d, o, ws, s in zip(cs, ds, outs, wss, streams):
+            with torch.cuda.stream(s):
+                c.run(ctx, out=o[0], lse=o[1], ws=ws, d=d)
+    torch.cuda.synchronize()
+    for c, w, o in zip(cs, wants, outs):
+        c.check(*w)
+        assert torch.equal(w[0], o[0]) and torch.equal(w[1], o[1])
+    assert ctx.device_status() == 0
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 def test_cache_past_32_bits(ctx, fmt):
     # a cache of more than 4 GB, the sequences' pages at its far end
     import torch
