@@ -12,10 +12,11 @@
 //
 // What bounds it: a step of 64 tokens one launch and the chain of loads lengths
 // -> page -> slot, 3.2 us. 16384 sequences with a million tokens, of which a ninth
-// end, 27 us (12.6 MB, 1.9 us at the copy rate): the sums over all sequences,
-// which every block makes for itself (about 10), the bisections and dependent
+// end, 25.8 us (12.6 MB, 1.9 us at the copy rate): the sums over all sequences,
+// which every block makes for itself (about 9), the bisections and dependent
 // loads of a thread's tokens (8), and of the pages that come back (5). With a walk
-// along 16 sequences for each token it took 57.
+// along 16 sequences for each token it took 57; with sums divided between the
+// four blocks of a cluster 28, for a cluster's launch and barriers take as long.
 #include <algorithm>
 
 #include "internal.cuh"
@@ -61,7 +62,27 @@ __device__ __forceinline__ Request request(const BatchPlanArgs& a, int b) {
 
 struct Sums {
   long long tokens, fresh, ended;
+  __device__ __forceinline__ void add(const Sums& x) {
+    tokens += x.tokens;
+    fresh += x.fresh;
+    ended += x.ended;
+  }
 };
+
+// over a warp's lanes, the own one included
+__device__ __forceinline__ Sums scan(Sums x) {
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const Sums y = {__shfl_up_sync(0xffffffffu, x.tokens, d), __shfl_up_sync(0xffffffffu, x.fresh, d),
+                    __shfl_up_sync(0xffffffffu, x.ended, d)};
+    if (static_cast<int>(threadIdx.x & 31) >= d) x.add(y);
+  }
+  return x;
+}
+
+__device__ __forceinline__ Sums shfl(const Sums& x, int from) {
+  return {__shfl_sync(0xffffffffu, x.tokens, from), __shfl_sync(0xffffffffu, x.fresh, from), __shfl_sync(0xffffffffu, x.ended, from)};
+}
 
 __device__ __forceinline__ int clamp_sum(long long x) { return static_cast<int>(min(x, static_cast<long long>(kMost))); }
 
@@ -107,7 +128,7 @@ __global__ void __launch_bounds__(THREADS) batch_plan_kernel(const BatchPlanArgs
   const int given = *a.free_count, count = min(max(given, 0), a.free_cap);
   __syncthreads();
   const int r0 = min(runs, tid * own), r1 = min(runs, r0 + own);
-  // pages: of up to 4 sequences of below 2^25 in up to 17 runs
+  // pages, below 2^25 of a sequence: in up to 17 runs of up to 4 sequences, or 33 of one
   long long sum_tokens = 0;
   uint32_t sum_fresh = 0, sum_ended = 0;
 #pragma unroll 4
@@ -116,32 +137,21 @@ __global__ void __launch_bounds__(THREADS) batch_plan_kernel(const BatchPlanArgs
     sum_fresh += s_fresh[r];
     sum_ended += s_ended[r];
   }
-  const Sums sum = {sum_tokens, sum_fresh, sum_ended};
-  Sums inc = sum;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const long long t = __shfl_up_sync(0xffffffffu, inc.tokens, d), f = __shfl_up_sync(0xffffffffu, inc.fresh, d),
-                    e = __shfl_up_sync(0xffffffffu, inc.ended, d);
-    if (lane >= d) {
-      inc.tokens += t;
-      inc.fresh += f;
-      inc.ended += e;
-    }
-  }
+  const Sums sum = {sum_tokens, sum_fresh, sum_ended}, inc = scan(sum);
   if (lane == 31) s_warp[warp] = inc;
   __syncthreads();
   Sums all = {0, 0, 0}, before = {inc.tokens - sum.tokens, inc.fresh - sum.fresh, inc.ended - sum.ended};
+  if constexpr (THREADS == 1024) {  // a warp's sums a lane: one after another they take a microsecond more
+    const Sums warps = scan(s_warp[lane]), x = shfl(warps, max(warp, 1) - 1);
+    if (warp) before.add(x);
+    all = shfl(warps, 31);
+  } else {
 #pragma unroll
-  for (int w = 0; w < THREADS / 32; ++w) {
-    const Sums x = s_warp[w];
-    if (w < warp) {
-      before.tokens += x.tokens;
-      before.fresh += x.fresh;
-      before.ended += x.ended;
+    for (int w = 0; w < THREADS / 32; ++w) {
+      const Sums x = s_warp[w];
+      if (w < warp) before.add(x);
+      all.add(x);
     }
-    all.tokens += x.tokens;
-    all.fresh += x.fresh;
-    all.ended += x.ended;
   }
 #pragma unroll 4
   for (int r = r0; r < r1; ++r) {
@@ -271,7 +281,7 @@ __global__ void __launch_bounds__(THREADS) batch_plan_kernel(const BatchPlanArgs
   if (tid == 0 && s_bad) atomicOr(a.status, DSA_DEV_BOUNDS);
 }
 
-constexpr int kSmallThreads = 128, kThreads = 1024;
+constexpr int kSmallThreads = 128, kMidThreads = 256, kThreads = 1024;
 
 template <int THREADS, int EACH>
 cudaError_t launch(const BatchPlanArgs& a, int grid, cudaStream_t stream) {
@@ -285,24 +295,29 @@ cudaError_t launch(const BatchPlanArgs& a, int grid, cudaStream_t stream) {
 dsa_status launch_batch_plan(dsa_ctx* ctx, const dsa_batch_args& args, cudaStream_t stream) {
   BatchPlanArgs a = {args, ctx->status};
   if (!ctx->batch_ready) {
-    for (auto kern : {batch_plan_kernel<kThreads, 1>, batch_plan_kernel<kThreads, 4>})
+    for (auto kern : {batch_plan_kernel<kMidThreads, 1>, batch_plan_kernel<kThreads, 1>, batch_plan_kernel<kThreads, 4>})
       if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 12 * kSums) != cudaSuccess) return DSA_ERR_CUDA;
     ctx->batch_ready = 1;
   }
   LaunchScope scope(ctx, DSA_K_BATCH_PLAN, stream);
   const int most = std::max(a.T, a.B);
-  // One small block for a decode step: fewer warps to meet. Four tokens a thread
-  // where sequences have as many. A block on each SM, or as many as
-  // have two sequences or tokens a thread, or eight pages that may come back.
+  // One small block for a decode step: fewer warps to meet. Blocks of 256 while
+  // they have few sums and tokens a thread (1000 sequences of a token each 6.5 us,
+  // in blocks of 1024 7.5; 100 of 1000 tokens 6.0 and 9.2; but 4000 of 64 tokens
+  // 15.9 and 14.0, 16384 of one 15.7 and 14.4). Beyond, four tokens a thread
+  // where sequences have as many (in the smaller blocks that takes 1 to 3 us more).
+  // A block on each SM, or as many as have two sequences or tokens a thread, or
+  // eight pages that may come back.
   const long long pages = static_cast<long long>(a.B) * a.max_pages;
   auto blocks = [&](int threads) {
     return static_cast<int>(std::min(std::max({1LL, (most + 2LL * threads - 1) / (2 * threads), pages / (8 * threads)}),
                                      static_cast<long long>(ctx->num_sms)));
   };
-  const int grid = blocks(kThreads);
-  const cudaError_t e = most <= 2 * kSmallThreads         ? launch<kSmallThreads, 1>(a, blocks(kSmallThreads), stream)
-                        : a.T / 8 >= a.B && a.T >= 16384 ? launch<kThreads, 4>(a, grid, stream)
-                                                          : launch<kThreads, 1>(a, grid, stream);
+  const bool mid = a.T <= 131072 && a.B <= 8192, four = a.T / 8 >= a.B && a.T >= 16384;
+  const cudaError_t e = most <= 2 * kSmallThreads ? launch<kSmallThreads, 1>(a, blocks(kSmallThreads), stream)
+                        : mid                     ? launch<kMidThreads, 1>(a, blocks(kMidThreads), stream)
+                        : four                    ? launch<kThreads, 4>(a, blocks(kThreads), stream)
+                                                  : launch<kThreads, 1>(a, blocks(kThreads), stream);
   return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 

@@ -83,6 +83,31 @@ def test_plan_matches_reference(ctx, B, most, ends, seed):
     _case(ctx, rng, old, new, 16, need + seed, own_from=own, T=int(new.clip(0).sum()) + [0, 1, 900][seed], slots=seed != 1)
 
 
+@pytest.mark.parametrize("B,most", [(300, 9000), (4095, 40), (8192, 3), (8193, 3), (16384, 40), (16385, 3), (40002, 12)])
+@pytest.mark.parametrize("shift", [0, 1])             # whether four tokens are one store
+def test_many_sequences_and_tokens(ctx, B, most, shift):
+    import torch
+    rng = np.random.default_rng([B, shift])
+    old = rng.integers(0, 200, B)
+    new = rng.integers(0, most, B)
+    new[rng.random(B) < 0.2] = -1
+    new[-3:] = [7, -1, 5]
+    own = rng.integers(0, 3, B)
+    width = -(-(200 + most) // 64)
+    table, stack, pages = _pool(rng, old, width, 30000)
+    T = int(new.clip(0).sum()) + 101
+    t = {}
+    _run(ctx, old, new, table, pages, stack, 30000, T, own, keep=t)
+    if shift:
+        for k, v in (("table", table), ("stack", stack)):
+            t[k].copy_(torch.from_numpy(v))
+        for k in ("seq", "pos", "slot"):
+            t[k] = torch.full((T + 1,), 99, dtype=torch.int32, device="cuda")[1:]
+        ctx.batch_plan(t["old"], t["new"], t["table"], pages, t["stack"], t["count"], t["left"], t["lens"], t["cu"],
+                       t["seq"], t["pos"], t["slot"], own_from=t["own"])
+    _check(ctx, t, S.batch_plan(old, new, table, pages, stack, 30000, T, own))
+
+
 def test_lengths_around_pages(ctx):
     rng = np.random.default_rng(1)
     old = [o for o in (0, 1, 63, 64, 65, 127, 128) for _ in range(6)]
