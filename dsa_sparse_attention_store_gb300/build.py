@@ -21,7 +21,8 @@ LIB = os.path.join(HERE, "libdsaidx.so")
 SOURCES = ["api.cu", "store.cu", "topk.cu", "topk_fp8.cu", "topk_fp4.cu", "topk_static.cu",
            "api_attn.cu", "rope.cu", "kv.cu", "attn.cu", "attn_fp8.cu", "attn_fp4.cu",
            "attn_span.cu", "span_bf16.cu", "span_fp8.cu", "span_fp4.cu", "span_cap_bf16.cu", "span_cap_fp8.cu",
-           "span_cap_fp4.cu", "span_bias_bf16.cu", "span_bias_fp8.cu", "span_bias_fp4.cu", "batch.cu"]
+           "span_cap_fp4.cu", "span_bias_bf16.cu", "span_bias_fp8.cu", "span_bias_fp4.cu", "span_wide_bf16.cu",
+           "span_wide_fp8.cu", "span_wide_fp4.cu", "batch.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-Xptxas", "-warn-spills"]

@@ -132,13 +132,20 @@ struct Token {
   int lo, hi, place, ctx;
 };
 
-struct SpanArgs : AttnArgs {
+struct Cap {
+  float cap2, to_cap;  // cap log2 e, 2 log2 e scale / cap; 0: no cap
+  // Capped score log2 e / x in powers of x^2, and where that holds. x = q.k; in
+  // kWideCap x = scale q.k / cap, a multiplication more, for there the powers of
+  // scale / cap may leave fp32's range.
+  float poly[5], poly_most;
+  float to_ratio;  // scale / cap
+};
+
+struct SpanArgs : AttnArgs, Cap {
   const int4* units;   // [slots][3], the words of a Unit; without one t0 = t1 = 0
   const int* tiles;    // [slots] tiles of a unit, 0 where there is none
   const int4* tokens;  // [Tq]
   const float* slopes; // [heads] or null
-  float cap2, to_cap;  // cap log2 e, 2 log2 e scale / cap; 0: no cap
-  float poly[5], poly_most;  // capped score log2 e / q.k in powers of (q.k)^2, and where that holds
   float fixed;               // what every row is weighed under where capped scores allow it, else -inf
   int units_n;
   int beside;          // this launch reads nothing that the one before it writes, see attn_kernel
@@ -169,8 +176,10 @@ struct Start {
 // forms. The listed units' kernels are apart, because one with all of their code
 // spilled (a chunk of 2048 tokens without a cap took 611 us in it, 568 alone):
 // scores as they are; capped ones, all weighed under one exponent; biased ones,
-// capped or not, and caps too wide for that.
-enum Scores { kUnlisted = 0, kAsTheyAre = 1, kCapped = 2, kBiased = 3, kScores = 4 };
+// capped or not; and caps too wide for one exponent, biased or not, whose small
+// scores need more care (the chunk with a bias and a cap of 20 took 1418 us by
+// that kernel, 1298 by the biased one's).
+enum Scores { kUnlisted = 0, kAsTheyAre = 1, kCapped = 2, kBiased = 3, kWideCap = 4, kScores = 5 };
 
 template <int FMT, int D, int FORM, int SCORES = kUnlisted>
 struct Cfg {
@@ -180,7 +189,7 @@ struct Cfg {
   // not move in every one (2048 tokens behind 8192 1176 -> 634 us). Without a
   // bias the first tile would be the one in which rows see the fewest keys
   // (packed documents 394 -> 429).
-  static constexpr bool BACKWARDS = SCORES == kBiased;
+  static constexpr bool BACKWARDS = SCORES == kBiased || SCORES == kWideCap;
   // Results over the sum of the weights as the product has them, rounded to bf16:
   // without a running maximum even the weight of a row's only key is not 1, and
   // its rounding would come on top of the result's. In tiles that some row does
@@ -550,14 +559,6 @@ __device__ __forceinline__ Token token_at(const SpanArgs& a, long long t) {
 __device__ __forceinline__ int nearest(const Token& y) { return max(y.lo, min(y.place, y.hi - 1)); }
 __device__ __forceinline__ float away(const Token& y) { return fabsf(static_cast<float>(y.place - nearest(y))); }
 
-// cap tanh(scale q.k / cap) of 64 keys, times log2 e. tanh y = 1 - 2 / (1 + e^2y),
-// within 2^-22, for infinities too: two more of the special-function unit's
-// operations a score, which a tile takes only where some |y| is above kCapPoly.
-// Below, y P(y^2) with a minimax polynomial (within 2^-23) on the fp32 pipe; its
-// coefficients are the host's, with scale and cap in them.
-constexpr int kCapTerms = 5;
-constexpr double kCapPoly = 0.625;
-
 // One step of turning four lanes' four 16-byte runs around: lanes that differ in
 // bit N exchange the runs that differ in it.
 template <int N>
@@ -588,15 +589,25 @@ __device__ __forceinline__ void store_runs(uint32_t (&w)[4][4], void* to) {
   }
 }
 
-// capped score log2 e / q.k of two scores whose squares are u
-__device__ __forceinline__ unsigned long long cap_factor(const SpanArgs& a, unsigned long long u) {
+// cap tanh(y), y = scale q.k / cap, times log2 e. Where all |y| are at most
+// kCapPoly y P(y^2) with a minimax polynomial on the fp32 pipe, within 2^-20 of
+// itself however small y is. Else 1 - 2 / (1 + e^2y), for infinities too, by two
+// operations of the special-function unit. Its error of 2^-22 is one of 1, for
+// the difference cancels where y is small, and so one of cap in the score: enough
+// for caps of up to 62 (2^-16).
+constexpr int kCapTerms = 5;
+constexpr double kCapPoly = 0.625;
+constexpr float kCapOne = 90.f;  // cap log2 e up to which the rows can be weighed under one exponent
+
+// Cap::poly at two x^2
+__device__ __forceinline__ unsigned long long cap_factor(const Cap& a, unsigned long long u) {
   unsigned long long y = pack2(a.poly[kCapTerms - 1], a.poly[kCapTerms - 1]);
 #pragma unroll
   for (int k = kCapTerms - 2; k >= 0; --k) y = fma2(y, u, pack2(a.poly[k], a.poly[k]));
   return y;
 }
 
-// in TMEM, where a tile's scores stay capped: in registers the 64 chains spill
+// In TMEM, where a tile's scores stay capped: in registers the 64 chains spill.
 __device__ __forceinline__ void cap_any(const SpanArgs& a, uint32_t taddr) {
 #pragma unroll 1
   for (int c = 0; c < 2; ++c) {
@@ -611,15 +622,45 @@ __device__ __forceinline__ void cap_any(const SpanArgs& a, uint32_t taddr) {
   tmem_st_wait();
 }
 
+// The same for wide caps: scores that are small enough take the polynomial beside
+// others that are not (a key at -cap has no weight, and those that have some may
+// have small scores). Not inlined: the code that few tiles reach cost the others
+// more registers (2048 tokens behind 8192 with a cap of 63 992 us, so 927).
+inline __device__ __noinline__ void cap_each(const Cap a, uint32_t taddr) {
+#pragma unroll 1
+  for (int c = 0; c < 2; ++c) {
+    uint32_t x[32];
+    tmem_ld32(taddr + 32 * c, x);
+    tmem_ld_wait32(x);
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+      const float x0 = __uint_as_float(x[i]), x1 = __uint_as_float(x[i + 1]);
+      const unsigned long long y = mul2(pack2(x0, x1), pack2(a.to_ratio, a.to_ratio)), u = mul2(y, y);
+      float u0, u1, y0, y1;
+      unpack2(u, u0, u1);
+      unpack2(mul2(cap_factor(a, u), y), y0, y1);
+      // twice the largest caps is no fp32 number
+      const float z0 = fmaf(-2.f * rcp(1.f + ex2(x0 * a.to_cap)), a.cap2, a.cap2);
+      const float z1 = fmaf(-2.f * rcp(1.f + ex2(x1 * a.to_cap)), a.cap2, a.cap2);
+      x[i] = __float_as_uint(u0 <= a.poly_most ? y0 : z0);
+      x[i + 1] = __float_as_uint(u1 <= a.poly_most ? y1 : z1);
+    }
+    tmem_st32(taddr + 32 * c, x);
+  }
+  tmem_st_wait();
+}
+
 // 64 scores capped by the polynomial, in place; whether all of a row's were
 // small enough for it.
+template <bool RATIO>
 __device__ __forceinline__ bool cap_near(const SpanArgs& a, uint32_t (&x)[2][32]) {
   float most = 0.f;
 #pragma unroll
   for (int c = 0; c < 2; ++c)
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const unsigned long long s = pack2(__uint_as_float(x[c][2 * i]), __uint_as_float(x[c][2 * i + 1]));
+      unsigned long long s = pack2(__uint_as_float(x[c][2 * i]), __uint_as_float(x[c][2 * i + 1]));
+      if constexpr (RATIO) s = mul2(s, pack2(a.to_ratio, a.to_ratio));
       const unsigned long long u = mul2(s, s);
       float u0, u1, y0, y1;
       unpack2(u, u0, u1);
@@ -974,7 +1015,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM, SCORES>::THREADS, Cfg<FMT, D
       [[maybe_unused]] float slope2 = 0.f;
       if constexpr (C::SPAN) {
         if constexpr (SCORES == kCapped) m = a.fixed;
-        if (SCORES == kBiased && a.slopes && valid) {
+        if (SCORES >= kBiased && a.slopes && valid) {
           near = nearest(token_at(a, s.q0 + qi));
           slope2 = a.slopes[s.h * a.G + mine.g] * 1.4426950408889634f;
         }
@@ -1063,8 +1104,8 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM, SCORES>::THREADS, Cfg<FMT, D
             if (valid && (p0 + kTile > s.full || p0 < s.lo)) see &= span_mask(a, s.q0 + qi, token_at(a, s.q0 + qi), p0);
             [[maybe_unused]] const float from = static_cast<float>(near - p0);
             const bool some = !__all_sync(0xffffffffu, see == ~0ull);  // a key that some row does not see
-            constexpr bool CAP = SCORES == kCapped, BIAS = SCORES == kBiased;
-            [[maybe_unused]] bool capped = !CAP && !(BIAS && a.cap2 != 0.f);  // in TMEM, or not to be
+            constexpr bool CAP = SCORES == kCapped, WIDE_CAP = SCORES == kWideCap, BIAS = SCORES == kBiased || WIDE_CAP;
+            [[maybe_unused]] bool capped = !CAP && !(BIAS && (WIDE_CAP || a.cap2 != 0.f));  // in TMEM, or not to be
             if constexpr (CAP) {
               if (some) {  // masks come after the cap, and few tiles have one
                 cap_any(a, tS);
@@ -1091,12 +1132,15 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM, SCORES>::THREADS, Cfg<FMT, D
               }
               float shift = 0.f;  // of all of the tile's exponents
               if constexpr (BIAS) {
-                if (!capped && !__all_sync(0xffffffffu, cap_near(a, x))) {
-                  cap_any(a, tS);
+                if (!capped && !__all_sync(0xffffffffu, cap_near<WIDE_CAP>(a, x))) {
+                  if constexpr (WIDE_CAP)
+                    cap_each(a, tS);
+                  else
+                    cap_any(a, tS);
                   capped = true;
                   continue;
                 }
-                if (a.cap2 == 0.f) {
+                if (!WIDE_CAP && a.cap2 == 0.f) {
 #pragma unroll
                   for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -1813,10 +1857,10 @@ dsa_status run_fp8(dsa_ctx* ctx, int form, int D, const CUtensorMap& tm, const A
 dsa_status run_fp4(dsa_ctx* ctx, int form, int D, const CUtensorMap& tm, const AttnArgs& a, int grid, cudaStream_t stream);
 
 // Listed units' kernels of one cache format and treatment of the scores:
-// span_*.cu, span_cap_*.cu, span_bias_*.cu, so that they compile in parallel.
+// span_*.cu, span_cap_*.cu, span_bias_*.cu, span_wide_*.cu, so that they compile in parallel.
 using RunSpan = dsa_status(dsa_ctx* ctx, int form, int D, const CUtensorMap& tm, const SpanArgs& a, int grid, cudaStream_t stream);
 RunSpan run_span_bf16, run_span_fp8, run_span_fp4, run_span_cap_bf16, run_span_cap_fp8, run_span_cap_fp4, run_span_bias_bf16,
-    run_span_bias_fp8, run_span_bias_fp4;
+    run_span_bias_fp8, run_span_bias_fp4, run_span_wide_bf16, run_span_wide_fp8, run_span_wide_fp4;
 
 }  // namespace at
 }  // namespace dsa

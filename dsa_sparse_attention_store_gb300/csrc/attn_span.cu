@@ -317,20 +317,27 @@ void cap_args(double scale, double cap, SpanArgs& a) {
   const double log2e = 1.4426950408889634, k = scale / cap;
   a.cap2 = static_cast<float>(cap * log2e);
   a.to_cap = static_cast<float>(2 * log2e * k);
-  double power = k * cap * log2e;
+  a.to_ratio = static_cast<float>(k);
+  const double range = cap * log2e;
+  if (range > kCapOne) {
+    for (int i = 0; i < kCapTerms; ++i) a.poly[i] = static_cast<float>(kTanh[i] * range);
+    a.poly_most = static_cast<float>(kCapPoly * kCapPoly);
+    return;
+  }
+  double power = k * range;
   bool fits = true;
   for (int i = 0; i < kCapTerms; ++i, power *= k * k) {
     a.poly[i] = static_cast<float>(kTanh[i] * power);
     fits = fits && std::isfinite(a.poly[i]) && std::fabs(a.poly[i]) >= 1.17549435e-38f;
   }
   a.poly_most = static_cast<float>(kCapPoly / k * (kCapPoly / k));
-  // caps thousands of times their usual size: never by the polynomial
+  // a scale far from the usual ones (for a cap of 50, below 0.003): never by the polynomial
   if (!fits || !std::isfinite(a.poly_most)) a.poly_most = -1.f;
   // Capped scores lie within cap of zero, so all rows can be weighed under the
   // same exponent and no maximum is looked for: 2^H for the largest possible
   // weight, H 8 or as much as keeps the smallest at 2^-120. Up to cap 62.
-  const double range = cap * log2e, room = std::fmax(8.0, 2 * range - 120);
-  if (range <= 90 && !a.slopes) a.fixed = static_cast<float>(range - room);
+  const double room = std::fmax(8.0, 2 * range - 120);
+  if (!a.slopes) a.fixed = static_cast<float>(range - room);
 }
 
 // What follows the attention's own workspace.
@@ -417,11 +424,12 @@ dsa_status launch_span(dsa_ctx* ctx, const dsa_attn_args& p, const dsa_span& spa
                    static_cast<const AttnArgs&>(a), plan) != cudaSuccess)
       return DSA_ERR_CUDA;
   }
-  static constexpr RunSpan* kRun[3][3] = {{run_span_bf16, run_span_fp8, run_span_fp4},
+  static constexpr RunSpan* kRun[4][3] = {{run_span_bf16, run_span_fp8, run_span_fp4},
                                           {run_span_cap_bf16, run_span_cap_fp8, run_span_cap_fp4},
-                                          {run_span_bias_bf16, run_span_bias_fp8, run_span_bias_fp4}};
-  // a cap too wide to weigh all rows under one exponent goes with slopes of zero
-  RunSpan* const run = kRun[a.slopes || (a.cap2 != 0.f && a.fixed == -INFINITY) ? 2 : a.cap2 != 0.f ? 1 : 0][p.fmt];
+                                          {run_span_bias_bf16, run_span_bias_fp8, run_span_bias_fp4},
+                                          {run_span_wide_bf16, run_span_wide_fp8, run_span_wide_fp4}};
+  const bool wide_cap = span.cap * 1.4426950408889634 > kCapOne;
+  RunSpan* const run = kRun[wide_cap ? 3 : a.slopes ? 2 : a.cap2 != 0.f ? 1 : 0][p.fmt];
   a.units = plan.units;
   a.tiles = plan.tiles;
   a.units_n = plan.n;

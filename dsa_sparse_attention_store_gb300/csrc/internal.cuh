@@ -31,7 +31,7 @@ struct dsa_ctx {
   float* gamma;          // [128]
   unsigned int* status;  // device status word
   void* encode_tiled;    // cuTensorMapEncodeTiled entry point
-  uint64_t attn_ready[2];  // attention kernels whose shared memory limit is raised
+  uint64_t attn_ready[3];  // attention kernels whose shared memory limit is raised
   int batch_ready;         // dsa_batch_plan's kernel, the same
   // kernel timing (dsa_profile_*)
   int prof_on;
