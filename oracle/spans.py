@@ -72,14 +72,21 @@ def tolerance(out, lse, wabs, qk, far, away, scale, D, keys, cap=0.0):
     """attention.tolerance, and what the changes add to a score's error. cap:
     tanh y = 1 - 2 / (1 + 2^z) has 2^z within 2^-22 (1 + |z| 2^-2), of which at
     most half and |z| 2^z / (1 + 2^z)^2 < 0.65 of the rest arrive, and a
-    reciprocal and two roundings within 2^-23 each: below cap 2^-21. Bias: a
-    rounded slope, product and sum, 3 2^-24 of the bias of a key with weight
-    (one below 1e-12 has none). lse takes the nearest key's bias off at its end.
+    reciprocal and two roundings within 2^-23 each: below cap 2^-21. An odd
+    polynomial of y, for |y| up to 0.625, is within 2^-20 of its value (its fit
+    2^-20.8, six roundings of 2^-24 each). Scores under a cap that needs a running
+    maximum (cap log2 e > 90) are owed that: where |y| is above 0.625, cap 2^-21 <
+    2^-20 cap tanh 0.625. A capped score is at most cap and at most scale sum
+    |q||k|. Bias: a rounded slope, product and sum, 3 2^-24 of the bias of a key
+    with weight (one below 1e-12 has none). lse takes the nearest key's bias off at
+    its end.
     The results are over the sum of the rounded weights w_i (1 + e_i), |e_i| <=
     2^-8: out = sum w_i (1 + e_i) v_i / (1 + sum w_i e_i), which is off by at most
     sum w_i |e_i| |v_i| <= 2^-8 wabs, as counted there, and by |out| |sum w_i e_i|
     <= 2^-8 |out| (1 + 2^-7) besides."""
-    extra = cap * 2.0 ** -21 + far * 3 * 2.0 ** -24 + (cap + far) * 2.0 ** -23
+    most = np.minimum(cap, scale * qk)
+    capped = cap * 2.0 ** -21 if cap * np.log2(np.e) <= 90 else np.minimum(cap * 2.0 ** -21, most * 2.0 ** -20)
+    extra = capped + far * 3 * 2.0 ** -24 + (most + far) * 2.0 ** -23
     to, tl = plain_tolerance(out, lse, wabs, qk, scale, D, keys)
     return to + wabs * (2.02 * extra)[..., None] + np.abs(out) * (1.01 * 2.0 ** -8), tl + 2 * extra + away * 2.0 ** -22
 
