@@ -334,9 +334,12 @@ void cap_args(double scale, double cap, SpanArgs& a) {
   // a scale far from the usual ones (for a cap of 50, below 0.003): never by the polynomial
   if (!fits || !std::isfinite(a.poly_most)) a.poly_most = -1.f;
   // Capped scores lie within cap of zero, so all rows can be weighed under the
-  // same exponent and no maximum is looked for: 2^H for the largest possible
-  // weight, H 8 or as much as keeps the smallest at 2^-120. Up to cap 62.
-  const double room = std::fmax(8.0, 2 * range - 120);
+  // same exponent and no maximum is looked for: the largest possible weight is 2^H.
+  // H is 8, or as much as keeps the smallest one at 2^-72 or, from a cap of 50 on,
+  // as far below 1 as 2^H is above: a row whose keys all score near -cap has no
+  // other weights, and its values are to keep their bits in fp32 sums just as the
+  // ones of a row near cap are to keep them finite.
+  const double room = std::fmax(8.0, std::fmin(2 * range - 72, range));
   if (!a.slopes) a.fixed = static_cast<float>(range - room);
 }
 

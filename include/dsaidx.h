@@ -432,9 +432,11 @@ typedef struct {
  * its distances from its own place or, where it lies outside its span, from the
  * nearest place in it, and adds the rest to lse.
  * Sums over the keys stay finite where the visible |v| add up to less than
- * 2^111, and with a cap of 44 to 62, whose weights are taken under one exponent
- * and reach 2^(2.89 cap - 120), where they add up to less than 2^(247 - 2.89
- * cap). cap and scale / cap (times 3) have to be normal fp32 numbers, else
+ * 2^111. With a cap of 31 to 62 that is 2^(127 - H), H the smaller of 2.89 cap -
+ * 72 and 1.45 cap, because weights are taken under one exponent; they are 2^-72 or
+ * more (2^(-1.45 cap) with a cap above 50), so that values keep their bits down to
+ * |v| of 2^-54 (2^(1.45 cap - 126)) in a row whose keys all score near -cap.
+ * cap and scale / cap (times 3) have to be normal fp32 numbers, else
  * DSA_ERR_INVALID_ARG. */
 size_t dsa_span_attn_workspace_size(const dsa_ctx* ctx, int32_t Tq, int32_t B, int32_t heads,
                                     int32_t kv_heads, int32_t head_dim);
