@@ -148,7 +148,6 @@ struct SpanArgs : AttnArgs, Cap {
   const float* slopes; // [heads] or null
   float fixed;               // what every row is weighed under where capped scores allow it, else -inf
   int units_n;
-  int beside;          // this launch reads nothing that the one before it writes, see attn_kernel
   int raw_mode;        // whole units' sums go to `raw`, for rows_join_kernel: 1 all, 2 those with Unit::base
   float2* raw_ml;      // [Tq][heads] maximum and sum of weights
   float* raw;          // [Tq][heads][D]
@@ -820,17 +819,10 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM, SCORES>::THREADS, Cfg<FMT, D
     tmem_alloc(&sh.tmem, C::TMEM);
     tmem_relinquish();
   }
-  // The second of two passes starts as the first one's CTAs make room: it reads
-  // what the launch before that wrote, which had ended before the first one let
-  // its successor start (the fence drops what this SM's L1 may have of it from
-  // before). It ends after the first one, for the join waits for it alone.
-  bool beside = false;
-  if constexpr (C::SPAN) beside = a.beside;
-  if (beside && tid == C::THREADS - 1) __threadfence();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (!beside) pdl_wait();
+  pdl_wait();
   pdl_trigger();
   long long begin, count;
   make_plan<C>(a, sh, cta, grid, begin, count);
@@ -1801,7 +1793,6 @@ __global__ void __launch_bounds__(Cfg<FMT, D, FORM, SCORES>::THREADS, Cfg<FMT, D
     tc_fence_after();
     tmem_dealloc(sh.tmem, C::TMEM);
   }
-  if (beside) pdl_wait();
 }
 
 template <int FMT, int D, int FORM, int SCORES, class Args>

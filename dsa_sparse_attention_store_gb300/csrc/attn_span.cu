@@ -449,13 +449,11 @@ dsa_status launch_span(dsa_ctx* ctx, const dsa_attn_args& p, const dsa_span& spa
     return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
   }
   a.raw_mode = 2;
-  a.beside = 1;
   a.ends = reinterpret_cast<int2*>(ws + w.ends);
   a.raw_ml = reinterpret_cast<float2*>(ws + w.raw_ml);
   a.raw = reinterpret_cast<float*>(ws + w.raw);
   SpanArgs b = a;
   b.raw_mode = 1;
-  b.beside = 0;
   b.units = plan.group_units;
   b.tiles = plan.group_tiles;
   b.units_n = plan.group_n;
