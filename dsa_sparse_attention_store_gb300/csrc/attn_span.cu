@@ -65,10 +65,14 @@ __device__ __forceinline__ bool read_group(const AttnArgs& a, const SpanPlan& p,
 }
 
 // Whole pages that group g's sequences read from the first one's row; one
-// sequence alone has none to share.
+// sequence alone has none to share. Nor has a group whose queries do not lie
+// between those of q: it has no units, and its good sequences read all their keys
+// themselves.
 __device__ __forceinline__ int shared_pages(const AttnArgs& a, const SpanPlan& p, int g) {
   int b0, b1, q0, nd, len;
   if (!read_group(a, p, g, b0, b1) || b1 - b0 < 2 || !read_seq(a, b0, q0, nd, len)) return 0;
+  const int q1 = a.cu_q[b1];
+  if (q1 < q0 || q1 > a.Tq) return 0;
   return max(0, min(p.shared[g], len)) / kTile;
 }
 

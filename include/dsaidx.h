@@ -427,10 +427,12 @@ typedef struct {
  * nor computed. Everything else is as in dsa_tree_attn: layouts, formats,
  * strides, rows that see no key, infinities and NaN in hidden places, bad
  * pages and lengths, limits; B <= 2^20. cu_q[B] may be less than Tq (a padded
- * batch): the rows behind are left as they are. The workspace holds the list of
- * units and 16 bytes a token besides dsa_attn_workspace_size's. A row measures
- * its distances from its own place or, where it lies outside its span, from the
- * nearest place in it, and adds the rest to lse.
+ * batch): the rows behind are left as they are. Units are found by bisection in
+ * cu_q: where it decreases, which is reported, any sequence may be left out. The
+ * workspace holds the list of units and 16 bytes a token besides
+ * dsa_attn_workspace_size's. A row measures its distances from its own place or,
+ * where it lies outside its span, from the nearest place in it, and adds the rest
+ * to lse.
  * Sums over the keys stay finite where the visible |v| add up to less than
  * 2^111. With a cap of 31 to 62 that is 2^(127 - H), H the smaller of 2.89 cap -
  * 72 and 1.45 cap, because weights are taken under one exponent; they are 2^-72 or
@@ -454,7 +456,9 @@ dsa_status dsa_span_attn(dsa_ctx* ctx, const dsa_attn_args* args, const dsa_span
  *  cu_groups    (device) [n_groups+1] int32, non-decreasing, within 0 .. B. A
  *               group out of range shares nothing and DSA_ERR_DEVICE_BOUNDS is
  *               recorded, as it is for a negative shared_lens[g]; one that is
- *               longer than the first sequence counts as that long.
+ *               longer than the first sequence counts as that long. A group
+ *               whose first sequence is inconsistent, or whose queries end past
+ *               Tq, shares nothing either.
  *  n_groups     1 .. 2^20.
  * The workspace also holds each row's fp32 sums over the prefix and over its own
  * keys (2 * Tq * heads * (head_dim + 2) * 4 bytes) and a second
