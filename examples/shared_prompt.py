@@ -12,7 +12,7 @@ A pool of pages serves every sequence. The server's steps are
 The decode steps are also made with span_attn, which reads the prompt once a
 sample, and the largest difference is reported.
 
-    python examples/shared_prompt.py [--prompt 4509] [--samples 8] [--steps 4] [--fmt bf16]
+    python examples/shared_prompt.py [--prompt 4509] [--document 700] [--samples 8] [--steps 4] [--fmt bf16]
 """
 from __future__ import annotations
 
@@ -25,8 +25,9 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 FORMATS = {"bf16": 0, "fp8": 1, "fp4": 2}
 
 
-def run(prompt=4509, samples=8, steps=4, fmt="bf16", heads=32, kv_heads=4, head_dim=128, cap=50.0, seed=0):
-    """Runs the steps, returns a dict of what they computed."""
+def run(prompt=4509, samples=8, steps=4, fmt="bf16", heads=32, kv_heads=4, head_dim=128, cap=50.0, seed=0, document=700):
+    """Runs the steps, returns a dict of what they computed. document: tokens of
+    each of the prompt's documents."""
     import torch
 
     from dsa_sparse_attention_store_gb300 import PAGE_SIZE, Context, Rope, kv_page_bytes
@@ -38,7 +39,7 @@ def run(prompt=4509, samples=8, steps=4, fmt="bf16", heads=32, kv_heads=4, head_
 
     # what a server keeps: the context, a rotary plan, the cache, the pool and the rows of B sequences
     B, width = samples + 1, -(-(prompt + steps) // PAGE_SIZE)
-    pages = width + 2 * samples
+    pages = -(-prompt // PAGE_SIZE) + samples * (width - prompt // PAGE_SIZE)  # the prompt's, and each sample's own behind its whole ones
     ctx = Context(max_pos=64)
     rope = Rope(ctx, rot_dim=head_dim, max_pos=prompt + steps)
     cache = torch.zeros(pages * kv_page_bytes(kv_heads, head_dim, f), dtype=torch.uint8, device=dev)
@@ -58,14 +59,14 @@ def run(prompt=4509, samples=8, steps=4, fmt="bf16", heads=32, kv_heads=4, head_
         ctx.kv_store(k, v, place, seq, table, cache, pages, f, rope=rope)
 
     got = {}
-    # 1. the prompt is sequence 0, packed from documents of 700 tokens
+    # 1. the prompt is sequence 0, packed from documents
     seq, place = step([prompt] + [0] * samples, prompt)
     k, v, q = normal(prompt, kv_heads, head_dim), normal(prompt, kv_heads, head_dim), normal(prompt, heads, head_dim) * 3
     write(seq, place, k, v)
     ctx.rope_apply(q, place, rope)
     out, lse = torch.empty_like(q), torch.empty((prompt, heads), device=dev)
     ws = torch.empty(ctx.span_attn_workspace_size(prompt, B, heads, kv_heads, head_dim), dtype=torch.uint8, device=dev)
-    ctx.span_attn(q, cache, pages, f, kv_heads, table, lens, cu_q, out, ws, lse=lse, cap=cap, first=place - place % 700)
+    ctx.span_attn(q, cache, pages, f, kv_heads, table, lens, cu_q, out, ws, lse=lse, cap=cap, first=place - place % document)
     got.update(prompt_q=q.clone(), prompt_out=out, prompt_lse=lse)
 
     # 2. the samples point to the prompt's whole pages; its last tokens they have for themselves
@@ -105,11 +106,12 @@ def run(prompt=4509, samples=8, steps=4, fmt="bf16", heads=32, kv_heads=4, head_
 def main():
     p = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     p.add_argument("--prompt", type=int, default=4509)
+    p.add_argument("--document", type=int, default=700)
     p.add_argument("--samples", type=int, default=8)
     p.add_argument("--steps", type=int, default=4)
     p.add_argument("--fmt", choices=FORMATS, default="bf16")
     a = p.parse_args()
-    r = run(a.prompt, a.samples, a.steps, a.fmt)
+    r = run(a.prompt, a.samples, a.steps, a.fmt, document=a.document)
     if r["status"]:
         raise SystemExit(f"device status {r['status']}")
     far = max(float((s["lse"] - s["alone_lse"]).abs().max()) for s in r["steps"])
