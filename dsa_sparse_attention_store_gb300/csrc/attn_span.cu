@@ -8,7 +8,10 @@
 // sequence b that begins at its row r0 = r rows has the place
 //   floor(cu_q[b] G / rows) + b + r
 // in the list: different for all units, in order, and with at most one gap a
-// sequence, so no scan over the sequences comes first.
+// sequence, so no scan over the sequences comes first. In the list of groups the
+// places of rows that share nothing are gaps too; the attention's warps pass gaps
+// one by one, where they come to the end of the list for a kv head (64 decode steps
+// behind a prefix beside a prefill of 8192 tokens 1432 us, apart 1241 and 91).
 //
 // Behind shared prefixes there are two lists. The first takes a group's
 // sequences for one, with all of their tokens, and the whole pages that they

@@ -511,7 +511,8 @@ class Context:
         """dsa_span_attn: as tree_attn(), each new token over a span of places.
         first, last: int32 [Tq], the first place and one past the last one that
         a token sees; window: how many places it looks back over, itself
-        included; cap: scores become cap * tanh(score / cap); slopes: fp32
+        included (of places, with a mask too: a drafted token's depth is not
+        counted); cap: scores become cap * tanh(score / cap); slopes: fp32
         [heads], times the distance in places, taken off the scores."""
         a = self._attn_args(q, cache, num_pages, fmt, kv_heads, page_table, seq_lens, cu_q, out, workspace, mask,
                             lse, scale)

@@ -409,7 +409,10 @@ dsa_status dsa_sparse_attn(dsa_ctx* ctx, const dsa_attn_args* args, const int32_
  *   j < seq_lens[b], and its mask bit where j is a new token and there is a mask.
  * So first cuts a packed prompt into documents, last lets the tokens of a
  * prefix see each other both ways (the larger of p + 1 and the prefix's
- * length), window looks back over so many places, itself included.
+ * length), window looks back over so many places, itself included. A window counts
+ * places also where a mask makes drafted tokens a tree: a token whose depth is less
+ * than its place among the new ones then sees that many keys fewer than a window of
+ * positions has. first can say such a window.
  * Scores are s = scale q.k; with cap > 0 they become cap tanh(s / cap), then
  * with slopes s - slopes[head] |p - j|. Distances are of places, so slopes
  * and a mask of drafted tokens (whose depth is not their place) together are
