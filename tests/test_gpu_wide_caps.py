@@ -83,3 +83,29 @@ def test_keys_at_the_largest_caps(ctx, slopes):  # noqa: F811
     y = c.q.astype(np.float64).sum(-1) * float(A.bf16_value(far)[0]) / cap
     assert np.allclose(lse.double().cpu().numpy(), cap * np.tanh(y), rtol=2.0 ** -17, atol=0)
     assert ctx.device_status() == 0
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("groups", [None, [(2, 256), (1, 0)]])
+@pytest.mark.parametrize("how", ["tree", "bias", "window"])
+def test_wide_caps_with_masks_biases_and_prefixes(ctx, fmt, groups, how):  # noqa: F811
+    for cap in (70.0, 1e6):
+        c = SpanCase(6, [400, 300, 90], [3, 40, 9], 2, 4, 128, fmt, groups=groups, masked=how == "tree", cap=cap,
+                     slopes=True if how == "bias" else None, window=150 if how == "window" else 0)
+        c.check(*c.run(ctx))
+    assert ctx.device_status() == 0
+
+
+@pytest.mark.parametrize("groups", [None, [(2, 64)]])
+def test_hidden_values_under_wide_caps(ctx, groups):  # noqa: F811
+    # keys and values that are not finite where no row sees them, in tiles that rows see in part
+    c = SpanCase(7, [200, 150], [4, 40], 2, 4, 64, A.BF16, groups=groups, cap=1e5)
+    c.mods["first"] = np.full(c.Tq, 40, np.int32)
+    ref = c.reference()
+    kc, _, vc, _ = A.fields(c.cache, c.pages, c.kv, c.D, c.fmt)
+    for bits, codes in ((0x7F80, kc), (0x7FC0, vc)):
+        for b in range(c.B):
+            codes.view(np.uint16)[c.table[b, 0], :, :40] = bits
+    out, lse = c.run(ctx)
+    c.check(out, lse, ref=ref)
+    assert ctx.device_status() == 0
